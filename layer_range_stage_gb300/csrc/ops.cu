@@ -12,15 +12,16 @@
 
 #include "../../include/stage_ops.h"
 #include "kernels.cuh"
+#include "ops_error.h"
 
 // Scratch of stage_op_attention_decode_static: one array per device for the life of the
 // process.  In host code this name is only a handle: its device address comes from
 // cudaGetSymbolAddress, looked up once per device with that device current.
 static __device__ __align__(256) unsigned char g_attn_static_scratch[STAGE_OP_STATIC_SCRATCH_BYTES];
 
-namespace {
+namespace lrs {
 
-thread_local std::string g_op_error;
+static thread_local std::string g_op_error;
 
 int op_err(int code, const char* fmt, ...) {
   char buf[512];
@@ -37,13 +38,22 @@ int op_cuda(cudaError_t e, const char* where) { return op_err(STAGE_E_CUDA, "%s:
 // A C++ exception inside an entry point (a host staging buffer that could not be allocated)
 // ends the call with STAGE_E_HOST instead of crossing the C ABI; recording the message may
 // itself fail, which is ignored.
-int host_failure(const char* what) noexcept {
+int op_host_failure(const char* what) noexcept {
   try {
     g_op_error = std::string("host: ") + what;
   } catch (...) {
   }
   return STAGE_E_HOST;
 }
+
+}  // namespace lrs
+
+using lrs::op_cuda;
+using lrs::op_err;
+
+namespace {
+
+int host_failure(const char* what) noexcept { return lrs::op_host_failure(what); }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
@@ -84,7 +94,7 @@ int check_attention(const float* q, const uint16_t* kc, const uint16_t* vc, cons
 
 extern "C" {
 
-const char* stage_op_last_error(void) { return g_op_error.c_str(); }
+const char* stage_op_last_error(void) { return lrs::g_op_error.c_str(); }
 
 int stage_op_q8_device_bytes(int64_t rows, int64_t cols, size_t* q_bytes, size_t* s_bytes) try {
   if (rows <= 0 || cols <= 0 || cols > (1 << 30) || !q_bytes || !s_bytes) return op_err(STAGE_E_INVALID, "bad shape");
