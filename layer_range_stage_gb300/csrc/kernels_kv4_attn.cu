@@ -1,4 +1,18 @@
 // Attention over the paged 4-bit KV cache (sm_103a).
+//
+// Mathematics.  With a score's exponent in base 2, z_j = log2(e) / sqrt(D) * sum_b sk_jb sum_{d in b} q_d (c_jd - 8),
+//   o_d = sum_j 2^(z_j - r) sv_jb (c'_jd - 8) / sum_j 2^(z_j - r)
+// for any r.  The codes minus 8 are exact in fp16, so both inner products run on the tensor cores
+// (mma.sync m16n8k16, float32 accumulation) on integers; the block scales multiply the K product's partial
+// sums and, because V's position is the summed index, the probabilities: x_jb = 2^(z_j - r) sv_jb.
+// q (scaled by a power of two into fp16's range) and x are each split into a high and a low fp16 value, 22
+// bits together: the result is float32's, not fp16's.  r runs above max_j (z_j + log2 |sv_j|) - 11, so that the
+// largest x lies near 2^11 .. 2^15 whatever the scales are, and fp16's range ends 2^36 below it.
+//
+// Split of the work.  Rows (sequence, KV head, block of columns) times units of 128 positions form one line
+// of units in memory order, cut into equal pieces, one per resident CTA: ragged batches load every SM
+// alike, whatever the lengths, which only the device knows.  A row cut by piece borders is merged by the last
+// of its CTAs to arrive, in the order of the positions.
 
 #include <cfloat>
 
@@ -8,76 +22,605 @@
 
 namespace lrs {
 
-// A warp has one (token, query head): its lanes hold D / 32 dims each, positions go by one after another
-// with a running maximum and sum.
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) { return (float)v; }
+namespace {
 
-template <int D, typename T>
-__global__ void __launch_bounds__(128) kv4_attn_kernel(const Kv4AttnArgs a) {
-  constexpr int NB = D / 32, N = D / 32;  // lane l has dims N l .. N l + N - 1
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(w / a.n_q_heads), j = (int)(w % a.n_q_heads);
-  if (t >= a.n_tok || t >= a.cu_q[a.n_seqs]) return;
-  int lo = 0;  // the last sequence that begins at or before t
-  for (int hi = a.n_seqs; hi - lo > 1;) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_q[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int k_in = t - a.cu_q[lo], c = a.cu_q[lo + 1] - a.cu_q[lo];
-  if (k_in < 0 || k_in >= a.max_q) return;
-  const long long len = min((long long)min(a.seq_len[lo], a.max_len), (long long)a.table_stride * a.c.page_len);
-  const long long last = len - c + k_in;
-  const int h = j / (a.n_q_heads / a.c.n_kv_heads);
-  float q[N], o[N], m = -INFINITY, sum = 0.f;
-  const T* qp = reinterpret_cast<const T*>(a.q) + (long long)t * a.q_stride + j * D + lane * N;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = to_f32(qp[i]) * a.scale;
-    o[i] = 0.f;
-  }
-  const int dim = lane * N, block = dim / 32, l = (dim / 4) & 7, sh = 4 * (dim & 3);
-  for (long long p = 0; p <= last; ++p) {
-    const int page = a.table[(long long)lo * a.table_stride + p / a.c.page_len];
-    if (page < 0 || page >= a.c.n_pages) continue;
-    const uint8_t* tile = kv4_tile<D>(a.c, page * a.c.page_len + (int)(p % a.c.page_len), h);
-    const int in = (int)(p % kKv4Tile);
-    const int ck = *reinterpret_cast<const uint16_t*>(tile + kv4_k_off<D>(in, block, l)) >> sh;
-    const int cv = *reinterpret_cast<const uint16_t*>(tile + kv4_half(D) + kv4_v_off<D>(in, block, l)) >> sh;
-    const float sk = h2f_bits(*reinterpret_cast<const uint16_t*>(tile + kv4_codes(D) + (in * NB + block) * 2));
-    const float sv = h2f_bits(*reinterpret_cast<const uint16_t*>(tile + kv4_half(D) + kv4_codes(D) + (in * NB + block) * 2));
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(q[i], sk * (float)((ck >> 4 * i & 15) - 8), s);
-    s = warp_sum(s);
-    const float top = fmaxf(m, s), keep = expf(m - top), e = expf(s - top);
-    sum = sum * keep + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = fmaf(e, sv * (float)((cv >> 4 * i & 15) - 8), o[i] * keep);
-    m = top;
-  }
-  T* out = reinterpret_cast<T*>(a.out) + (long long)t * a.out_stride + j * D + dim;
-#pragma unroll
-  for (int i = 0; i < N; ++i) out[i] = (T)(sum != 0.f ? o[i] / sum : 0.f);
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kUnitTiles = kWarps;  // a unit: one tile of 16 positions per warp
+constexpr int kStages = 4;          // tiles in flight per warp, less one
+constexpr int kFlush = 16;          // tiles between two flushes of the accumulators
+constexpr int kMaxCtas = 1024;
+constexpr int kSlack = 4;           // r is raised when a score passes it by 2^kSlack
+constexpr float kTop = 11.f;
+
+// floats of a partial result in the workspace: eight columns' outputs, (r, sum) of each column
+__host__ __device__ constexpr int slot_floats(int D) { return 8 * D + 16; }
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-size_t kv4_attention_ws_bytes(int, int, int, int, int, int) { return 256; }
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
+  return (uint32_t)__half_as_ushort(lo) | (uint32_t)__half_as_ushort(hi) << 16;
+}
+
+// Eight codes to four half2: h[t] = (code t, code t + 4) - 8, the odd t times 16.  1024 + c is the fp16 number
+// 0x6400 | c, and 1024 + 16 c is 0x6400 | c << 4: one logic operation and one addition per pair, both exact.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {
+  const __half2 o1 = __floats2half2_rn(-1032.f, -1032.f), o16 = __floats2half2_rn(-1152.f, -1152.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = i ? w >> 8 : w;
+    const uint32_t a = (x & 0x000f000fu) | 0x64006400u, b = (x & 0x00f000f0u) | 0x64006400u;
+    const __half2 ha = __hadd2(*reinterpret_cast<const __half2*>(&a), o1);
+    const __half2 hb = __hadd2(*reinterpret_cast<const __half2*>(&b), o16);
+    h[2 * i] = *reinterpret_cast<const uint32_t*>(&ha);
+    h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+  }
+}
+
+__device__ __forceinline__ float2 h2_to_f2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+
+// A bound of the exponents of the numbers in these fp16 pairs: 2^e > |s| for every finite one.
+template <int N>
+__device__ __forceinline__ float exponent_above(const uint32_t (&s)[N]) {
+  __half2 m = __habs2(*reinterpret_cast<const __half2*>(&s[0]));
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&s[i])));  // NaN loses
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+  const uint32_t top = max(u >> 16, u & 0xffffu);
+  return (float)(int)min(top >> 10, 30u) - 14.f;
+}
+
+struct AttnRow {
+  int seq, head, cbase;      // sequence, KV head, first column
+  int start, count, len;     // first query token of the sequence, its tokens, its positions
+};
+
+// Eight neighbouring elements (i a multiple of 8, rows 16-byte aligned).
+__device__ __forceinline__ void load8(const void* p, int dtype, long long i, float (&v)[8]) {
+  if (dtype == KV4_F32) {
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+    const float4 x = q[0], y = q[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    return;
+  }
+  const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (dtype == KV4_F16) {
+      const float2 f = h2_to_f2(w[k]);
+      v[2 * k] = f.x, v[2 * k + 1] = f.y;
+    } else {
+      v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void store_elem(void* p, int dtype, long long i, float v) {
+  if (dtype == KV4_F32) reinterpret_cast<float*>(p)[i] = v;
+  else if (dtype == KV4_F16) reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+  else reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ int seq_positions(const Kv4AttnArgs& a, int s) {
+  const long long most = min((long long)a.max_len, (long long)a.table_stride * a.c.page_len);
+  return (int)max(0ll, min((long long)a.seq_len[s], most));
+}
+// Query tokens of a sequence that get an output, and the first.
+__device__ __forceinline__ int seq_tokens(const Kv4AttnArgs& a, int s, int* start) {
+  const int b = a.cu_q[s], e = a.cu_q[s + 1];
+  *start = b;
+  if (b < 0 || e <= b || e > a.n_tok) return 0;
+  return e - b;
+}
+
+template <int D, int NC>
+struct __align__(16) AttnSmem {
+  uint8_t ring[kWarps][kStages][kv4_tile_bytes(D)];
+  float acc[kWarps][8 * D];     // flushed accumulators, then the warps' results: [register][lane]
+  float ref[kWarps][8], sum[kWarps][8];
+  long long wsum[kWarps];
+  long long first_unit;         // of the sequence that holds this CTA's first unit
+  int first_seq;
+  int last;
+};
+
+// Columns: NC = 8 has eight (token, head of the group) pairs, their high parts in rows 0-7 and their low parts in
+// rows 8-15 of the score product, and two products for V.  NC = 4 has four: rows 4-7 repeat rows 0-3, and the
+// columns 4-7 of the V product carry the low parts, so one product does.
+template <int D, int NC>
+__global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs a, int dtype, unsigned* counters, float* slots) {
+  constexpr int NB = D / 32, MT = D / 16;  // blocks of a row, row tiles of the V product
+  constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  AttnSmem<D, NC>& sm = *reinterpret_cast<AttnSmem<D, NC>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
+  const int group = a.n_q_heads / a.c.n_kv_heads, tpp = a.c.page_len / kKv4Tile;
+
+  // ---- this CTA's piece of the line of units
+  // piece c begins at unit c * piece + min(c, longer)
+  const int cta = blockIdx.x;
+  int ncta;
+  long long total = 0, piece, longer;
+  {
+    const int per = (a.n_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(a.n_seqs, tid * per), s1 = min(a.n_seqs, s0 + per);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) {
+      int start;
+      const int c = min(seq_tokens(a, s, &start), a.max_q);
+      const int units = max(1, (seq_positions(a, s) + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+      mine += (long long)((c * (long long)group + NC - 1) / NC) * a.c.n_kv_heads * units;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    if (tid == 0) sm.first_seq = a.n_seqs;
+    __syncthreads();
+    long long before = incl - mine;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm.wsum[w];
+      total += sm.wsum[w];
+    }
+    ncta = (int)min((long long)gridDim.x, total);  // every piece has a unit
+    if (cta >= ncta) return;
+    piece = total / ncta;
+    longer = total % ncta;
+    const long long u0 = cta * piece + min((long long)cta, longer);
+    if (u0 >= before && u0 < before + mine) {
+      long long at = before;
+      for (int s = s0; s < s1; ++s) {
+        int start;
+        const int c = min(seq_tokens(a, s, &start), a.max_q);
+        const int units = max(1, (seq_positions(a, s) + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+        const long long n = (long long)((c * (long long)group + NC - 1) / NC) * a.c.n_kv_heads * units;
+        if (u0 < at + n) {
+          sm.first_seq = s;
+          sm.first_unit = at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+  }
+  long long u = cta * piece + min((long long)cta, longer);
+  const long long u_end = u + piece + (cta < longer ? 1 : 0);
+  int seq = sm.first_seq;
+  long long seq_unit = sm.first_unit;
+
+  while (u < u_end) {
+    AttnRow row;
+    row.seq = seq;
+    row.count = seq_tokens(a, seq, &row.start);
+    row.len = seq_positions(a, seq);
+    const int ctok = min(row.count, a.max_q), ncols = ctok * group;
+    const int units = max(1, (row.len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+    const int cblocks = (ncols + NC - 1) / NC;
+    const long long nrows = (long long)cblocks * a.c.n_kv_heads;
+    if (u >= seq_unit + nrows * units) {  // the next sequence (those without a token have no unit)
+      seq_unit += nrows * units;
+      ++seq;
+      continue;
+    }
+    const long long r = (u - seq_unit) / units, row_unit = seq_unit + r * units;
+    row.head = (int)(r / cblocks);
+    row.cbase = (int)(r % cblocks) * NC;
+    const long long seg_end = min(u_end, row_unit + units);
+    const int t_begin = (int)(u - row_unit) * kUnitTiles;
+    const int k_hi = min(ctok - 1, (row.cbase + NC - 1) / group), k_lo = row.cbase / group;
+    const int lim_hi = max(0, row.len - row.count + k_hi + 1);  // positions that some column sees
+    const int lim_lo = max(0, row.len - row.count + k_lo + 1);  // positions that every column sees
+    const int t_end = min((int)(seg_end - row_unit) * kUnitTiles, (lim_hi + kKv4Tile - 1) / kKv4Tile);
+
+    // ---- the columns' q as the A operand: rows gid (high) and gid + 8 (low)
+    const int col = row.cbase + (NC == 8 ? gid : gid & 3);
+    const bool col_live = col < ncols;
+    const int col_k = col / group;
+    const int lim = col_live ? max(0, row.len - row.count + col_k + 1) : 0;
+    uint32_t qa[2 * NB][4];
+    float zscale;
+    {
+      const long long base = col_live ? (long long)(row.start + col_k) * a.q_stride + (row.head * group + col % group) * D : 0;
+      float qv[NB][8], top = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (col_live) {
+          load8(a.q, dtype, base + b * 32 + tig * 8, qv[b]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) qv[b][i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(qv[b][i]));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest |q| to 2^13 .. 2^14 by a power of two (2^-100 is as good as 0)
+      const int e = top <= FLT_MAX ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+      zscale = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+      const float up[2] = {__uint_as_float((uint32_t)(13 - e + 127) << 23), __uint_as_float((uint32_t)(9 - e + 127) << 23)};
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {  // dims 2 s + o and 2 s + o + 4 of the lane's eight; odd ones face codes times 16
+            const float x0 = qv[b][2 * s + o] * up[o], x1 = qv[b][2 * s + o + 4] * up[o];
+            const __half h0 = __float2half_rn(x0), h1 = __float2half_rn(x1);
+            qa[2 * b + s][2 * o] = pack_h2(h0, h1);
+            qa[2 * b + s][2 * o + 1] = pack_h2(__float2half_rn(x0 - __half2float(h0)), __float2half_rn(x1 - __half2float(h1)));
+          }
+    }
+
+    float acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    float ref = -INFINITY, sum = 0.f;          // of column gid (over this lane's positions: sum)
+    float ref_flushed = -INFINITY;
+    bool flushed = false;
+    float* my_acc = sm.acc[warp];
+
+    // ---- the warp's tiles t_begin + warp, + kWarps, ...
+    const int n_it = max(0, (t_end - t_begin - warp + kWarps - 1) / kWarps);
+    const int* trow = a.table + (long long)row.seq * a.table_stride;
+    int page_ids = -1, in_page = 0;  // of tile number 32 * batch + lane
+    uint32_t present = 0;            // bit i % 32: tile i is there
+    auto issue = [&](int i) {
+      if (i < n_it) {
+        if ((i & 31) == 0) {
+          const int t = t_begin + warp + (i + lane) * kWarps;
+          const int pg = t / tpp;
+          in_page = t - pg * tpp;
+          page_ids = i + lane < n_it ? trow[pg] : -1;
+          if (page_ids < 0 || page_ids >= a.c.n_pages) page_ids = -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, page_ids, i & 31), in = __shfl_sync(0xffffffffu, in_page, i & 31);
+        if (id >= 0) {
+          present |= 1u << (i & 31);
+          const uint8_t* src = a.c.data + (((long long)id * a.c.n_kv_heads + row.head) * tpp + in) * TILE;
+          uint8_t* dst = sm.ring[warp][i % kStages];
+#pragma unroll
+          for (int j = 0; j < (TILE / 16 + 31) / 32; ++j) {
+            const int o = lane + 32 * j;
+            if (o < TILE / 16) cp_async16(dst + o * 16, src + o * 16);
+          }
+        } else {
+          present &= ~(1u << (i & 31));
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    int since = 0;
+    for (int i = 0; i < n_it; ++i) {
+      cp_async_wait_group<kStages - 2>();
+      __syncwarp();
+      const bool here = present >> (i & 31) & 1;
+      issue(i + kStages - 1);
+      if (!here) continue;
+      const uint8_t* tile = sm.ring[warp][i % kStages];
+      const int pos0 = (t_begin + warp + i * kWarps) * kKv4Tile;
+
+      // scores of positions 8 n + 2 tig + {0, 1} and column gid
+      float z[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t kw[NB], ks[NB];  // ks: fp16 pairs (blocks 2 i, 2 i + 1) of the first, then of the second position
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(tile + (8 * n + gid) * (D / 2) + tig * 16);
+          kw[0] = w.x, kw[1] = w.y, kw[2] = w.z, kw[3] = w.w;
+          const uint4 s = *reinterpret_cast<const uint4*>(tile + CODES + (8 * n + 2 * tig) * (2 * NB));
+          ks[0] = s.x, ks[1] = s.y, ks[2] = s.z, ks[3] = s.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(tile + (8 * n + gid) * (D / 2) + tig * 8);
+          kw[0] = w.x, kw[1] = w.y;
+          const uint2 s = *reinterpret_cast<const uint2*>(tile + CODES + (8 * n + 2 * tig) * (2 * NB));
+          ks[0] = s.x, ks[1] = s.y;
+        }
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t h[4];
+          codes_to_half(kw[b], h);
+          const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+          float c[4];
+          mma16816(c, qa[2 * b], h[0], h[1], zero);
+          mma16816(c, qa[2 * b + 1], h[2], h[3], c);
+          const float2 sa = h2_to_f2(ks[b / 2]), sb = h2_to_f2(ks[NB / 2 + b / 2]);
+          s0 = fmaf(b & 1 ? sa.y : sa.x, c[0] + c[2], s0);
+          s1 = fmaf(b & 1 ? sb.y : sb.x, c[1] + c[3], s1);
+        }
+        z[n][0] = s0 * zscale;
+        z[n][1] = s1 * zscale;
+      }
+
+      // V's codes and scales; the scales of positions that no column sees count as 0
+      uint32_t vs[2][NB];  // as ks
+      float above[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if constexpr (D == 128) {
+          const uint4 s = *reinterpret_cast<const uint4*>(tile + HALF + CODES + (8 * n + 2 * tig) * (2 * NB));
+          vs[n][0] = s.x, vs[n][1] = s.y, vs[n][2] = s.z, vs[n][3] = s.w;
+        } else {
+          const uint2 s = *reinterpret_cast<const uint2*>(tile + HALF + CODES + (8 * n + 2 * tig) * (2 * NB));
+          vs[n][0] = s.x, vs[n][1] = s.y;
+        }
+      }
+      const bool whole = pos0 + kKv4Tile <= lim_lo;
+      if (!whole) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (pos0 + 8 * n + 2 * tig + e >= lim) {
+              z[n][e] = -INFINITY;
+#pragma unroll
+              for (int b = 0; b < NB / 2; ++b) vs[n][e * (NB / 2) + b] = 0;
+            }
+      }
+      float most = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t one[NB / 2];
+#pragma unroll
+          for (int b = 0; b < NB / 2; ++b) one[b] = vs[n][e * (NB / 2) + b];
+          above[n][e] = exponent_above(one);
+          most = fmaxf(most, z[n][e] + above[n][e]);
+        }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const bool raise = most - kTop > ref + kSlack;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float now = raise ? most - kTop : ref;
+        const float keep = ref == now ? 1.f : exp2_approx(ref - now);
+        ref = now;
+        sum *= keep;
+        const float k0 = __shfl_sync(0xffffffffu, keep, 8 * tig), k1 = __shfl_sync(0xffffffffu, keep, 8 * tig + 4);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          acc[m][0] *= k0;
+          acc[m][1] *= k1;
+          acc[m][2] *= k0;
+          acc[m][3] *= k1;
+        }
+      }
+      const float base = ref == -INFINITY ? 0.f : ref;
+      float p[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[n][e] = exp2_approx(z[n][e] - base);
+          sum += p[n][e];
+        }
+
+      // x = p * scale, split; then the product with V's codes
+      uint32_t vw[2][NB];  // [half][block]: the lane's four dims of the first position, then of the second
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(tile + HALF + n * 4 * D + lane * 16);
+          vw[n][0] = __byte_perm(w.x, w.z, 0x5410), vw[n][1] = __byte_perm(w.x, w.z, 0x7632);
+          vw[n][2] = __byte_perm(w.y, w.w, 0x5410), vw[n][3] = __byte_perm(w.y, w.w, 0x7632);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(tile + HALF + n * 4 * D + lane * 8);
+          vw[n][0] = __byte_perm(w.x, w.y, 0x5410), vw[n][1] = __byte_perm(w.x, w.y, 0x7632);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 sa = h2_to_f2(vs[n][b / 2]), sb = h2_to_f2(vs[n][NB / 2 + b / 2]);
+          const float x0 = p[n][0] * (b & 1 ? sa.y : sa.x), x1 = p[n][1] * (b & 1 ? sb.y : sb.x);
+          const __half2 h = __floats2half2_rn(x0, x1);
+          const float2 f = __half22float2(h);
+          const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+          hi[n] = *reinterpret_cast<const uint32_t*>(&h);
+          lo[n] = *reinterpret_cast<const uint32_t*>(&l);
+        }
+        uint32_t v0[4], v1[4];
+        codes_to_half(vw[0][b], v0);  // dims 4 gid + {0, 1, 2, 3} of the block; (first, second position)
+        codes_to_half(vw[1][b], v1);
+        const uint32_t even[4] = {v0[0], v0[1], v1[0], v1[1]}, odd[4] = {v0[2], v0[3], v1[2], v1[3]};
+        if constexpr (NC == 8) {
+          mma16816(acc[2 * b], even, hi[0], hi[1], acc[2 * b]);
+          mma16816(acc[2 * b + 1], odd, hi[0], hi[1], acc[2 * b + 1]);
+          mma16816(acc[2 * b], even, lo[0], lo[1], acc[2 * b]);
+          mma16816(acc[2 * b + 1], odd, lo[0], lo[1], acc[2 * b + 1]);
+        } else {
+          const uint32_t x0 = gid < 4 ? hi[0] : lo[0], x1 = gid < 4 ? hi[1] : lo[1];
+          mma16816(acc[2 * b], even, x0, x1, acc[2 * b]);
+          mma16816(acc[2 * b + 1], odd, x0, x1, acc[2 * b + 1]);
+        }
+      }
+      // the tensor cores' additions truncate: their chains stay short, longer sums are rounded to nearest
+      if (++since == kFlush) {
+        since = 0;
+        const float keep = flushed ? (ref_flushed == ref ? 1.f : exp2_approx(ref_flushed - ref)) : 0.f;
+        const float k0 = __shfl_sync(0xffffffffu, keep, 8 * tig), k1 = __shfl_sync(0xffffffffu, keep, 8 * tig + 4);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float* f = my_acc + (4 * m + j) * 32 + lane;
+            *f = flushed ? fmaf(*f, j & 1 ? k1 : k0, acc[m][j]) : acc[m][j];
+            acc[m][j] = 0.f;
+          }
+        ref_flushed = ref;
+        flushed = true;
+      }
+    }
+    cp_async_wait_all();
+
+    // ---- the warp's result
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    {
+      const float keep = flushed ? (ref_flushed == ref ? 1.f : exp2_approx(ref_flushed - ref)) : 0.f;
+      const float k0 = __shfl_sync(0xffffffffu, keep, 8 * tig), k1 = __shfl_sync(0xffffffffu, keep, 8 * tig + 4);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float* f = my_acc + (4 * m + j) * 32 + lane;
+          float v = flushed ? fmaf(*f, j & 1 ? k1 : k0, acc[m][j]) : acc[m][j];
+          if (j >= 2) v *= 0.0625f;  // the odd dims' codes were times 16
+          if constexpr (NC == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);  // high and low part
+          *f = v;
+        }
+    }
+    if (tig == 0) {
+      sm.ref[warp][gid] = ref;
+      sm.sum[warp][gid] = sum;
+    }
+    __syncthreads();
+
+    // ---- the CTA's result: entry e = register * 32 + lane holds (dim, column)
+    const bool split = u > row_unit || seg_end < row_unit + units;
+    float* slot = nullptr;
+    if (split) slot = slots + (size_t)(2 * cta + (u == row_unit ? 1 : 0)) * slot_floats(D);
+    auto owner = [&](long long x) {  // of unit x
+      const long long cut = longer * (piece + 1);
+      return (int)(x < cut ? x / (piece + 1) : longer + (x - cut) / piece);
+    };
+    auto entry_dim = [&](int e) { return (e >> 8) * 32 + ((e & 31) >> 2) * 4 + ((e >> 7) & 1) * 2 + ((e >> 6) & 1); };
+    auto entry_col = [&](int e) { return (e & 3) * 2 + ((e >> 5) & 1); };
+    auto put = [&](int e, float v, float s) {
+      const int c = row.cbase + entry_col(e);
+      if (entry_col(e) >= NC || c >= ncols) return;
+      const long long at = (long long)(row.start + c / group) * a.out_stride + (row.head * group + c % group) * D + entry_dim(e);
+      store_elem(a.out, dtype, at, s != 0.f ? v / s : 0.f);
+    };
+    for (int e = tid; e < 8 * D; e += kThreads) {
+      const int c = entry_col(e);
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.ref[w][c]);
+      float v = 0.f, s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float r_w = sm.ref[w][c];
+        const float k = r_w == top ? 1.f : exp2_approx(r_w - top);
+        if (r_w != -INFINITY) {
+          v = fmaf(sm.acc[w][e], k, v);
+          s = fmaf(sm.sum[w][c], k, s);
+        } else {
+          v += sm.acc[w][e] != 0.f ? sm.acc[w][e] : 0.f;  // NaN stays NaN
+          s += sm.sum[w][c];
+        }
+      }
+      if (split) {
+        __stcg(slot + e, v);
+        if (e < 64 && (e >> 2 & 7) == 0) {  // registers 0 and 1 of lanes 0-3: one entry for every column
+          __stcg(slot + 8 * D + c, top);
+          __stcg(slot + 8 * D + 8 + c, s);
+        }
+      } else {
+        put(e, v, s);
+      }
+    }
+    if (split) {
+      __syncthreads();
+      const int c0 = owner(row_unit), c1 = owner(row_unit + units - 1), parts = c1 - c0 + 1;
+      if (tid == 0) {
+        const unsigned old = atom_add_acq_rel(&counters[c0], 1u);
+        sm.last = old == (unsigned)(parts - 1);
+        if (sm.last) counters[c0] = 0;
+      }
+      __syncthreads();
+      if (sm.last) {
+        // weights of the parts, then the sums in the order of the positions
+        float* wt = reinterpret_cast<float*>(sm.ring);  // [part][8]
+        float* den = &sm.sum[0][0];
+        auto part = [&](int i) { return slots + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * slot_floats(D); };
+        if (tid < 8) {
+          float top = -INFINITY, s = 0.f;
+          for (int i = 0; i < parts; ++i) top = fmaxf(top, __ldcg(part(i) + 8 * D + tid));
+          for (int i = 0; i < parts; ++i) {
+            const float r_i = __ldcg(part(i) + 8 * D + tid);
+            const float k = r_i == top ? 1.f : exp2_approx(r_i - top);
+            wt[i * 8 + tid] = k;
+            s = fmaf(__ldcg(part(i) + 8 * D + 8 + tid), k, s);
+          }
+          den[tid] = s;
+        }
+        __syncthreads();
+        for (int e4 = tid; e4 < 2 * D; e4 += kThreads) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+          for (int i = 0; i < parts; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i)) + e4);
+            const float* w = wt + i * 8;
+            const int b = (e4 >> 3) & 1;
+            v[0] = fmaf(x.x, w[b], v[0]);
+            v[1] = fmaf(x.y, w[2 + b], v[1]);
+            v[2] = fmaf(x.z, w[4 + b], v[2]);
+            v[3] = fmaf(x.w, w[6 + b], v[3]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) put(4 * e4 + j, v[j], den[entry_col(4 * e4 + j)]);
+        }
+      }
+    }
+    __syncthreads();
+    u = seg_end;
+  }
+}
+
+constexpr size_t kCounterBytes = kMaxCtas * sizeof(unsigned);
+
+template <int D, int NC>
+cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
+  constexpr size_t smem = sizeof(AttnSmem<D, NC>);
+  static_assert(smem <= 113 * 1024, "two CTAs share an SM");
+  static_assert(sizeof(((AttnSmem<D, NC>*)nullptr)->ring) >= kMaxCtas * 8 * sizeof(float), "weights of a row's parts");
+  auto* kern = kv4_attn_kernel<D, NC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than units at the stated bounds
+  const int group = a.n_q_heads / a.c.n_kv_heads;
+  const long long len = min((long long)a.max_len, (long long)a.table_stride * a.c.page_len);
+  const long long most = (long long)a.n_seqs * a.c.n_kv_heads * (((long long)a.max_q * group + NC - 1) / NC) *
+                         ((len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+  const int grid = (int)min(min(most, 2ll * sm_count()), (long long)kMaxCtas);
+  unsigned* counters = (unsigned*)a.ws;
+  kern<<<grid, kThreads, smem, st>>>(a, dtype, counters, (float*)((char*)a.ws + kCounterBytes));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv4_attention_ws_bytes(int, int, int, int head_dim, int, int) {
+  return kCounterBytes + (size_t)2 * kMaxCtas * slot_floats(head_dim) * sizeof(float);
+}
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st) {
-  const long long warps = (long long)a.n_tok * a.n_q_heads;
-  const unsigned grid = (unsigned)((warps + 3) / 4);
-  if (head_dim == 128) {
-    if (dtype == KV4_F32) kv4_attn_kernel<128, float><<<grid, 128, 0, st>>>(a);
-    else if (dtype == KV4_F16) kv4_attn_kernel<128, __half><<<grid, 128, 0, st>>>(a);
-    else kv4_attn_kernel<128, __nv_bfloat16><<<grid, 128, 0, st>>>(a);
-  } else {
-    if (dtype == KV4_F32) kv4_attn_kernel<64, float><<<grid, 128, 0, st>>>(a);
-    else if (dtype == KV4_F16) kv4_attn_kernel<64, __half><<<grid, 128, 0, st>>>(a);
-    else kv4_attn_kernel<64, __nv_bfloat16><<<grid, 128, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
+  if (head_dim == 128) return cols <= 4 ? launch<128, 4>(a, dtype, st) : launch<128, 8>(a, dtype, st);
+  return cols <= 4 ? launch<64, 4>(a, dtype, st) : launch<64, 8>(a, dtype, st);
 }
 
 }  // namespace lrs

@@ -80,15 +80,17 @@ def rows(cache: np.ndarray, slots, is_v: bool) -> np.ndarray:
 
 
 def attention(cache, q, cu, seq_len, table, max_q=None, max_len=None):
-    """(out, weight): softmax attention of the rows that get an output (NaN elsewhere), float64, and for each output
-    value sum_j p_j |v_j| -- what rounding errors of the probabilities are relative to -- times the size of
-    the largest sum_d |q_d k_d| / sqrt(D) of its row in `spread` [rows, heads]."""
+    """Softmax attention in float64, and what rounding errors are relative to, as
+    (out, weight, spread, peak, seen): out [rows, heads, d], NaN in rows that get no output; weight the same for
+    sum_j p_j |v_j|; per row and head: spread, the largest sum_d |q_d k_jd| / sqrt(D); peak, the largest
+    p_j max_d |v_jd|; seen, the number of positions."""
     n_pages, hkv, tiles, nbytes = cache.shape
     d, page_len = nbytes // 18, tiles * 16
     q = np.asarray(q, np.float64)
     group = q.shape[1] // hkv
     out = np.full(q.shape, np.nan)
-    weight, spread = np.zeros(q.shape), np.zeros(q.shape[:2])
+    weight = np.zeros(q.shape)
+    spread, peak, count = (np.zeros(q.shape[:2]) for _ in range(3))
     for i, n in enumerate(seq_len):
         c = int(cu[i + 1]) - int(cu[i])
         n = min(int(n), table.shape[1] * page_len, max_len or 1 << 60)
@@ -112,7 +114,9 @@ def attention(cache, q, cu, seq_len, table, max_q=None, max_len=None):
                     out[t, h] = p @ vh
                     weight[t, h] = p @ np.abs(vh)
                     spread[t, h] = (np.abs(kh) @ np.abs(q[t, h])).max() / np.sqrt(d)
-    return out, weight, spread
+                    peak[t, h] = (p * np.abs(vh).max(-1)).max()
+                    count[t, h] = len(kh)
+    return out, weight, spread, peak, count
 
 
 def plan(page_len, seq_len, new_len, table, ring, free_state, n_tok, n_pages, keep_len=None):

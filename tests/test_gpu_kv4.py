@@ -12,6 +12,13 @@ which X covers), in numerator and denominator: 2 (2^-19 X + 2^-20).  The probabi
 2^-38 of the largest), the sums (chains of at most 64 truncating additions, 64 * 2^-24 = 2^-18, then chains of
 additions to nearest over the rest: 2^-18 again at these lengths), the merge and the division (2^-21) add under 2^-16.  So
     |got - want| <= (2^-18 X + 2^-16) A.
+The low halves of the pairs end at fp16's smallest step, 2^-24: with x_j = 2^(z_j - r) s_j (s_j: the block's V scale, e_j the
+least integer with s_j < 2^(e_j) for the row's largest scale, at least -14; r <= max_j (z_j + e_j) - 11) each x_j is off by at most
+2^-25 more, times |c - 8| <= 8.  The sum that divides it is at least 2^(z_j - r) / p_j >= 2^(11 - e_j) / p_j for the
+position j that sets r, so this adds at most, over N positions,
+    N 2^-22 2^(e_j - 11) p_j <= N p_j max(2^-35 (8 s_j), 2^-47) <= N (2^-34 max_jd p_j |v_jd| + 2^-47):
+2^(e_j) <= 2 s_j, or 2^-14 where s_j is subnormal, and a block's largest |v| is at least 4 s_j at any s_j (8 s_j
+rounded to a code, a code cut off at 15 still 7 s_j).
 In the 16-bit types a probability may be rounded once to fp16 or a pair of bf16 (2^-11 A), and the output is
 rounded once: eps / 2 of its value.
 """
@@ -48,9 +55,9 @@ def same(a, b):
 
 
 def check_attention(got, ref, dtype, rows=None):
-    out, weight, spread = ref
+    out, weight, spread, peak, seen = ref
     got = got.detach().double().cpu().numpy()
-    tol = (2.0 ** -18 * spread[..., None] + 2.0 ** -16) * weight
+    tol = (2.0 ** -18 * spread[..., None] + 2.0 ** -16) * weight + (seen * (2.0 ** -34 * peak + 2.0 ** -47))[..., None]
     if dtype != "f32":
         tol = tol + 2.0 ** -11 * weight + torch.finfo(DT[dtype]).eps / 2 * np.abs(out)
     some = ~np.isnan(out) if rows is None else rows

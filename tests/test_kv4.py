@@ -87,12 +87,12 @@ def test_attention_of_equal_scores_is_the_mean():
     slots = np.concatenate([32 + np.arange(16), np.arange(5)])
     kv4.append(cache, np.zeros((21, 2, 64), np.float32), rng.standard_normal((21, 2, 64)).astype(np.float32), slots)
     q = rng.standard_normal((3, 4, 64))
-    out, _, _ = kv4.attention(cache, q, [0, 3], [21], table)
+    out, *_ = kv4.attention(cache, q, [0, 3], [21], table)
     v = kv4.rows(cache, slots, True)
     for j in range(3):
         for h in range(4):
             assert np.allclose(out[j, h], v[:19 + j, h // 2].mean(0), atol=1e-14)
-    out, _, _ = kv4.attention(cache, q, [0, 3], [1], table)   # two tokens before the first position
+    out, *_ = kv4.attention(cache, q, [0, 3], [1], table)   # two tokens before the first position
     assert (out[:2] == 0).all() and np.allclose(out[2, 0], v[0, 0])
 
 
