@@ -14,6 +14,7 @@
 // alike, whatever the lengths, which only the device knows.  A row cut by piece borders is merged by the last
 // of its CTAs to arrive, in the order of the positions.
 
+#include <atomic>
 #include <cfloat>
 
 #include "common.cuh"
@@ -28,7 +29,7 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kUnitTiles = kWarps;  // a unit: one tile of 16 positions per warp
 constexpr int kStages = 4;          // tiles in flight per warp, less one
 constexpr int kFlush = 16;          // tiles between two flushes of the accumulators
-constexpr int kMaxCtas = 1024;
+constexpr int kMaxCtas = 512;
 constexpr int kSlack = 4;           // r is raised when a score passes it by 2^kSlack
 constexpr float kTop = 11.f;
 
@@ -54,12 +55,24 @@ __device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
 
 // Eight codes to four half2: h[t] = (code t, code t + 4) - 8, the odd t times 16.  1024 + c is the fp16 number
 // 0x6400 | c, and 1024 + 16 c is 0x6400 | c << 4: one logic operation and one addition per pair, both exact.
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+// The exponent's bits in a register that the compiler takes for a variable: as a constant they would make two
+// operations of and_or, which has room for one immediate.
+__device__ __forceinline__ uint32_t exponent_bits() {
+  uint32_t y;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(y));
+  return y;
+}
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t ex, uint32_t (&h)[4]) {
   const __half2 o1 = __floats2half2_rn(-1032.f, -1032.f), o16 = __floats2half2_rn(-1152.f, -1152.f);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t x = i ? w >> 8 : w;
-    const uint32_t a = (x & 0x000f000fu) | 0x64006400u, b = (x & 0x00f000f0u) | 0x64006400u;
+    const uint32_t a = and_or(x, 0x000f000fu, ex), b = and_or(x, 0x00f000f0u, ex);
     const __half2 ha = __hadd2(*reinterpret_cast<const __half2*>(&a), o1);
     const __half2 hb = __hadd2(*reinterpret_cast<const __half2*>(&b), o16);
     h[2 * i] = *reinterpret_cast<const uint32_t*>(&ha);
@@ -69,20 +82,48 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&h)[4]) {
 
 __device__ __forceinline__ float2 h2_to_f2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
 
-// A bound of the exponents of the numbers in these fp16 pairs: 2^e > |s| for every finite one.
-template <int N>
-__device__ __forceinline__ float exponent_above(const uint32_t (&s)[N]) {
-  __half2 m = __habs2(*reinterpret_cast<const __half2*>(&s[0]));
-#pragma unroll
-  for (int i = 1; i < N; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&s[i])));  // NaN loses
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
-  const uint32_t top = max(u >> 16, u & 0xffffu);
-  return (float)(int)min(top >> 10, 30u) - 14.f;
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t x, y, d;
+  float2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t x, y, d;
+  float2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, d;
+  float2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A segment: units [begin, end) of the row (sequence, KV head, block of columns) that has [unit, unit + units).
 struct AttnRow {
-  int seq, head, cbase;      // sequence, KV head, first column
+  int head, cbase, ncols;    // KV head, first column, columns of the sequence
   int start, count, len;     // first query token of the sequence, its tokens, its positions
+  int units;
+  long long unit, begin, end;
 };
 
 // Eight neighbouring elements (i a multiple of 8, rows 16-byte aligned).
@@ -130,6 +171,9 @@ struct __align__(16) AttnSmem {
   float ref[kWarps][8], sum[kWarps][8];
   long long wsum[kWarps];
   long long first_unit;         // of the sequence that holds this CTA's first unit
+  long long piece, longer;      // piece c of the line begins at unit c * piece + min(c, longer)
+  int ncta;
+  AttnRow seg;                  // the segment in work
   int first_seq;
   int last;
 };
@@ -147,11 +191,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
   const int group = a.n_q_heads / a.c.n_kv_heads, tpp = a.c.page_len / kKv4Tile;
 
   // ---- this CTA's piece of the line of units
-  // piece c begins at unit c * piece + min(c, longer)
   const int cta = blockIdx.x;
-  int ncta;
-  long long total = 0, piece, longer;
+  long long u, u_end;
   {
+    long long total = 0;
     const int per = (a.n_seqs + kThreads - 1) / kThreads;
     const int s0 = min(a.n_seqs, tid * per), s1 = min(a.n_seqs, s0 + per);
     long long mine = 0;
@@ -175,19 +218,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       if (w < warp) before += sm.wsum[w];
       total += sm.wsum[w];
     }
-    ncta = (int)min((long long)gridDim.x, total);  // every piece has a unit
+    const int ncta = (int)min((long long)gridDim.x, total);  // every piece has a unit
     if (cta >= ncta) return;
-    piece = total / ncta;
-    longer = total % ncta;
-    const long long u0 = cta * piece + min((long long)cta, longer);
-    if (u0 >= before && u0 < before + mine) {
+    const long long piece = total / ncta, longer = total % ncta;
+    u = cta * piece + min((long long)cta, longer);
+    u_end = u + piece + (cta < longer ? 1 : 0);
+    if (tid == 0) {
+      sm.ncta = ncta;
+      sm.piece = piece;
+      sm.longer = longer;
+    }
+    if (u >= before && u < before + mine) {
       long long at = before;
       for (int s = s0; s < s1; ++s) {
         int start;
         const int c = min(seq_tokens(a, s, &start), a.max_q);
         const int units = max(1, (seq_positions(a, s) + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
         const long long n = (long long)((c * (long long)group + NC - 1) / NC) * a.c.n_kv_heads * units;
-        if (u0 < at + n) {
+        if (u < at + n) {
           sm.first_seq = s;
           sm.first_unit = at;
           break;
@@ -197,38 +245,210 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     }
     __syncthreads();
   }
-  long long u = cta * piece + min((long long)cta, longer);
-  const long long u_end = u + piece + (cta < longer ? 1 : 0);
   int seq = sm.first_seq;
   long long seq_unit = sm.first_unit;
 
-  while (u < u_end) {
-    AttnRow row;
-    row.seq = seq;
-    row.count = seq_tokens(a, seq, &row.start);
-    row.len = seq_positions(a, seq);
-    const int ctok = min(row.count, a.max_q), ncols = ctok * group;
-    const int units = max(1, (row.len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
-    const int cblocks = (ncols + NC - 1) / NC;
-    const long long nrows = (long long)cblocks * a.c.n_kv_heads;
-    if (u >= seq_unit + nrows * units) {  // the next sequence (those without a token have no unit)
-      seq_unit += nrows * units;
-      ++seq;
-      continue;
+  float acc[MT][4];
+  float ref = -INFINITY;               // of column gid
+  float2 sum = make_float2(0.f, 0.f);  // over this lane's positions, the first and the second of each pair
+  float ref_flushed = -INFINITY;
+  bool flushed = false, pending = false;  // pending: a segment's sums wait to be put down
+  float* my_acc = sm.acc[warp];
+
+  // Each round finds the next segment and starts its copies, puts the last one's results down meanwhile, and runs
+  // the next one.
+  while (true) {
+    AttnRow row = {};
+    int n_it = 0, t_begin = 0, lim_lo = 0;
+    const bool more = u < u_end;
+    uint32_t present = 0;            // bit i % 32: tile i is there
+    int page_ids = -1, in_page = 0;  // of tile number 32 * batch + lane
+    const int* trow = nullptr;
+    auto issue = [&](int i) {
+      if (i < n_it) {
+        if ((i & 31) == 0) {
+          const int t = t_begin + warp + (i + lane) * kWarps;
+          const int pg = t / tpp;
+          in_page = t - pg * tpp;
+          page_ids = i + lane < n_it ? trow[pg] : -1;
+          if (page_ids < 0 || page_ids >= a.c.n_pages) page_ids = -1;
+        }
+        const int id = __shfl_sync(0xffffffffu, page_ids, i & 31), in = __shfl_sync(0xffffffffu, in_page, i & 31);
+        if (id >= 0) {
+          present |= 1u << (i & 31);
+          const uint8_t* src = a.c.data + (((long long)id * a.c.n_kv_heads + row.head) * tpp + in) * TILE;
+          uint8_t* dst = sm.ring[warp][i % kStages];
+#pragma unroll
+          for (int j = 0; j < (TILE / 16 + 31) / 32; ++j) {
+            const int o = lane + 32 * j;
+            if (o < TILE / 16) cp_async16(dst + o * 16, src + o * 16);
+          }
+        } else {
+          present &= ~(1u << (i & 31));
+        }
+      }
+      cp_async_commit();
+    };
+    if (more) {
+      while (true) {
+        row.count = seq_tokens(a, seq, &row.start);
+        row.len = seq_positions(a, seq);
+        row.ncols = min(row.count, a.max_q) * group;
+        row.units = max(1, (row.len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+        const int cblocks = (row.ncols + NC - 1) / NC;
+        const long long all = (long long)cblocks * a.c.n_kv_heads * row.units;
+        if (u < seq_unit + all) {
+          const long long r = (u - seq_unit) / row.units;
+          row.unit = seq_unit + r * row.units;
+          row.head = (int)(r / cblocks);
+          row.cbase = (int)(r % cblocks) * NC;
+          break;
+        }
+        seq_unit += all;  // the next sequence (those without a token have no unit)
+        ++seq;
+      }
+      row.begin = u;
+      row.end = min(u_end, row.unit + row.units);
+      u = row.end;
+      t_begin = (int)(row.begin - row.unit) * kUnitTiles;
+      const int k_hi = min(row.ncols - 1, row.cbase + NC - 1) / group, k_lo = row.cbase / group;
+      const int lim_hi = max(0, row.len - row.count + k_hi + 1);  // positions that some column sees
+      lim_lo = max(0, row.len - row.count + k_lo + 1);            // positions that every column sees
+      const int t_end = min((int)(row.end - row.unit) * kUnitTiles, (lim_hi + kKv4Tile - 1) / kKv4Tile);
+      // the warp's tiles: t_begin + warp, + kWarps, ...
+      n_it = max(0, (t_end - t_begin - warp + kWarps - 1) / kWarps);
+      trow = a.table + (long long)seq * a.table_stride;
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(i);
     }
-    const long long r = (u - seq_unit) / units, row_unit = seq_unit + r * units;
-    row.head = (int)(r / cblocks);
-    row.cbase = (int)(r % cblocks) * NC;
-    const long long seg_end = min(u_end, row_unit + units);
-    const int t_begin = (int)(u - row_unit) * kUnitTiles;
-    const int k_hi = min(ctok - 1, (row.cbase + NC - 1) / group), k_lo = row.cbase / group;
-    const int lim_hi = max(0, row.len - row.count + k_hi + 1);  // positions that some column sees
-    const int lim_lo = max(0, row.len - row.count + k_lo + 1);  // positions that every column sees
-    const int t_end = min((int)(seg_end - row_unit) * kUnitTiles, (lim_hi + kKv4Tile - 1) / kKv4Tile);
+    if (pending) {
+      // ---- the warp's result
+      float den = sum.x + sum.y;
+      den += __shfl_xor_sync(0xffffffffu, den, 1);
+      den += __shfl_xor_sync(0xffffffffu, den, 2);
+      {
+        const float keep = flushed ? (ref_flushed == ref ? 1.f : exp2_approx(ref_flushed - ref)) : 0.f;
+        const float k0 = __shfl_sync(0xffffffffu, keep, 8 * tig), k1 = __shfl_sync(0xffffffffu, keep, 8 * tig + 4);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float* f = my_acc + (4 * m + j) * 32 + lane;
+            float v = flushed ? fmaf(*f, j & 1 ? k1 : k0, acc[m][j]) : acc[m][j];
+            if (j >= 2) v *= 0.0625f;  // the odd dims' codes were times 16
+            if constexpr (NC == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);  // high and low part
+            *f = v;
+          }
+      }
+      if (tig == 0) {
+        sm.ref[warp][gid] = ref;
+        sm.sum[warp][gid] = den;
+      }
+      __syncthreads();
+
+      const AttnRow& done = sm.seg;
+      const int ncta = sm.ncta;
+      const long long piece = sm.piece, longer = sm.longer;
+      // ---- the CTA's result: entry e = register * 32 + lane holds (dim, column)
+      const bool split = done.begin > done.unit || done.end < done.unit + done.units;
+      float* slot = nullptr;
+      if (split) slot = slots + (size_t)(2 * cta + (done.begin == done.unit ? 1 : 0)) * slot_floats(D);
+      auto owner = [&](long long x) {  // of unit x
+        const long long cut = longer * (piece + 1);
+        return (int)(x < cut ? x / (piece + 1) : longer + (x - cut) / piece);
+      };
+      auto entry_dim = [&](int e) { return (e >> 8) * 32 + ((e & 31) >> 2) * 4 + ((e >> 7) & 1) * 2 + ((e >> 6) & 1); };
+      auto entry_col = [&](int e) { return (e & 3) * 2 + ((e >> 5) & 1); };
+      auto put = [&](int e, float v, float s) {
+        const int c = done.cbase + entry_col(e);
+        if (entry_col(e) >= NC || c >= done.ncols) return;
+        const long long at = (long long)(done.start + c / group) * a.out_stride + (done.head * group + c % group) * D + entry_dim(e);
+        store_elem(a.out, dtype, at, s != 0.f ? v / s : 0.f);
+      };
+      for (int e = tid; e < 8 * D; e += kThreads) {
+        const int c = entry_col(e);
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.ref[w][c]);
+        float v = 0.f, s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float r_w = sm.ref[w][c];
+          const float k = r_w == top ? 1.f : exp2_approx(r_w - top);
+          if (r_w != -INFINITY) {
+            v = fmaf(sm.acc[w][e], k, v);
+            s = fmaf(sm.sum[w][c], k, s);
+          } else {
+            v += sm.acc[w][e] != 0.f ? sm.acc[w][e] : 0.f;  // NaN stays NaN
+            s += sm.sum[w][c];
+          }
+        }
+        if (split) {
+          __stcg(slot + e, v);
+          if (e < 64 && (e >> 2 & 7) == 0) {  // registers 0 and 1 of lanes 0-3: one entry for every column
+            __stcg(slot + 8 * D + c, top);
+            __stcg(slot + 8 * D + 8 + c, s);
+          }
+        } else {
+          put(e, v, s);
+        }
+      }
+      if (split) {
+        __syncthreads();
+        const int c0 = owner(done.unit), c1 = owner(done.unit + done.units - 1), parts = c1 - c0 + 1;
+        if (tid == 0) {
+          const unsigned old = atom_add_acq_rel(&counters[c0], 1u);
+          sm.last = old == (unsigned)(parts - 1);
+          if (sm.last) counters[c0] = 0;
+        }
+        __syncthreads();
+        if (sm.last) {
+          // weights of the parts, then the sums in the order of the positions
+          float* wt = &sm.acc[0][0];  // [part][8]: r, then the weight
+          float* den = &sm.sum[0][0];
+          auto part = [&](int i) { return slots + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * slot_floats(D); };
+          for (int i = tid; i < parts * 8; i += kThreads) wt[i] = __ldcg(part(i >> 3) + 8 * D + (i & 7));
+          __syncthreads();
+          // a warp per column
+          {
+            float top = -INFINITY, s = 0.f;
+            for (int i = lane; i < parts; i += 32) top = fmaxf(top, wt[i * 8 + warp]);
+            top = warp_max(top);
+            for (int i = lane; i < parts; i += 32) {
+              const float r_i = wt[i * 8 + warp];
+              const float k = r_i == top ? 1.f : exp2_approx(r_i - top);
+              wt[i * 8 + warp] = k;
+              s = fmaf(__ldcg(part(i) + 8 * D + 8 + warp), k, s);
+            }
+            s = warp_sum(s);
+            if (lane == 0) den[warp] = s;
+          }
+          __syncthreads();
+          for (int e4 = tid; e4 < 2 * D; e4 += kThreads) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+            for (int i = 0; i < parts; ++i) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i)) + e4);
+              const float* w = wt + i * 8;
+              const int b = (e4 >> 3) & 1;
+              v[0] = fmaf(x.x, w[b], v[0]);
+              v[1] = fmaf(x.y, w[2 + b], v[1]);
+              v[2] = fmaf(x.z, w[4 + b], v[2]);
+              v[3] = fmaf(x.w, w[6 + b], v[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) put(4 * e4 + j, v[j], den[entry_col(4 * e4 + j)]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (!more) break;
+    if (tid == 0) sm.seg = row;  // read after the barriers that follow the segment's tiles
 
     // ---- the columns' q as the A operand: rows gid (high) and gid + 8 (low)
     const int col = row.cbase + (NC == 8 ? gid : gid & 3);
-    const bool col_live = col < ncols;
+    const bool col_live = col < row.ncols;
     const int col_k = col / group;
     const int lim = col_live ? max(0, row.len - row.count + col_k + 1) : 0;
     uint32_t qa[2 * NB][4];
@@ -266,49 +486,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           }
     }
 
-    float acc[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-    float ref = -INFINITY, sum = 0.f;          // of column gid (over this lane's positions: sum)
-    float ref_flushed = -INFINITY;
-    bool flushed = false;
-    float* my_acc = sm.acc[warp];
-
-    // ---- the warp's tiles t_begin + warp, + kWarps, ...
-    const int n_it = max(0, (t_end - t_begin - warp + kWarps - 1) / kWarps);
-    const int* trow = a.table + (long long)row.seq * a.table_stride;
-    int page_ids = -1, in_page = 0;  // of tile number 32 * batch + lane
-    uint32_t present = 0;            // bit i % 32: tile i is there
-    auto issue = [&](int i) {
-      if (i < n_it) {
-        if ((i & 31) == 0) {
-          const int t = t_begin + warp + (i + lane) * kWarps;
-          const int pg = t / tpp;
-          in_page = t - pg * tpp;
-          page_ids = i + lane < n_it ? trow[pg] : -1;
-          if (page_ids < 0 || page_ids >= a.c.n_pages) page_ids = -1;
-        }
-        const int id = __shfl_sync(0xffffffffu, page_ids, i & 31), in = __shfl_sync(0xffffffffu, in_page, i & 31);
-        if (id >= 0) {
-          present |= 1u << (i & 31);
-          const uint8_t* src = a.c.data + (((long long)id * a.c.n_kv_heads + row.head) * tpp + in) * TILE;
-          uint8_t* dst = sm.ring[warp][i % kStages];
-#pragma unroll
-          for (int j = 0; j < (TILE / 16 + 31) / 32; ++j) {
-            const int o = lane + 32 * j;
-            if (o < TILE / 16) cp_async16(dst + o * 16, src + o * 16);
-          }
-        } else {
-          present &= ~(1u << (i & 31));
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-
+    ref = ref_flushed = -INFINITY;
+    sum = make_float2(0.f, 0.f);
+    flushed = false;
+    const uint32_t ex = exponent_bits();
     int since = 0;
     for (int i = 0; i < n_it; ++i) {
       cp_async_wait_group<kStages - 2>();
@@ -320,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       const int pos0 = (t_begin + warp + i * kWarps) * kKv4Tile;
 
       // scores of positions 8 n + 2 tig + {0, 1} and column gid
-      float z[2][2];
+      float2 z[2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         uint32_t kw[NB], ks[NB];  // ks: fp16 pairs (blocks 2 i, 2 i + 1) of the first, then of the second position
@@ -335,59 +520,66 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           const uint2 s = *reinterpret_cast<const uint2*>(tile + CODES + (8 * n + 2 * tig) * (2 * NB));
           ks[0] = s.x, ks[1] = s.y;
         }
-        float s0 = 0.f, s1 = 0.f;
+        z[n] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t h[4];
-          codes_to_half(kw[b], h);
+          codes_to_half(kw[b], ex, h);
           const float zero[4] = {0.f, 0.f, 0.f, 0.f};
           float c[4];
           mma16816(c, qa[2 * b], h[0], h[1], zero);
           mma16816(c, qa[2 * b + 1], h[2], h[3], c);
           const float2 sa = h2_to_f2(ks[b / 2]), sb = h2_to_f2(ks[NB / 2 + b / 2]);
-          s0 = fmaf(b & 1 ? sa.y : sa.x, c[0] + c[2], s0);
-          s1 = fmaf(b & 1 ? sb.y : sb.x, c[1] + c[3], s1);
+          const float2 both = add2(make_float2(c[0], c[1]), make_float2(c[2], c[3]));  // high and low part of q
+          z[n] = fma2(b & 1 ? make_float2(sa.y, sb.y) : make_float2(sa.x, sb.x), both, z[n]);
         }
-        z[n][0] = s0 * zscale;
-        z[n][1] = s1 * zscale;
       }
 
-      // V's codes and scales; the scales of positions that no column sees count as 0
-      uint32_t vs[2][NB];  // as ks
-      float above[2][2];
+      // V's scales, (first, second position) of each block; those of positions that the column does not see count as 0
+      float2 vs[2][NB];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
+        uint32_t s[NB];
         if constexpr (D == 128) {
-          const uint4 s = *reinterpret_cast<const uint4*>(tile + HALF + CODES + (8 * n + 2 * tig) * (2 * NB));
-          vs[n][0] = s.x, vs[n][1] = s.y, vs[n][2] = s.z, vs[n][3] = s.w;
+          const uint4 u4 = *reinterpret_cast<const uint4*>(tile + HALF + CODES + (8 * n + 2 * tig) * (2 * NB));
+          s[0] = u4.x, s[1] = u4.y, s[2] = u4.z, s[3] = u4.w;
         } else {
-          const uint2 s = *reinterpret_cast<const uint2*>(tile + HALF + CODES + (8 * n + 2 * tig) * (2 * NB));
-          vs[n][0] = s.x, vs[n][1] = s.y;
+          const uint2 u2 = *reinterpret_cast<const uint2*>(tile + HALF + CODES + (8 * n + 2 * tig) * (2 * NB));
+          s[0] = u2.x, s[1] = u2.y;
+        }
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) {
+          const float2 first = h2_to_f2(s[b]), second = h2_to_f2(s[NB / 2 + b]);
+          vs[n][2 * b] = make_float2(first.x, second.x);
+          vs[n][2 * b + 1] = make_float2(first.y, second.y);
         }
       }
-      const bool whole = pos0 + kKv4Tile <= lim_lo;
-      if (!whole) {
+      if (pos0 + kKv4Tile > lim_lo) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n) {
+          const int at = pos0 + 8 * n + 2 * tig;
+          if (at >= lim) z[n].x = -INFINITY;
+          if (at + 1 >= lim) z[n].y = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (pos0 + 8 * n + 2 * tig + e >= lim) {
-              z[n][e] = -INFINITY;
-#pragma unroll
-              for (int b = 0; b < NB / 2; ++b) vs[n][e * (NB / 2) + b] = 0;
-            }
+          for (int b = 0; b < NB; ++b) {
+            if (at >= lim) vs[n][b].x = 0.f;
+            if (at + 1 >= lim) vs[n][b].y = 0.f;
+          }
+        }
       }
+      // the largest z + log2 of a position's largest scale (at least fp16's smallest; NaN loses)
       float most = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n) {
+        float2 top = make_float2(5.9604645e-8f, 5.9604645e-8f);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t one[NB / 2];
-#pragma unroll
-          for (int b = 0; b < NB / 2; ++b) one[b] = vs[n][e * (NB / 2) + b];
-          above[n][e] = exponent_above(one);
-          most = fmaxf(most, z[n][e] + above[n][e]);
+        for (int b = 0; b < NB; ++b) {
+          top.x = fmaxf(top.x, fabsf(vs[n][b].x));
+          top.y = fmaxf(top.y, fabsf(vs[n][b].y));
         }
+        most = fmaxf(most, fmaf(z[n].x, zscale, log2_approx(top.x)));
+        most = fmaxf(most, fmaf(z[n].y, zscale, log2_approx(top.y)));
+      }
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const bool raise = most - kTop > ref + kSlack;
@@ -395,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         const float now = raise ? most - kTop : ref;
         const float keep = ref == now ? 1.f : exp2_approx(ref - now);
         ref = now;
-        sum *= keep;
+        sum = mul2(sum, make_float2(keep, keep));
         const float k0 = __shfl_sync(0xffffffffu, keep, 8 * tig), k1 = __shfl_sync(0xffffffffu, keep, 8 * tig + 4);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -406,14 +598,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         }
       }
       const float base = ref == -INFINITY ? 0.f : ref;
-      float p[2][2];
+      float2 p[2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          p[n][e] = exp2_approx(z[n][e] - base);
-          sum += p[n][e];
-        }
+      for (int n = 0; n < 2; ++n) {
+        p[n].x = exp2_approx(fmaf(z[n].x, zscale, -base));
+        p[n].y = exp2_approx(fmaf(z[n].y, zscale, -base));
+        sum = add2(sum, p[n]);
+      }
 
       // x = p * scale, split; then the product with V's codes
       uint32_t vw[2][NB];  // [half][block]: the lane's four dims of the first position, then of the second
@@ -433,17 +624,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float2 sa = h2_to_f2(vs[n][b / 2]), sb = h2_to_f2(vs[n][NB / 2 + b / 2]);
-          const float x0 = p[n][0] * (b & 1 ? sa.y : sa.x), x1 = p[n][1] * (b & 1 ? sb.y : sb.x);
-          const __half2 h = __floats2half2_rn(x0, x1);
+          const float2 x = mul2(p[n], vs[n][b]);
+          const __half2 h = __floats2half2_rn(x.x, x.y);
           const float2 f = __half22float2(h);
-          const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+          const float2 rest = add2(x, make_float2(-f.x, -f.y));
+          const __half2 l = __floats2half2_rn(rest.x, rest.y);
           hi[n] = *reinterpret_cast<const uint32_t*>(&h);
           lo[n] = *reinterpret_cast<const uint32_t*>(&l);
         }
         uint32_t v0[4], v1[4];
-        codes_to_half(vw[0][b], v0);  // dims 4 gid + {0, 1, 2, 3} of the block; (first, second position)
-        codes_to_half(vw[1][b], v1);
+        codes_to_half(vw[0][b], ex, v0);  // dims 4 gid + {0, 1, 2, 3} of the block; (first, second position)
+        codes_to_half(vw[1][b], ex, v1);
         const uint32_t even[4] = {v0[0], v0[1], v1[0], v1[1]}, odd[4] = {v0[2], v0[3], v1[2], v1[3]};
         if constexpr (NC == 8) {
           mma16816(acc[2 * b], even, hi[0], hi[1], acc[2 * b]);
@@ -473,120 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         flushed = true;
       }
     }
-    cp_async_wait_all();
-
-    // ---- the warp's result
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    {
-      const float keep = flushed ? (ref_flushed == ref ? 1.f : exp2_approx(ref_flushed - ref)) : 0.f;
-      const float k0 = __shfl_sync(0xffffffffu, keep, 8 * tig), k1 = __shfl_sync(0xffffffffu, keep, 8 * tig + 4);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float* f = my_acc + (4 * m + j) * 32 + lane;
-          float v = flushed ? fmaf(*f, j & 1 ? k1 : k0, acc[m][j]) : acc[m][j];
-          if (j >= 2) v *= 0.0625f;  // the odd dims' codes were times 16
-          if constexpr (NC == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);  // high and low part
-          *f = v;
-        }
-    }
-    if (tig == 0) {
-      sm.ref[warp][gid] = ref;
-      sm.sum[warp][gid] = sum;
-    }
-    __syncthreads();
-
-    // ---- the CTA's result: entry e = register * 32 + lane holds (dim, column)
-    const bool split = u > row_unit || seg_end < row_unit + units;
-    float* slot = nullptr;
-    if (split) slot = slots + (size_t)(2 * cta + (u == row_unit ? 1 : 0)) * slot_floats(D);
-    auto owner = [&](long long x) {  // of unit x
-      const long long cut = longer * (piece + 1);
-      return (int)(x < cut ? x / (piece + 1) : longer + (x - cut) / piece);
-    };
-    auto entry_dim = [&](int e) { return (e >> 8) * 32 + ((e & 31) >> 2) * 4 + ((e >> 7) & 1) * 2 + ((e >> 6) & 1); };
-    auto entry_col = [&](int e) { return (e & 3) * 2 + ((e >> 5) & 1); };
-    auto put = [&](int e, float v, float s) {
-      const int c = row.cbase + entry_col(e);
-      if (entry_col(e) >= NC || c >= ncols) return;
-      const long long at = (long long)(row.start + c / group) * a.out_stride + (row.head * group + c % group) * D + entry_dim(e);
-      store_elem(a.out, dtype, at, s != 0.f ? v / s : 0.f);
-    };
-    for (int e = tid; e < 8 * D; e += kThreads) {
-      const int c = entry_col(e);
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.ref[w][c]);
-      float v = 0.f, s = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float r_w = sm.ref[w][c];
-        const float k = r_w == top ? 1.f : exp2_approx(r_w - top);
-        if (r_w != -INFINITY) {
-          v = fmaf(sm.acc[w][e], k, v);
-          s = fmaf(sm.sum[w][c], k, s);
-        } else {
-          v += sm.acc[w][e] != 0.f ? sm.acc[w][e] : 0.f;  // NaN stays NaN
-          s += sm.sum[w][c];
-        }
-      }
-      if (split) {
-        __stcg(slot + e, v);
-        if (e < 64 && (e >> 2 & 7) == 0) {  // registers 0 and 1 of lanes 0-3: one entry for every column
-          __stcg(slot + 8 * D + c, top);
-          __stcg(slot + 8 * D + 8 + c, s);
-        }
-      } else {
-        put(e, v, s);
-      }
-    }
-    if (split) {
-      __syncthreads();
-      const int c0 = owner(row_unit), c1 = owner(row_unit + units - 1), parts = c1 - c0 + 1;
-      if (tid == 0) {
-        const unsigned old = atom_add_acq_rel(&counters[c0], 1u);
-        sm.last = old == (unsigned)(parts - 1);
-        if (sm.last) counters[c0] = 0;
-      }
-      __syncthreads();
-      if (sm.last) {
-        // weights of the parts, then the sums in the order of the positions
-        float* wt = reinterpret_cast<float*>(sm.ring);  // [part][8]
-        float* den = &sm.sum[0][0];
-        auto part = [&](int i) { return slots + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * slot_floats(D); };
-        if (tid < 8) {
-          float top = -INFINITY, s = 0.f;
-          for (int i = 0; i < parts; ++i) top = fmaxf(top, __ldcg(part(i) + 8 * D + tid));
-          for (int i = 0; i < parts; ++i) {
-            const float r_i = __ldcg(part(i) + 8 * D + tid);
-            const float k = r_i == top ? 1.f : exp2_approx(r_i - top);
-            wt[i * 8 + tid] = k;
-            s = fmaf(__ldcg(part(i) + 8 * D + 8 + tid), k, s);
-          }
-          den[tid] = s;
-        }
-        __syncthreads();
-        for (int e4 = tid; e4 < 2 * D; e4 += kThreads) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-          for (int i = 0; i < parts; ++i) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(part(i)) + e4);
-            const float* w = wt + i * 8;
-            const int b = (e4 >> 3) & 1;
-            v[0] = fmaf(x.x, w[b], v[0]);
-            v[1] = fmaf(x.y, w[2 + b], v[1]);
-            v[2] = fmaf(x.z, w[4 + b], v[2]);
-            v[3] = fmaf(x.w, w[6 + b], v[3]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) put(4 * e4 + j, v[j], den[entry_col(4 * e4 + j)]);
-        }
-      }
-    }
-    __syncthreads();
-    u = seg_end;
+    pending = true;
   }
 }
 
@@ -595,11 +673,19 @@ constexpr size_t kCounterBytes = kMaxCtas * sizeof(unsigned);
 template <int D, int NC>
 cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
   constexpr size_t smem = sizeof(AttnSmem<D, NC>);
+  static_assert(kWarps == 8, "a warp per column");
   static_assert(smem <= 113 * 1024, "two CTAs share an SM");
-  static_assert(sizeof(((AttnSmem<D, NC>*)nullptr)->ring) >= kMaxCtas * 8 * sizeof(float), "weights of a row's parts");
+  static_assert(sizeof(((AttnSmem<D, NC>*)nullptr)->acc) >= kMaxCtas * 8 * sizeof(float), "weights of a row's parts");
   auto* kern = kv4_attn_kernel<D, NC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   // no more CTAs than units at the stated bounds
   const int group = a.n_q_heads / a.c.n_kv_heads;
   const long long len = min((long long)a.max_len, (long long)a.table_stride * a.c.page_len);
