@@ -502,7 +502,18 @@ def stage_op_attention_decode_static(q, k_cache, v_cache, seq, pos, out, n_chunk
 # the entry points take its sizes from the shape.  Unlike the entry points above, which take raw buffers, these
 # check types, shapes and devices: an index array of another type would be read as garbage.
 
-_KV4_DTYPE = {"torch.float32": STAGE_F32, "torch.float16": STAGE_F16, "torch.bfloat16": STAGE_BF16}
+# They are called once per block and step, so the checks are kept short.
+
+_torch = None
+_KV4_DTYPE: dict = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _KV4_DTYPE.update({torch.float32: STAGE_F32, torch.float16: STAGE_F16, torch.bfloat16: STAGE_BF16})
+    _torch = torch
+    return torch
 
 
 def _invalid(msg: str):
@@ -510,45 +521,50 @@ def _invalid(msg: str):
 
 
 def _kv4_cache(cache):
-    if cache.dim() != 4 or str(cache.dtype) != "torch.uint8" or not cache.is_contiguous():
+    torch = _torch or _load_torch()
+    shape = cache.shape
+    if len(shape) != 4 or cache.dtype is not torch.uint8 or not cache.is_contiguous():
         _invalid("cache must be a contiguous uint8 tensor [n_pages, n_kv_heads, page_len / 16, 18 * head_dim]")
-    n_pages, hkv, tiles, nb = cache.shape
+    n_pages, hkv, tiles, nb = shape
     if nb % 18:
         _invalid("the cache's last dimension must be 18 * head_dim")
     return cache.data_ptr(), n_pages, tiles * 16, hkv, nb // 18
 
 
-def _kv4_device(device, *tensors) -> None:
-    """Every tensor on `device`, and that one the current one: a launch goes to the current device."""
-    import torch
-    if device.type != "cuda":
-        _invalid("device tensors are needed")
+def _kv4_launch(stream, *tensors) -> int:
+    """The stream to launch on, once every tensor is known to be on the current device: a launch goes there."""
+    torch = _torch or _load_torch()
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            _invalid(f"tensors on {device} and {t.device}")
-    if device.index != torch.cuda.current_device():
-        _invalid(f"tensors on {device}, but the current device is {torch.cuda.current_device()}")
+        if t.get_device() != dev:
+            _invalid("tensors on several devices")
+    if dev < 0:
+        _invalid("device tensors are needed")
+    if dev != torch.cuda.current_device():
+        _invalid(f"tensors on device {dev}, but the current one is {torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _i32dev(t, what: str, n: Optional[int] = None, least: Optional[int] = None) -> int:
-    if str(t.dtype) != "torch.int32" or not t.is_contiguous():
+def _i32dev(t, what: str, n: int) -> int:
+    if t.dtype is not _torch.int32 or not t.is_contiguous():
         _invalid(f"{what} must be a contiguous int32 tensor")
-    if (n is not None and t.numel() != n) or (least is not None and t.numel() < least):
-        _invalid(f"{what} has {t.numel()} entries, not {n if n is not None else least}")
+    if t.numel() != n:
+        _invalid(f"{what} has {t.numel()} entries, not {n}")
     return t.data_ptr()
 
 
 def _rows(t, heads: int, head_dim: int, what: str):
     """(pointer, dtype, row stride) of rows [n, heads, head_dim], which may lie apart (a slice of a fused output)."""
-    dt = _KV4_DTYPE.get(str(t.dtype))
+    dt = _KV4_DTYPE.get(t.dtype)
     if dt is None:
         _invalid(f"{what} must be float32, float16 or bfloat16")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         _invalid(f"{what} must be [n_tok, {heads}, {head_dim}]")
-    s = t.stride()
-    if t.shape[0] and (s[2] != 1 or (heads > 1 and s[1] != head_dim)):
+    s0, s1, s2 = t.stride()
+    if shape[0] and (s2 != 1 or (heads > 1 and s1 != head_dim)):
         _invalid(f"the heads of a row of {what} must lie side by side")
-    return t.data_ptr(), dt, s[0] if t.shape[0] > 1 else heads * head_dim
+    return t.data_ptr(), dt, s0 if shape[0] > 1 else heads * head_dim
 
 
 def stage_op_kv4_cache_bytes(n_pages: int, page_len: int, n_kv_heads: int, head_dim: int) -> int:
@@ -567,47 +583,54 @@ def stage_op_kv4_plan(page_len: int, seq_len, new_len, table, free_ring, free_st
     """Block tables and slot maps of one step (include/stage_kv4.h).  Device int32 tensors: seq_len, keep_len,
     new_len, seq_len_out [n]; table [n, stride]; free_ring; free_state, free_state_out [2]; cu_new [n + 1];
     slot, pos, seq [n_tok]; status [1].  n_pages: the cache's pages (default: as many as the ring holds)."""
-    n = seq_len.numel()
-    _kv4_device(seq_len.device, keep_len, new_len, table, free_ring, free_state, seq_len_out, free_state_out, cu_new, slot,
-                pos, seq, status)
+    tensors = (seq_len, new_len, table, free_ring, free_state, seq_len_out, free_state_out, cu_new, slot, pos, seq, status)
+    stream = _kv4_launch(stream, *tensors) if keep_len is None else _kv4_launch(stream, *tensors, keep_len)
+    n, n_tok, ring_len = seq_len.numel(), slot.numel(), free_ring.numel()
     if table.dim() != 2 or table.shape[0] != n:
         _invalid("table must be [n_seqs, stride]")
-    n_tok = slot.numel()
-    _opcheck(lib().stage_op_kv4_plan(
-        n, page_len, free_ring.numel() if n_pages is None else n_pages, _i32dev(seq_len, "seq_len"),
+    stride = table.shape[1]
+    rc = (_lib or lib()).stage_op_kv4_plan(
+        n, page_len, ring_len if n_pages is None else n_pages, _i32dev(seq_len, "seq_len", n),
         None if keep_len is None else _i32dev(keep_len, "keep_len", n), _i32dev(new_len, "new_len", n),
-        _i32dev(table, "table"), table.shape[1], _i32dev(free_ring, "free_ring"), free_ring.numel(),
+        _i32dev(table, "table", n * stride), stride, _i32dev(free_ring, "free_ring", ring_len), ring_len,
         _i32dev(free_state, "free_state", 2), _i32dev(seq_len_out, "seq_len_out", n),
-        _i32dev(free_state_out, "free_state_out", 2), n_tok, _i32dev(cu_new, "cu_new", n + 1), _i32dev(slot, "slot"),
-        _i32dev(pos, "pos", n_tok), _i32dev(seq, "seq", n_tok), _i32dev(status, "status", 1), _stream(stream)))
+        _i32dev(free_state_out, "free_state_out", 2), n_tok, _i32dev(cu_new, "cu_new", n + 1),
+        _i32dev(slot, "slot", n_tok), _i32dev(pos, "pos", n_tok), _i32dev(seq, "seq", n_tok),
+        _i32dev(status, "status", 1), stream)
+    if rc:
+        _opcheck(rc)
 
 
 def stage_op_kv4_append(cache, k, v, slot, stream=None) -> None:
     """Quantise rows k, v [n_tok, n_kv_heads, head_dim] (float32, float16 or bfloat16; rows may lie apart) and write
     them to their slots (int32 [n_tok]; outside the cache: skipped)."""
     ptr, n_pages, page_len, hkv, d = _kv4_cache(cache)
-    _kv4_device(cache.device, k, v, slot)
+    stream = _kv4_launch(stream, cache, k, v, slot)
     kp, kt, ks = _rows(k, hkv, d, "k")
     vp, vt, vs = _rows(v, hkv, d, "v")
     n_tok = k.shape[0]
     if v.shape[0] != n_tok or kt != vt or ks != vs:
         _invalid("k and v must have one length, type and row stride")
-    _opcheck(lib().stage_op_kv4_append(ptr, n_pages, page_len, hkv, d, kp, vp, kt, ks, _i32dev(slot, "slot", n_tok), n_tok,
-                                       _stream(stream)))
+    rc = (_lib or lib()).stage_op_kv4_append(ptr, n_pages, page_len, hkv, d, kp, vp, kt, ks, _i32dev(slot, "slot", n_tok),
+                                             n_tok, stream)
+    if rc:
+        _opcheck(rc)
 
 
 def stage_op_kv4_read(cache, slot, k_out, v_out, stream=None) -> None:
     """Rows at the slots (int32 [n_tok]) as values into k_out, v_out [n_tok, n_kv_heads, head_dim]; rows of slots
     outside the cache stay as they were."""
     ptr, n_pages, page_len, hkv, d = _kv4_cache(cache)
-    _kv4_device(cache.device, k_out, v_out, slot)
+    stream = _kv4_launch(stream, cache, k_out, v_out, slot)
     kp, kt, ks = _rows(k_out, hkv, d, "k_out")
     vp, vt, vs = _rows(v_out, hkv, d, "v_out")
     n_tok = k_out.shape[0]
     if v_out.shape[0] != n_tok or kt != vt or ks != vs:
         _invalid("k_out and v_out must have one length, type and row stride")
-    _opcheck(lib().stage_op_kv4_read(ptr, n_pages, page_len, hkv, d, _i32dev(slot, "slot", n_tok), n_tok, kp, vp, kt, ks,
-                                     _stream(stream)))
+    rc = (_lib or lib()).stage_op_kv4_read(ptr, n_pages, page_len, hkv, d, _i32dev(slot, "slot", n_tok), n_tok, kp, vp, kt,
+                                           ks, stream)
+    if rc:
+        _opcheck(rc)
 
 
 def stage_op_kv4_attention_workspace_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int,
@@ -620,10 +643,10 @@ def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_
     [n_seqs, stride]; max_q, max_len bound the query tokens and the length of a sequence; workspace: a tensor of
     stage_op_kv4_attention_workspace_bytes(...) bytes, zero before its first use."""
     ptr, n_pages, page_len, hkv, d = _kv4_cache(cache)
-    _kv4_device(cache.device, q, cu_q, seq_len, table, out, workspace)
+    stream = _kv4_launch(stream, cache, q, cu_q, seq_len, table, out, workspace)
     if q.dim() != 3 or out.shape != q.shape:
         _invalid("q and out must be [n_tok, n_q_heads, head_dim]")
-    hq = q.shape[1]
+    n_tok, hq, _ = q.shape
     qp, qt, qs = _rows(q, hq, d, "q")
     op, ot, os_ = _rows(out, hq, d, "out")
     n = seq_len.numel()
@@ -631,7 +654,10 @@ def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_
         _invalid("q and out must have one type")
     if table.dim() != 2 or table.shape[0] != n or not workspace.is_contiguous():
         _invalid("table must be [n_seqs, stride], and workspace contiguous")
-    _opcheck(lib().stage_op_kv4_attention(
-        ptr, n_pages, page_len, hkv, d, qp, qt, qs, q.shape[0], hq, _i32dev(cu_q, "cu_q", n + 1),
-        _i32dev(seq_len, "seq_len", n), _i32dev(table, "table"), table.shape[1], n, max_q, max_len, op, os_,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    stride = table.shape[1]
+    rc = (_lib or lib()).stage_op_kv4_attention(
+        ptr, n_pages, page_len, hkv, d, qp, qt, qs, n_tok, hq, _i32dev(cu_q, "cu_q", n + 1),
+        _i32dev(seq_len, "seq_len", n), _i32dev(table, "table", n * stride), stride, n, max_q, max_len, op, os_,
+        workspace.data_ptr(), workspace.nbytes, stream)
+    if rc:
+        _opcheck(rc)
