@@ -19,7 +19,7 @@ LIB = os.path.join(LIB_DIR, "libstage.so")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kernels_decode.cu", "kernels_prefill.cu", "kernels_mega.cu", "kernels_mega_moe.cu", "kernels_kv4.cu",
-           "kernels_kv4_attn.cu", "stage.cu", "ops.cu", "ops_kv4.cu"]
+           "kernels_kv4_attn.cu", "kernels_kv4_chunk.cu", "stage.cu", "ops.cu", "ops_kv4.cu"]
 
 
 def nvcc() -> str:

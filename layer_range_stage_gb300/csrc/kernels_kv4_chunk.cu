@@ -1,0 +1,645 @@
+// Attention of many query tokens per sequence (prompt chunks) over the paged 4-bit KV cache (sm_103a): tcgen05 tiles.
+//
+// A CTA has 128 rows -- (token, head of the group) pairs of one sequence and KV head -- and walks the positions in tiles
+// of 64.  Roles, joined by mbarriers:
+//   warps 0-7   softmax: warp w has the rows 32 (w % 4) .. + 31 (the TMEM lanes it may read), w / 4 the half of a tile's
+//               positions, and of the output's dims, that its threads take;
+//   warps 8-11  copy the packed tiles in (cp.async, one tile ahead) and turn them into fp16 operands in the tensor
+//               core's swizzled layout, K as [position][dim], V as [dim][position];
+//   warp 12     issues the products: S = Q K^T into TMEM, O = P V with P read from TMEM.
+// Every tile's O is added to float32 registers (rounded to nearest), so no sum in TMEM runs over more than one tile
+// and a change of the softmax's reference needs no pass over TMEM.
+//
+// Precision: a value s (c - 8) has 15 significant bits, so two fp16 numbers hold it exactly; q and the probabilities are
+// float32 and two fp16 numbers hold 22 bits.  STAGE_F32 multiplies high by high, low by high and high by low (three
+// products each for S and O); STAGE_F16 has an exact q in one number and keeps K and V exact (two); STAGE_BF16, whose
+// output keeps 8 bits, rounds K, V and the probabilities to fp16 once (one).  Scales are divided by a power of two
+// above the largest one, so that fp16's range holds them whatever they are, and what lies below 2^-25 of the largest is
+// lost: of a tile's K scales, where it moves a score by 2^-24 of the largest one; of a position's V scales in
+// STAGE_F32, of a tile's in the 16-bit types.  The power goes into the score's factor (K) and the probabilities (V).
+
+#include <atomic>
+#include <cfloat>
+#include <climits>
+#include <cstddef>
+
+#include "kernels.cuh"
+#include "kv4_attn.cuh"
+#include "tc.cuh"
+
+namespace lrs {
+
+namespace {
+
+constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
+constexpr int kSoftWarps = 8, kProdWarps = 4, kProd = 32 * kProdWarps;
+constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 1);
+constexpr int kInfo = 8;  // ring of what the tiles' producers tell the softmax
+constexpr float kChunkTop = 11.f, kChunkSlack = 4.f;
+constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kColO = 256;
+
+struct ChunkBars {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+};
+
+struct alignas(16) ChunkMisc {
+  ChunkBars bar;
+  float k_pow[kInfo], v_exp[kInfo], v_inv[kInfo];  // 2^E_k; E_v; 2^-E_v
+  alignas(16) float v_pos_exp[kInfo][kPosTile];  // read in 16-byte pieces
+  alignas(16) float v_pos_inv[kInfo][kPosTile];  // STAGE_F32: E_v and 2^-E_v of each position
+  uint32_t v_norm[kProdWarps][kPosTile / 2];                     // and 2^-E_v of two positions in fp16, one copy per warp
+  int absent[kInfo];                               // bit i: the tile's i-th 16 positions are not there
+  int bad[kInfo];                                  // whether some V scale is no number
+  int first_bad[kInfo][4];                         // per block of dims: the first such position
+  float top[2][2][kRowsTile];                      // [tile parity][half][row]
+  uint32_t tmem;
+  int abort;
+};
+
+static_assert(offsetof(ChunkMisc, v_pos_exp) % 16 == 0 && offsetof(ChunkMisc, v_pos_inv) % 16 == 0, "vector reads");
+
+template <int D, int NQ, int NKV>
+struct ChunkLayout {
+  static constexpr int q_part = kRowsTile * D * 2, k_part = kPosTile * D * 2, v_part = D * kPosTile * 2;
+  static constexpr int sub_stride = kv4_tile_bytes(D) + 32, stage_bytes = kSub * sub_stride;
+  static constexpr int off_k = NQ * q_part, off_v = off_k + 2 * NKV * k_part, off_raw = off_v + 2 * NKV * v_part;
+  static constexpr int off_misc = off_raw + 2 * stage_bytes;
+  static_assert(off_k % 1024 == 0 && off_v % 1024 == 0 && k_part % 1024 == 0 && v_part % 1024 == 0, "swizzled tiles");
+  static_assert(off_raw % 16 == 0 && stage_bytes % 16 == 0 && sub_stride % 16 == 0 && off_misc % 16 == 0, "16-byte pieces");
+  static constexpr int bytes = off_misc + (int)sizeof(ChunkMisc) + 1024;  // and the alignment to 1024
+};
+
+// Bounded wait that also gives up as soon as another role of the CTA has given up.
+__device__ __forceinline__ bool cwait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// The codes of (1024 + c) and (1024 + 16 c) pairs minus 8.
+__device__ __forceinline__ __half2 code_low(uint32_t x, uint32_t ex) {
+  return __hadd2(as_h2(and_or(x, 0x000f000fu, ex)), __floats2half2_rn(-1032.f, -1032.f));
+}
+__device__ __forceinline__ __half2 code_high(uint32_t x, uint32_t ex) {
+  return __hfma2(as_h2(and_or(x, 0x00f000f0u, ex)), __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-72.f, -72.f));
+}
+
+// 2^-e as fp16, e in [-14, 16].
+__device__ __forceinline__ uint16_t half_power(int e) { return (uint16_t)(e <= 14 ? (15 - e) << 10 : 0x400 >> (e - 14)); }
+
+template <int D, int NQ, int NKV, int NP>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a, int dtype) {
+  using L = ChunkLayout<D, NQ, NKV>;
+  constexpr int NB = D / 32, TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
+  constexpr int HD = D / 2;  // dims of a softmax thread
+  extern __shared__ unsigned char chunk_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)chunk_raw + 1023) & ~(uintptr_t)1023);
+  ChunkMisc& M = *reinterpret_cast<ChunkMisc*>(sm + L::off_misc);
+  ChunkBars& B = M.bar;
+  volatile int* abort_flag = &M.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- the CTA's rows
+  const int seq = blockIdx.z, head = blockIdx.y, group = a.n_q_heads / a.c.n_kv_heads;
+  int start;
+  const int count = seq_tokens(a, seq, &start), len = seq_positions(a, seq);
+  const int ncols = min(count, a.max_q) * group;
+  const int row0 = (int)(gridDim.x - 1 - blockIdx.x) * kRowsTile;  // the longest walks first
+  if (row0 >= ncols) return;
+  const int k_last = min(ncols - 1, row0 + kRowsTile - 1) / group;
+  const int lim_hi = max(0, len - count + k_last + 1);                // positions that some row sees
+  const int lim_lo = max(0, len - count + row0 / group + 1);          // positions that every row sees
+  const int nt = (lim_hi + kPosTile - 1) / kPosTile;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.k_full[i], kProd);
+      mbar_init(&B.v_full[i], kProd);
+      mbar_init(&B.k_empty[i], 1);
+      mbar_init(&B.v_empty[i], 1);
+      mbar_init(&B.s_full[i], 2);
+      mbar_init(&B.o_full[i], 2);
+      mbar_init(&B.p_full[i], 32 * kSoftWarps);
+    }
+    mbar_init(&B.drain, 1);
+    M.abort = 0;
+    for (int i = 0; i < kInfo; ++i) {
+      M.bad[i] = 0;
+      for (int b = 0; b < 4; ++b) M.first_bad[i][b] = INT_MAX;
+    }
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&M.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+
+  // ---- q into shared memory: scaled by a power of two per row, high and low part; within eight dims the order of the
+  // unpacked codes (0, 4, 1, 5, 2, 6, 3, 7)
+  const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1;
+  const int col = row0 + row;
+  const bool live = warp < kSoftWarps && col < ncols;
+  const int col_k = col / group;
+  const int lim = live ? max(0, len - count + col_k + 1) : 0;
+  const long long elem = live ? (long long)(head * group + col % group) * D + half * HD : 0;
+  float zscale = 0.f;
+  if (warp < kSoftWarps) {
+    float q[HD / 8][8], top = 0.f;
+#pragma unroll
+    for (int g = 0; g < HD / 8; ++g) {
+      if (live) {
+        load8(a.q, dtype, (long long)(start + col_k) * a.q_stride + elem + 8 * g, q[g]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[g][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[g][i]));
+    }
+    M.top[0][half][row] = top;
+    named_bar(1 + (warp & 3), 64);
+    top = fmaxf(top, M.top[0][half ^ 1][row]);
+    const int e = top <= FLT_MAX ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+    zscale = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+    const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+#pragma unroll
+    for (int g = 0; g < HD / 8; ++g) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float x0 = q[g][t] * up, x1 = q[g][t + 4] * up;
+        const __half2 h = __floats2half2_rn(x0, x1);
+        const float2 f = __half22float2(h);
+        hi[t] = as_u32(h);
+        lo[t] = as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
+      }
+      const int dim = half * HD + 8 * g;
+      unsigned char* at = sm + (dim >> 6) * (kRowsTile * 128) + sw128_offset(row, dim & 63);
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (NQ == 2) *reinterpret_cast<uint4*>(at + L::q_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = M.tmem;
+
+  if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
+    // ---------------- producers ----------------
+    const int p = tid - 32 * kSoftWarps, pw = p >> 5;
+    const int tpp = a.c.page_len / kKv4Tile, n16 = (lim_hi + kKv4Tile - 1) / kKv4Tile;
+    const int* trow = a.table + (long long)seq * a.table_stride;
+    auto fetch = [&](int i) {  // returns the absent parts
+      int absent = 0;
+      unsigned char* raw = sm + L::off_raw + (i & 1) * L::stage_bytes;
+#pragma unroll
+      for (int s = 0; s < kSub; ++s) {
+        const int t = i * kSub + s, pg = t / tpp;
+        const int id = t < n16 ? trow[pg] : -1;
+        if (id < 0 || id >= a.c.n_pages) {
+          absent |= 1 << s;
+          continue;
+        }
+        const uint8_t* src = a.c.data + (((long long)id * a.c.n_kv_heads + head) * tpp + (t - pg * tpp)) * TILE;
+        for (int o = p * 16; o < TILE; o += kProd * 16)  // V's second half 16 bytes on: see the reads below
+          cp_async16(raw + s * L::sub_stride + o + (o >= HALF + CODES / 2 ? 16 : 0), src + o);
+      }
+      cp_async_commit();
+      return absent;
+    };
+    const uint32_t ex = exponent_bits();
+    int absent_next = nt ? fetch(0) : 0;
+    bool ok = true;  // once a wait has run out every thread still goes through the barriers, and does nothing else
+    for (int i = 0; i < nt; ++i) {
+      const int st = i & 1, inf = i & (kInfo - 1), absent = absent_next;
+      cp_async_wait_all();
+      named_bar(5, kProd);  // tile i is there, and nobody reads tile i - 1 any more
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;
+      if (i + 1 < nt) absent_next = fetch(i + 1);
+      const unsigned char* raw = sm + L::off_raw + st * L::stage_bytes;
+      const bool ragged = absent || (i + 1) * kPosTile > lim_hi;  // some positions do not count: their scales read as 0
+
+      // the largest scales (every warp for itself)
+      int e_k, e_v;
+      bool v_bad = false;
+      {
+        const int s = lane >> 3, at = i * kPosTile + s * kKv4Tile + 2 * (lane & 7);
+        const bool ok0 = !(absent >> s & 1) && at < lim_hi, ok1 = !(absent >> s & 1) && at + 1 < lim_hi;
+        const unsigned char* base = raw + s * L::sub_stride + (lane & 7) * (4 * NB);
+        uint32_t top[2];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const unsigned char* sc = base + (side ? HALF + CODES + 16 : CODES);
+          uint32_t w[NB];
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(sc);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(sc);
+            w[0] = u.x, w[1] = u.y;
+          }
+          __half2 m = __floats2half2_rn(0.f, 0.f), first = m;  // first: of the first position alone
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t u = (b < NB / 2 ? ok0 : ok1) ? w[b] & 0x7fff7fffu : 0u;
+            if (side) v_bad |= (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
+            if (NP == 2 && side && b == NB / 2) {
+              first = m;
+              m = __floats2half2_rn(0.f, 0.f);
+            }
+            m = __hmax2(m, as_h2(u));  // NaN loses
+          }
+          top[side] = max(as_u32(m) >> 16, as_u32(m) & 0xffffu);
+          if (NP == 2 && side) {
+            const int e0 = (int)min(max(as_u32(first) >> 16, as_u32(first) & 0xffffu) >> 10, 30u) - 14;
+            const int e1 = (int)min(top[1] >> 10, 30u) - 14;
+            M.v_norm[pw][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
+            if (pw == 0) {
+              *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
+              *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
+                  make_float2(__uint_as_float((uint32_t)(127 - e0) << 23), __uint_as_float((uint32_t)(127 - e1) << 23));
+            }
+          }
+        }
+        e_k = (int)min(__reduce_max_sync(0xffffffffu, top[0]) >> 10, 30u) - 14;
+        e_v = NP == 2 ? 0 : (int)min(__reduce_max_sync(0xffffffffu, top[1]) >> 10, 30u) - 14;
+        v_bad = __any_sync(0xffffffffu, v_bad);
+      }
+      const __half2 norm_k = __half2half2(__ushort_as_half(half_power(e_k)));
+      const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
+      if (NP == 2) __syncwarp();  // v_norm
+      if (p == 0) {
+        M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
+        M.v_exp[inf] = (float)e_v;
+        M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
+        M.absent[inf] = absent;
+        M.bad[inf] = v_bad;
+        const int next = (inf + 1) & (kInfo - 1);  // read last before the softmax's sixth tile before
+        for (int b = 0; b < 4; ++b) M.first_bad[next][b] = INT_MAX;
+      }
+
+      // K: 64 positions x 4 x (the word of eight dims of every block)
+      if (i >= 2) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag));
+      if (!ok) continue;
+      unsigned char* kt = sm + L::off_k + st * NKV * L::k_part;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * (pw + 4 * j), s = pos >> 4;
+        const unsigned char* src = raw + s * L::sub_stride;
+        uint32_t w[NB], sc[NB / 2];
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + (pos & 15) * (D / 2) + tig * 16);
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+          const uint2 v = *reinterpret_cast<const uint2*>(src + CODES + (pos & 15) * (2 * NB));
+          sc[0] = v.x, sc[1] = v.y;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(src + (pos & 15) * (D / 2) + tig * 8);
+          w[0] = u.x, w[1] = u.y;
+          sc[0] = *reinterpret_cast<const uint32_t*>(src + CODES + (pos & 15) * (2 * NB));
+        }
+        if (ragged && ((absent >> s & 1) || i * kPosTile + pos >= lim_hi)) {
+#pragma unroll
+          for (int b = 0; b < NB / 2; ++b) sc[b] = 0;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[b / 2], 0, b & 1 ? 0x3232 : 0x1010)), norm_k);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t x = t < 2 ? w[b] : w[b] >> 8;
+            const __half2 n = t & 1 ? code_high(x, ex) : code_low(x, ex);
+            const __half2 h = __hmul2(n, s2);
+            hi[t] = as_u32(h);
+            if (NKV == 2) lo[t] = as_u32(__hfma2(n, s2, __hneg2(h)));
+          }
+          unsigned char* at = kt + (b >> 1) * (kPosTile * 128) + sw128_offset(pos, 32 * (b & 1) + 8 * tig);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (NKV == 2) *reinterpret_cast<uint4*>(at + L::k_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(&B.k_full[st]);
+
+      // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of every block.  Eight lanes with the
+      // same dims and different chunks read 16 bytes each from places 16 bytes apart modulo 128 (hence the paddings
+      // of the raw tiles) and write a whole row of 64 positions
+      if (i >= 2) ok = __all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag));
+      if (!ok) continue;
+      {
+        unsigned char* vt = sm + L::off_v + st * NKV * L::v_part;
+        const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
+        const unsigned char* src = raw + s * L::sub_stride + HALF;
+        const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
+        const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB);
+        uint32_t hi[NB][2][4], lo[NB][2][4];
+#pragma unroll
+        for (int tig = 0; tig < 4; ++tig) {
+          uint32_t w[NB], sc[NB];  // the first position's blocks in pairs, then the second's
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4*>(codes + tig * 16);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(scales + tig * 16);
+            sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(codes + tig * 8);
+            w[0] = u.x, w[1] = u.y;
+            const uint2 v = *reinterpret_cast<const uint2*>(scales + tig * 8);
+            sc[0] = v.x, sc[1] = v.y;
+          }
+          if (ragged || v_bad) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at = i * kPosTile + chunk * 8 + 2 * tig + e;
+              const bool off = (absent >> s & 1) || at >= lim_hi;
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                uint32_t& u = sc[e * (NB / 2) + b / 2];
+                const uint32_t mask = b & 1 ? 0xffff0000u : 0xffffu;
+                const bool bad = (u & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
+                if (bad && !off) atomicMin(&M.first_bad[inf][b], at);
+                if (bad || off) u &= ~mask;
+              }
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[b / 2], sc[NB / 2 + b / 2], b & 1 ? 0x7632 : 0x5410)),
+                                       NP == 2 ? as_h2(M.v_norm[pw][4 * chunk + tig]) : norm_v);
+            // byte dsel of the block's two bytes, of both positions
+            const uint32_t x = __byte_perm(w[b / 2], w[NB / 2 + b / 2], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
+            const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
+            const __half2 h0 = __hmul2(n0, s2), h1 = __hmul2(n1, s2);
+            hi[b][0][tig] = as_u32(h0);
+            hi[b][1][tig] = as_u32(h1);
+            if (NKV == 2) {
+              lo[b][0][tig] = as_u32(__hfma2(n0, s2, __hneg2(h0)));
+              lo[b][1][tig] = as_u32(__hfma2(n1, s2, __hneg2(h1)));
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int dim = 32 * b + 4 * gid + 2 * dsel + k;
+            unsigned char* at = vt + sw128_offset(dim, 8 * chunk);
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[b][k][0], hi[b][k][1], hi[b][k][2], hi[b][k][3]);
+            if (NKV == 2) *reinterpret_cast<uint4*>(at + L::v_part) = make_uint4(lo[b][k][0], lo[b][k][1], lo[b][k][2], lo[b][k][3]);
+          }
+      }
+      fence_async_smem();
+      mbar_arrive(&B.v_full[st]);
+    }
+    cp_async_wait_all();
+  } else if (warp == kSoftWarps + kProdWarps) {
+    // ---------------- products ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_f16_f32(kRowsTile, kPosTile), id_o = idesc_f16_f32(kRowsTile, D);
+      const uint32_t q0 = smem_u32(sm);
+      auto scores = [&](int i) {
+        const int st = i & 1;
+        if (!cwait(&B.k_full[st], (uint32_t)(i >> 1) & 1u, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t k0 = smem_u32(sm + L::off_k + st * NKV * L::k_part);
+        uint32_t acc = 0;
+#pragma unroll
+        for (int part = 0; part < NQ + NKV - 1; ++part) {  // high high, [low high,] [high low]
+          const uint32_t qp = q0 + (NQ == 2 && part == 1 ? L::q_part : 0);
+          const uint32_t kp = k0 + (part > 0 && part == NQ ? L::k_part : 0);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            umma_f16_ss(tmem + kColS + st * kPosTile, desc_sw128(qp + (ks >> 2) * (kRowsTile * 128) + (ks & 3) * 32),
+                        desc_sw128(kp + (ks >> 2) * (kPosTile * 128) + (ks & 3) * 32), id_s, acc);
+            acc = 1;
+          }
+        }
+        umma_commit(&B.k_empty[st]);
+        umma_commit(&B.s_full[st]);
+        mbar_arrive(&B.s_full[st]);  // hands on what the producers wrote beside the tile
+        return true;
+      };
+      bool ok = nt == 0 || scores(0);
+      if (ok && nt > 1) ok = scores(1);
+      for (int i = 0; ok && i < nt; ++i) {
+        const int st = i & 1;
+        const uint32_t parity = (uint32_t)(i >> 1) & 1u;
+        ok = cwait(&B.v_full[st], parity, abort_flag) && cwait(&B.p_full[st], parity, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v0 = smem_u32(sm + L::off_v + st * NKV * L::v_part);
+        uint32_t acc = 0;
+#pragma unroll
+        for (int part = 0; part < NP + NKV - 1; ++part) {
+          const uint32_t pp = tmem + kColP + st * 64 + (NP == 2 && part == 1 ? 32 : 0);
+          const uint32_t vp = v0 + (part > 0 && part == NP ? L::v_part : 0);
+#pragma unroll
+          for (int ks = 0; ks < kPosTile / 16; ++ks) {
+            umma_f16_ts(tmem + kColO + st * D, pp + ks * 8, desc_sw128(vp + ks * 32), id_o, acc);
+            acc = 1;
+          }
+        }
+        umma_commit(&B.v_empty[st]);
+        umma_commit(&B.o_full[st]);
+        mbar_arrive(&B.o_full[st]);
+        // the softmax of tile i has read its scores: their place is free
+        if (i + 2 < nt) ok = scores(i + 2);
+      }
+      if (!ok) {  // given up: the products already issued finish before TMEM is released
+        umma_commit(&B.drain);
+        mbar_wait(&B.drain, 0u, kDrainNs);
+      }
+    }
+  } else {
+    // ---------------- softmax ----------------
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    float2 o[HD / 2];
+#pragma unroll
+    for (int j = 0; j < HD / 2; ++j) o[j] = make_float2(0.f, 0.f);
+    float ref = -INFINITY, sum = 0.f;
+    bool ok = true;
+    // adds tile i's O, then the change of reference that followed it
+    auto collect = [&](int i, float keep) {
+      if (!__all_sync(0xffffffffu, cwait(&B.o_full[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag))) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(lanes + kColO + (i & 1) * D + half * HD + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          o[c / 2 + j] = add2(o[c / 2 + j], make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+      }
+      if (M.bad[i & (kInfo - 1)]) {
+#pragma unroll
+        for (int b = 0; b < HD / 32; ++b)
+          if (M.first_bad[i & (kInfo - 1)][half * (HD / 32) + b] < lim) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[16 * b + j] = make_float2(NAN, NAN);
+          }
+      }
+      if (__any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+        for (int j = 0; j < HD / 2; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
+      }
+      return true;
+    };
+    for (int i = 0; i < nt; ++i) {
+      const int st = i & 1, inf = i & (kInfo - 1);
+      // as for the producers: the barriers stay matched when a wait has run out
+      ok = ok && __all_sync(0xffffffffu, cwait(&B.s_full[st], (uint32_t)(i >> 1) & 1u, abort_flag));
+      if (!ok) {
+        named_bar(1 + (warp & 3), 64);
+        continue;
+      }
+      tc_fence_after();
+      uint32_t s[32];
+      tmem_ld32(lanes + kColS + st * kPosTile + half * 32, s);
+      const float f = zscale * M.k_pow[inf], ev = M.v_exp[inf], v_inv = M.v_inv[inf];
+      const int absent = M.absent[inf] >> (2 * half) & 3;
+      tmem_wait_ld();
+      const int pos0 = i * kPosTile + 32 * half;
+      if (pos0 + 32 > lim_lo || absent) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (pos0 + j >= lim || (absent >> (j >> 4) & 1)) s[j] = 0xff800000u;
+      }
+      // exponents in base 2; STAGE_F32: with each position's power of V
+      float most = -INFINITY;
+      if constexpr (NP == 2) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 e4 = *reinterpret_cast<const float4*>(&M.v_pos_exp[inf][32 * half + j]);
+          const float2 w0 = fma2(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), make_float2(f, f), make_float2(e4.x, e4.y));
+          const float2 w1 = fma2(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), make_float2(f, f), make_float2(e4.z, e4.w));
+          s[j] = __float_as_uint(w0.x), s[j + 1] = __float_as_uint(w0.y), s[j + 2] = __float_as_uint(w1.x), s[j + 3] = __float_as_uint(w1.y);
+          most = fmaxf(fmaxf(most, fmaxf(w0.x, w0.y)), fmaxf(w1.x, w1.y));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) most = fmaxf(most, __uint_as_float(s[j]));
+        most = fmaf(most, f, ev);
+      }
+      M.top[st][half][row] = most;
+      named_bar(1 + (warp & 3), 64);
+      most = fmaxf(most, M.top[st][half ^ 1][row]);
+      float keep = 1.f;
+      if (most - kChunkTop > ref + kChunkSlack) {
+        keep = exp2_approx(ref - (most - kChunkTop));
+        ref = most - kChunkTop;
+        sum *= keep;
+      }
+      const float c = ev - (ref == -INFINITY ? 0.f : ref);
+      float2 part = make_float2(0.f, 0.f);
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 sj = make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+        const float2 z = NP == 2 ? add2(sj, make_float2(c, c)) : fma2(sj, make_float2(f, f), make_float2(c, c));
+        const float2 x = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+        part = NP == 2 ? fma2(x, *reinterpret_cast<const float2*>(&M.v_pos_inv[inf][32 * half + 2 * j]), part) : add2(part, x);
+        const __half2 h = __floats2half2_rn(x.x, x.y);
+        hi[j] = as_u32(h);
+        if (NP == 2) {
+          const float2 b = __half22float2(h);
+          const float2 rest = add2(x, make_float2(-b.x, -b.y));
+          lo[j] = as_u32(__floats2half2_rn(rest.x, rest.y));
+        }
+      }
+      sum = fmaf(part.x + part.y, v_inv, sum);
+      tmem_st16(lanes + kColP + st * 64 + half * 16, hi);
+      if (NP == 2) tmem_st16(lanes + kColP + st * 64 + 32 + half * 16, lo);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&B.p_full[st]);
+      if (i > 0) ok = collect(i - 1, keep);
+    }
+    if (ok && nt > 0) ok = collect(nt - 1, 1.f);
+    M.top[nt & 1][half][row] = sum;
+    named_bar(1 + (warp & 3), 64);
+    sum += M.top[nt & 1][half ^ 1][row];
+    if (live) {
+      const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+      const long long at = (long long)(start + col_k) * a.out_stride + elem;
+#pragma unroll
+      for (int j = 0; j < HD / 2; ++j) o[j] = mul2(o[j], make_float2(inv, inv));
+      if (dtype == KV4_F32) {
+        float4* out = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
+#pragma unroll
+        for (int j = 0; j < HD / 4; ++j) out[j] = make_float4(o[2 * j].x, o[2 * j].y, o[2 * j + 1].x, o[2 * j + 1].y);
+      } else {
+        uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j) {
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = o[4 * j + k];
+            if (dtype == KV4_F16) {
+              u[k] = as_u32(__floats2half2_rn(v.x, v.y));
+            } else {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+              u[k] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
+          out[j] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, int NQ, int NKV, int NP>
+cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
+  constexpr int smem = ChunkLayout<D, NQ, NKV>::bytes;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  auto* kern = kv4_chunk_kernel<D, NQ, NKV, NP>;
+  static std::atomic<uint64_t> ready{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
+  const dim3 grid((unsigned)((cols + kRowsTile - 1) / kRowsTile), a.c.n_kv_heads, a.n_seqs);
+  kern<<<grid, kChunkThreads, smem, st>>>(a, dtype);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st) {
+  if (head_dim == 128) {
+    if (dtype == KV4_F32) return launch_chunk<128, 2, 2, 2>(a, dtype, st);
+    if (dtype == KV4_F16) return launch_chunk<128, 1, 2, 1>(a, dtype, st);
+    return launch_chunk<128, 1, 1, 1>(a, dtype, st);
+  }
+  if (dtype == KV4_F32) return launch_chunk<64, 2, 2, 2>(a, dtype, st);
+  if (dtype == KV4_F16) return launch_chunk<64, 1, 2, 1>(a, dtype, st);
+  return launch_chunk<64, 1, 1, 1>(a, dtype, st);
+}
+
+}  // namespace lrs

@@ -87,6 +87,7 @@ struct Kv4AttnArgs {
   void* ws = nullptr;
 };
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
+cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
 size_t kv4_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int max_len);
 
 }  // namespace lrs
