@@ -4,9 +4,10 @@
 // of 64.  Roles, joined by mbarriers:
 //   warps 0-7   softmax: warp w has the rows 32 (w % 4) .. + 31 (the TMEM lanes it may read), w / 4 the half of a tile's
 //               positions, and of the output's dims, that its threads take;
-//   warps 8-11  copy the packed tiles in (cp.async, one tile ahead) and turn them into fp16 operands in the tensor
-//               core's swizzled layout, K as [position][dim], V as [dim][position];
-//   warp 12     issues the products: S = Q K^T into TMEM, O = P V with P read from TMEM.
+//   warps 8-15  turn the packed tiles into fp16 operands in the tensor core's swizzled layout, K as [position][dim],
+//               V as [dim][position];
+//   warp 16     issues the products: S = Q K^T into TMEM, O = P V with P read from TMEM;
+//   warp 17     copies the packed tiles in (bulk copies, two tiles ahead).
 // Every tile's O is added to float32 registers (rounded to nearest), so no sum in TMEM runs over more than one tile
 // and a change of the softmax's reference needs no pass over TMEM.
 //
@@ -32,15 +33,19 @@ namespace lrs {
 namespace {
 
 constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
-constexpr int kSoftWarps = 8, kProdWarps = 4, kProd = 32 * kProdWarps;
-constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 1);
+constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 32 * kProdWarps;
+constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpgroups
+// Registers per thread: the block starts with kRegsStart and its warpgroups trade them.
+constexpr int kRegsStart = 96, kRegsSoft = 136, kRegsProd = 72, kRegsRest = 64;
+static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
+static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
 constexpr int kInfo = 8;  // ring of what the tiles' producers tell the softmax
 constexpr float kChunkTop = 11.f, kChunkSlack = 4.f;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kColO = 256;
 
 struct ChunkBars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
 };
 
 struct alignas(16) ChunkMisc {
@@ -84,6 +89,15 @@ __device__ __forceinline__ bool cwait(uint64_t* bar, uint32_t parity, volatile i
   return true;
 }
 
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
@@ -124,6 +138,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.raw_full[i], 1);
+      mbar_init(&B.raw_empty[i], kProd);
       mbar_init(&B.k_full[i], kProd);
       mbar_init(&B.v_full[i], kProd);
       mbar_init(&B.k_empty[i], 1);
@@ -198,37 +214,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
     // ---------------- producers ----------------
+    regs_down<kRegsProd>();
     const int p = tid - 32 * kSoftWarps, pw = p >> 5;
-    const int tpp = a.c.page_len / kKv4Tile, n16 = (lim_hi + kKv4Tile - 1) / kKv4Tile;
-    const int* trow = a.table + (long long)seq * a.table_stride;
-    auto fetch = [&](int i) {  // returns the absent parts
-      int absent = 0;
-      unsigned char* raw = sm + L::off_raw + (i & 1) * L::stage_bytes;
-#pragma unroll
-      for (int s = 0; s < kSub; ++s) {
-        const int t = i * kSub + s, pg = t / tpp;
-        const int id = t < n16 ? trow[pg] : -1;
-        if (id < 0 || id >= a.c.n_pages) {
-          absent |= 1 << s;
-          continue;
-        }
-        const uint8_t* src = a.c.data + (((long long)id * a.c.n_kv_heads + head) * tpp + (t - pg * tpp)) * TILE;
-        for (int o = p * 16; o < TILE; o += kProd * 16)  // V's second half 16 bytes on: see the reads below
-          cp_async16(raw + s * L::sub_stride + o + (o >= HALF + CODES / 2 ? 16 : 0), src + o);
-      }
-      cp_async_commit();
-      return absent;
-    };
     const uint32_t ex = exponent_bits();
-    int absent_next = nt ? fetch(0) : 0;
-    bool ok = true;  // once a wait has run out every thread still goes through the barriers, and does nothing else
-    for (int i = 0; i < nt; ++i) {
-      const int st = i & 1, inf = i & (kInfo - 1), absent = absent_next;
-      cp_async_wait_all();
-      named_bar(5, kProd);  // tile i is there, and nobody reads tile i - 1 any more
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) continue;
-      if (i + 1 < nt) absent_next = fetch(i + 1);
+    for (int i = 0; i < nt; ++i) {  // a warp in which a wait has run out leaves as a whole
+      const int st = i & 1, inf = i & (kInfo - 1);
+      if (!__all_sync(0xffffffffu, cwait(&B.raw_full[st], (uint32_t)(i >> 1) & 1u, abort_flag))) break;
+      const int absent = M.absent[inf];
       const unsigned char* raw = sm + L::off_raw + st * L::stage_bytes;
       const bool ragged = absent || (i + 1) * kPosTile > lim_hi;  // some positions do not count: their scales read as 0
 
@@ -285,19 +277,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
         M.v_exp[inf] = (float)e_v;
         M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
-        M.absent[inf] = absent;
         M.bad[inf] = v_bad;
-        const int next = (inf + 1) & (kInfo - 1);  // read last before the softmax's sixth tile before
+        // For tile i + 2, which no warp has begun: its copy waits until every warp is done with tile i.  The entry's last
+        // tile, i - 6, has been read: V of tile i - 1 was written after the product of tile i - 3, so after the softmax
+        // had taken in tile i - 5.
+        const int next = (inf + 2) & (kInfo - 1);
         for (int b = 0; b < 4; ++b) M.first_bad[next][b] = INT_MAX;
       }
 
       // K: 64 positions x 4 x (the word of eight dims of every block)
-      if (i >= 2) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag));
-      if (!ok) continue;
+      if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
       unsigned char* kt = sm + L::off_k + st * NKV * L::k_part;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * (pw + 4 * j), s = pos >> 4;
+      {
+        const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * pw, s = pos >> 4;
         const unsigned char* src = raw + s * L::sub_stride;
         uint32_t w[NB], sc[NB / 2];
         if constexpr (D == 128) {
@@ -334,31 +326,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       fence_async_smem();
       mbar_arrive(&B.k_full[st]);
 
-      // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of every block.  Eight lanes with the
+      // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of half the blocks.  Eight lanes with the
       // same dims and different chunks read 16 bytes each from places 16 bytes apart modulo 128 (hence the paddings
       // of the raw tiles) and write a whole row of 64 positions
-      if (i >= 2) ok = __all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag));
-      if (!ok) continue;
+      if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
       {
         unsigned char* vt = sm + L::off_v + st * NKV * L::v_part;
-        const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
+        constexpr int VB = NB / 2;
+        const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = (pw & 3) * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
+        const int b0 = (pw >> 2) * VB;  // the first of the thread's blocks
         const unsigned char* src = raw + s * L::sub_stride + HALF;
         const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
         const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB);
-        uint32_t hi[NB][2][4], lo[NB][2][4];
+        uint32_t hi[VB][2][4], lo[VB][2][4];
 #pragma unroll
         for (int tig = 0; tig < 4; ++tig) {
-          uint32_t w[NB], sc[NB];  // the first position's blocks in pairs, then the second's
+          uint32_t w[2], sc[2];  // of the first and the second position: D = 128: the two blocks; D = 64: both, of which one counts
           if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(codes + tig * 16);
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-            const uint4 v = *reinterpret_cast<const uint4*>(scales + tig * 16);
-            sc[0] = v.x, sc[1] = v.y, sc[2] = v.z, sc[3] = v.w;
+            w[0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + b0 * 2);
+            w[1] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + 8 + b0 * 2);
+            sc[0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + b0 * 2);
+            sc[1] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + 8 + b0 * 2);
           } else {
             const uint2 u = *reinterpret_cast<const uint2*>(codes + tig * 8);
-            w[0] = u.x, w[1] = u.y;
+            w[0] = u.x >> (16 * b0), w[1] = u.y >> (16 * b0);
             const uint2 v = *reinterpret_cast<const uint2*>(scales + tig * 8);
-            sc[0] = v.x, sc[1] = v.y;
+            sc[0] = v.x >> (16 * b0), sc[1] = v.y >> (16 * b0);
           }
           if (ragged || v_bad) {
 #pragma unroll
@@ -366,21 +359,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
               const int at = i * kPosTile + chunk * 8 + 2 * tig + e;
               const bool off = (absent >> s & 1) || at >= lim_hi;
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                uint32_t& u = sc[e * (NB / 2) + b / 2];
+              for (int b = 0; b < VB; ++b) {
                 const uint32_t mask = b & 1 ? 0xffff0000u : 0xffffu;
-                const bool bad = (u & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
-                if (bad && !off) atomicMin(&M.first_bad[inf][b], at);
-                if (bad || off) u &= ~mask;
+                const bool bad = (sc[e] & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
+                if (bad && !off) atomicMin(&M.first_bad[inf][b0 + b], at);
+                if (bad || off) sc[e] &= ~mask;
               }
             }
           }
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[b / 2], sc[NB / 2 + b / 2], b & 1 ? 0x7632 : 0x5410)),
+          for (int b = 0; b < VB; ++b) {
+            const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0], sc[1], b & 1 ? 0x7632 : 0x5410)),
                                        NP == 2 ? as_h2(M.v_norm[pw][4 * chunk + tig]) : norm_v);
             // byte dsel of the block's two bytes, of both positions
-            const uint32_t x = __byte_perm(w[b / 2], w[NB / 2 + b / 2], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
+            const uint32_t x = __byte_perm(w[0], w[1], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
             const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
             const __half2 h0 = __hmul2(n0, s2), h1 = __hmul2(n1, s2);
             hi[b][0][tig] = as_u32(h0);
@@ -391,11 +383,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
             }
           }
         }
+        mbar_arrive(&B.raw_empty[st]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < VB; ++b)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int dim = 32 * b + 4 * gid + 2 * dsel + k;
+            const int dim = 32 * (b0 + b) + 4 * gid + 2 * dsel + k;
             unsigned char* at = vt + sw128_offset(dim, 8 * chunk);
             *reinterpret_cast<uint4*>(at) = make_uint4(hi[b][k][0], hi[b][k][1], hi[b][k][2], hi[b][k][3]);
             if (NKV == 2) *reinterpret_cast<uint4*>(at + L::v_part) = make_uint4(lo[b][k][0], lo[b][k][1], lo[b][k][2], lo[b][k][3]);
@@ -404,10 +397,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       fence_async_smem();
       mbar_arrive(&B.v_full[st]);
     }
-    cp_async_wait_all();
-  } else if (warp == kSoftWarps + kProdWarps) {
-    // ---------------- products ----------------
-    if (lane == 0) {
+  } else if (warp >= kSoftWarps + kProdWarps) {
+    regs_down<kRegsRest>();
+    if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) {
+      // ---------------- copies ----------------
+      const int tpp = a.c.page_len / kKv4Tile, n16 = (lim_hi + kKv4Tile - 1) / kKv4Tile;
+      const int* trow = a.table + (long long)seq * a.table_stride;
+      // the pages of a tile are asked for a tile ahead; places go on without a division
+      int ids[kSub], places[kSub], next_t = 0, next_page = 0, next_place = 0, issued = 0;
+      auto ask = [&]() {
+#pragma unroll
+        for (int s = 0; s < kSub; ++s) {
+          ids[s] = next_t < n16 ? trow[next_page] : -1;
+          places[s] = next_place;
+          ++next_t;
+          if (++next_place == tpp) {
+            next_place = 0;
+            ++next_page;
+          }
+        }
+      };
+      ask();
+      for (int i = 0; i < nt; ++i) {
+        const int st = i & 1;
+        if (i >= 2 && !cwait(&B.raw_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag)) break;
+        unsigned char* raw = sm + L::off_raw + st * L::stage_bytes;
+        const uint8_t* src[kSub];
+        int absent = 0, here = 0;
+#pragma unroll
+        for (int s = 0; s < kSub; ++s) {
+          const bool there = ids[s] >= 0 && ids[s] < a.c.n_pages;
+          absent |= there ? 0 : 1 << s;
+          here += there;
+          src[s] = a.c.data + (((long long)ids[s] * a.c.n_kv_heads + head) * tpp + places[s]) * TILE;
+        }
+        M.absent[i & (kInfo - 1)] = absent;
+        mbar_arrive_expect_tx(&B.raw_full[st], here * TILE);
+        ++issued;
+        constexpr int cut = HALF + CODES / 2;  // V's second half goes 16 bytes on: see its reads
+#pragma unroll
+        for (int s = 0; s < kSub; ++s)
+          if (!(absent >> s & 1)) {
+            bulk_g2s(raw + s * L::sub_stride, src[s], cut, &B.raw_full[st]);
+            bulk_g2s(raw + s * L::sub_stride + cut + 16, src[s] + cut, TILE - cut, &B.raw_full[st]);
+          }
+        ask();
+      }
+      if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
+        for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&B.raw_full[i & 1], (uint32_t)(i >> 1) & 1u, kDrainNs);
+    }
+    if (warp == kSoftWarps + kProdWarps && lane == 0) {
+      // ---------------- products ----------------
       constexpr uint32_t id_s = idesc_f16_f32(kRowsTile, kPosTile), id_o = idesc_f16_f32(kRowsTile, D);
       const uint32_t q0 = smem_u32(sm);
       auto scores = [&](int i) {
@@ -465,6 +505,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     }
   } else {
     // ---------------- softmax ----------------
+    regs_up<kRegsSoft>();
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     float2 o[HD / 2];
 #pragma unroll
