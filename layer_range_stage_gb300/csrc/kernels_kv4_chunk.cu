@@ -5,11 +5,13 @@
 //   warps 0-7   softmax: warp w has the rows 32 (w % 4) .. + 31 (the TMEM lanes it may read), w / 4 the half of a tile's
 //               positions, and of the output's dims, that its threads take;
 //   warps 8-15  turn the packed tiles into fp16 operands in the tensor core's swizzled layout, K as [position][dim],
-//               V as [dim][position];
+//               V as [dim][position]: four warps have the even tiles, four the odd ones, so each has two tiles' time
+//               for its chain of waits, reads and writes;
 //   warp 16     issues the products: S = Q K^T into TMEM, O = P V with P read from TMEM;
 //   warp 17     copies the packed tiles in (bulk copies, two tiles ahead).
-// Every tile's O is added to float32 registers (rounded to nearest), so no sum in TMEM runs over more than one tile
-// and a change of the softmax's reference needs no pass over TMEM.
+// In STAGE_F32 the sums in TMEM run over kGroup tiles and are then added to float32 registers, rounded to nearest (the
+// tensor cores' own additions truncate); the 16-bit types keep the whole sum in TMEM.  A row's change of reference, which
+// is rare, rescales its sums in TMEM.
 //
 // Precision: a value s (c - 8) has 15 significant bits, so two fp16 numbers hold it exactly; q and the probabilities are
 // float32 and two fp16 numbers hold 22 bits.  STAGE_F32 multiplies high by high, low by high and high by low (three
@@ -33,14 +35,20 @@ namespace lrs {
 namespace {
 
 constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
-constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 32 * kProdWarps;
+constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 16 * kProdWarps;  // kProd: threads of a group of four warps
 constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpgroups
 // Registers per thread: the block starts with kRegsStart and its warpgroups trade them.
 constexpr int kRegsStart = 96, kRegsSoft = 136, kRegsProd = 72, kRegsRest = 64;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
 constexpr int kInfo = 8;  // ring of what the tiles' producers tell the softmax
-constexpr float kChunkTop = 11.f, kChunkSlack = 4.f;
+constexpr int kGroup = 4;  // tiles of a sum in TMEM (STAGE_F32)
+// The largest probability (times its power of V) lies at 2^top when the reference is set, and may grow by 2^slack before
+// it is set again: fp16 ends at 2^16.  With one fp16 value per probability fewer changes count more than the range below.
+template <int NP>
+constexpr float kChunkTop = NP == 2 ? 11.f : 7.f;
+template <int NP>
+constexpr float kChunkSlack = 15.f - kChunkTop<NP>;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kColO = 256;
 
@@ -215,9 +223,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
     // ---------------- producers ----------------
     regs_down<kRegsProd>();
-    const int p = tid - 32 * kSoftWarps, pw = p >> 5;
+    const int group_of = (warp - kSoftWarps) >> 2, p = tid - 32 * (kSoftWarps + 4 * group_of), pw = p >> 5;
     const uint32_t ex = exponent_bits();
-    for (int i = 0; i < nt; ++i) {  // a warp in which a wait has run out leaves as a whole
+    for (int i = group_of; i < nt; i += 2) {  // a warp in which a wait has run out leaves as a whole
       const int st = i & 1, inf = i & (kInfo - 1);
       if (!__all_sync(0xffffffffu, cwait(&B.raw_full[st], (uint32_t)(i >> 1) & 1u, abort_flag))) break;
       const int absent = M.absent[inf];
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
           if (NP == 2 && side) {
             const int e0 = (int)min(max(as_u32(first) >> 16, as_u32(first) & 0xffffu) >> 10, 30u) - 14;
             const int e1 = (int)min(top[1] >> 10, 30u) - 14;
-            M.v_norm[pw][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
+            M.v_norm[warp - kSoftWarps][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
             if (pw == 0) {
               *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
               *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
@@ -273,23 +281,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       const __half2 norm_k = __half2half2(__ushort_as_half(half_power(e_k)));
       const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
       if (NP == 2) __syncwarp();  // v_norm
+      // K: 64 positions x 4 x (the word of eight dims of every block)
+      if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
       if (p == 0) {
         M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
         M.v_exp[inf] = (float)e_v;
         M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
         M.bad[inf] = v_bad;
-        // For tile i + 2, which no warp has begun: its copy waits until every warp is done with tile i.  The entry's last
-        // tile, i - 6, has been read: V of tile i - 1 was written after the product of tile i - 3, so after the softmax
-        // had taken in tile i - 5.
+        // For tile i + 2, which no warp has begun: its copy waits until every warp of the group is done with tile i.  The
+        // entry's last tile, i - 6, is read before the probabilities of tile i - 4 are handed on, which the product of tile
+        // i - 2's scores has waited for; a later wait here is for that product, so the reset follows it.
         const int next = (inf + 2) & (kInfo - 1);
         for (int b = 0; b < 4; ++b) M.first_bad[next][b] = INT_MAX;
       }
-
-      // K: 64 positions x 4 x (the word of eight dims of every block)
-      if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
       unsigned char* kt = sm + L::off_k + st * NKV * L::k_part;
-      {
-        const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * pw, s = pos >> 4;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * (pw + 4 * j), s = pos >> 4;
         const unsigned char* src = raw + s * L::sub_stride;
         uint32_t w[NB], sc[NB / 2];
         if constexpr (D == 128) {
@@ -326,18 +334,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       fence_async_smem();
       mbar_arrive(&B.k_full[st]);
 
-      // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of half the blocks.  Eight lanes with the
+      // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of every block.  Eight lanes with the
       // same dims and different chunks read 16 bytes each from places 16 bytes apart modulo 128 (hence the paddings
       // of the raw tiles) and write a whole row of 64 positions
       if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
       {
         unsigned char* vt = sm + L::off_v + st * NKV * L::v_part;
         constexpr int VB = NB / 2;
-        const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = (pw & 3) * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
-        const int b0 = (pw >> 2) * VB;  // the first of the thread's blocks
+        const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
         const unsigned char* src = raw + s * L::sub_stride + HALF;
         const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
         const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB);
+#pragma unroll 1
+        for (int b0 = 0; b0 < NB; b0 += VB) {  // half of the blocks at a time, for the registers
         uint32_t hi[VB][2][4], lo[VB][2][4];
 #pragma unroll
         for (int tig = 0; tig < 4; ++tig) {
@@ -370,7 +379,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 #pragma unroll
           for (int b = 0; b < VB; ++b) {
             const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0], sc[1], b & 1 ? 0x7632 : 0x5410)),
-                                       NP == 2 ? as_h2(M.v_norm[pw][4 * chunk + tig]) : norm_v);
+                                       NP == 2 ? as_h2(M.v_norm[warp - kSoftWarps][4 * chunk + tig]) : norm_v);
             // byte dsel of the block's two bytes, of both positions
             const uint32_t x = __byte_perm(w[0], w[1], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
             const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
             }
           }
         }
-        mbar_arrive(&B.raw_empty[st]);
+        if (b0 + VB == NB) mbar_arrive(&B.raw_empty[st]);
 #pragma unroll
         for (int b = 0; b < VB; ++b)
 #pragma unroll
@@ -393,6 +402,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
             *reinterpret_cast<uint4*>(at) = make_uint4(hi[b][k][0], hi[b][k][1], hi[b][k][2], hi[b][k][3]);
             if (NKV == 2) *reinterpret_cast<uint4*>(at + L::v_part) = make_uint4(lo[b][k][0], lo[b][k][1], lo[b][k][2], lo[b][k][3]);
           }
+        }
       }
       fence_async_smem();
       mbar_arrive(&B.v_full[st]);
@@ -481,14 +491,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         if (!ok) break;
         tc_fence_after();
         const uint32_t v0 = smem_u32(sm + L::off_v + st * NKV * L::v_part);
-        uint32_t acc = 0;
+        uint32_t acc = (NP == 2 ? i % kGroup : i) ? 1u : 0u;
+        const uint32_t od = tmem + kColO + (NP == 2 ? (i / kGroup & 1) * D : 0);
 #pragma unroll
         for (int part = 0; part < NP + NKV - 1; ++part) {
           const uint32_t pp = tmem + kColP + st * 64 + (NP == 2 && part == 1 ? 32 : 0);
           const uint32_t vp = v0 + (part > 0 && part == NP ? L::v_part : 0);
 #pragma unroll
           for (int ks = 0; ks < kPosTile / 16; ++ks) {
-            umma_f16_ts(tmem + kColO + st * D, pp + ks * 8, desc_sw128(vp + ks * 32), id_o, acc);
+            umma_f16_ts(od, pp + ks * 8, desc_sw128(vp + ks * 32), id_o, acc);
             acc = 1;
           }
         }
@@ -507,41 +518,43 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     // ---------------- softmax ----------------
     regs_up<kRegsSoft>();
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    float2 o[HD / 2];
+    constexpr int NO = NP == 2 ? HD / 2 : 1;
+    float2 o[NO];  // STAGE_F32: the sums over the groups of tiles that are done
 #pragma unroll
-    for (int j = 0; j < HD / 2; ++j) o[j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < NO; ++j) o[j] = make_float2(0.f, 0.f);
     float ref = -INFINITY, sum = 0.f;
+    int nan_blocks = 0;  // the thread's blocks of dims in which its row sees a V scale that is no number
     bool ok = true;
-    // adds tile i's O, then the change of reference that followed it
-    auto collect = [&](int i, float keep) {
+    auto products_done = [&](int i) {
       if (!__all_sync(0xffffffffu, cwait(&B.o_full[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag))) return false;
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(lanes + kColO + (i & 1) * D + half * HD + c, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          o[c / 2 + j] = add2(o[c / 2 + j], make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
-      }
+      return true;
+    };
+    auto note_bad = [&](int i) {
       if (M.bad[i & (kInfo - 1)]) {
 #pragma unroll
         for (int b = 0; b < HD / 32; ++b)
-          if (M.first_bad[i & (kInfo - 1)][half * (HD / 32) + b] < lim) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[16 * b + j] = make_float2(NAN, NAN);
-          }
+          if (M.first_bad[i & (kInfo - 1)][half * (HD / 32) + b] < lim) nan_blocks |= 1 << b;
       }
-      if (__any_sync(0xffffffffu, keep != 1.f)) {
+    };
+    // adds a group's sums to the registers
+    auto collect = [&](int g) {
+      if constexpr (NP == 2) {
 #pragma unroll
-        for (int j = 0; j < HD / 2; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(lanes + kColO + (g & 1) * D + half * HD + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            o[c / 2 + j] = add2(o[c / 2 + j], make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])));
+        }
       }
-      return true;
     };
     for (int i = 0; i < nt; ++i) {
       const int st = i & 1, inf = i & (kInfo - 1);
-      // as for the producers: the barriers stay matched when a wait has run out
+      // S of tile i is there, and so is the product of tile i - 2, issued before it: P's place is free.  When a wait has run
+      // out every thread still goes through the barriers, and does nothing else
       ok = ok && __all_sync(0xffffffffu, cwait(&B.s_full[st], (uint32_t)(i >> 1) & 1u, abort_flag));
       if (!ok) {
         named_bar(1 + (warp & 3), 64);
@@ -552,6 +565,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       tmem_ld32(lanes + kColS + st * kPosTile + half * 32, s);
       const float f = zscale * M.k_pow[inf], ev = M.v_exp[inf], v_inv = M.v_inv[inf];
       const int absent = M.absent[inf] >> (2 * half) & 3;
+      if (i >= 2) note_bad(i - 2);
       tmem_wait_ld();
       const int pos0 = i * kPosTile + 32 * half;
       if (pos0 + 32 > lim_lo || absent) {
@@ -568,30 +582,57 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
           const float2 w0 = fma2(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), make_float2(f, f), make_float2(e4.x, e4.y));
           const float2 w1 = fma2(make_float2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), make_float2(f, f), make_float2(e4.z, e4.w));
           s[j] = __float_as_uint(w0.x), s[j + 1] = __float_as_uint(w0.y), s[j + 2] = __float_as_uint(w1.x), s[j + 3] = __float_as_uint(w1.y);
-          most = fmaxf(fmaxf(most, fmaxf(w0.x, w0.y)), fmaxf(w1.x, w1.y));
         }
-      } else {
+      }
+      {
+        float m4[4];  // four chains
 #pragma unroll
-        for (int j = 0; j < 32; ++j) most = fmaxf(most, __uint_as_float(s[j]));
-        most = fmaf(most, f, ev);
+        for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(s[j]);
+#pragma unroll
+        for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(s[j]));
+        most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        if (NP == 1) most = fmaf(most, f, ev);
       }
       M.top[st][half][row] = most;
       named_bar(1 + (warp & 3), 64);
       most = fmaxf(most, M.top[st][half ^ 1][row]);
       float keep = 1.f;
-      if (most - kChunkTop > ref + kChunkSlack) {
-        keep = exp2_approx(ref - (most - kChunkTop));
-        ref = most - kChunkTop;
+      if (most - kChunkTop<NP> > ref + kChunkSlack<NP>) {
+        keep = exp2_approx(ref - (most - kChunkTop<NP>));
+        ref = most - kChunkTop<NP>;
         sum *= keep;
       }
+      const bool fresh = NP == 2 ? i % kGroup == 0 : i == 0;  // a new sum in TMEM begins
+      if (__any_sync(0xffffffffu, keep != 1.f) && !fresh) {
+        if (NP == 2) {
+#pragma unroll
+          for (int j = 0; j < NO; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
+        }
+        ok = products_done(i - 1);
+        if (ok) {
+          const uint32_t at = lanes + kColO + (NP == 2 ? (i / kGroup & 1) * D : 0) + half * HD;
+#pragma unroll
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(at + c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * keep);
+            tmem_st16(at + c, r);
+          }
+        }
+      }
       const float c = ev - (ref == -INFINITY ? 0.f : ref);
-      float2 part = make_float2(0.f, 0.f);
+      float2 part4[4];  // four chains
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part4[j] = make_float2(0.f, 0.f);
       uint32_t hi[16], lo[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float2 sj = make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
         const float2 z = NP == 2 ? add2(sj, make_float2(c, c)) : fma2(sj, make_float2(f, f), make_float2(c, c));
         const float2 x = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+        float2& part = part4[j & 3];
         part = NP == 2 ? fma2(x, *reinterpret_cast<const float2*>(&M.v_pos_inv[inf][32 * half + 2 * j]), part) : add2(part, x);
         const __half2 h = __floats2half2_rn(x.x, x.y);
         hi[j] = as_u32(h);
@@ -601,45 +642,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
           lo[j] = as_u32(__floats2half2_rn(rest.x, rest.y));
         }
       }
+      const float2 part = add2(add2(part4[0], part4[1]), add2(part4[2], part4[3]));
       sum = fmaf(part.x + part.y, v_inv, sum);
       tmem_st16(lanes + kColP + st * 64 + half * 16, hi);
       if (NP == 2) tmem_st16(lanes + kColP + st * 64 + 32 + half * 16, lo);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&B.p_full[st]);
-      if (i > 0) ok = collect(i - 1, keep);
+      if (NP == 2 && fresh && i > 0) {  // the last group's sums, while the products of this tile run
+        ok = ok && products_done(i - 1);
+        if (ok) collect(i / kGroup - 1);
+        if (__any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+          for (int j = 0; j < NO; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
+        }
+      }
     }
-    if (ok && nt > 0) ok = collect(nt - 1, 1.f);
+    if (ok && nt > 0) {
+      ok = products_done(nt - 1);
+      if (ok) collect((nt - 1) / kGroup);
+      if (nt > 1) note_bad(nt - 2);
+      note_bad(nt - 1);
+    }
     M.top[nt & 1][half][row] = sum;
     named_bar(1 + (warp & 3), 64);
     sum += M.top[nt & 1][half ^ 1][row];
-    if (live) {
-      const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
-      const long long at = (long long)(start + col_k) * a.out_stride + elem;
+    const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
 #pragma unroll
-      for (int j = 0; j < HD / 2; ++j) o[j] = mul2(o[j], make_float2(inv, inv));
-      if (dtype == KV4_F32) {
+    for (int c = 0; c < HD; c += 32) {  // 32 dims: a block
+      float v[32];
+      if constexpr (NP == 2) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[2 * j] = o[c / 2 + j].x, v[2 * j + 1] = o[c / 2 + j].y;
+      } else {
+        uint32_t r[32];
+        if (nt > 0 && ok) {
+          tmem_ld32(lanes + kColO + half * HD + c, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      }
+      const float factor = nan_blocks >> (c >> 5) & 1 ? NAN : inv;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] *= factor;
+      const long long at = (long long)(start + col_k) * a.out_stride + elem + c;
+      if (!live) {
+      } else if (dtype == KV4_F32) {
         float4* out = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
 #pragma unroll
-        for (int j = 0; j < HD / 4; ++j) out[j] = make_float4(o[2 * j].x, o[2 * j].y, o[2 * j + 1].x, o[2 * j + 1].y);
+        for (int j = 0; j < 8; ++j) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       } else {
         uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
 #pragma unroll
-        for (int j = 0; j < HD / 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           uint32_t u[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 v = o[4 * j + k];
+            const float x = v[8 * j + 2 * k], y = v[8 * j + 2 * k + 1];
             if (dtype == KV4_F16) {
-              u[k] = as_u32(__floats2half2_rn(v.x, v.y));
+              u[k] = as_u32(__floats2half2_rn(x, y));
             } else {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
               u[k] = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
           out[j] = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
+      __syncwarp();  // the next block's TMEM read is the whole warp's
     }
   }
   tc_fence_before();
