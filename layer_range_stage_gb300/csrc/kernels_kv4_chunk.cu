@@ -1,14 +1,17 @@
 // Attention of many query tokens per sequence (prompt chunks) over the paged 4-bit KV cache (sm_103a): tcgen05 tiles.
 //
-// A CTA has 128 rows -- (token, head of the group) pairs of one sequence and KV head -- and walks the positions in tiles
-// of 64.  Roles, joined by mbarriers:
+// A work item is 128 rows -- (token, head of the group) pairs of one sequence and KV head -- against the positions they
+// see, in tiles of 64.  One CTA per SM goes through its items (the longest first, dealt in turn) without a barrier
+// between them: a tile's number n runs on over the items, and the copies and the expansion of the next item's first
+// tiles go on while the last item's results are put down.  Roles, joined by mbarriers:
 //   warps 0-7   softmax: warp w has the rows 32 (w % 4) .. + 31 (the TMEM lanes it may read), w / 4 the half of a tile's
 //               positions, and of the output's dims, that its threads take;
 //   warps 8-15  turn the packed tiles into fp16 operands in the tensor core's swizzled layout, K as [position][dim],
 //               V as [dim][position]: four warps have the even tiles, four the odd ones, so each has two tiles' time
 //               for its chain of waits, reads and writes;
-//   warp 16     issues the products: S = Q K^T into TMEM, O = P V with P read from TMEM;
-//   warp 17     copies the packed tiles in (bulk copies, two tiles ahead).
+//   warp 16     issues the products: S = Q K^T and O = P V, with Q and P read from TMEM (an operand of 128 rows from shared
+//               memory would be read again by every product);
+//   warp 17     copies the packed tiles in (bulk copies, up to four tiles ahead).
 // In STAGE_F32 the sums in TMEM run over kGroup tiles and are then added to float32 registers, rounded to nearest (the
 // tensor cores' own additions truncate); the 16-bit types keep the whole sum in TMEM.  A row's change of reference, which
 // is rare, rescales its sums in TMEM.
@@ -41,7 +44,7 @@ constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpg
 constexpr int kRegsStart = 96, kRegsSoft = 136, kRegsProd = 72, kRegsRest = 64;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
-constexpr int kInfo = 8;  // ring of what the tiles' producers tell the softmax
+constexpr int kInfo = 16;  // ring of what the tiles' producers tell the softmax
 constexpr int kGroup = 4;  // tiles of a sum in TMEM (STAGE_F32)
 // The largest probability (times its power of V) lies at 2^top when the reference is set, and may grow by 2^slack before
 // it is set again: fp16 ends at 2^16.  With one fp16 value per probability fewer changes count more than the range below.
@@ -50,10 +53,11 @@ constexpr float kChunkTop = NP == 2 ? 11.f : 7.f;
 template <int NP>
 constexpr float kChunkSlack = 15.f - kChunkTop<NP>;
 constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
-constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kColO = 256;
+constexpr int kRaw = 4;    // packed tiles in shared memory
+constexpr uint32_t kTmemCols = 512, kColQ = 0, kColS = 128, kColP = 256, kColO = 384;
 
 struct ChunkBars {
-  uint64_t raw_full[2], raw_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
 };
 
 struct alignas(16) ChunkMisc {
@@ -65,19 +69,19 @@ struct alignas(16) ChunkMisc {
   int absent[kInfo];                               // bit i: the tile's i-th 16 positions are not there
   int bad[kInfo];                                  // whether some V scale is no number
   int first_bad[kInfo][4];                         // per block of dims: the first such position
-  float top[2][2][kRowsTile];                      // [tile parity][half][row]
+  float top[2][2][kRowsTile], q_top[2][kRowsTile]; // [tile parity][half][row]
   uint32_t tmem;
   int abort;
 };
 
 static_assert(offsetof(ChunkMisc, v_pos_exp) % 16 == 0 && offsetof(ChunkMisc, v_pos_inv) % 16 == 0, "vector reads");
 
-template <int D, int NQ, int NKV>
+template <int D, int NKV>
 struct ChunkLayout {
-  static constexpr int q_part = kRowsTile * D * 2, k_part = kPosTile * D * 2, v_part = D * kPosTile * 2;
+  static constexpr int k_part = kPosTile * D * 2, v_part = D * kPosTile * 2;
   static constexpr int sub_stride = kv4_tile_bytes(D) + 32, stage_bytes = kSub * sub_stride;
-  static constexpr int off_k = NQ * q_part, off_v = off_k + 2 * NKV * k_part, off_raw = off_v + 2 * NKV * v_part;
-  static constexpr int off_misc = off_raw + 2 * stage_bytes;
+  static constexpr int off_k = 0, off_v = off_k + 2 * NKV * k_part, off_raw = off_v + 2 * NKV * v_part;
+  static constexpr int off_misc = off_raw + kRaw * stage_bytes;
   static_assert(off_k % 1024 == 0 && off_v % 1024 == 0 && k_part % 1024 == 0 && v_part % 1024 == 0, "swizzled tiles");
   static_assert(off_raw % 16 == 0 && stage_bytes % 16 == 0 && sub_stride % 16 == 0 && off_misc % 16 == 0, "16-byte pieces");
   static constexpr int bytes = off_misc + (int)sizeof(ChunkMisc) + 1024;  // and the alignment to 1024
@@ -96,6 +100,12 @@ __device__ __forceinline__ bool cwait(uint64_t* bar, uint32_t parity, volatile i
   }
   return true;
 }
+
+struct ChunkItem {
+  int seq, head, row0;             // sequence, KV head, first row
+  int start, count, len, ncols;    // first query token of the sequence, its tokens, its positions, its rows
+  int lim_hi, nt;                  // positions that some row sees, tiles
+};
 
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -122,7 +132,7 @@ __device__ __forceinline__ uint16_t half_power(int e) { return (uint16_t)(e <= 1
 
 template <int D, int NQ, int NKV, int NP>
 __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a, int dtype) {
-  using L = ChunkLayout<D, NQ, NKV>;
+  using L = ChunkLayout<D, NKV>;
   constexpr int NB = D / 32, TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
   constexpr int HD = D / 2;  // dims of a softmax thread
   extern __shared__ unsigned char chunk_raw[];
@@ -132,22 +142,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- the CTA's rows
-  const int seq = blockIdx.z, head = blockIdx.y, group = a.n_q_heads / a.c.n_kv_heads;
-  int start;
-  const int count = seq_tokens(a, seq, &start), len = seq_positions(a, seq);
-  const int ncols = min(count, a.max_q) * group;
-  const int row0 = (int)(gridDim.x - 1 - blockIdx.x) * kRowsTile;  // the longest walks first
-  if (row0 >= ncols) return;
-  const int k_last = min(ncols - 1, row0 + kRowsTile - 1) / group;
-  const int lim_hi = max(0, len - count + k_last + 1);                // positions that some row sees
-  const int lim_lo = max(0, len - count + row0 / group + 1);          // positions that every row sees
-  const int nt = (lim_hi + kPosTile - 1) / kPosTile;
+  const int group = a.n_q_heads / a.c.n_kv_heads;
+  // Items: row tiles from the last (which sees most) down, then KV heads, then sequences.
+  const int tiles_max = (int)(((long long)a.max_q * group + kRowsTile - 1) / kRowsTile);
+  const long long n_items = (long long)tiles_max * a.c.n_kv_heads * a.n_seqs;
+  ChunkItem it;
+  auto next_item = [&](long long& w) {  // the CTA's next item from number w on; false behind the last
+    for (; w < n_items; w += gridDim.x) {
+      const int row_tile = tiles_max - 1 - (int)(w / ((long long)a.c.n_kv_heads * a.n_seqs));
+      const int rest = (int)(w % ((long long)a.c.n_kv_heads * a.n_seqs));
+      it.seq = rest / a.c.n_kv_heads;
+      it.head = rest % a.c.n_kv_heads;
+      it.row0 = row_tile * kRowsTile;
+      it.count = seq_tokens(a, it.seq, &it.start);
+      it.len = seq_positions(a, it.seq);
+      it.ncols = min(it.count, a.max_q) * group;
+      if (it.row0 >= it.ncols) continue;
+      const int k_last = min(it.ncols - 1, it.row0 + kRowsTile - 1) / group;
+      it.lim_hi = max(0, it.len - it.count + k_last + 1);
+      it.nt = (it.lim_hi + kPosTile - 1) / kPosTile;
+      w += gridDim.x;
+      return true;
+    }
+    return false;
+  };
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kRaw; ++i) {
       mbar_init(&B.raw_full[i], 1);
       mbar_init(&B.raw_empty[i], kProd);
+    }
+    mbar_init(&B.q_full, 32 * kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&B.k_full[i], kProd);
       mbar_init(&B.v_full[i], kProd);
       mbar_init(&B.k_empty[i], 1);
@@ -169,52 +195,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     tmem_relinquish();
   }
 
-  // ---- q into shared memory: scaled by a power of two per row, high and low part; within eight dims the order of the
-  // unpacked codes (0, 4, 1, 5, 2, 6, 3, 7)
-  const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1;
-  const int col = row0 + row;
-  const bool live = warp < kSoftWarps && col < ncols;
-  const int col_k = col / group;
-  const int lim = live ? max(0, len - count + col_k + 1) : 0;
-  const long long elem = live ? (long long)(head * group + col % group) * D + half * HD : 0;
-  float zscale = 0.f;
-  if (warp < kSoftWarps) {
-    float q[HD / 8][8], top = 0.f;
-#pragma unroll
-    for (int g = 0; g < HD / 8; ++g) {
-      if (live) {
-        load8(a.q, dtype, (long long)(start + col_k) * a.q_stride + elem + 8 * g, q[g]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[g][i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[g][i]));
-    }
-    M.top[0][half][row] = top;
-    named_bar(1 + (warp & 3), 64);
-    top = fmaxf(top, M.top[0][half ^ 1][row]);
-    const int e = top <= FLT_MAX ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
-    zscale = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
-    const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-#pragma unroll
-    for (int g = 0; g < HD / 8; ++g) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float x0 = q[g][t] * up, x1 = q[g][t + 4] * up;
-        const __half2 h = __floats2half2_rn(x0, x1);
-        const float2 f = __half22float2(h);
-        hi[t] = as_u32(h);
-        lo[t] = as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
-      }
-      const int dim = half * HD + 8 * g;
-      unsigned char* at = sm + (dim >> 6) * (kRowsTile * 128) + sw128_offset(row, dim & 63);
-      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (NQ == 2) *reinterpret_cast<uint4*>(at + L::q_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-    fence_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -225,11 +205,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     regs_down<kRegsProd>();
     const int group_of = (warp - kSoftWarps) >> 2, p = tid - 32 * (kSoftWarps + 4 * group_of), pw = p >> 5;
     const uint32_t ex = exponent_bits();
-    for (int i = group_of; i < nt; i += 2) {  // a warp in which a wait has run out leaves as a whole
-      const int st = i & 1, inf = i & (kInfo - 1);
-      if (!__all_sync(0xffffffffu, cwait(&B.raw_full[st], (uint32_t)(i >> 1) & 1u, abort_flag))) break;
+    bool ok = true;  // a warp in which a wait has run out leaves as a whole
+    int n = 0;
+    for (long long w = blockIdx.x; ok && next_item(w); n += it.nt)
+    for (int i = (n & 1) == group_of ? 0 : 1; i < it.nt; i += 2) {
+      const int ni = n + i, st = ni & 1, rs = ni & (kRaw - 1), inf = ni & (kInfo - 1), lim_hi = it.lim_hi;
+      ok = __all_sync(0xffffffffu, cwait(&B.raw_full[rs], (uint32_t)(ni / kRaw) & 1u, abort_flag));
+      if (!ok) break;
       const int absent = M.absent[inf];
-      const unsigned char* raw = sm + L::off_raw + st * L::stage_bytes;
+      const unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
       const bool ragged = absent || (i + 1) * kPosTile > lim_hi;  // some positions do not count: their scales read as 0
 
       // the largest scales (every warp for itself)
@@ -242,7 +226,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         uint32_t top[2];
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-          const unsigned char* sc = base + (side ? HALF + CODES + 16 : CODES);
+          const unsigned char* sc = base + (side ? HALF + CODES + 16 + ((lane & 4) << 2) : CODES);
           uint32_t w[NB];
           if constexpr (D == 128) {
             const uint4 u = *reinterpret_cast<const uint4*>(sc);
@@ -282,16 +266,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
       if (NP == 2) __syncwarp();  // v_norm
       // K: 64 positions x 4 x (the word of eight dims of every block)
-      if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
+      if (ni >= 2) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((ni >> 1) + 1) & 1u, abort_flag));
+      if (!ok) break;
       if (p == 0) {
         M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
         M.v_exp[inf] = (float)e_v;
         M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
         M.bad[inf] = v_bad;
-        // For tile i + 2, which no warp has begun: its copy waits until every warp of the group is done with tile i.  The
-        // entry's last tile, i - 6, is read before the probabilities of tile i - 4 are handed on, which the product of tile
-        // i - 2's scores has waited for; a later wait here is for that product, so the reset follows it.
-        const int next = (inf + 2) & (kInfo - 1);
+        // For tile n + kRaw, which no warp has begun: its copy waits until every warp of the group has read tile n.  The
+        // entry's last tile, n + kRaw - kInfo, was read by the softmax before the probabilities of tile n - 4 were handed
+        // on, which the scores of tile n - 2 waited for; and those are done.
+        const int next = (inf + kRaw) & (kInfo - 1);
         for (int b = 0; b < 4; ++b) M.first_bad[next][b] = INT_MAX;
       }
       unsigned char* kt = sm + L::off_k + st * NKV * L::k_part;
@@ -337,30 +322,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of every block.  Eight lanes with the
       // same dims and different chunks read 16 bytes each from places 16 bytes apart modulo 128 (hence the paddings
       // of the raw tiles) and write a whole row of 64 positions
-      if (i >= 2 && !__all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag))) break;
+      if (ni >= 2) ok = __all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((ni >> 1) + 1) & 1u, abort_flag));
+      if (!ok) break;
       {
         unsigned char* vt = sm + L::off_v + st * NKV * L::v_part;
-        constexpr int VB = NB / 2;
+        constexpr int VB = NKV == 1 ? NB : NB / 2;  // blocks at a time, for the registers
         const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
         const unsigned char* src = raw + s * L::sub_stride + HALF;
         const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
-        const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB);
+        const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB + 16);
 #pragma unroll 1
-        for (int b0 = 0; b0 < NB; b0 += VB) {  // half of the blocks at a time, for the registers
+        for (int b0 = 0; b0 < NB; b0 += VB) {
         uint32_t hi[VB][2][4], lo[VB][2][4];
 #pragma unroll
         for (int tig = 0; tig < 4; ++tig) {
-          uint32_t w[2], sc[2];  // of the first and the second position: D = 128: the two blocks; D = 64: both, of which one counts
-          if constexpr (D == 128) {
-            w[0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + b0 * 2);
-            w[1] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + 8 + b0 * 2);
-            sc[0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + b0 * 2);
-            sc[1] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + 8 + b0 * 2);
+          constexpr int W = (VB + 1) / 2;  // words of a position's blocks
+          uint32_t w[2][W], sc[2][W];      // of the first and the second position
+          if constexpr (D == 128 && VB == 4) {
+            const uint4 u = *reinterpret_cast<const uint4*>(codes + tig * 16);
+            w[0][0] = u.x, w[0][1] = u.y, w[1][0] = u.z, w[1][1] = u.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(scales + tig * 16);
+            sc[0][0] = v.x, sc[0][1] = v.y, sc[1][0] = v.z, sc[1][1] = v.w;
+          } else if constexpr (D == 128) {
+            w[0][0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + b0 * 2);
+            w[1][0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + 8 + b0 * 2);
+            sc[0][0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + b0 * 2);
+            sc[1][0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + 8 + b0 * 2);
           } else {
             const uint2 u = *reinterpret_cast<const uint2*>(codes + tig * 8);
-            w[0] = u.x >> (16 * b0), w[1] = u.y >> (16 * b0);
+            w[0][0] = u.x >> (16 * b0), w[1][0] = u.y >> (16 * b0);
             const uint2 v = *reinterpret_cast<const uint2*>(scales + tig * 8);
-            sc[0] = v.x >> (16 * b0), sc[1] = v.y >> (16 * b0);
+            sc[0][0] = v.x >> (16 * b0), sc[1][0] = v.y >> (16 * b0);
           }
           if (ragged || v_bad) {
 #pragma unroll
@@ -370,18 +362,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 #pragma unroll
               for (int b = 0; b < VB; ++b) {
                 const uint32_t mask = b & 1 ? 0xffff0000u : 0xffffu;
-                const bool bad = (sc[e] & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
+                const bool bad = (sc[e][b / 2] & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
                 if (bad && !off) atomicMin(&M.first_bad[inf][b0 + b], at);
-                if (bad || off) sc[e] &= ~mask;
+                if (bad || off) sc[e][b / 2] &= ~mask;
               }
             }
           }
 #pragma unroll
           for (int b = 0; b < VB; ++b) {
-            const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0], sc[1], b & 1 ? 0x7632 : 0x5410)),
+            const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0][b / 2], sc[1][b / 2], b & 1 ? 0x7632 : 0x5410)),
                                        NP == 2 ? as_h2(M.v_norm[warp - kSoftWarps][4 * chunk + tig]) : norm_v);
             // byte dsel of the block's two bytes, of both positions
-            const uint32_t x = __byte_perm(w[0], w[1], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
+            const uint32_t x = __byte_perm(w[0][b / 2], w[1][b / 2], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
             const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
             const __half2 h0 = __hmul2(n0, s2), h1 = __hmul2(n1, s2);
             hi[b][0][tig] = as_u32(h0);
@@ -392,7 +384,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
             }
           }
         }
-        if (b0 + VB == NB) mbar_arrive(&B.raw_empty[st]);
+        if (b0 + VB == NB) mbar_arrive(&B.raw_empty[rs]);
 #pragma unroll
         for (int b = 0; b < VB; ++b)
 #pragma unroll
@@ -411,55 +403,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     regs_down<kRegsRest>();
     if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) {
       // ---------------- copies ----------------
-      const int tpp = a.c.page_len / kKv4Tile, n16 = (lim_hi + kKv4Tile - 1) / kKv4Tile;
-      const int* trow = a.table + (long long)seq * a.table_stride;
-      // the pages of a tile are asked for a tile ahead; places go on without a division
-      int ids[kSub], places[kSub], next_t = 0, next_page = 0, next_place = 0, issued = 0;
-      auto ask = [&]() {
+      const int tpp = a.c.page_len / kKv4Tile;
+      bool ok = true;
+      int n = 0;
+      for (long long w = blockIdx.x; ok && next_item(w);) {
+        const int n16 = (it.lim_hi + kKv4Tile - 1) / kKv4Tile;
+        const int* trow = a.table + (long long)it.seq * a.table_stride;
+        // the pages of a tile are asked for a tile ahead; places go on without a division
+        int ids[kSub], places[kSub], next_t = 0, next_page = 0, next_place = 0;
+        auto ask = [&]() {
 #pragma unroll
-        for (int s = 0; s < kSub; ++s) {
-          ids[s] = next_t < n16 ? trow[next_page] : -1;
-          places[s] = next_place;
-          ++next_t;
-          if (++next_place == tpp) {
-            next_place = 0;
-            ++next_page;
+          for (int s = 0; s < kSub; ++s) {
+            ids[s] = next_t < n16 ? trow[next_page] : -1;
+            places[s] = next_place;
+            ++next_t;
+            if (++next_place == tpp) {
+              next_place = 0;
+              ++next_page;
+            }
           }
-        }
-      };
-      ask();
-      for (int i = 0; i < nt; ++i) {
-        const int st = i & 1;
-        if (i >= 2 && !cwait(&B.raw_empty[st], (uint32_t)((i >> 1) + 1) & 1u, abort_flag)) break;
-        unsigned char* raw = sm + L::off_raw + st * L::stage_bytes;
-        const uint8_t* src[kSub];
-        int absent = 0, here = 0;
-#pragma unroll
-        for (int s = 0; s < kSub; ++s) {
-          const bool there = ids[s] >= 0 && ids[s] < a.c.n_pages;
-          absent |= there ? 0 : 1 << s;
-          here += there;
-          src[s] = a.c.data + (((long long)ids[s] * a.c.n_kv_heads + head) * tpp + places[s]) * TILE;
-        }
-        M.absent[i & (kInfo - 1)] = absent;
-        mbar_arrive_expect_tx(&B.raw_full[st], here * TILE);
-        ++issued;
-        constexpr int cut = HALF + CODES / 2;  // V's second half goes 16 bytes on: see its reads
-#pragma unroll
-        for (int s = 0; s < kSub; ++s)
-          if (!(absent >> s & 1)) {
-            bulk_g2s(raw + s * L::sub_stride, src[s], cut, &B.raw_full[st]);
-            bulk_g2s(raw + s * L::sub_stride + cut + 16, src[s] + cut, TILE - cut, &B.raw_full[st]);
-          }
+        };
         ask();
+        for (int i = 0; i < it.nt; ++i, ++n) {
+          const int rs = n & (kRaw - 1);
+          ok = n < kRaw || cwait(&B.raw_empty[rs], (uint32_t)(n / kRaw + 1) & 1u, abort_flag);
+          if (!ok) break;
+          unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
+          int absent = 0, here = 0;
+#pragma unroll
+          for (int s = 0; s < kSub; ++s) {
+            const bool there = ids[s] >= 0 && ids[s] < a.c.n_pages;
+            absent |= there ? 0 : 1 << s;
+            here += there;
+          }
+          M.absent[n & (kInfo - 1)] = absent;
+          mbar_arrive_expect_tx(&B.raw_full[rs], here * TILE);
+          // V's second half, and the second half of its scales, go 16 bytes on each: see their reads
+          constexpr int cut = HALF + CODES / 2, cut2 = HALF + CODES + kv4_scales(D) / 2;
+#pragma unroll
+          for (int s = 0; s < kSub; ++s)
+            if (!(absent >> s & 1)) {
+              const uint8_t* src = a.c.data + (((long long)ids[s] * a.c.n_kv_heads + it.head) * tpp + places[s]) * TILE;
+              unsigned char* dst = raw + s * L::sub_stride;
+              bulk_g2s(dst, src, cut, &B.raw_full[rs]);
+              bulk_g2s(dst + cut + 16, src + cut, cut2 - cut, &B.raw_full[rs]);
+              bulk_g2s(dst + cut2 + 32, src + cut2, TILE - cut2, &B.raw_full[rs]);
+            }
+          ask();
+        }
       }
       if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
-        for (int i = max(0, issued - 2); i < issued; ++i) mbar_wait(&B.raw_full[i & 1], (uint32_t)(i >> 1) & 1u, kDrainNs);
+        for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
     }
     if (warp == kSoftWarps + kProdWarps && lane == 0) {
       // ---------------- products ----------------
       constexpr uint32_t id_s = idesc_f16_f32(kRowsTile, kPosTile), id_o = idesc_f16_f32(kRowsTile, D);
-      const uint32_t q0 = smem_u32(sm);
       auto scores = [&](int i) {
         const int st = i & 1;
         if (!cwait(&B.k_full[st], (uint32_t)(i >> 1) & 1u, abort_flag)) return false;
@@ -468,11 +466,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         uint32_t acc = 0;
 #pragma unroll
         for (int part = 0; part < NQ + NKV - 1; ++part) {  // high high, [low high,] [high low]
-          const uint32_t qp = q0 + (NQ == 2 && part == 1 ? L::q_part : 0);
+          const uint32_t qp = tmem + kColQ + (NQ == 2 && part == 1 ? D / 2 : 0);
           const uint32_t kp = k0 + (part > 0 && part == NQ ? L::k_part : 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            umma_f16_ss(tmem + kColS + st * kPosTile, desc_sw128(qp + (ks >> 2) * (kRowsTile * 128) + (ks & 3) * 32),
+            umma_f16_ts(tmem + kColS + st * kPosTile, qp + ks * 8,
                         desc_sw128(kp + (ks >> 2) * (kPosTile * 128) + (ks & 3) * 32), id_s, acc);
             acc = 1;
           }
@@ -482,17 +480,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         mbar_arrive(&B.s_full[st]);  // hands on what the producers wrote beside the tile
         return true;
       };
-      bool ok = nt == 0 || scores(0);
-      if (ok && nt > 1) ok = scores(1);
-      for (int i = 0; ok && i < nt; ++i) {
-        const int st = i & 1;
-        const uint32_t parity = (uint32_t)(i >> 1) & 1u;
+      bool ok = true;
+      int n = 0, items = 0;
+      for (long long w = blockIdx.x; ok && next_item(w); n += it.nt) {
+      if (it.nt == 0) continue;  // its q is not waited for, and not announced
+      ok = cwait(&B.q_full, (uint32_t)items & 1u, abort_flag);
+      ++items;
+      if (!ok) break;
+      tc_fence_after();
+      ok = scores(n);
+      if (ok && it.nt > 1) ok = scores(n + 1);
+      for (int i = 0; ok && i < it.nt; ++i) {
+        const int st = (n + i) & 1;
+        const uint32_t parity = (uint32_t)((n + i) >> 1) & 1u;
         ok = cwait(&B.v_full[st], parity, abort_flag) && cwait(&B.p_full[st], parity, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint32_t v0 = smem_u32(sm + L::off_v + st * NKV * L::v_part);
         uint32_t acc = (NP == 2 ? i % kGroup : i) ? 1u : 0u;
-        const uint32_t od = tmem + kColO + (NP == 2 ? (i / kGroup & 1) * D : 0);
+        const uint32_t od = tmem + kColO;
 #pragma unroll
         for (int part = 0; part < NP + NKV - 1; ++part) {
           const uint32_t pp = tmem + kColP + st * 64 + (NP == 2 && part == 1 ? 32 : 0);
@@ -507,7 +513,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         umma_commit(&B.o_full[st]);
         mbar_arrive(&B.o_full[st]);
         // the softmax of tile i has read its scores: their place is free
-        if (i + 2 < nt) ok = scores(i + 2);
+        if (i + 2 < it.nt) ok = scores(n + i + 2);
+      }
       }
       if (!ok) {  // given up: the products already issued finish before TMEM is released
         umma_commit(&B.drain);
@@ -518,13 +525,64 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     // ---------------- softmax ----------------
     regs_up<kRegsSoft>();
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1;
+    bool ok = true;
+    int n = 0;
+    for (long long w_item = blockIdx.x; next_item(w_item); n += it.nt) {
+    const int nt = it.nt, lim_lo = max(0, it.len - it.count + it.row0 / group + 1);  // positions that every row sees
+    const int col = it.row0 + row;
+    const bool live = col < it.ncols;
+    const int col_k = col / group;
+    const int lim = live ? max(0, it.len - it.count + col_k + 1) : 0;
+    const long long elem = live ? (long long)(it.head * group + col % group) * D + half * HD : 0;
+    // ---- q into TMEM: scaled by a power of two per row, high and low part; within eight dims in the order of the unpacked
+    // codes (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with its q: this thread has waited for them
+    float zscale;
+    {
+      float q[HD / 8][8], top = 0.f;
+#pragma unroll
+      for (int g = 0; g < HD / 8; ++g) {
+        if (live) {
+          load8(a.q, dtype, (long long)(it.start + col_k) * a.q_stride + elem + 8 * g, q[g]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[g][i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[g][i]));
+      }
+      M.q_top[half][row] = top;
+      named_bar(1 + (warp & 3), 64);
+      top = fmaxf(top, M.q_top[half ^ 1][row]);
+      const int e = top <= FLT_MAX ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+      zscale = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+      const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+#pragma unroll
+      for (int c = 0; c < HD / 2; c += 16) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int g = (c + j) >> 2, t = j & 3;
+          const float x0 = q[g][t] * up, x1 = q[g][t + 4] * up;
+          const __half2 h = __floats2half2_rn(x0, x1);
+          const float2 f = __half22float2(h);
+          hi[j] = as_u32(h);
+          lo[j] = as_u32(__floats2half2_rn(x0 - f.x, x1 - f.y));
+        }
+        tmem_st16(lanes + kColQ + half * (HD / 2) + c, hi);
+        if (NQ == 2) tmem_st16(lanes + kColQ + D / 2 + half * (HD / 2) + c, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      if (nt > 0) mbar_arrive(&B.q_full);
+    }
+
     constexpr int NO = NP == 2 ? HD / 2 : 1;
     float2 o[NO];  // STAGE_F32: the sums over the groups of tiles that are done
 #pragma unroll
     for (int j = 0; j < NO; ++j) o[j] = make_float2(0.f, 0.f);
     float ref = -INFINITY, sum = 0.f;
     int nan_blocks = 0;  // the thread's blocks of dims in which its row sees a V scale that is no number
-    bool ok = true;
     auto products_done = [&](int i) {
       if (!__all_sync(0xffffffffu, cwait(&B.o_full[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag))) return false;
       tc_fence_after();
@@ -538,12 +596,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       }
     };
     // adds a group's sums to the registers
-    auto collect = [&](int g) {
+    auto collect = [&]() {
       if constexpr (NP == 2) {
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           uint32_t r[32];
-          tmem_ld32(lanes + kColO + (g & 1) * D + half * HD + c, r);
+          tmem_ld32(lanes + kColO + half * HD + c, r);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -552,10 +610,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       }
     };
     for (int i = 0; i < nt; ++i) {
-      const int st = i & 1, inf = i & (kInfo - 1);
+      const int ni = n + i, st = ni & 1, inf = ni & (kInfo - 1);
       // S of tile i is there, and so is the product of tile i - 2, issued before it: P's place is free.  When a wait has run
       // out every thread still goes through the barriers, and does nothing else
-      ok = ok && __all_sync(0xffffffffu, cwait(&B.s_full[st], (uint32_t)(i >> 1) & 1u, abort_flag));
+      ok = ok && __all_sync(0xffffffffu, cwait(&B.s_full[st], (uint32_t)(ni >> 1) & 1u, abort_flag));
       if (!ok) {
         named_bar(1 + (warp & 3), 64);
         continue;
@@ -565,7 +623,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       tmem_ld32(lanes + kColS + st * kPosTile + half * 32, s);
       const float f = zscale * M.k_pow[inf], ev = M.v_exp[inf], v_inv = M.v_inv[inf];
       const int absent = M.absent[inf] >> (2 * half) & 3;
-      if (i >= 2) note_bad(i - 2);
+      if (i >= 2) note_bad(ni - 2);
       tmem_wait_ld();
       const int pos0 = i * kPosTile + 32 * half;
       if (pos0 + 32 > lim_lo || absent) {
@@ -603,14 +661,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         sum *= keep;
       }
       const bool fresh = NP == 2 ? i % kGroup == 0 : i == 0;  // a new sum in TMEM begins
-      if (__any_sync(0xffffffffu, keep != 1.f) && !fresh) {
-        if (NP == 2) {
+      const bool moved = __any_sync(0xffffffffu, keep != 1.f);
+      if (NP == 2 && fresh && i > 0) {  // the last group's sums leave TMEM before the first product of this one
+        ok = products_done(ni - 1);
+        if (ok) collect();
+      }
+      if (NP == 2 && moved) {
 #pragma unroll
-          for (int j = 0; j < NO; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
-        }
-        ok = products_done(i - 1);
+        for (int j = 0; j < NO; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
+      }
+      if (moved && !fresh) {
+        ok = products_done(ni - 1);
         if (ok) {
-          const uint32_t at = lanes + kColO + (NP == 2 ? (i / kGroup & 1) * D : 0) + half * HD;
+          const uint32_t at = lanes + kColO + half * HD;
 #pragma unroll
           for (int c = 0; c < HD; c += 16) {
             uint32_t r[16];
@@ -649,24 +712,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&B.p_full[st]);
-      if (NP == 2 && fresh && i > 0) {  // the last group's sums, while the products of this tile run
-        ok = ok && products_done(i - 1);
-        if (ok) collect(i / kGroup - 1);
-        if (__any_sync(0xffffffffu, keep != 1.f)) {
-#pragma unroll
-          for (int j = 0; j < NO; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
-        }
-      }
     }
     if (ok && nt > 0) {
-      ok = products_done(nt - 1);
-      if (ok) collect((nt - 1) / kGroup);
-      if (nt > 1) note_bad(nt - 2);
-      note_bad(nt - 1);
+      ok = products_done(n + nt - 1);
+      if (ok && NP == 2) collect();
+      if (nt > 1) note_bad(n + nt - 2);
+      note_bad(n + nt - 1);
     }
-    M.top[nt & 1][half][row] = sum;
+    M.top[(n + nt) & 1][half][row] = sum;
     named_bar(1 + (warp & 3), 64);
-    sum += M.top[nt & 1][half ^ 1][row];
+    sum += M.top[(n + nt) & 1][half ^ 1][row];
+    named_bar(1 + (warp & 3), 64);  // read before the next item writes there
     const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
 #pragma unroll
     for (int c = 0; c < HD; c += 32) {  // 32 dims: a block
@@ -689,7 +745,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       const float factor = nan_blocks >> (c >> 5) & 1 ? NAN : inv;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= factor;
-      const long long at = (long long)(start + col_k) * a.out_stride + elem + c;
+      const long long at = (long long)(it.start + col_k) * a.out_stride + elem + c;
       if (!live) {
       } else if (dtype == KV4_F32) {
         float4* out = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
@@ -715,6 +771,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       }
       __syncwarp();  // the next block's TMEM read is the whole warp's
     }
+    tc_fence_before();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -726,7 +784,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 
 template <int D, int NQ, int NKV, int NP>
 cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
-  constexpr int smem = ChunkLayout<D, NQ, NKV>::bytes;
+  constexpr int smem = ChunkLayout<D, NKV>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   auto* kern = kv4_chunk_kernel<D, NQ, NKV, NP>;
   static std::atomic<uint64_t> ready{0};  // one bit per device
@@ -739,7 +797,8 @@ cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
-  const dim3 grid((unsigned)((cols + kRowsTile - 1) / kRowsTile), a.c.n_kv_heads, a.n_seqs);
+  const long long items = (cols + kRowsTile - 1) / kRowsTile * a.c.n_kv_heads * a.n_seqs;
+  const int grid = (int)min(items, (long long)sm_count());
   kern<<<grid, kChunkThreads, smem, st>>>(a, dtype);
   return cudaGetLastError();
 }

@@ -34,11 +34,7 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// fp16 operands, from shared memory and (A) from TMEM: a row per lane, two neighbouring K elements per 32-bit column
-__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  umma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);  // one kind: the types are in the instruction descriptor
-}
+// The same with A from TMEM: a row per lane, two neighbouring K elements per 32-bit column.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
