@@ -455,68 +455,72 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
         for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
     }
-    if (warp == kSoftWarps + kProdWarps && lane == 0) {
+    if (warp == kSoftWarps + kProdWarps) {
       // ---------------- products ----------------
+      // The whole warp goes through the loops and one elected thread issues: addresses and descriptors then are uniform
+      // values, which the instructions take as they are.
+      const bool leader = elect_one();
       constexpr uint32_t id_s = idesc_f16_f32(kRowsTile, kPosTile), id_o = idesc_f16_f32(kRowsTile, D);
-      auto scores = [&](int i) {
-        const int st = i & 1;
-        if (!cwait(&B.k_full[st], (uint32_t)(i >> 1) & 1u, abort_flag)) return false;
+      const uint64_t kd = desc_sw128(smem_u32(sm + L::off_k)), vd = desc_sw128(smem_u32(sm + L::off_v));
+      uint32_t s_st = 0, s_ph = 0, o_st = 0, o_ph = 0;  // stage and parity of the next tile's scores and outputs
+      auto scores = [&]() {
+        if (!__all_sync(0xffffffffu, cwait(&B.k_full[s_st], s_ph, abort_flag))) return false;
         tc_fence_after();
-        const uint32_t k0 = smem_u32(sm + L::off_k + st * NKV * L::k_part);
-        uint32_t acc = 0;
+        const uint64_t kb = kd + s_st * (uint32_t)(NKV * L::k_part >> 4);
+        const uint32_t d = tmem + kColS + s_st * kPosTile;
+        if (leader) {
 #pragma unroll
-        for (int part = 0; part < NQ + NKV - 1; ++part) {  // high high, [low high,] [high low]
-          const uint32_t qp = tmem + kColQ + (NQ == 2 && part == 1 ? D / 2 : 0);
-          const uint32_t kp = k0 + (part > 0 && part == NQ ? L::k_part : 0);
+          for (int part = 0; part < NQ + NKV - 1; ++part)  // high high, [low high,] [high low]
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            umma_f16_ts(tmem + kColS + st * kPosTile, qp + ks * 8,
-                        desc_sw128(kp + (ks >> 2) * (kPosTile * 128) + (ks & 3) * 32), id_s, acc);
-            acc = 1;
-          }
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_f16_ts(d, tmem + kColQ + (NQ == 2 && part == 1 ? D / 2 : 0) + ks * 8,
+                          kb + (((part > 0 && part == NQ ? L::k_part : 0) + (ks >> 2) * (kPosTile * 128) + (ks & 3) * 32) >> 4),
+                          id_s, part || ks ? 1u : 0u);
+          umma_commit(&B.k_empty[s_st]);
+          umma_commit(&B.s_full[s_st]);
+          mbar_arrive(&B.s_full[s_st]);  // hands on what the producers wrote beside the tile
         }
-        umma_commit(&B.k_empty[st]);
-        umma_commit(&B.s_full[st]);
-        mbar_arrive(&B.s_full[st]);  // hands on what the producers wrote beside the tile
+        __syncwarp();
+        s_st ^= 1;
+        s_ph ^= s_st ? 0u : 1u;
         return true;
       };
       bool ok = true;
-      int n = 0, items = 0;
-      for (long long w = blockIdx.x; ok && next_item(w); n += it.nt) {
-      if (it.nt == 0) continue;  // its q is not waited for, and not announced
-      ok = cwait(&B.q_full, (uint32_t)items & 1u, abort_flag);
-      ++items;
-      if (!ok) break;
-      tc_fence_after();
-      ok = scores(n);
-      if (ok && it.nt > 1) ok = scores(n + 1);
-      for (int i = 0; ok && i < it.nt; ++i) {
-        const int st = (n + i) & 1;
-        const uint32_t parity = (uint32_t)((n + i) >> 1) & 1u;
-        ok = cwait(&B.v_full[st], parity, abort_flag) && cwait(&B.p_full[st], parity, abort_flag);
+      uint32_t q_ph = 0;
+      for (long long w = blockIdx.x; ok && next_item(w);) {
+        if (it.nt == 0) continue;  // its q is not waited for, and not announced
+        ok = __all_sync(0xffffffffu, cwait(&B.q_full, q_ph, abort_flag));
+        q_ph ^= 1;
         if (!ok) break;
         tc_fence_after();
-        const uint32_t v0 = smem_u32(sm + L::off_v + st * NKV * L::v_part);
-        uint32_t acc = (NP == 2 ? i % kGroup : i) ? 1u : 0u;
-        const uint32_t od = tmem + kColO;
+        ok = scores();
+        if (ok && it.nt > 1) ok = scores();
+        for (int i = 0; ok && i < it.nt; ++i) {
+          ok = __all_sync(0xffffffffu, cwait(&B.v_full[o_st], o_ph, abort_flag) && cwait(&B.p_full[o_st], o_ph, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vb = vd + o_st * (uint32_t)(NKV * L::v_part >> 4);
+          const uint32_t pc = tmem + kColP + o_st * 64;
+          const uint32_t again = (NP == 2 ? i % kGroup : i) ? 1u : 0u;
+          if (leader) {
 #pragma unroll
-        for (int part = 0; part < NP + NKV - 1; ++part) {
-          const uint32_t pp = tmem + kColP + st * 64 + (NP == 2 && part == 1 ? 32 : 0);
-          const uint32_t vp = v0 + (part > 0 && part == NP ? L::v_part : 0);
+            for (int part = 0; part < NP + NKV - 1; ++part)
 #pragma unroll
-          for (int ks = 0; ks < kPosTile / 16; ++ks) {
-            umma_f16_ts(od, pp + ks * 8, desc_sw128(vp + ks * 32), id_o, acc);
-            acc = 1;
+              for (int ks = 0; ks < kPosTile / 16; ++ks)
+                umma_f16_ts(tmem + kColO, pc + (NP == 2 && part == 1 ? 32 : 0) + ks * 8,
+                            vb + (((part > 0 && part == NP ? L::v_part : 0) + ks * 32) >> 4), id_o, part || ks ? 1u : again);
+            umma_commit(&B.v_empty[o_st]);
+            umma_commit(&B.o_full[o_st]);
+            mbar_arrive(&B.o_full[o_st]);
           }
+          __syncwarp();
+          o_st ^= 1;
+          o_ph ^= o_st ? 0u : 1u;
+          // the softmax of tile i has read its scores: their place is free
+          if (i + 2 < it.nt) ok = scores();
         }
-        umma_commit(&B.v_empty[st]);
-        umma_commit(&B.o_full[st]);
-        mbar_arrive(&B.o_full[st]);
-        // the softmax of tile i has read its scores: their place is free
-        if (i + 2 < it.nt) ok = scores(n + i + 2);
       }
-      }
-      if (!ok) {  // given up: the products already issued finish before TMEM is released
+      if (!ok && leader) {  // given up: the products already issued finish before TMEM is released
         umma_commit(&B.drain);
         mbar_wait(&B.drain, 0u, kDrainNs);
       }
