@@ -588,15 +588,17 @@ def stage_op_kv4_plan(page_len: int, seq_len, new_len, table, free_ring, free_st
     n, n_tok, ring_len = seq_len.numel(), slot.numel(), free_ring.numel()
     if table.dim() != 2 or table.shape[0] != n:
         _invalid("table must be [n_seqs, stride]")
-    stride = table.shape[1]
+    sizes = (n, n, table.numel(), ring_len, 2, n, 2, n + 1, n_tok, n_tok, n_tok, 1)
+    i32 = _torch.int32
+    for t, size in zip(tensors, sizes):
+        if t.dtype is not i32 or t.numel() != size or not t.is_contiguous():
+            _invalid("plan takes contiguous int32 tensors: seq_len, new_len, seq_len_out [n], table [n, stride], free_ring, "
+                     "free_state, free_state_out [2], cu_new [n + 1], slot, pos, seq [n_tok], status [1]")
+    p = [t.data_ptr() for t in tensors]
     rc = (_lib or lib()).stage_op_kv4_plan(
-        n, page_len, ring_len if n_pages is None else n_pages, _i32dev(seq_len, "seq_len", n),
-        None if keep_len is None else _i32dev(keep_len, "keep_len", n), _i32dev(new_len, "new_len", n),
-        _i32dev(table, "table", n * stride), stride, _i32dev(free_ring, "free_ring", ring_len), ring_len,
-        _i32dev(free_state, "free_state", 2), _i32dev(seq_len_out, "seq_len_out", n),
-        _i32dev(free_state_out, "free_state_out", 2), n_tok, _i32dev(cu_new, "cu_new", n + 1),
-        _i32dev(slot, "slot", n_tok), _i32dev(pos, "pos", n_tok), _i32dev(seq, "seq", n_tok),
-        _i32dev(status, "status", 1), stream)
+        n, page_len, ring_len if n_pages is None else n_pages, p[0],
+        None if keep_len is None else _i32dev(keep_len, "keep_len", n), p[1], p[2], table.shape[1], p[3], ring_len, p[4], p[5],
+        p[6], n_tok, p[7], p[8], p[9], p[10], p[11], stream)
     if rc:
         _opcheck(rc)
 

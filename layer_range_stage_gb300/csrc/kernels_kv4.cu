@@ -2,6 +2,8 @@
 
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "kv4.cuh"
@@ -13,54 +15,49 @@ namespace lrs {
 // ------------------------------------------------------------------------------------------
 // Plan: take_i = max(0, need_i - have_i), give_i = max(0, have_i - need_i) and new_i are summed over
 // the requests before each one (exclusive prefix sums), which places every page taken, every
-// page given back and every token.  One cluster of CTAs does a step in one launch: the lengths
-// are read in the first part and written after the cluster's barrier, so in and out may be the
-// same arrays; nothing is kept between calls.
+// page given back and every token.  A step is bound by the latency of its few dependent reads.  One cluster of CTAs does
+// it in one launch: every CTA computes the sums of all requests for itself, in shared memory, and then they share out
+// the page moves and the tokens one by one, each of which looks its request up by a binary search -- so a request of
+// thousands of pages or tokens is no longer work than as many small ones (1021 requests with 49 thousand tokens: @@ us,
+// 47 us when a warp moved a request's pages).  The lengths are read before the cluster's barrier and written after it, so
+// in and out may be the same arrays; nothing is kept between calls.
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024, kPlanFew = 256;  // threads of a CTA, and of a lone one
 constexpr int kPlanCluster = 8;
+constexpr int kPlanBatch = 4096;  // requests whose sums lie in shared memory at a time
 
 struct PlanReq {
-  int have, need, fresh;
+  int have, need, fresh, end;  // pages before and after, new tokens, positions after
   bool bad;
 };
 
 __device__ __forceinline__ PlanReq plan_request(const Kv4PlanArgs& a, int i) {
   const int len = a.seq_len[i], keep = a.keep_len ? a.keep_len[i] : len, fresh = a.new_len[i];
-  PlanReq r = {0, 0, 0, true};
+  PlanReq r = {0, 0, 0, 0, true};
   if (len < 0 || keep < 0 || keep > len || fresh < 0) return r;
-  const long long have = ((long long)len + a.page_len - 1) / a.page_len;
-  const long long need = ((long long)keep + fresh + a.page_len - 1) / a.page_len;
-  if (have > a.table_stride || (need > a.table_stride && fresh <= a.n_tok)) return r;
+  const int some = min(fresh, a.n_tok + 1);  // more is refused by the total; the sums below fit 32 bits
+  const unsigned pl = (unsigned)a.page_len, stride = (unsigned)a.table_stride;
+  const unsigned have = ((unsigned)len + pl - 1) / pl, need = ((unsigned)keep + (unsigned)some + pl - 1) / pl;
+  if (have > stride || (need > stride && fresh <= a.n_tok)) return r;
   r.bad = false;
   r.have = (int)have;
-  r.need = (int)(need > a.table_stride ? have : need);  // more tokens than the slot map holds: refused by the total
-  r.fresh = fresh > a.n_tok ? a.n_tok + 1 : fresh;
+  r.need = (int)(need > stride ? have : need);
+  r.fresh = some;
+  r.end = (int)((unsigned)keep + (unsigned)some);
   return r;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArgs a) {
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), nranks = (int)cluster.num_blocks();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NW = kPlanThreads / 32;
-  __shared__ long long wsum[3][NW];
-  __shared__ long long total[4];  // this CTA's sums of take, give, new; whether a length is bad
+struct PlanSmem {
+  // per request of the batch: the first of its page moves and of its tokens (batch-wide numbers; one more entry), where
+  // its pages lie in the ring, the first table column that moves (negative, less one: given back), its positions
+  int move[kPlanBatch + 1], token[kPlanBatch + 1], ring[kPlanBatch], col[kPlanBatch], end[kPlanBatch];
+  long long part[3][kPlanThreads / 32];
+};
 
-  const int head = a.free_state[0], count = a.free_state[1];
-  const int g = rank * kPlanThreads + tid, nthr = nranks * kPlanThreads;
-  const int seg = (a.n_seqs + nthr - 1) / nthr;
-  const int i0 = min(a.n_seqs, g * seg), i1 = min(a.n_seqs, i0 + seg);
-  long long v[3] = {0, 0, 0};
-  bool bad = head < 0 || head >= a.ring_len || count < 0 || count > a.ring_len;
-  for (int i = i0; i < i1; ++i) {
-    const PlanReq r = plan_request(a, i);
-    bad |= r.bad;
-    v[0] += max(0, r.need - r.have);
-    v[1] += max(0, r.have - r.need);
-    v[2] += r.fresh;
-  }
-  long long before[3];
+// Sums of v over the block, and over the threads before this one.
+__device__ __forceinline__ void plan_scan(PlanSmem& sm, const long long (&v)[3], long long (&before)[3], long long (&sum)[3]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  __syncthreads();  // the last scan's parts are read
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     long long s = v[k];
@@ -70,108 +67,161 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
       if (lane >= o) s += u;
     }
     before[k] = s - v[k];
-    if (lane == 31) wsum[k][warp] = s;
+    if (lane == 31) sm.part[k][warp] = s;
   }
-  const bool any_bad = __syncthreads_or(bad);
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    long long all = 0;
-    for (int w = 0; w < NW; ++w) {
-      if (w == warp) before[k] += all;
-      all += wsum[k][w];
-    }
-    if (tid == 0) total[k] = all;
-  }
-  if (tid == 0) total[3] = any_bad;
-  cluster.sync();  // every CTA has read the lengths and the ring's state
-  long long sum[4] = {0, 0, 0, 0};
-  for (int r = 0; r < nranks; ++r) {
-    const long long* t = cluster.map_shared_rank(total, r);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const long long x = t[k];
-      if (k < 3 && r < rank) before[k] += x;
-      sum[k] += x;
+    sum[k] = 0;
+#pragma unroll 8
+    for (int w = 0; w < warps; ++w) {
+      if (w == warp) before[k] += sum[k];
+      sum[k] += sm.part[k][w];
     }
   }
-  int status = 0;
-  if (sum[3] || count + sum[1] > a.ring_len) status = 2;
-  else if (sum[2] > a.n_tok) status = 3;
-  else if (sum[0] > count) status = 1;
+}
 
+// The last i in [0, n) with first[i] <= x (first[0] <= x).
+__device__ __forceinline__ int plan_find(const int* first, int n, int x) {
+  int lo = 0;
+  for (int hi = n; hi - lo > 1;) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArgs a) {
+  extern __shared__ __align__(16) unsigned char plan_raw[];
+  PlanSmem& sm = *reinterpret_cast<PlanSmem*>(plan_raw);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, nt = blockDim.x, g = (int)cluster.block_rank() * nt + tid;
+  const int nthr = (int)cluster.num_blocks() * nt, R = a.ring_len;
+  const int head = a.free_state[0], count = a.free_state[1];
+  auto wrap = [R](int x) { return x >= R ? x - R : x; };  // a place in the ring, from less than twice its length
+
+  // May the step be done?  Of one batch the sums below say it
+  long long total[3] = {0, 0, 0};
+  bool bad = head < 0 || head >= R || count < 0 || count > R;
+  int status = 0;
+  auto judge = [&]() {
+    if (__syncthreads_or(bad) || count + total[1] > R) status = 2;
+    else if (total[2] > a.n_tok) status = 3;
+    else if (total[0] > count) status = 1;
+  };
+  const bool one = a.n_seqs <= kPlanBatch;
+  if (!one) {
+    long long v[3] = {0, 0, 0}, before[3];
+    for (int i = tid; i < a.n_seqs; i += nt) {
+      const PlanReq r = plan_request(a, i);
+      bad |= r.bad;
+      v[0] += max(0, r.need - r.have);
+      v[1] += max(0, r.have - r.need);
+      v[2] += r.fresh;
+    }
+    plan_scan(sm, v, before, total);
+    judge();
+  }
+
+  int done[3] = {0, 0, 0};  // takes, gives and tokens of the batches before
+  for (int b = 0; b < a.n_seqs || b == 0; b += kPlanBatch) {
+    const int m = min(kPlanBatch, a.n_seqs - b), seg = (m + nt - 1) / nt;
+    const int i0 = min(m, tid * seg), i1 = min(m, i0 + seg);
+    long long v[3] = {0, 0, 0}, before[3], sum[3];
+    if (!status) {
+      for (int i = i0; i < i1; ++i) {
+        const PlanReq r = plan_request(a, b + i);
+        bad |= r.bad;
+        v[0] += max(0, r.need - r.have);
+        v[1] += max(0, r.have - r.need);
+        v[2] += r.fresh;
+      }
+    }
+    plan_scan(sm, v, before, sum);
+    if (one) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) total[k] = sum[k];
+      judge();
+    }
+    if (status) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) before[k] = sum[k] = 0;
+    }
+    for (int i = i0; i < i1; ++i) {
+      PlanReq r = {0, 0, 0, 0, false};
+      if (!status) r = plan_request(a, b + i);
+      const int take = max(0, r.need - r.have), give = max(0, r.have - r.need);
+      sm.move[i] = (int)(before[0] + before[1]);
+      sm.token[i] = (int)before[2];
+      if (!status) sm.ring[i] = wrap(head + (take ? done[0] + (int)before[0] : count + done[1] + (int)before[1]));
+      sm.col[i] = give ? -1 - r.need : r.have;
+      sm.end[i] = status ? a.seq_len[b + i] : r.end;
+      before[0] += take;
+      before[1] += give;
+      before[2] += r.fresh;
+    }
+    const int moves = (int)(sum[0] + sum[1]), tokens = (int)sum[2];
+    if (tid == 0) {
+      sm.move[m] = moves;
+      sm.token[m] = tokens;
+    }
+    cluster.sync();  // this batch's lengths (and the ring's state) are read by every CTA
+
+    for (int i = g; i < m; i += nthr) {
+      a.seq_len_out[b + i] = sm.end[i];
+      a.cu_new[b + i] = done[2] + sm.token[i];
+    }
+#pragma unroll 2
+    for (int x = g; x < moves; x += nthr) {
+      const int i = plan_find(sm.move, m, x), j = x - sm.move[i], col = sm.col[i];
+      int* ring = a.ring + wrap(sm.ring[i] + j);
+      int* entry = a.table + (long long)(b + i) * a.table_stride + (col < 0 ? -1 - col : col) + j;
+      if (col < 0) *ring = *entry;
+      else *entry = *ring;
+    }
+    // a token's page: of the columns that stay, or the ring's (which nobody writes in this step: what is given back goes
+    // behind its last page)
+#pragma unroll 2
+    for (int x = g; x < tokens; x += nthr) {
+      const int i = plan_find(sm.token, m, x), pos = sm.end[i] - (sm.token[i + 1] - x), c = pos / a.page_len, col = sm.col[i];
+      const int page = col < 0 || c < col ? a.table[(long long)(b + i) * a.table_stride + c]
+                                          : a.ring[wrap(sm.ring[i] + c - col)];
+      const int t = done[2] + x;
+      a.slot[t] = page >= 0 && page < a.n_pages ? page * a.page_len + (pos - c * a.page_len) : -1;
+      a.pos[t] = pos;
+      a.seq[t] = b + i;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) done[k] += (int)sum[k];
+    __syncthreads();  // the sums are read
+  }
+  for (int t = done[2] + g; t < a.n_tok; t += nthr) a.slot[t] = a.pos[t] = a.seq[t] = -1;
   if (g == 0) {
     a.status[0] = status;
-    a.cu_new[a.n_seqs] = status ? 0 : (int)sum[2];
-    a.free_state_out[0] = status ? head : (int)((head + sum[0]) % a.ring_len);
-    a.free_state_out[1] = status ? count : (int)(count - sum[0] + sum[1]);
-  }
-  // pages: few by the lane itself, more by the whole warp
-  for (int k = 0; k < seg; ++k) {
-    const int i = i0 + k;
-    PlanReq r = {0, 0, 0, false};
-    if (i < i1) {
-      const int len = a.seq_len[i], keep = a.keep_len ? a.keep_len[i] : len;
-      if (!status) r = plan_request(a, i);
-      a.cu_new[i] = status ? 0 : (int)before[2];
-      a.seq_len_out[i] = status ? len : keep + r.fresh;
-    }
-    const int take = max(0, r.need - r.have), give = max(0, r.have - r.need), n = take + give;
-    // taken pages go from the ring's place `at` on to the table from `have`; given ones the other way
-    const int at = (int)(take ? (head + before[0]) % a.ring_len : (head + count + before[1]) % a.ring_len);
-    const int col = min(r.have, r.need);
-    unsigned many = __ballot_sync(0xffffffffu, n > 4);
-    if (n <= 4) {
-      for (int j = 0; j < n; ++j) {
-        int* ring = a.ring + ((long long)at + j) % a.ring_len;
-        int* entry = a.table + (long long)i * a.table_stride + col + j;
-        if (take) *entry = *ring;
-        else *ring = *entry;
-      }
-    }
-    while (many) {
-      const int src = __ffs(many) - 1;
-      many &= many - 1;
-      const int wi = __shfl_sync(0xffffffffu, i, src), wn = __shfl_sync(0xffffffffu, n, src);
-      const int wat = __shfl_sync(0xffffffffu, at, src), wcol = __shfl_sync(0xffffffffu, col, src);
-      const int wtake = __shfl_sync(0xffffffffu, take, src);
-      for (int j = lane; j < wn; j += 32) {
-        int* ring = a.ring + ((long long)wat + j) % a.ring_len;
-        int* entry = a.table + (long long)wi * a.table_stride + wcol + j;
-        if (wtake) *entry = *ring;
-        else *ring = *entry;
-      }
-    }
-    before[0] += take;
-    before[1] += give;
-    before[2] += r.fresh;
-  }
-  cluster.sync();  // table, cu_new and seq_len_out are written
-  const int tokens = status ? 0 : (int)sum[2];
-  for (int t = g; t < a.n_tok; t += nthr) {
-    int slot = -1, pos = -1, lo = -1;
-    if (t < tokens) {
-      lo = 0;  // the last request that begins at or before t
-      for (int hi = a.n_seqs; hi - lo > 1;) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_new[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      pos = a.seq_len_out[lo] - (a.cu_new[lo + 1] - t);
-      const int page = a.table[(long long)lo * a.table_stride + pos / a.page_len];
-      if (page >= 0 && page < a.n_pages) slot = page * a.page_len + pos % a.page_len;
-    }
-    a.slot[t] = slot;
-    a.pos[t] = pos;
-    a.seq[t] = lo;
+    a.cu_new[a.n_seqs] = done[2];
+    a.free_state_out[0] = status ? head : wrap(head + (int)total[0]);
+    a.free_state_out[1] = status ? count : (int)(count - total[0] + total[1]);
   }
 }
 
 cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PlanSmem));
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  const int ncta = a.n_seqs > kPlanThreads || a.n_tok > 4 * kPlanThreads ? kPlanCluster : 1;
+  // one CTA where it has a few dozen steps at most: a cluster's launch and barrier cost more than they save
+  const int ncta = a.n_seqs > 2 * kPlanFew || a.n_tok > 8 * kPlanFew ? kPlanCluster : 1;
   cfg.gridDim = dim3(ncta);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(ncta > 1 ? kPlanThreads : kPlanFew);
+  cfg.dynamicSmemBytes = sizeof(PlanSmem);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ncta;
@@ -182,186 +232,256 @@ cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------------
-// Append and read.  A lane has four neighbouring dims of a row, so a block of 32 dims is eight
-// lanes and its codes are two bytes a lane.
+// Append and read.  A lane has eight neighbouring dims of a row: 16 bytes of a 16-bit type, one word of K codes, two
+// half-words of V codes; a block of 32 dims is four lanes.  A warp has a token (whose slot is taken apart once) and goes
+// through its KV heads, 256 / D of them at a time, two such passes in flight; where the tokens alone would leave SMs
+// without work, a warp has one pass.
 
 template <typename T>
-struct Row4;
+struct Row8;
 template <>
-struct Row4<float> {
-  static __device__ __forceinline__ float4 load(const float* p) { return *reinterpret_cast<const float4*>(p); }
-  static __device__ __forceinline__ void store(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-};
-template <>
-struct Row4<__half> {
-  static __device__ __forceinline__ float4 load(const __half* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
+struct Row8<float> {
+  static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-  static __device__ __forceinline__ void store(__half* p, float4 v) {
-    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-    uint2 u;
-    u.x = *reinterpret_cast<const uint32_t*>(&a);
-    u.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = u;
+  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
 };
 template <>
-struct Row4<__nv_bfloat16> {
-  static __device__ __forceinline__ float4 load(const __nv_bfloat16* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
+struct Row8<__half> {
+  static __device__ __forceinline__ void load(const __half* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, float4 v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    uint2 u;
-    u.x = *reinterpret_cast<const uint32_t*>(&a);
-    u.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p) = u;
+  static __device__ __forceinline__ void store(__half* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Row8<__nv_bfloat16> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
-// Code of x for the scale s (finite, not 0): the nearest integer to x / s, ties to even, plus 8, in
-// [0, 15].  n is the rounded product with the reciprocal, at most one off; the remainder x - s n
-// is exact wherever it is near s / 2 (s has 11 bits, n four), so comparing it with s / 2 decides.
-__device__ __forceinline__ int kv4_code(float x, float s, float inv) {
-  float n = rintf(x * inv);
-  const float r = fmaf(-n, s, x), h = 0.5f * fabsf(s);
-  const bool odd = ((int)n) & 1;
-  if (fabsf(r) > h || (fabsf(r) == h && odd)) n += (r > 0.f) == (s > 0.f) ? 1.f : -1.f;
-  return (int)fminf(fmaxf(n + 8.f, 0.f), 15.f);
-}
-
-// Quantise the four values of this lane with the block's eight lanes: two bytes of codes, the scale's bits.
-__device__ __forceinline__ uint32_t kv4_quantise(float4 v, int lane, uint16_t* scale) {
-  const float x[4] = {v.x, v.y, v.z, v.w};
+// Quantise the eight values of this lane with the block's four lanes: the codes, eight to a word, and the scale's bits.
+// Code of x for the scale s (finite, not 0): the nearest integer to x / s, ties to even, plus 8, in [0, 15].  n, the
+// rounded product with the reciprocal, is at most one off, and only where the product lies next to a half (its own error
+// is under 2^-20); there the remainder x - s n, which is exact (s has 11 bits, n four), is compared with s / 2.
+__device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], int lane, uint16_t* scale) {
   // largest magnitude by the bits of |x|, which order like the values and put NaN above infinity
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
   const uint32_t mine = top;
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  float m = x[7];
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float m = x[3];
-#pragma unroll
-  for (int i = 2; i >= 0; --i)
+  for (int i = 6; i >= 0; --i)
     if ((__float_as_uint(x[i]) & 0x7fffffffu) == mine) m = x[i];  // the lowest index with this lane's largest
-  const uint32_t has = __ballot_sync(0xffffffffu, mine == top) & (0xffu << (lane & 24));
+  const uint32_t has = __ballot_sync(0xffffffffu, mine == top) & (0xfu << (lane & 28));
   m = __shfl_sync(0xffffffffu, m, __ffs(has) - 1);
   const __half s16 = __float2half_rn(m * -0.125f);
   const float s = __half2float(s16);
-  if (!(fabsf(s) <= 65504.f)) {
-    *scale = 0x7fffu;  // NaN
-    return 0x8888u;
+  const bool bad = !(fabsf(s) <= 65504.f), flat = bad || s == 0.f;
+  *scale = bad ? 0x7fffu : __half_as_ushort(s16);
+  const float inv = flat ? 0.f : 1.f / s;
+  float n[8];
+  bool close = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = flat ? 0.f : x[i] * inv;
+    n[i] = rintf(y);
+    close |= fabsf(y - n[i]) > 0.4999f;
   }
-  *scale = __half_as_ushort(s16);
-  if (s == 0.f) return 0x8888u;
-  const float inv = 1.f / s;
+  if (close && !flat) {
+    const float h = 0.5f * fabsf(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = fmaf(-n[i], s, x[i]);
+      const bool odd = ((int)n[i]) & 1;
+      if (fabsf(r) > h || (fabsf(r) == h && odd)) n[i] += (r > 0.f) == (s > 0.f) ? 1.f : -1.f;
+    }
+  }
   uint32_t c = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c |= (uint32_t)kv4_code(x[i], s, inv) << (4 * i);
+  for (int i = 0; i < 8; ++i) c |= (uint32_t)min(max((int)n[i] + 8, 0), 15) << (4 * i);
   return c;
 }
 
 constexpr int kRowsThreads = 256;
 
+// Where a warp's token lies: its tile of KV head 0 and its position there; the tiles of a page's next KV head are
+// `stride` bytes on.  Null for a slot outside the cache.
+template <int D>
+__device__ __forceinline__ uint8_t* kv4_place(const Kv4Cache& c, int slot, int* p, long long* stride) {
+  *p = slot & (kKv4Tile - 1);
+  *stride = (long long)(c.page_len / kKv4Tile) * kv4_tile_bytes(D);
+  if (slot < 0 || slot >= c.n_pages * c.page_len) return nullptr;
+  const int page = slot / c.page_len, in = slot - page * c.page_len;
+  return c.data + (long long)page * c.n_kv_heads * *stride + (in / kKv4Tile) * kv4_tile_bytes(D);
+}
+
 template <int D, typename T>
-__global__ void __launch_bounds__(kRowsThreads) kv4_append_kernel(const Kv4RowsArgs a) {
-  constexpr int NB = D / 32, LPR = D / 4;  // lanes per row
+__global__ void __launch_bounds__(kRowsThreads) kv4_append_kernel(const Kv4RowsArgs a, int passes) {
+  constexpr int NB = D / 32, LPR = D / 8, RPP = 32 / LPR;  // lanes per row, rows per pass
   const int lane = threadIdx.x & 31;
-  const int heads = a.c.n_kv_heads;
-  const long long cap = a.c.n_pages * a.c.page_len;
-  const long long rows = (long long)a.n_tok * heads;
-  const long long step = (long long)gridDim.x * (kRowsThreads / LPR);
-  // whole warps go round together: the quantiser shuffles
-  const long long first = ((long long)blockIdx.x * kRowsThreads + (threadIdx.x & ~31)) / LPR;
-  for (long long base = first; base < rows; base += step) {
-    const long long row = base + lane / LPR;
-    const int t = (int)(row / heads), h = (int)(row % heads);
-    const int slot = row < rows ? a.slot[t] : -1;
-    const bool live = slot >= 0 && slot < cap;
-    const int dim = 4 * (lane % LPR), block = dim / 32, l = lane & 7;
-    uint8_t* tile = live ? kv4_tile<D>(a.c, slot, h) : nullptr;
-    const int p = live ? slot % kKv4Tile : 0;
+  const long long t = (long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.n_tok) return;
+  int p;
+  long long stride;
+  uint8_t* tile = kv4_place<D>(a.c, a.slot[t], &p, &stride);
+  if (!tile) return;
+  const int l8 = lane % LPR, block = l8 >> 2, tig = l8 & 3;
+  const int first = blockIdx.y * passes * RPP + lane / LPR;
+  const long long at = t * a.row_stride + 8 * l8;
+  for (int i = 0; i < passes; i += 2) {
+    float x[2][2][8];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const T* in = reinterpret_cast<const T*>(side ? a.v_in : a.k_in) + (long long)t * a.row_stride + h * D + dim;
-      const float4 x = live ? Row4<T>::load(in) : make_float4(0.f, 0.f, 0.f, 0.f);
-      uint16_t scale;
-      const uint32_t c = kv4_quantise(x, lane, &scale);
-      if (live) {
-        uint8_t* part = tile + side * kv4_half(D);
-        const int off = side ? kv4_v_off<D>(p, block, l) : kv4_k_off<D>(p, block, l);
-        *reinterpret_cast<uint16_t*>(part + off) = (uint16_t)c;
-        if (l == 0) *reinterpret_cast<uint16_t*>(part + kv4_codes(D) + (p * NB + block) * 2) = scale;
+    for (int j = 0; j < 2; ++j) {
+      const int h = first + (i + j) * RPP;
+      const bool live = i + j < passes && h < a.c.n_kv_heads;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const T* in = reinterpret_cast<const T*>(side ? a.v_in : a.k_in) + at + (long long)h * D;
+        if (live) {
+          Row8<T>::load(in, x[j][side]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[j][side][k] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (i + j >= passes) break;  // the same for the whole warp
+      const int h = first + (i + j) * RPP;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        uint16_t scale;
+        const uint32_t c = kv4_quantise(x[j][side], lane, &scale);
+        if (h < a.c.n_kv_heads) {
+          uint8_t* part = tile + h * stride + side * kv4_half(D);
+          if (side == 0) {
+            *reinterpret_cast<uint32_t*>(part + kv4_k_off<D>(p, block, 2 * tig)) = c;
+          } else {
+            *reinterpret_cast<uint16_t*>(part + kv4_v_off<D>(p, block, 2 * tig)) = (uint16_t)c;
+            *reinterpret_cast<uint16_t*>(part + kv4_v_off<D>(p, block, 2 * tig + 1)) = (uint16_t)(c >> 16);
+          }
+          if (tig == 0) *reinterpret_cast<uint16_t*>(part + kv4_codes(D) + (p * NB + block) * 2) = scale;
+        }
       }
     }
   }
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsArgs a) {
-  constexpr int NB = D / 32, LPR = D / 4;
-  const int heads = a.c.n_kv_heads;
-  const long long cap = a.c.n_pages * a.c.page_len;
-  const long long n = (long long)a.n_tok * heads * LPR;
-  for (long long i = (long long)blockIdx.x * kRowsThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kRowsThreads) {
-    const int dim = 4 * (int)(i % LPR), block = dim / 32, l = (dim / 4) & 7;
-    const long long row = i / LPR;
-    const int t = (int)(row / heads), h = (int)(row % heads);
-    const int slot = a.slot[t];
-    if (slot < 0 || slot >= cap) continue;
-    const uint8_t* tile = kv4_tile<D>(a.c, slot, h);
-    const int p = slot % kKv4Tile;
+__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsArgs a, int passes) {
+  constexpr int NB = D / 32, LPR = D / 8, RPP = 32 / LPR;
+  const int lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.n_tok) return;
+  int p;
+  long long stride;
+  const uint8_t* tile = kv4_place<D>(a.c, a.slot[t], &p, &stride);
+  if (!tile) return;
+  const int l8 = lane % LPR, block = l8 >> 2, tig = l8 & 3;
+  const int first = blockIdx.y * passes * RPP + lane / LPR;
+  const long long at = t * a.row_stride + 8 * l8;
+  for (int i = 0; i < passes; i += 4) {
+    uint32_t c[4][2];
+    uint16_t s[4][2];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const uint8_t* part = tile + side * kv4_half(D);
-      const int off = side ? kv4_v_off<D>(p, block, l) : kv4_k_off<D>(p, block, l);
-      const int c = *reinterpret_cast<const uint16_t*>(part + off);
-      const float s = h2f_bits(*reinterpret_cast<const uint16_t*>(part + kv4_codes(D) + (p * NB + block) * 2));
-      float4 x;
-      x.x = s * (float)((c & 15) - 8);
-      x.y = s * (float)((c >> 4 & 15) - 8);
-      x.z = s * (float)((c >> 8 & 15) - 8);
-      x.w = s * (float)((c >> 12 & 15) - 8);
-      Row4<T>::store(reinterpret_cast<T*>(side ? a.v_out : a.k_out) + (long long)t * a.row_stride + h * D + dim, x);
+    for (int j = 0; j < 4; ++j) {
+      const int h = first + (i + j) * RPP;
+      if (i + j < passes && h < a.c.n_kv_heads) {
+        const uint8_t* part = tile + h * stride;
+        c[j][0] = *reinterpret_cast<const uint32_t*>(part + kv4_k_off<D>(p, block, 2 * tig));
+        s[j][0] = *reinterpret_cast<const uint16_t*>(part + kv4_codes(D) + (p * NB + block) * 2);
+        part += kv4_half(D);
+        c[j][1] = *reinterpret_cast<const uint16_t*>(part + kv4_v_off<D>(p, block, 2 * tig)) |
+                  (uint32_t)*reinterpret_cast<const uint16_t*>(part + kv4_v_off<D>(p, block, 2 * tig + 1)) << 16;
+        s[j][1] = *reinterpret_cast<const uint16_t*>(part + kv4_codes(D) + (p * NB + block) * 2);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int h = first + (i + j) * RPP;
+      if (i + j < passes && h < a.c.n_kv_heads) {
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const float sc = h2f_bits(s[j][side]);
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = sc * (float)((int)(c[j][side] >> (4 * k) & 15) - 8);
+          Row8<T>::store(reinterpret_cast<T*>(side ? a.v_out : a.k_out) + at + (long long)h * D, x);
+        }
+      }
     }
   }
 }
 
-static int rows_grid(const Kv4RowsArgs& a, int head_dim) {
-  const long long work = (long long)a.n_tok * a.c.n_kv_heads * (head_dim / 4);
-  const long long ctas = (work + kRowsThreads - 1) / kRowsThreads;
-  return (int)(ctas < (1 << 20) ? ctas : (1 << 20));
+// Passes per warp, and the grid: a warp goes through all heads of its token from 4096 tokens on; below, one pass each.
+static int rows_passes(const Kv4RowsArgs& a, int head_dim, dim3* grid) {
+  const int per = 256 / head_dim, all = (a.c.n_kv_heads + per - 1) / per;
+  const int passes = a.n_tok >= 4096 ? all : 1;
+  *grid = dim3((unsigned)((a.n_tok + kRowsThreads / 32 - 1) / (kRowsThreads / 32)), (unsigned)((all + passes - 1) / passes));
+  return passes;
 }
 
 cudaError_t launch_kv4_append(const Kv4RowsArgs& a, int head_dim, int dtype, cudaStream_t st) {
-  const int grid = rows_grid(a, head_dim);
+  dim3 grid;
+  const int passes = rows_passes(a, head_dim, &grid);
   if (head_dim == 128) {
-    if (dtype == KV4_F32) kv4_append_kernel<128, float><<<grid, kRowsThreads, 0, st>>>(a);
-    else if (dtype == KV4_F16) kv4_append_kernel<128, __half><<<grid, kRowsThreads, 0, st>>>(a);
-    else kv4_append_kernel<128, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a);
+    if (dtype == KV4_F32) kv4_append_kernel<128, float><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else if (dtype == KV4_F16) kv4_append_kernel<128, __half><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else kv4_append_kernel<128, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a, passes);
   } else {
-    if (dtype == KV4_F32) kv4_append_kernel<64, float><<<grid, kRowsThreads, 0, st>>>(a);
-    else if (dtype == KV4_F16) kv4_append_kernel<64, __half><<<grid, kRowsThreads, 0, st>>>(a);
-    else kv4_append_kernel<64, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a);
+    if (dtype == KV4_F32) kv4_append_kernel<64, float><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else if (dtype == KV4_F16) kv4_append_kernel<64, __half><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else kv4_append_kernel<64, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a, passes);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_read(const Kv4RowsArgs& a, int head_dim, int dtype, cudaStream_t st) {
-  const int grid = rows_grid(a, head_dim);
+  dim3 grid;
+  const int passes = rows_passes(a, head_dim, &grid);
   if (head_dim == 128) {
-    if (dtype == KV4_F32) kv4_read_kernel<128, float><<<grid, kRowsThreads, 0, st>>>(a);
-    else if (dtype == KV4_F16) kv4_read_kernel<128, __half><<<grid, kRowsThreads, 0, st>>>(a);
-    else kv4_read_kernel<128, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a);
+    if (dtype == KV4_F32) kv4_read_kernel<128, float><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else if (dtype == KV4_F16) kv4_read_kernel<128, __half><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else kv4_read_kernel<128, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a, passes);
   } else {
-    if (dtype == KV4_F32) kv4_read_kernel<64, float><<<grid, kRowsThreads, 0, st>>>(a);
-    else if (dtype == KV4_F16) kv4_read_kernel<64, __half><<<grid, kRowsThreads, 0, st>>>(a);
-    else kv4_read_kernel<64, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a);
+    if (dtype == KV4_F32) kv4_read_kernel<64, float><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else if (dtype == KV4_F16) kv4_read_kernel<64, __half><<<grid, kRowsThreads, 0, st>>>(a, passes);
+    else kv4_read_kernel<64, __nv_bfloat16><<<grid, kRowsThreads, 0, st>>>(a, passes);
   }
   return cudaGetLastError();
 }

@@ -33,13 +33,6 @@ struct Kv4Cache {
   int page_len = 0, n_kv_heads = 0;
 };
 
-// Address of the tile that holds `slot` of KV head h.
-template <int D>
-__device__ __forceinline__ uint8_t* kv4_tile(const Kv4Cache& c, int slot, int h) {
-  const int page = slot / c.page_len, in = slot - page * c.page_len;
-  return c.data + (((long long)page * c.n_kv_heads + h) * (c.page_len / kKv4Tile) + in / kKv4Tile) * kv4_tile_bytes(D);
-}
-
 enum Kv4Type { KV4_F32 = 0, KV4_F16 = 1, KV4_BF16 = 2 };
 
 struct Kv4PlanArgs {
