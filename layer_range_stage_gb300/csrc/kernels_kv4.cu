@@ -245,9 +245,18 @@ struct Row8<float> {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  // Neighbouring lanes swap halves, so that each of the two stores fills whole 32-byte sectors (`live` is the same in both).
+  static __device__ __forceinline__ void store(float* p, const float (&v)[8], bool live) {
+    const bool odd = threadIdx.x & 1;
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[4 + i], 1);
+    if (live) {
+      const float4 own = odd ? make_float4(v[4], v[5], v[6], v[7]) : make_float4(v[0], v[1], v[2], v[3]);
+      const float4 got = make_float4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<float4*>(odd ? p - 4 : p) = odd ? got : own;      // the even lane's dims
+      *reinterpret_cast<float4*>(odd ? p + 4 : p + 8) = odd ? own : got;  // the odd lane's
+    }
   }
 };
 template <>
@@ -261,14 +270,14 @@ struct Row8<__half> {
       v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
   }
-  static __device__ __forceinline__ void store(__half* p, const float (&v)[8]) {
+  static __device__ __forceinline__ void store(__half* p, const float (&v)[8], bool live) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (live) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <>
@@ -279,61 +288,90 @@ struct Row8<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8], bool live) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (live) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // Quantise the eight values of this lane with the block's four lanes: the codes, eight to a word, and the scale's bits.
-// Code of x for the scale s (finite, not 0): the nearest integer to x / s, ties to even, plus 8, in [0, 15].  n, the
-// rounded product with the reciprocal, is at most one off, and only where the product lies next to a half (its own error
-// is under 2^-20); there the remainder x - s n, which is exact (s has 11 bits, n four), is compared with s / 2.
+// Code of x for the scale s (finite, not 0): the nearest integer to x / s, ties to even, plus 8, in [0, 15].  Adding
+// 1.5 * 2^23 to the product with the reciprocal leaves the integer n in the sum's low bits.  The product is off by less
+// than 2^-18, so n is the nearest integer unless x / s lies next to a half; there the remainder x - s n, which is exact
+// (s has 11 bits, n four), is compared with s / 2.  The sums' bits, shifted four apart and added up, are the eight
+// codes and a constant.
 __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], int lane, uint16_t* scale) {
-  // largest magnitude by the bits of |x|, which order like the values and put NaN above infinity
-  uint32_t top = 0;
+  float high = x[0], low = x[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  const uint32_t mine = top;
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  float m = x[7];
+  for (int i = 1; i < 8; ++i) {
+    high = max_nan(high, x[i]);
+    low = min_nan(low, x[i]);
+  }
 #pragma unroll
-  for (int i = 6; i >= 0; --i)
-    if ((__float_as_uint(x[i]) & 0x7fffffffu) == mine) m = x[i];  // the lowest index with this lane's largest
-  const uint32_t has = __ballot_sync(0xffffffffu, mine == top) & (0xfu << (lane & 28));
-  m = __shfl_sync(0xffffffffu, m, __ffs(has) - 1);
+  for (int o = 1; o < 4; o <<= 1) {
+    high = max_nan(high, __shfl_xor_sync(0xffffffffu, high, o));
+    low = min_nan(low, __shfl_xor_sync(0xffffffffu, low, o));
+  }
+  float m = high > -low ? high : low;  // NaN stays
+  if (__any_sync(0xffffffffu, high == -low && high > 0.f)) {  // both signs of the largest: the lowest index decides
+    const float top = fmaxf(high, -low);
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+      if (fabsf(x[i]) == top) mine = x[i];
+    const uint32_t has = __ballot_sync(0xffffffffu, mine != 0.f) & (0xfu << (lane & 28));
+    const float first = __shfl_sync(0xffffffffu, mine, has ? __ffs(has) - 1 : lane);
+    if (high == -low) m = first;
+  }
   const __half s16 = __float2half_rn(m * -0.125f);
-  const float s = __half2float(s16);
-  const bool bad = !(fabsf(s) <= 65504.f), flat = bad || s == 0.f;
+  float s = __half2float(s16);
+  const bool bad = !(fabsf(s) <= 65504.f);
   *scale = bad ? 0x7fffu : __half_as_ushort(s16);
-  const float inv = flat ? 0.f : 1.f / s;
-  float n[8];
-  bool close = false;
+  if (bad) s = 0.f;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  if (s == 0.f) inv = 0.f;
+  constexpr float kMagic = 12582912.f;
+  float t[8], far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = flat ? 0.f : x[i] * inv;
-    n[i] = rintf(y);
-    close |= fabsf(y - n[i]) > 0.4999f;
+    t[i] = fmaf(x[i], inv, kMagic);
+    far = fmaxf(far, fabsf(fmaf(kMagic - t[i], s, x[i])));
   }
-  if (close && !flat) {
-    const float h = 0.5f * fabsf(s);
+  const float h = 0.5f * fabsf(s);
+  if (far > 0.9998f * h && s != 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float r = fmaf(-n[i], s, x[i]);
-      const bool odd = ((int)n[i]) & 1;
-      if (fabsf(r) > h || (fabsf(r) == h && odd)) n[i] += (r > 0.f) == (s > 0.f) ? 1.f : -1.f;
+      const float n = t[i] - kMagic, r = fmaf(-n, s, x[i]);
+      const bool odd = __float_as_uint(t[i]) & 1;
+      if (fabsf(r) > h || (fabsf(r) == h && odd)) t[i] += (r > 0.f) == (s > 0.f) ? 1.f : -1.f;
     }
   }
   uint32_t c = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c |= (uint32_t)min(max((int)n[i] + 8, 0), 15) << (4 * i);
-  return c;
+  for (int i = 7; i >= 0; --i) {
+    // NaN and infinities were taken care of by the scale: their product with inv = 0 counts as 0
+    const float v = s == 0.f ? kMagic : fminf(fmaxf(t[i], kMagic - 8.f), kMagic + 7.f);
+    c = c * 16u + __float_as_uint(v);
+  }
+  constexpr uint32_t kOnes = 0x11111111u;
+  return c - (0x4B400000u - 8u) * kOnes;
 }
 
 constexpr int kRowsThreads = 256;
@@ -416,8 +454,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsArg
   const int first = blockIdx.y * passes * RPP + lane / LPR;
   const long long at = t * a.row_stride + 8 * l8;
   for (int i = 0; i < passes; i += 4) {
-    uint32_t c[4][2];
-    uint16_t s[4][2];
+    uint32_t c[4][2] = {};
+    uint16_t s[4][2] = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int h = first + (i + j) * RPP;
@@ -433,16 +471,15 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsArg
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (i + j >= passes) break;  // the same for the whole warp
       const int h = first + (i + j) * RPP;
-      if (i + j < passes && h < a.c.n_kv_heads) {
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const float sc = h2f_bits(s[j][side]);
-          float x[8];
+      for (int side = 0; side < 2; ++side) {
+        const float sc = h2f_bits(s[j][side]);
+        float x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = sc * (float)((int)(c[j][side] >> (4 * k) & 15) - 8);
-          Row8<T>::store(reinterpret_cast<T*>(side ? a.v_out : a.k_out) + at + (long long)h * D, x);
-        }
+        for (int k = 0; k < 8; ++k) x[k] = sc * (float)((int)(c[j][side] >> (4 * k) & 15) - 8);
+        Row8<T>::store(reinterpret_cast<T*>(side ? a.v_out : a.k_out) + at + (long long)h * D, x, h < a.c.n_kv_heads);
       }
     }
   }
