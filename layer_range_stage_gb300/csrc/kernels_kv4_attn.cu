@@ -11,7 +11,8 @@
 //
 // Split of the work.  Rows (sequence, KV head, block of columns) times units of 128 positions form one line
 // of units in memory order, cut into equal pieces, one per resident CTA: ragged batches load every SM
-// alike, whatever the lengths, which only the device knows.  A row cut by piece borders is merged by the last
+// alike, whatever the lengths, which only the device knows.  A row has kRowCost empty units more, at its front, for what
+// a row costs by itself (its q, the merge of the warps, its output).  A row cut by piece borders is merged by the last
 // of its CTAs to arrive, in the order of the positions.
 
 #include <atomic>
@@ -30,6 +31,7 @@ constexpr int kUnitTiles = kWarps;  // a unit: one tile of 16 positions per warp
 constexpr int kStages = 4;          // tiles in flight per warp, less one
 constexpr int kFlush = 16;          // tiles between two flushes of the accumulators
 constexpr int kMaxCtas = 512;
+constexpr int kRowCost = 4;  // 64 ragged sequences (64/8 heads): 91 us with 0, 74 with 2, 68 with 3, 69 with 5
 constexpr int kSlack = 4;           // r is raised when a score passes it by 2^kSlack
 constexpr float kTop = 11.f;
 
@@ -45,6 +47,15 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
   return (uint32_t)__half_as_ushort(lo) | (uint32_t)__half_as_ushort(hi) << 16;
+}
+
+// Units of a row of this many positions, the empty ones among them.
+__device__ __forceinline__ int row_units(int len) {
+  return kRowCost + max(1, (len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+}
+// Quotients of counts, which rarely need 64 bits.
+__device__ __forceinline__ long long quotient(long long x, int y) {
+  return x >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
 }
 
 // A segment: units [begin, end) of the row (sequence, KV head, block of columns) that has [unit, unit + units).
@@ -92,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     for (int s = s0; s < s1; ++s) {
       int start;
       const int c = min(seq_tokens(a, s, &start), a.max_q);
-      const int units = max(1, (seq_positions(a, s) + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+      const int units = row_units(seq_positions(a, s));
       mine += (long long)((c * (long long)group + NC - 1) / NC) * a.c.n_kv_heads * units;
     }
     long long incl = mine;
@@ -124,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       for (int s = s0; s < s1; ++s) {
         int start;
         const int c = min(seq_tokens(a, s, &start), a.max_q);
-        const int units = max(1, (seq_positions(a, s) + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+        const int units = row_units(seq_positions(a, s));
         const long long n = (long long)((c * (long long)group + NC - 1) / NC) * a.c.n_kv_heads * units;
         if (u < at + n) {
           sm.first_seq = s;
@@ -151,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
   while (true) {
     AttnRow row = {};
     int n_it = 0, t_begin = 0, lim_lo = 0;
-    const bool more = u < u_end;
+    bool more = u < u_end;
     uint32_t present = 0;            // bit i % 32: tile i is there
     int page_ids = -1, in_page = 0;  // of tile number 32 * batch + lane
     const int* trow = nullptr;
@@ -185,21 +196,27 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         row.count = seq_tokens(a, seq, &row.start);
         row.len = seq_positions(a, seq);
         row.ncols = min(row.count, a.max_q) * group;
-        row.units = max(1, (row.len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
+        row.units = row_units(row.len);
         const int cblocks = (row.ncols + NC - 1) / NC;
         const long long all = (long long)cblocks * a.c.n_kv_heads * row.units;
         if (u < seq_unit + all) {
-          const long long r = (u - seq_unit) / row.units;
+          const long long r = quotient(u - seq_unit, row.units);
           row.unit = seq_unit + r * row.units;
-          row.head = (int)(r / cblocks);
-          row.cbase = (int)(r % cblocks) * NC;
+          row.head = (int)quotient(r, cblocks);
+          row.cbase = (int)(r - (long long)row.head * cblocks) * NC;
           break;
         }
         seq_unit += all;  // the next sequence (those without a token have no unit)
         ++seq;
       }
-      row.begin = u;
+      // from here on the row's own units alone
+      row.unit += kRowCost;
+      row.units -= kRowCost;
+      row.begin = max(u, row.unit);
       row.end = min(u_end, row.unit + row.units);
+      more = row.begin < row.end;  // the piece may end among the empty ones
+    }
+    if (more) {
       u = row.end;
       t_begin = (int)(row.begin - row.unit) * kUnitTiles;
       const int k_hi = min(row.ncols - 1, row.cbase + NC - 1) / group, k_lo = row.cbase / group;
@@ -211,6 +228,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       trow = a.table + (long long)seq * a.table_stride;
 #pragma unroll
       for (int i = 0; i < kStages - 1; ++i) issue(i);
+      // the segment's q into L1 (a line per lane), while the last segment's results are put down
+      const int col = row.cbase + (lane >> 2), esize = dtype == KV4_F32 ? 4 : 2;
+      if ((lane >> 2) < NC && col < row.ncols && (lane & 3) * 128 < D * esize) {
+        const long long at = (long long)(row.start + col / group) * a.q_stride + (row.head * group + col % group) * D;
+        uint32_t unused;
+        asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(unused) : "l"((const char*)a.q + at * esize + (lane & 3) * 128));
+      }
     }
     if (pending) {
       // ---- the warp's result
@@ -256,32 +280,27 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         const long long at = (long long)(done.start + c / group) * a.out_stride + (done.head * group + c % group) * D + entry_dim(e);
         store_elem(a.out, dtype, at, s != 0.f ? v / s : 0.f);
       };
-      for (int e = tid; e < 8 * D; e += kThreads) {
-        const int c = entry_col(e);
-        float top = -INFINITY;
+      {
+        static_assert(kThreads % 256 == 0, "all entries of a thread have one column");
+        const int c = entry_col(tid);
+        float top = -INFINITY, s = 0.f, k[kWarps];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.ref[w][c]);
-        float v = 0.f, s = 0.f;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, k[w] = sm.ref[w][c]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float r_w = sm.ref[w][c];
-          const float k = r_w == top ? 1.f : exp2_approx(r_w - top);
-          if (r_w != -INFINITY) {
-            v = fmaf(sm.acc[w][e], k, v);
-            s = fmaf(sm.sum[w][c], k, s);
-          } else {
-            v += sm.acc[w][e] != 0.f ? sm.acc[w][e] : 0.f;  // NaN stays NaN
-            s += sm.sum[w][c];
-          }
+          k[w] = k[w] == top ? 1.f : exp2_approx(k[w] - top);  // 0 for a warp without a position; NaN sums stay NaN
+          s = fmaf(sm.sum[w][c], k[w], s);
         }
-        if (split) {
-          __stcg(slot + e, v);
-          if (e < 64 && (e >> 2 & 7) == 0) {  // registers 0 and 1 of lanes 0-3: one entry for every column
-            __stcg(slot + 8 * D + c, top);
-            __stcg(slot + 8 * D + 8 + c, s);
-          }
-        } else {
-          put(e, v, s);
+        for (int e = tid; e < 8 * D; e += kThreads) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) v = fmaf(sm.acc[w][e], k[w], v);
+          if (split) __stcg(slot + e, v);
+          else put(e, v, s);
+        }
+        if (split && tid < 64 && (tid >> 2 & 7) == 0) {  // registers 0 and 1 of lanes 0-3: one thread for every column
+          __stcg(slot + 8 * D + c, top);
+          __stcg(slot + 8 * D + 8 + c, s);
         }
       }
       if (split) {
