@@ -45,10 +45,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
-  return (uint32_t)__half_as_ushort(lo) | (uint32_t)__half_as_ushort(hi) << 16;
-}
-
 // Units of a row of this many positions, the empty ones among them.
 __device__ __forceinline__ int row_units(int len) {
   return kRowCost + max(1, (len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
@@ -74,23 +70,23 @@ struct __align__(16) AttnSmem {
   long long wsum[kWarps];
   long long first_unit;         // of the sequence that holds this CTA's first unit
   long long piece, longer;      // piece c of the line begins at unit c * piece + min(c, longer)
-  int ncta;
   AttnRow seg;                  // the segment in work
   int first_seq;
-  int last;
+  int last, part0, parts;
 };
 
 // Columns: NC = 8 has eight (token, head of the group) pairs, their high parts in rows 0-7 and their low parts in
 // rows 8-15 of the score product, and two products for V.  NC = 4 has four: rows 4-7 repeat rows 0-3, and the
 // columns 4-7 of the V product carry the low parts, so one product does.
 template <int D, int NC>
-__global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs a, int dtype, unsigned* counters, float* slots) {
+__global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs a, int dtype, unsigned* counters, float* slots, const Quotient by_group,
+                    const Quotient by_page) {
   constexpr int NB = D / 32, MT = D / 16;  // blocks of a row, row tiles of the V product
   constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
   extern __shared__ __align__(16) unsigned char smem_raw[];
   AttnSmem<D, NC>& sm = *reinterpret_cast<AttnSmem<D, NC>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
-  const int group = a.n_q_heads / a.c.n_kv_heads, tpp = a.c.page_len / kKv4Tile;
+  const int group = by_group.d, tpp = by_page.d;  // query heads per KV head, tiles per page
 
   // ---- this CTA's piece of the line of units
   const int cta = blockIdx.x;
@@ -126,7 +122,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     u = cta * piece + min((long long)cta, longer);
     u_end = u + piece + (cta < longer ? 1 : 0);
     if (tid == 0) {
-      sm.ncta = ncta;
       sm.piece = piece;
       sm.longer = longer;
     }
@@ -170,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       if (i < n_it) {
         if ((i & 31) == 0) {
           const int t = t_begin + warp + (i + lane) * kWarps;
-          const int pg = t / tpp;
+          const int pg = by_page(t);
           in_page = t - pg * tpp;
           page_ids = i + lane < n_it ? trow[pg] : -1;
           if (page_ids < 0 || page_ids >= a.c.n_pages) page_ids = -1;
@@ -219,22 +214,23 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     if (more) {
       u = row.end;
       t_begin = (int)(row.begin - row.unit) * kUnitTiles;
-      const int k_hi = min(row.ncols - 1, row.cbase + NC - 1) / group, k_lo = row.cbase / group;
+      const int k_hi = by_group(min(row.ncols - 1, row.cbase + NC - 1)), k_lo = by_group(row.cbase);
       const int lim_hi = max(0, row.len - row.count + k_hi + 1);  // positions that some column sees
       lim_lo = max(0, row.len - row.count + k_lo + 1);            // positions that every column sees
       const int t_end = min((int)(row.end - row.unit) * kUnitTiles, (lim_hi + kKv4Tile - 1) / kKv4Tile);
       // the warp's tiles: t_begin + warp, + kWarps, ...
       n_it = max(0, (t_end - t_begin - warp + kWarps - 1) / kWarps);
       trow = a.table + (long long)seq * a.table_stride;
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(i);
-      // the segment's q into L1 (a line per lane), while the last segment's results are put down
+      // the segment's q into L1 (a line per lane), while its pages are looked up and the last segment's results put down
       const int col = row.cbase + (lane >> 2), esize = dtype == KV4_F32 ? 4 : 2;
       if ((lane >> 2) < NC && col < row.ncols && (lane & 3) * 128 < D * esize) {
-        const long long at = (long long)(row.start + col / group) * a.q_stride + (row.head * group + col % group) * D;
+        const int k = by_group(col);
+        const long long at = (long long)(row.start + k) * a.q_stride + (row.head * group + col - k * group) * D;
         uint32_t unused;
         asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(unused) : "l"((const char*)a.q + at * esize + (lane & 3) * 128));
       }
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(i);
     }
     if (pending) {
       // ---- the warp's result
@@ -262,23 +258,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       __syncthreads();
 
       const AttnRow& done = sm.seg;
-      const int ncta = sm.ncta;
-      const long long piece = sm.piece, longer = sm.longer;
       // ---- the CTA's result: entry e = register * 32 + lane holds (dim, column)
       const bool split = done.begin > done.unit || done.end < done.unit + done.units;
       float* slot = nullptr;
       if (split) slot = slots + (size_t)(2 * cta + (done.begin == done.unit ? 1 : 0)) * slot_floats(D);
-      auto owner = [&](long long x) {  // of unit x
-        const long long cut = longer * (piece + 1);
-        return (int)(x < cut ? x / (piece + 1) : longer + (x - cut) / piece);
-      };
-      auto entry_dim = [&](int e) { return (e >> 8) * 32 + ((e & 31) >> 2) * 4 + ((e >> 7) & 1) * 2 + ((e >> 6) & 1); };
       auto entry_col = [&](int e) { return (e & 3) * 2 + ((e >> 5) & 1); };
-      auto put = [&](int e, float v, float s) {
-        const int c = done.cbase + entry_col(e);
-        if (entry_col(e) >= NC || c >= done.ncols) return;
-        const long long at = (long long)(done.start + c / group) * a.out_stride + (done.head * group + c % group) * D + entry_dim(e);
-        store_elem(a.out, dtype, at, s != 0.f ? v / s : 0.f);
+      // Output of column c (of the block): its row, and a value at entry e.
+      auto out_row = [&](int c) {
+        const int at = done.cbase + c, k = by_group(at);
+        return (long long)(done.start + k) * a.out_stride + (done.head * group + at - k * group) * D;
+      };
+      auto put = [&](long long row_at, int e, float v) {
+        store_elem(a.out, dtype, row_at + (e >> 8) * 32 + ((e & 31) >> 2) * 4 + ((e >> 7) & 1) * 2 + ((e >> 6) & 1), v);
       };
       {
         static_assert(kThreads % 256 == 0, "all entries of a thread have one column");
@@ -291,12 +282,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           k[w] = k[w] == top ? 1.f : exp2_approx(k[w] - top);  // 0 for a warp without a position; NaN sums stay NaN
           s = fmaf(sm.sum[w][c], k[w], s);
         }
+        const bool real = !split && c < NC && done.cbase + c < done.ncols;
+        const long long row_at = real ? out_row(c) : 0;
+        const float inv = s != 0.f ? 1.f / s : 0.f;
         for (int e = tid; e < 8 * D; e += kThreads) {
           float v = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) v = fmaf(sm.acc[w][e], k[w], v);
           if (split) __stcg(slot + e, v);
-          else put(e, v, s);
+          else if (real) put(row_at, e, s != 0.f ? v * inv : 0.f);
         }
         if (split && tid < 64 && (tid >> 2 & 7) == 0) {  // registers 0 and 1 of lanes 0-3: one thread for every column
           __stcg(slot + 8 * D + c, top);
@@ -305,14 +299,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
       }
       if (split) {
         __syncthreads();
-        const int c0 = owner(done.unit), c1 = owner(done.unit + done.units - 1), parts = c1 - c0 + 1;
         if (tid == 0) {
+          const long long piece = sm.piece, cut = sm.longer * (piece + 1);
+          auto owner = [&](long long x) {  // of unit x
+            return (int)(x < cut ? x / (piece + 1) : sm.longer + (x - cut) / piece);
+          };
+          const int c0 = owner(done.unit), parts = owner(done.unit + done.units - 1) - c0 + 1;
           const unsigned old = atom_add_acq_rel(&counters[c0], 1u);
           sm.last = old == (unsigned)(parts - 1);
           if (sm.last) counters[c0] = 0;
+          sm.part0 = c0;
+          sm.parts = parts;
         }
         __syncthreads();
         if (sm.last) {
+          const int c0 = sm.part0, parts = sm.parts;
           // weights of the parts, then the sums in the order of the positions
           float* wt = &sm.acc[0][0];  // [part][8]: r, then the weight
           float* den = &sm.sum[0][0];
@@ -347,7 +348,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
               v[3] = fmaf(x.w, w[6 + b], v[3]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) put(4 * e4 + j, v[j], den[entry_col(4 * e4 + j)]);
+            for (int j = 0; j < 4; ++j) {
+              const int c = entry_col(4 * e4 + j);
+              if (c < NC && done.cbase + c < done.ncols) put(out_row(c), 4 * e4 + j, den[c] != 0.f ? v[j] / den[c] : 0.f);
+            }
           }
         }
       }
@@ -359,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
     // ---- the columns' q as the A operand: rows gid (high) and gid + 8 (low)
     const int col = row.cbase + (NC == 8 ? gid : gid & 3);
     const bool col_live = col < row.ncols;
-    const int col_k = col / group;
+    const int col_k = by_group(col);
     const int lim = col_live ? max(0, row.len - row.count + col_k + 1) : 0;
     uint32_t qa[2 * NB][4];
     float zscale;
     {
-      const long long base = col_live ? (long long)(row.start + col_k) * a.q_stride + (row.head * group + col % group) * D : 0;
+      const long long base = col_live ? (long long)(row.start + col_k) * a.q_stride + (row.head * group + col - col_k * group) * D : 0;
       float qv[NB][8], top = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -389,10 +393,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int o = 0; o < 2; ++o) {  // dims 2 s + o and 2 s + o + 4 of the lane's eight; odd ones face codes times 16
-            const float x0 = qv[b][2 * s + o] * up[o], x1 = qv[b][2 * s + o + 4] * up[o];
-            const __half h0 = __float2half_rn(x0), h1 = __float2half_rn(x1);
-            qa[2 * b + s][2 * o] = pack_h2(h0, h1);
-            qa[2 * b + s][2 * o + 1] = pack_h2(__float2half_rn(x0 - __half2float(h0)), __float2half_rn(x1 - __half2float(h1)));
+            const float2 x = mul2(make_float2(qv[b][2 * s + o], qv[b][2 * s + o + 4]), make_float2(up[o], up[o]));
+            const __half2 h = __floats2half2_rn(x.x, x.y);
+            const float2 l = fma2(__half22float2(h), make_float2(-1.f, -1.f), x);
+            const __half2 r = __floats2half2_rn(l.x, l.y);
+            qa[2 * b + s][2 * o] = *reinterpret_cast<const uint32_t*>(&h);
+            qa[2 * b + s][2 * o + 1] = *reinterpret_cast<const uint32_t*>(&r);
           }
     }
 
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           const float2 x = mul2(p[n], vs[n][b]);
           const __half2 h = __floats2half2_rn(x.x, x.y);
           const float2 f = __half22float2(h);
-          const float2 rest = add2(x, make_float2(-f.x, -f.y));
+          const float2 rest = fma2(f, make_float2(-1.f, -1.f), x);
           const __half2 l = __floats2half2_rn(rest.x, rest.y);
           hi[n] = *reinterpret_cast<const uint32_t*>(&h);
           lo[n] = *reinterpret_cast<const uint32_t*>(&l);
@@ -603,7 +609,8 @@ cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
                          ((len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
   const int grid = (int)min(min(most, 2ll * sm_count()), (long long)kMaxCtas);
   unsigned* counters = (unsigned*)a.ws;
-  kern<<<grid, kThreads, smem, st>>>(a, dtype, counters, (float*)((char*)a.ws + kCounterBytes));
+  kern<<<grid, kThreads, smem, st>>>(a, dtype, counters, (float*)((char*)a.ws + kCounterBytes), Quotient(group),
+                                     Quotient(a.c.page_len / kKv4Tile));
   return cudaGetLastError();
 }
 

@@ -6,6 +6,21 @@
 
 namespace lrs {
 
+// x / d for 0 <= x < 2^31, without a division on the device: with 2^(s - 1) < d <= 2^s and m = floor(2^(31 + s) / d) + 1,
+// x m / 2^(31 + s) exceeds x / d by less than 1 / d.
+struct Quotient {
+  int d = 1;
+  uint32_t m = 0, shift = 0;
+  explicit Quotient(int divisor) : d(divisor) {
+    if (d == 1) return;
+    int s = 1;
+    while ((1ll << s) < d) ++s;
+    m = (uint32_t)((1ull << (31 + s)) / (uint32_t)d + 1);
+    shift = (uint32_t)(s - 1);
+  }
+  __device__ __forceinline__ int operator()(int x) const { return d == 1 ? x : (int)(__umulhi((uint32_t)x, m) >> shift); }
+};
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
