@@ -12,9 +12,10 @@
 //   warp 16     issues the products: S = Q K^T and O = P V, with Q and P read from TMEM (an operand of 128 rows from shared
 //               memory would be read again by every product);
 //   warp 17     copies the packed tiles in (bulk copies, up to four tiles ahead).
-// In STAGE_F32 the sums in TMEM run over kGroup tiles and are then added to float32 registers, rounded to nearest (the
-// tensor cores' own additions truncate); the 16-bit types keep the whole sum in TMEM.  A row's change of reference, which
-// is rare, rescales its sums in TMEM.
+// The tensor cores' additions truncate: over a long sum the result shrinks (by 1e-4 of itself at 32768 positions).  So in
+// STAGE_F32 every tile's O is added to float32 registers, rounded to nearest, and the products with low parts come
+// first, where the sums they truncate are still small: 2e-6 of error became 5e-7.  The 16-bit types keep the whole sum
+// in TMEM; there a row's change of reference, which is rare, rescales its sums.
 //
 // Precision: a value s (c - 8) has 15 significant bits, so two fp16 numbers hold it exactly; q and the probabilities are
 // float32 and two fp16 numbers hold 22 bits.  STAGE_F32 multiplies high by high, low by high and high by low (three
@@ -45,7 +46,6 @@ constexpr int kRegsStart = 96, kRegsSoft = 136, kRegsProd = 72, kRegsRest = 64;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
 constexpr int kInfo = 16;  // ring of what the tiles' producers tell the softmax
-constexpr int kGroup = 4;  // tiles of a sum in TMEM (STAGE_F32)
 // The largest probability (times its power of V) lies at 2^top when the reference is set, and may grow by 2^slack before
 // it is set again: fp16 ends at 2^16.  With one fp16 value per probability fewer changes count more than the range below.
 template <int NP>
@@ -470,12 +470,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         const uint32_t d = tmem + kColS + s_st * kPosTile;
         if (leader) {
 #pragma unroll
-          for (int part = 0; part < NQ + NKV - 1; ++part)  // high high, [low high,] [high low]
+          for (int part = NQ + NKV - 2; part >= 0; --part)  // [high low,] [low high,] high high
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
               umma_f16_ts(d, tmem + kColQ + (NQ == 2 && part == 1 ? D / 2 : 0) + ks * 8,
                           kb + (((part > 0 && part == NQ ? L::k_part : 0) + (ks >> 2) * (kPosTile * 128) + (ks & 3) * 32) >> 4),
-                          id_s, part || ks ? 1u : 0u);
+                          id_s, part < NQ + NKV - 2 || ks ? 1u : 0u);
           umma_commit(&B.k_empty[s_st]);
           umma_commit(&B.s_full[s_st]);
           mbar_arrive(&B.s_full[s_st]);  // hands on what the producers wrote beside the tile
@@ -501,14 +501,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
           tc_fence_after();
           const uint64_t vb = vd + o_st * (uint32_t)(NKV * L::v_part >> 4);
           const uint32_t pc = tmem + kColP + o_st * 64;
-          const uint32_t again = (NP == 2 ? i % kGroup : i) ? 1u : 0u;
+          const uint32_t again = NP == 1 && i > 0 ? 1u : 0u;
           if (leader) {
 #pragma unroll
-            for (int part = 0; part < NP + NKV - 1; ++part)
+            for (int part = NP + NKV - 2; part >= 0; --part)
 #pragma unroll
               for (int ks = 0; ks < kPosTile / 16; ++ks)
                 umma_f16_ts(tmem + kColO, pc + (NP == 2 && part == 1 ? 32 : 0) + ks * 8,
-                            vb + (((part > 0 && part == NP ? L::v_part : 0) + ks * 32) >> 4), id_o, part || ks ? 1u : again);
+                            vb + (((part > 0 && part == NP ? L::v_part : 0) + ks * 32) >> 4), id_o,
+                            part < NP + NKV - 2 || ks ? 1u : again);
             umma_commit(&B.v_empty[o_st]);
             umma_commit(&B.o_full[o_st]);
             mbar_arrive(&B.o_full[o_st]);
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     }
 
     constexpr int NO = NP == 2 ? HD / 2 : 1;
-    float2 o[NO];  // STAGE_F32: the sums over the groups of tiles that are done
+    float2 o[NO];  // STAGE_F32: the sums over the tiles that are done
 #pragma unroll
     for (int j = 0; j < NO; ++j) o[j] = make_float2(0.f, 0.f);
     float ref = -INFINITY, sum = 0.f;
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
           if (M.first_bad[i & (kInfo - 1)][half * (HD / 32) + b] < lim) nan_blocks |= 1 << b;
       }
     };
-    // adds a group's sums to the registers
+    // adds a tile's sums to the registers
     auto collect = [&]() {
       if constexpr (NP == 2) {
 #pragma unroll
@@ -664,9 +665,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
         ref = most - kChunkTop<NP>;
         sum *= keep;
       }
-      const bool fresh = NP == 2 ? i % kGroup == 0 : i == 0;  // a new sum in TMEM begins
       const bool moved = __any_sync(0xffffffffu, keep != 1.f);
-      if (NP == 2 && fresh && i > 0) {  // the last group's sums leave TMEM before the first product of this one
+      if (NP == 2 && i > 0) {  // the last tile's sums leave TMEM before this one's products
         ok = products_done(ni - 1);
         if (ok) collect();
       }
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 #pragma unroll
         for (int j = 0; j < NO; ++j) o[j] = mul2(o[j], make_float2(keep, keep));
       }
-      if (moved && !fresh) {
+      if (NP == 1 && moved && i > 0) {
         ok = products_done(ni - 1);
         if (ok) {
           const uint32_t at = lanes + kColO + half * HD;
