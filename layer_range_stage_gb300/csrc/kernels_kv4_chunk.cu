@@ -57,7 +57,9 @@ constexpr int kRaw = 4;    // packed tiles in shared memory
 constexpr uint32_t kTmemCols = 512, kColQ = 0, kColS = 128, kColP = 256, kColO = 384;
 
 struct ChunkBars {
-  uint64_t q_full, raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, raw_full[kRaw], raw_empty[kRaw], k_full[3], k_empty[3], v_full[3], v_empty[3],
+      s_full[2], p_full[2], o_full[2], drain;
+  uint64_t pair_q[2], pair_s[2][2], pair_p[2][2], pair_o[2][2];  // of the kernel with two row tiles: [tile][buffer]
 };
 
 struct alignas(16) ChunkMisc {
@@ -76,11 +78,12 @@ struct alignas(16) ChunkMisc {
 
 static_assert(offsetof(ChunkMisc, v_pos_exp) % 16 == 0 && offsetof(ChunkMisc, v_pos_inv) % 16 == 0, "vector reads");
 
-template <int D, int NKV>
+// Shared memory: KS stages of K and of V operands behind QB bytes of q.
+template <int D, int NKV, int KS, int QB>
 struct ChunkLayout {
   static constexpr int k_part = kPosTile * D * 2, v_part = D * kPosTile * 2;
   static constexpr int sub_stride = kv4_tile_bytes(D) + 32, stage_bytes = kSub * sub_stride;
-  static constexpr int off_k = 0, off_v = off_k + 2 * NKV * k_part, off_raw = off_v + 2 * NKV * v_part;
+  static constexpr int off_k = QB, off_v = off_k + KS * NKV * k_part, off_raw = off_v + KS * NKV * v_part;
   static constexpr int off_misc = off_raw + kRaw * stage_bytes;
   static_assert(off_k % 1024 == 0 && off_v % 1024 == 0 && k_part % 1024 == 0 && v_part % 1024 == 0, "swizzled tiles");
   static_assert(off_raw % 16 == 0 && stage_bytes % 16 == 0 && sub_stride % 16 == 0 && off_misc % 16 == 0, "16-byte pieces");
@@ -107,6 +110,40 @@ struct ChunkItem {
   int lim_hi, nt;                  // positions that some row sees, tiles
 };
 
+// Items: row tiles from the last (which sees most) down, then KV heads, then sequences; a CTA has every gridDim.x-th.
+struct ChunkItems {
+  const Kv4AttnArgs& a;
+  int group, rows, row_tiles;
+  long long count;
+  ChunkItem it;
+  __device__ __forceinline__ ChunkItems(const Kv4AttnArgs& args, int rows_of_item) : a(args), rows(rows_of_item) {
+    group = a.n_q_heads / a.c.n_kv_heads;
+    row_tiles = (int)(((long long)a.max_q * group + rows - 1) / rows);
+    count = (long long)row_tiles * a.c.n_kv_heads * a.n_seqs;
+  }
+  // The next item from number w on; false behind the last.
+  __device__ __forceinline__ bool next(long long& w) {
+    const long long per = (long long)a.c.n_kv_heads * a.n_seqs;
+    for (; w < count; w += gridDim.x) {
+      const int row_tile = row_tiles - 1 - (int)(w / per), rest = (int)(w % per);
+      it.seq = rest / a.c.n_kv_heads;
+      it.head = rest % a.c.n_kv_heads;
+      it.row0 = row_tile * rows;
+      it.count = seq_tokens(a, it.seq, &it.start);
+      it.len = seq_positions(a, it.seq);
+      it.ncols = min(it.count, a.max_q) * group;
+      if (it.row0 >= it.ncols) continue;
+      it.lim_hi = seen(min(it.ncols, it.row0 + rows) - 1);
+      it.nt = (it.lim_hi + kPosTile - 1) / kPosTile;
+      w += gridDim.x;
+      return true;
+    }
+    return false;
+  }
+  // Positions that the item's sequence shows to row r.
+  __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.count + r / group + 1); }
+};
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -130,10 +167,311 @@ __device__ __forceinline__ __half2 code_high(uint32_t x, uint32_t ex) {
 // 2^-e as fp16, e in [-14, 16].
 __device__ __forceinline__ uint16_t half_power(int e) { return (uint16_t)(e <= 14 ? (15 - e) << 10 : 0x400 >> (e - 14)); }
 
+// ---------------- what both kernels have ----------------
+
+__device__ void chunk_init(ChunkMisc& M) {
+  ChunkBars& B = M.bar;
+  for (int i = 0; i < kRaw; ++i) {
+    mbar_init(&B.raw_full[i], 1);
+    mbar_init(&B.raw_empty[i], kProd);
+  }
+  for (int i = 0; i < 3; ++i) {
+    mbar_init(&B.k_full[i], kProd);
+    mbar_init(&B.v_full[i], kProd);
+    mbar_init(&B.k_empty[i], 1);
+    mbar_init(&B.v_empty[i], 1);
+  }
+  mbar_init(&B.q_full, 32 * kSoftWarps);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&B.s_full[i], 2);
+    mbar_init(&B.o_full[i], 2);
+    mbar_init(&B.p_full[i], 32 * kSoftWarps);
+    mbar_init(&B.pair_q[i], 16 * kSoftWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&B.pair_s[i][b], 2);
+      mbar_init(&B.pair_o[i][b], 2);
+      mbar_init(&B.pair_p[i][b], 16 * kSoftWarps);
+    }
+  }
+  mbar_init(&B.drain, 1);
+  M.abort = 0;
+  for (int i = 0; i < kInfo; ++i) {
+    M.bad[i] = 0;
+    for (int b = 0; b < 4; ++b) M.first_bad[i][b] = INT_MAX;
+  }
+  mbar_fence_init();
+}
+
+// Expansion, by two groups of four warps: group g has the tiles n with n % 2 = g, in KS stages of operands.
+template <int D, int NKV, int NP, int KS, typename L>
+__device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, ChunkItems& items) {
+  constexpr int NB = D / 32, HALF = kv4_half(D), CODES = kv4_codes(D);
+  ChunkBars& B = M.bar;
+  volatile int* abort_flag = &M.abort;
+  const ChunkItem& it = items.it;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group_of = (warp - kSoftWarps) >> 2, p = tid - 32 * (kSoftWarps + 4 * group_of), pw = p >> 5;
+  const uint32_t ex = exponent_bits();
+  bool ok = true;  // a warp in which a wait has run out leaves as a whole
+  int n = 0;
+  for (long long w = blockIdx.x; ok && items.next(w); n += it.nt)
+  for (int i = (n & 1) == group_of ? 0 : 1; i < it.nt; i += 2) {
+    const int ni = n + i, st = ni % KS, rs = ni & (kRaw - 1), inf = ni & (kInfo - 1), lim_hi = it.lim_hi;
+    ok = __all_sync(0xffffffffu, cwait(&B.raw_full[rs], (uint32_t)(ni / kRaw) & 1u, abort_flag));
+    if (!ok) break;
+    const int absent = M.absent[inf];
+    const unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
+    const bool ragged = absent || (i + 1) * kPosTile > lim_hi;  // some positions do not count: their scales read as 0
+
+    // the largest scales (every warp for itself)
+    int e_k, e_v;
+    bool v_bad = false;
+    {
+      const int s = lane >> 3, at = i * kPosTile + s * kKv4Tile + 2 * (lane & 7);
+      const bool ok0 = !(absent >> s & 1) && at < lim_hi, ok1 = !(absent >> s & 1) && at + 1 < lim_hi;
+      const unsigned char* base = raw + s * L::sub_stride + (lane & 7) * (4 * NB);
+      uint32_t top[2];
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const unsigned char* sc = base + (side ? HALF + CODES + 16 + ((lane & 4) << 2) : CODES);
+        uint32_t w[NB];
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sc);
+          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(sc);
+          w[0] = u.x, w[1] = u.y;
+        }
+        __half2 m = __floats2half2_rn(0.f, 0.f), first = m;  // first: of the first position alone
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t u = (b < NB / 2 ? ok0 : ok1) ? w[b] & 0x7fff7fffu : 0u;
+          if (side) v_bad |= (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
+          if (NP == 2 && side && b == NB / 2) {
+            first = m;
+            m = __floats2half2_rn(0.f, 0.f);
+          }
+          m = __hmax2(m, as_h2(u));  // NaN loses
+        }
+        top[side] = max(as_u32(m) >> 16, as_u32(m) & 0xffffu);
+        if (NP == 2 && side) {
+          const int e0 = (int)min(max(as_u32(first) >> 16, as_u32(first) & 0xffffu) >> 10, 30u) - 14;
+          const int e1 = (int)min(top[1] >> 10, 30u) - 14;
+          M.v_norm[warp - kSoftWarps][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
+          if (pw == 0) {
+            *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
+            *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
+                make_float2(__uint_as_float((uint32_t)(127 - e0) << 23), __uint_as_float((uint32_t)(127 - e1) << 23));
+          }
+        }
+      }
+      e_k = (int)min(__reduce_max_sync(0xffffffffu, top[0]) >> 10, 30u) - 14;
+      e_v = NP == 2 ? 0 : (int)min(__reduce_max_sync(0xffffffffu, top[1]) >> 10, 30u) - 14;
+      v_bad = __any_sync(0xffffffffu, v_bad);
+    }
+    const __half2 norm_k = __half2half2(__ushort_as_half(half_power(e_k)));
+    const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
+    if (NP == 2) __syncwarp();  // v_norm
+    // K: 64 positions x 4 x (the word of eight dims of every block)
+    if (ni >= KS) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)(ni / KS + 1) & 1u, abort_flag));
+    if (!ok) break;
+    if (p == 0) {
+      M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
+      M.v_exp[inf] = (float)e_v;
+      M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
+      M.bad[inf] = v_bad;
+      // For tile n + kRaw, which no warp has begun: its copy waits until every warp of the group has read tile n.  The
+      // entry's last tile, n + kRaw - kInfo, was read by the softmax before it handed on the probabilities of a tile whose
+      // products the scores of tile n - KS waited for; and those are done.
+      const int next = (inf + kRaw) & (kInfo - 1);
+      for (int b = 0; b < 4; ++b) M.first_bad[next][b] = INT_MAX;
+    }
+    unsigned char* kt = sm + L::off_k + st * NKV * L::k_part;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * (pw + 4 * j), s = pos >> 4;
+      const unsigned char* src = raw + s * L::sub_stride;
+      uint32_t w[NB], sc[NB / 2];
+      if constexpr (D == 128) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + (pos & 15) * (D / 2) + tig * 16);
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        const uint2 v = *reinterpret_cast<const uint2*>(src + CODES + (pos & 15) * (2 * NB));
+        sc[0] = v.x, sc[1] = v.y;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(src + (pos & 15) * (D / 2) + tig * 8);
+        w[0] = u.x, w[1] = u.y;
+        sc[0] = *reinterpret_cast<const uint32_t*>(src + CODES + (pos & 15) * (2 * NB));
+      }
+      if (ragged && ((absent >> s & 1) || i * kPosTile + pos >= lim_hi)) {
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) sc[b] = 0;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[b / 2], 0, b & 1 ? 0x3232 : 0x1010)), norm_k);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t x = t < 2 ? w[b] : w[b] >> 8;
+          const __half2 n = t & 1 ? code_high(x, ex) : code_low(x, ex);
+          const __half2 h = __hmul2(n, s2);
+          hi[t] = as_u32(h);
+          if (NKV == 2) lo[t] = as_u32(__hfma2(n, s2, __hneg2(h)));
+        }
+        unsigned char* at = kt + (b >> 1) * (kPosTile * 128) + sw128_offset(pos, 32 * (b & 1) + 8 * tig);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (NKV == 2) *reinterpret_cast<uint4*>(at + L::k_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(&B.k_full[st]);
+
+    // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of every block.  Eight lanes with the
+    // same dims and different chunks read 16 bytes each from places 16 bytes apart modulo 128 (hence the paddings
+    // of the raw tiles) and write a whole row of 64 positions
+    if (ni >= KS) ok = __all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)(ni / KS + 1) & 1u, abort_flag));
+    if (!ok) break;
+    {
+      unsigned char* vt = sm + L::off_v + st * NKV * L::v_part;
+      constexpr int VB = NKV == 1 ? NB : NB / 2;  // blocks at a time, for the registers
+      const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
+      const unsigned char* src = raw + s * L::sub_stride + HALF;
+      const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
+      const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB + 16);
+#pragma unroll 1
+      for (int b0 = 0; b0 < NB; b0 += VB) {
+      uint32_t hi[VB][2][4], lo[VB][2][4];
+#pragma unroll
+      for (int tig = 0; tig < 4; ++tig) {
+        constexpr int W = (VB + 1) / 2;  // words of a position's blocks
+        uint32_t w[2][W], sc[2][W];      // of the first and the second position
+        if constexpr (D == 128 && VB == 4) {
+          const uint4 u = *reinterpret_cast<const uint4*>(codes + tig * 16);
+          w[0][0] = u.x, w[0][1] = u.y, w[1][0] = u.z, w[1][1] = u.w;
+          const uint4 v = *reinterpret_cast<const uint4*>(scales + tig * 16);
+          sc[0][0] = v.x, sc[0][1] = v.y, sc[1][0] = v.z, sc[1][1] = v.w;
+        } else if constexpr (D == 128) {
+          w[0][0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + b0 * 2);
+          w[1][0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + 8 + b0 * 2);
+          sc[0][0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + b0 * 2);
+          sc[1][0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + 8 + b0 * 2);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(codes + tig * 8);
+          w[0][0] = u.x >> (16 * b0), w[1][0] = u.y >> (16 * b0);
+          const uint2 v = *reinterpret_cast<const uint2*>(scales + tig * 8);
+          sc[0][0] = v.x >> (16 * b0), sc[1][0] = v.y >> (16 * b0);
+        }
+        if (ragged || v_bad) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = i * kPosTile + chunk * 8 + 2 * tig + e;
+            const bool off = (absent >> s & 1) || at >= lim_hi;
+#pragma unroll
+            for (int b = 0; b < VB; ++b) {
+              const uint32_t mask = b & 1 ? 0xffff0000u : 0xffffu;
+              const bool bad = (sc[e][b / 2] & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
+              if (bad && !off) atomicMin(&M.first_bad[inf][b0 + b], at);
+              if (bad || off) sc[e][b / 2] &= ~mask;
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < VB; ++b) {
+          const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0][b / 2], sc[1][b / 2], b & 1 ? 0x7632 : 0x5410)),
+                                     NP == 2 ? as_h2(M.v_norm[warp - kSoftWarps][4 * chunk + tig]) : norm_v);
+          // byte dsel of the block's two bytes, of both positions
+          const uint32_t x = __byte_perm(w[0][b / 2], w[1][b / 2], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
+          const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
+          const __half2 h0 = __hmul2(n0, s2), h1 = __hmul2(n1, s2);
+          hi[b][0][tig] = as_u32(h0);
+          hi[b][1][tig] = as_u32(h1);
+          if (NKV == 2) {
+            lo[b][0][tig] = as_u32(__hfma2(n0, s2, __hneg2(h0)));
+            lo[b][1][tig] = as_u32(__hfma2(n1, s2, __hneg2(h1)));
+          }
+        }
+      }
+      if (b0 + VB == NB) mbar_arrive(&B.raw_empty[rs]);
+#pragma unroll
+      for (int b = 0; b < VB; ++b)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int dim = 32 * (b0 + b) + 4 * gid + 2 * dsel + k;
+          unsigned char* at = vt + sw128_offset(dim, 8 * chunk);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[b][k][0], hi[b][k][1], hi[b][k][2], hi[b][k][3]);
+          if (NKV == 2) *reinterpret_cast<uint4*>(at + L::v_part) = make_uint4(lo[b][k][0], lo[b][k][1], lo[b][k][2], lo[b][k][3]);
+        }
+      }
+    }
+    fence_async_smem();
+    mbar_arrive(&B.v_full[st]);
+  }
+}
+
+// Copies of the packed tiles, by one thread.
+template <int D, typename L>
+__device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, ChunkItems& items) {
+  constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
+  ChunkBars& B = M.bar;
+  volatile int* abort_flag = &M.abort;
+  const Kv4AttnArgs& a = items.a;
+  const ChunkItem& it = items.it;
+  const int tpp = a.c.page_len / kKv4Tile;
+  bool ok = true;
+  int n = 0;
+  for (long long w = blockIdx.x; ok && items.next(w);) {
+    const int n16 = (it.lim_hi + kKv4Tile - 1) / kKv4Tile;
+    const int* trow = a.table + (long long)it.seq * a.table_stride;
+    // the pages of a tile are asked for a tile ahead; places go on without a division
+    int ids[kSub], places[kSub], next_t = 0, next_page = 0, next_place = 0;
+    auto ask = [&]() {
+#pragma unroll
+      for (int s = 0; s < kSub; ++s) {
+        ids[s] = next_t < n16 ? trow[next_page] : -1;
+        places[s] = next_place;
+        ++next_t;
+        if (++next_place == tpp) {
+          next_place = 0;
+          ++next_page;
+        }
+      }
+    };
+    ask();
+    for (int i = 0; i < it.nt; ++i, ++n) {
+      const int rs = n & (kRaw - 1);
+      ok = n < kRaw || cwait(&B.raw_empty[rs], (uint32_t)(n / kRaw + 1) & 1u, abort_flag);
+      if (!ok) break;
+      unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
+      int absent = 0, here = 0;
+#pragma unroll
+      for (int s = 0; s < kSub; ++s) {
+        const bool there = ids[s] >= 0 && ids[s] < a.c.n_pages;
+        absent |= there ? 0 : 1 << s;
+        here += there;
+      }
+      M.absent[n & (kInfo - 1)] = absent;
+      mbar_arrive_expect_tx(&B.raw_full[rs], here * TILE);
+      // V's second half, and the second half of its scales, go 16 bytes on each: see their reads
+      constexpr int cut = HALF + CODES / 2, cut2 = HALF + CODES + kv4_scales(D) / 2;
+#pragma unroll
+      for (int s = 0; s < kSub; ++s)
+        if (!(absent >> s & 1)) {
+          const uint8_t* src = a.c.data + (((long long)ids[s] * a.c.n_kv_heads + it.head) * tpp + places[s]) * TILE;
+          unsigned char* dst = raw + s * L::sub_stride;
+          bulk_g2s(dst, src, cut, &B.raw_full[rs]);
+          bulk_g2s(dst + cut + 16, src + cut, cut2 - cut, &B.raw_full[rs]);
+          bulk_g2s(dst + cut2 + 32, src + cut2, TILE - cut2, &B.raw_full[rs]);
+        }
+      ask();
+    }
+  }
+  if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
+    for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
+}
+
 template <int D, int NQ, int NKV, int NP>
 __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a, int dtype) {
-  using L = ChunkLayout<D, NKV>;
-  constexpr int NB = D / 32, TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
+  using L = ChunkLayout<D, NKV, 2, 0>;
   constexpr int HD = D / 2;  // dims of a softmax thread
   extern __shared__ unsigned char chunk_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)chunk_raw + 1023) & ~(uintptr_t)1023);
@@ -142,54 +480,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  const int group = a.n_q_heads / a.c.n_kv_heads;
-  // Items: row tiles from the last (which sees most) down, then KV heads, then sequences.
-  const int tiles_max = (int)(((long long)a.max_q * group + kRowsTile - 1) / kRowsTile);
-  const long long n_items = (long long)tiles_max * a.c.n_kv_heads * a.n_seqs;
-  ChunkItem it;
-  auto next_item = [&](long long& w) {  // the CTA's next item from number w on; false behind the last
-    for (; w < n_items; w += gridDim.x) {
-      const int row_tile = tiles_max - 1 - (int)(w / ((long long)a.c.n_kv_heads * a.n_seqs));
-      const int rest = (int)(w % ((long long)a.c.n_kv_heads * a.n_seqs));
-      it.seq = rest / a.c.n_kv_heads;
-      it.head = rest % a.c.n_kv_heads;
-      it.row0 = row_tile * kRowsTile;
-      it.count = seq_tokens(a, it.seq, &it.start);
-      it.len = seq_positions(a, it.seq);
-      it.ncols = min(it.count, a.max_q) * group;
-      if (it.row0 >= it.ncols) continue;
-      const int k_last = min(it.ncols - 1, it.row0 + kRowsTile - 1) / group;
-      it.lim_hi = max(0, it.len - it.count + k_last + 1);
-      it.nt = (it.lim_hi + kPosTile - 1) / kPosTile;
-      w += gridDim.x;
-      return true;
-    }
-    return false;
-  };
+  ChunkItems items(a, kRowsTile);
+  const ChunkItem& it = items.it;
+  const int group = items.group;
 
-  if (tid == 0) {
-    for (int i = 0; i < kRaw; ++i) {
-      mbar_init(&B.raw_full[i], 1);
-      mbar_init(&B.raw_empty[i], kProd);
-    }
-    mbar_init(&B.q_full, 32 * kSoftWarps);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.k_full[i], kProd);
-      mbar_init(&B.v_full[i], kProd);
-      mbar_init(&B.k_empty[i], 1);
-      mbar_init(&B.v_empty[i], 1);
-      mbar_init(&B.s_full[i], 2);
-      mbar_init(&B.o_full[i], 2);
-      mbar_init(&B.p_full[i], 32 * kSoftWarps);
-    }
-    mbar_init(&B.drain, 1);
-    M.abort = 0;
-    for (int i = 0; i < kInfo; ++i) {
-      M.bad[i] = 0;
-      for (int b = 0; b < 4; ++b) M.first_bad[i][b] = INT_MAX;
-    }
-    mbar_fence_init();
-  }
+  if (tid == 0) chunk_init(M);
   if (warp == 0) {
     tmem_alloc(&M.tmem, kTmemCols);
     tmem_relinquish();
@@ -203,257 +498,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
     // ---------------- producers ----------------
     regs_down<kRegsProd>();
-    const int group_of = (warp - kSoftWarps) >> 2, p = tid - 32 * (kSoftWarps + 4 * group_of), pw = p >> 5;
-    const uint32_t ex = exponent_bits();
-    bool ok = true;  // a warp in which a wait has run out leaves as a whole
-    int n = 0;
-    for (long long w = blockIdx.x; ok && next_item(w); n += it.nt)
-    for (int i = (n & 1) == group_of ? 0 : 1; i < it.nt; i += 2) {
-      const int ni = n + i, st = ni & 1, rs = ni & (kRaw - 1), inf = ni & (kInfo - 1), lim_hi = it.lim_hi;
-      ok = __all_sync(0xffffffffu, cwait(&B.raw_full[rs], (uint32_t)(ni / kRaw) & 1u, abort_flag));
-      if (!ok) break;
-      const int absent = M.absent[inf];
-      const unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
-      const bool ragged = absent || (i + 1) * kPosTile > lim_hi;  // some positions do not count: their scales read as 0
-
-      // the largest scales (every warp for itself)
-      int e_k, e_v;
-      bool v_bad = false;
-      {
-        const int s = lane >> 3, at = i * kPosTile + s * kKv4Tile + 2 * (lane & 7);
-        const bool ok0 = !(absent >> s & 1) && at < lim_hi, ok1 = !(absent >> s & 1) && at + 1 < lim_hi;
-        const unsigned char* base = raw + s * L::sub_stride + (lane & 7) * (4 * NB);
-        uint32_t top[2];
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const unsigned char* sc = base + (side ? HALF + CODES + 16 + ((lane & 4) << 2) : CODES);
-          uint32_t w[NB];
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4*>(sc);
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(sc);
-            w[0] = u.x, w[1] = u.y;
-          }
-          __half2 m = __floats2half2_rn(0.f, 0.f), first = m;  // first: of the first position alone
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint32_t u = (b < NB / 2 ? ok0 : ok1) ? w[b] & 0x7fff7fffu : 0u;
-            if (side) v_bad |= (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
-            if (NP == 2 && side && b == NB / 2) {
-              first = m;
-              m = __floats2half2_rn(0.f, 0.f);
-            }
-            m = __hmax2(m, as_h2(u));  // NaN loses
-          }
-          top[side] = max(as_u32(m) >> 16, as_u32(m) & 0xffffu);
-          if (NP == 2 && side) {
-            const int e0 = (int)min(max(as_u32(first) >> 16, as_u32(first) & 0xffffu) >> 10, 30u) - 14;
-            const int e1 = (int)min(top[1] >> 10, 30u) - 14;
-            M.v_norm[warp - kSoftWarps][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
-            if (pw == 0) {
-              *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
-              *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
-                  make_float2(__uint_as_float((uint32_t)(127 - e0) << 23), __uint_as_float((uint32_t)(127 - e1) << 23));
-            }
-          }
-        }
-        e_k = (int)min(__reduce_max_sync(0xffffffffu, top[0]) >> 10, 30u) - 14;
-        e_v = NP == 2 ? 0 : (int)min(__reduce_max_sync(0xffffffffu, top[1]) >> 10, 30u) - 14;
-        v_bad = __any_sync(0xffffffffu, v_bad);
-      }
-      const __half2 norm_k = __half2half2(__ushort_as_half(half_power(e_k)));
-      const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
-      if (NP == 2) __syncwarp();  // v_norm
-      // K: 64 positions x 4 x (the word of eight dims of every block)
-      if (ni >= 2) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)((ni >> 1) + 1) & 1u, abort_flag));
-      if (!ok) break;
-      if (p == 0) {
-        M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
-        M.v_exp[inf] = (float)e_v;
-        M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
-        M.bad[inf] = v_bad;
-        // For tile n + kRaw, which no warp has begun: its copy waits until every warp of the group has read tile n.  The
-        // entry's last tile, n + kRaw - kInfo, was read by the softmax before the probabilities of tile n - 4 were handed
-        // on, which the scores of tile n - 2 waited for; and those are done.
-        const int next = (inf + kRaw) & (kInfo - 1);
-        for (int b = 0; b < 4; ++b) M.first_bad[next][b] = INT_MAX;
-      }
-      unsigned char* kt = sm + L::off_k + st * NKV * L::k_part;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int tig = lane & 3, pos = ((lane >> 2) & 1) * 4 + ((lane >> 3) & 3) + 8 * (pw + 4 * j), s = pos >> 4;
-        const unsigned char* src = raw + s * L::sub_stride;
-        uint32_t w[NB], sc[NB / 2];
-        if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(src + (pos & 15) * (D / 2) + tig * 16);
-          w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-          const uint2 v = *reinterpret_cast<const uint2*>(src + CODES + (pos & 15) * (2 * NB));
-          sc[0] = v.x, sc[1] = v.y;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(src + (pos & 15) * (D / 2) + tig * 8);
-          w[0] = u.x, w[1] = u.y;
-          sc[0] = *reinterpret_cast<const uint32_t*>(src + CODES + (pos & 15) * (2 * NB));
-        }
-        if (ragged && ((absent >> s & 1) || i * kPosTile + pos >= lim_hi)) {
-#pragma unroll
-          for (int b = 0; b < NB / 2; ++b) sc[b] = 0;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[b / 2], 0, b & 1 ? 0x3232 : 0x1010)), norm_k);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t x = t < 2 ? w[b] : w[b] >> 8;
-            const __half2 n = t & 1 ? code_high(x, ex) : code_low(x, ex);
-            const __half2 h = __hmul2(n, s2);
-            hi[t] = as_u32(h);
-            if (NKV == 2) lo[t] = as_u32(__hfma2(n, s2, __hneg2(h)));
-          }
-          unsigned char* at = kt + (b >> 1) * (kPosTile * 128) + sw128_offset(pos, 32 * (b & 1) + 8 * tig);
-          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (NKV == 2) *reinterpret_cast<uint4*>(at + L::k_part) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(&B.k_full[st]);
-
-      // V: a thread has eight positions (chunk) and two of the four dims 4 gid .. + 3 of every block.  Eight lanes with the
-      // same dims and different chunks read 16 bytes each from places 16 bytes apart modulo 128 (hence the paddings
-      // of the raw tiles) and write a whole row of 64 positions
-      if (ni >= 2) ok = __all_sync(0xffffffffu, cwait(&B.v_empty[st], (uint32_t)((ni >> 1) + 1) & 1u, abort_flag));
-      if (!ok) break;
-      {
-        unsigned char* vt = sm + L::off_v + st * NKV * L::v_part;
-        constexpr int VB = NKV == 1 ? NB : NB / 2;  // blocks at a time, for the registers
-        const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
-        const unsigned char* src = raw + s * L::sub_stride + HALF;
-        const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
-        const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB + 16);
-#pragma unroll 1
-        for (int b0 = 0; b0 < NB; b0 += VB) {
-        uint32_t hi[VB][2][4], lo[VB][2][4];
-#pragma unroll
-        for (int tig = 0; tig < 4; ++tig) {
-          constexpr int W = (VB + 1) / 2;  // words of a position's blocks
-          uint32_t w[2][W], sc[2][W];      // of the first and the second position
-          if constexpr (D == 128 && VB == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(codes + tig * 16);
-            w[0][0] = u.x, w[0][1] = u.y, w[1][0] = u.z, w[1][1] = u.w;
-            const uint4 v = *reinterpret_cast<const uint4*>(scales + tig * 16);
-            sc[0][0] = v.x, sc[0][1] = v.y, sc[1][0] = v.z, sc[1][1] = v.w;
-          } else if constexpr (D == 128) {
-            w[0][0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + b0 * 2);
-            w[1][0] = *reinterpret_cast<const uint32_t*>(codes + tig * 16 + 8 + b0 * 2);
-            sc[0][0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + b0 * 2);
-            sc[1][0] = *reinterpret_cast<const uint32_t*>(scales + tig * 16 + 8 + b0 * 2);
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(codes + tig * 8);
-            w[0][0] = u.x >> (16 * b0), w[1][0] = u.y >> (16 * b0);
-            const uint2 v = *reinterpret_cast<const uint2*>(scales + tig * 8);
-            sc[0][0] = v.x >> (16 * b0), sc[1][0] = v.y >> (16 * b0);
-          }
-          if (ragged || v_bad) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int at = i * kPosTile + chunk * 8 + 2 * tig + e;
-              const bool off = (absent >> s & 1) || at >= lim_hi;
-#pragma unroll
-              for (int b = 0; b < VB; ++b) {
-                const uint32_t mask = b & 1 ? 0xffff0000u : 0xffffu;
-                const bool bad = (sc[e][b / 2] & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
-                if (bad && !off) atomicMin(&M.first_bad[inf][b0 + b], at);
-                if (bad || off) sc[e][b / 2] &= ~mask;
-              }
-            }
-          }
-#pragma unroll
-          for (int b = 0; b < VB; ++b) {
-            const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0][b / 2], sc[1][b / 2], b & 1 ? 0x7632 : 0x5410)),
-                                       NP == 2 ? as_h2(M.v_norm[warp - kSoftWarps][4 * chunk + tig]) : norm_v);
-            // byte dsel of the block's two bytes, of both positions
-            const uint32_t x = __byte_perm(w[0][b / 2], w[1][b / 2], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
-            const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
-            const __half2 h0 = __hmul2(n0, s2), h1 = __hmul2(n1, s2);
-            hi[b][0][tig] = as_u32(h0);
-            hi[b][1][tig] = as_u32(h1);
-            if (NKV == 2) {
-              lo[b][0][tig] = as_u32(__hfma2(n0, s2, __hneg2(h0)));
-              lo[b][1][tig] = as_u32(__hfma2(n1, s2, __hneg2(h1)));
-            }
-          }
-        }
-        if (b0 + VB == NB) mbar_arrive(&B.raw_empty[rs]);
-#pragma unroll
-        for (int b = 0; b < VB; ++b)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int dim = 32 * (b0 + b) + 4 * gid + 2 * dsel + k;
-            unsigned char* at = vt + sw128_offset(dim, 8 * chunk);
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[b][k][0], hi[b][k][1], hi[b][k][2], hi[b][k][3]);
-            if (NKV == 2) *reinterpret_cast<uint4*>(at + L::v_part) = make_uint4(lo[b][k][0], lo[b][k][1], lo[b][k][2], lo[b][k][3]);
-          }
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(&B.v_full[st]);
-    }
+    chunk_expand<D, NKV, NP, 2, L>(sm, M, items);
   } else if (warp >= kSoftWarps + kProdWarps) {
     regs_down<kRegsRest>();
     if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) {
       // ---------------- copies ----------------
-      const int tpp = a.c.page_len / kKv4Tile;
-      bool ok = true;
-      int n = 0;
-      for (long long w = blockIdx.x; ok && next_item(w);) {
-        const int n16 = (it.lim_hi + kKv4Tile - 1) / kKv4Tile;
-        const int* trow = a.table + (long long)it.seq * a.table_stride;
-        // the pages of a tile are asked for a tile ahead; places go on without a division
-        int ids[kSub], places[kSub], next_t = 0, next_page = 0, next_place = 0;
-        auto ask = [&]() {
-#pragma unroll
-          for (int s = 0; s < kSub; ++s) {
-            ids[s] = next_t < n16 ? trow[next_page] : -1;
-            places[s] = next_place;
-            ++next_t;
-            if (++next_place == tpp) {
-              next_place = 0;
-              ++next_page;
-            }
-          }
-        };
-        ask();
-        for (int i = 0; i < it.nt; ++i, ++n) {
-          const int rs = n & (kRaw - 1);
-          ok = n < kRaw || cwait(&B.raw_empty[rs], (uint32_t)(n / kRaw + 1) & 1u, abort_flag);
-          if (!ok) break;
-          unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
-          int absent = 0, here = 0;
-#pragma unroll
-          for (int s = 0; s < kSub; ++s) {
-            const bool there = ids[s] >= 0 && ids[s] < a.c.n_pages;
-            absent |= there ? 0 : 1 << s;
-            here += there;
-          }
-          M.absent[n & (kInfo - 1)] = absent;
-          mbar_arrive_expect_tx(&B.raw_full[rs], here * TILE);
-          // V's second half, and the second half of its scales, go 16 bytes on each: see their reads
-          constexpr int cut = HALF + CODES / 2, cut2 = HALF + CODES + kv4_scales(D) / 2;
-#pragma unroll
-          for (int s = 0; s < kSub; ++s)
-            if (!(absent >> s & 1)) {
-              const uint8_t* src = a.c.data + (((long long)ids[s] * a.c.n_kv_heads + it.head) * tpp + places[s]) * TILE;
-              unsigned char* dst = raw + s * L::sub_stride;
-              bulk_g2s(dst, src, cut, &B.raw_full[rs]);
-              bulk_g2s(dst + cut + 16, src + cut, cut2 - cut, &B.raw_full[rs]);
-              bulk_g2s(dst + cut2 + 32, src + cut2, TILE - cut2, &B.raw_full[rs]);
-            }
-          ask();
-        }
-      }
-      if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
-        for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
+      chunk_copy<D, L>(sm, M, items);
     }
     if (warp == kSoftWarps + kProdWarps) {
       // ---------------- products ----------------
@@ -487,7 +537,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       };
       bool ok = true;
       uint32_t q_ph = 0;
-      for (long long w = blockIdx.x; ok && next_item(w);) {
+      for (long long w = blockIdx.x; ok && items.next(w);) {
         if (it.nt == 0) continue;  // its q is not waited for, and not announced
         ok = __all_sync(0xffffffffu, cwait(&B.q_full, q_ph, abort_flag));
         q_ph ^= 1;
@@ -533,12 +583,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1;
     bool ok = true;
     int n = 0;
-    for (long long w_item = blockIdx.x; next_item(w_item); n += it.nt) {
-    const int nt = it.nt, lim_lo = max(0, it.len - it.count + it.row0 / group + 1);  // positions that every row sees
+    for (long long w_item = blockIdx.x; items.next(w_item); n += it.nt) {
+    const int nt = it.nt, lim_lo = items.seen(it.row0);  // positions that every row sees
     const int col = it.row0 + row;
     const bool live = col < it.ncols;
     const int col_k = col / group;
-    const int lim = live ? max(0, it.len - it.count + col_k + 1) : 0;
+    const int lim = live ? items.seen(col) : 0;
     const long long elem = live ? (long long)(it.head * group + col % group) * D + half * HD : 0;
     // ---- q into TMEM: scaled by a power of two per row, high and low part; within eight dims in the order of the unpacked
     // codes (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with its q: this thread has waited for them
@@ -786,25 +836,332 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   }
 }
 
-template <int D, int NQ, int NKV, int NP>
-cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
-  constexpr int smem = ChunkLayout<D, NKV>::bytes;
-  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  auto* kern = kv4_chunk_kernel<D, NQ, NKV, NP>;
-  static std::atomic<uint64_t> ready{0};  // one bit per device
+// ---------------- two row tiles per item ----------------
+// Where K, V and the probabilities need one fp16 value each, an item is 256 rows: two tiles of 128 share every expanded
+// K and V, and their softmaxes, four warps each with a whole row per thread, are independent, so one's chain of
+// reads, maxima, exponentials and writes runs beside the other's.  P takes the place of its S in TMEM; the next
+// scores that are written there wait for the product that reads P.  q lies in shared memory: TMEM holds the two tiles'
+// S and P, two of each, and O.
+constexpr uint32_t kColPairS = 0, kColPairO = 256;
+constexpr int kRegsPairSoft = 144, kRegsPairRest = 48;  // a whole row of scores per thread
+static_assert(32 * (kSoftWarps * kRegsPairSoft + kProdWarps * kRegsProd + 4 * kRegsPairRest) <= kChunkThreads * kRegsStart, "the trade adds up");
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4AttnArgs a, int /* STAGE_BF16 */) {
+  constexpr int KS = 3, q_tile = kRowsTile * D * 2;
+  using L = ChunkLayout<D, 1, KS, 2 * q_tile>;
+  extern __shared__ unsigned char chunk_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)chunk_raw + 1023) & ~(uintptr_t)1023);
+  ChunkMisc& M = *reinterpret_cast<ChunkMisc*>(sm + L::off_misc);
+  ChunkBars& B = M.bar;
+  volatile int* abort_flag = &M.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  ChunkItems items(a, 2 * kRowsTile);
+  const ChunkItem& it = items.it;
+  const int group = items.group;
+  // tiles of positions that row tile g of the item sees (0: it has no rows)
+  auto tiles_of = [&](int g) {
+    const int r0 = it.row0 + g * kRowsTile;
+    return r0 < it.ncols ? (items.seen(min(it.ncols, r0 + kRowsTile) - 1) + kPosTile - 1) / kPosTile : 0;
+  };
+
+  if (tid == 0) chunk_init(M);
+  if (warp == 0) {
+    tmem_alloc(&M.tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = M.tmem;
+
+  if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
+    regs_down<kRegsProd>();
+    chunk_expand<D, 1, 1, KS, L>(sm, M, items);
+  } else if (warp >= kSoftWarps + kProdWarps) {
+    regs_down<kRegsPairRest>();
+    if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) chunk_copy<D, L>(sm, M, items);
+    if (warp == kSoftWarps + kProdWarps) {
+      // ---------------- products (as in the kernel with one row tile: one elected thread of a converged warp) ----------------
+      const bool leader = elect_one();
+      constexpr uint32_t id_s = idesc_f16_f32(kRowsTile, kPosTile), id_o = idesc_f16_f32(kRowsTile, D);
+      const uint64_t qd = desc_sw128(smem_u32(sm)), kd = desc_sw128(smem_u32(sm + L::off_k)), vd = desc_sw128(smem_u32(sm + L::off_v));
+      uint32_t s_count[2] = {0, 0}, o_count[2] = {0, 0}, q_ph[2] = {0, 0};  // of each row tile: scores and outputs so far
+      // scores of row tile g and tile number ni; `last`: nobody reads this K after
+      auto scores = [&](int g, int ni, bool last) {
+        const uint32_t c = s_count[g], b = c & 1, st = (uint32_t)ni % KS;
+        bool ok = cwait(&B.k_full[st], (uint32_t)ni / KS & 1u, abort_flag);
+        if (c >= 2) ok = ok && cwait(&B.pair_o[g][b], (c / 2 + 1) & 1u, abort_flag);  // the product that read this place's P
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+        const uint64_t kb = kd + st * (uint32_t)(L::k_part >> 4), qb = qd + (uint32_t)g * (uint32_t)(q_tile >> 4);
+        const uint32_t d = tmem + kColPairS + g * 128 + b * kPosTile;
+        if (leader) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_bf16(d, qb + (((ks >> 2) * (kRowsTile * 128) + (ks & 3) * 32) >> 4),
+                      kb + (((ks >> 2) * (kPosTile * 128) + (ks & 3) * 32) >> 4), id_s, ks ? 1u : 0u);
+          if (last) umma_commit(&B.k_empty[st]);
+          umma_commit(&B.pair_s[g][b]);
+          mbar_arrive(&B.pair_s[g][b]);  // hands on what the producers wrote beside the tile
+        }
+        __syncwarp();
+        ++s_count[g];
+        return true;
+      };
+      // its output; `more`: added to the last tile's
+      auto outputs = [&](int g, int ni, bool more, bool last) {
+        const uint32_t c = o_count[g], b = c & 1, st = (uint32_t)ni % KS;
+        const bool ok = cwait(&B.v_full[st], (uint32_t)ni / KS & 1u, abort_flag) && cwait(&B.pair_p[g][b], c / 2 & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+        const uint64_t vb = vd + st * (uint32_t)(L::v_part >> 4);
+        if (leader) {
+#pragma unroll
+          for (int ks = 0; ks < kPosTile / 16; ++ks)
+            umma_f16_ts(tmem + kColPairO + g * 128, tmem + kColPairS + g * 128 + b * kPosTile + ks * 8, vb + ((ks * 32) >> 4), id_o,
+                        more || ks ? 1u : 0u);
+          if (last) umma_commit(&B.v_empty[st]);
+          umma_commit(&B.pair_o[g][b]);
+          mbar_arrive(&B.pair_o[g][b]);
+        }
+        __syncwarp();
+        ++o_count[g];
+        return true;
+      };
+      bool ok = true;
+      int n = 0;
+      for (long long w = blockIdx.x; ok && items.next(w); n += it.nt) {
+        const int nt0 = tiles_of(0), nt1 = tiles_of(1);
+        for (int g = 0; g < 2; ++g)
+          if (ok && (g ? nt1 : nt0) > 0) {
+            ok = __all_sync(0xffffffffu, cwait(&B.pair_q[g], q_ph[g], abort_flag));
+            q_ph[g] ^= 1;
+          }
+        if (!ok) break;
+        tc_fence_after();
+        if (nt0 > 0) ok = scores(0, n, nt1 <= 0);
+        if (ok && nt1 > 0) ok = scores(1, n, true);
+        if (ok && nt0 > 1) ok = scores(0, n + 1, nt1 <= 1);
+        for (int i = 0; ok && i < it.nt; ++i) {
+          if (i < nt0) ok = outputs(0, n + i, i > 0, i >= nt1);
+          if (ok && i + 1 < nt1) ok = scores(1, n + i + 1, true);
+          if (ok && i < nt1) ok = outputs(1, n + i, i > 0, true);
+          if (ok && i + 2 < nt0) ok = scores(0, n + i + 2, i + 2 >= nt1);
+        }
+      }
+      if (!ok && leader) {  // given up: the products already issued finish before TMEM is released
+        umma_commit(&B.drain);
+        mbar_wait(&B.drain, 0u, kDrainNs);
+      }
+    }
+  } else {
+    // ---------------- softmax ----------------
+    regs_up<kRegsPairSoft>();
+    const int g = warp >> 2, row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t place_s = lanes + kColPairS + g * 128, place_o = lanes + kColPairO + g * 128;
+    bool ok = true;
+    int n = 0;
+    uint32_t c = 0;  // tiles of this row tile so far
+    for (long long w_item = blockIdx.x; items.next(w_item); n += it.nt) {
+      const int r0 = it.row0 + g * kRowsTile, nt = tiles_of(g);
+      if (r0 >= it.ncols) continue;
+      const int lim_lo = items.seen(r0), col = r0 + row, col_k = col / group;
+      const bool live = col < it.ncols;
+      const int lim = live ? items.seen(col) : 0;
+      const long long elem = live ? (long long)(it.head * group + col % group) * D : 0;
+      // ---- q into shared memory: fp16, scaled by a power of two per row, eight dims in the order of the unpacked codes
+      // (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with their q: this thread has waited for them
+      float zscale;
+      {
+        uint4 raw[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                          (live ? (long long)(it.start + col_k) * a.q_stride + elem : 0));
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          raw[j] = live ? src[j] : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
+        }
+        const int e = top <= FLT_MAX ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 0;
+        zscale = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+        const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+        unsigned char* tile = sm + g * q_tile;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {  // dims t and t + 4
+            const uint32_t lo = u[t >> 1], hi = u[2 + (t >> 1)];
+            const float x0 = t & 1 ? __uint_as_float(lo & 0xffff0000u) : __uint_as_float(lo << 16);
+            const float x1 = t & 1 ? __uint_as_float(hi & 0xffff0000u) : __uint_as_float(hi << 16);
+            h[t] = as_u32(__floats2half2_rn(x0 * up, x1 * up));
+          }
+          *reinterpret_cast<uint4*>(tile + (j >> 3) * (kRowsTile * 128) + sw128_offset(row, 8 * (j & 7))) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        fence_async_smem();
+        if (nt > 0) mbar_arrive(&B.pair_q[g]);
+      }
+
+      float ref = -INFINITY, sum = 0.f;
+      int nan_blocks = 0;  // the blocks of dims in which the row sees a V scale that is no number
+      auto products_done = [&](uint32_t count) {  // of the row tile's tile number `count`
+        if (!__all_sync(0xffffffffu, cwait(&B.pair_o[g][count & 1], count / 2 & 1u, abort_flag))) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto note_bad = [&](int i) {
+        if (M.bad[i & (kInfo - 1)]) {
+#pragma unroll
+          for (int b = 0; b < D / 32; ++b)
+            if (M.first_bad[i & (kInfo - 1)][b] < lim) nan_blocks |= 1 << b;
+        }
+      };
+      for (int i = 0; ok && i < nt; ++i, ++c) {
+        const int ni = n + i, inf = ni & (kInfo - 1);
+        const uint32_t b = c & 1;
+        ok = __all_sync(0xffffffffu, cwait(&B.pair_s[g][b], c / 2 & 1u, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[2][32];
+        tmem_ld32(place_s + b * kPosTile, s[0]);
+        tmem_ld32(place_s + b * kPosTile + 32, s[1]);
+        const float f = zscale * M.k_pow[inf], ev = M.v_exp[inf], v_inv = M.v_inv[inf];
+        const int absent = M.absent[inf];
+        if (i >= 2) note_bad(ni - 2);
+        tmem_wait_ld();
+        const int pos0 = i * kPosTile;
+        if (pos0 + kPosTile > lim_lo || absent) {
+#pragma unroll
+          for (int j = 0; j < kPosTile; ++j)
+            if (pos0 + j >= lim || (absent >> (j >> 4) & 1)) s[j >> 5][j & 31] = 0xff800000u;
+        }
+        float m4[4];  // four chains
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(s[0][j]);
+#pragma unroll
+        for (int j = 4; j < kPosTile; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(s[j >> 5][j & 31]));
+        const float most = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f, ev);
+        float keep = 1.f;
+        if (most - kChunkTop<1> > ref + kChunkSlack<1>) {
+          keep = exp2_approx(ref - (most - kChunkTop<1>));
+          ref = most - kChunkTop<1>;
+          sum *= keep;
+        }
+        if (__any_sync(0xffffffffu, keep != 1.f) && i > 0) {
+          ok = products_done(c - 1);
+          if (!ok) break;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            uint32_t r[16];
+            tmem_ld16(place_o + d, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * keep);
+            tmem_st16(place_o + d, r);
+          }
+        }
+        const float base = ev - (ref == -INFINITY ? 0.f : ref);
+        float2 part4[4];  // four chains
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part4[j] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t hi[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 z = fma2(make_float2(__uint_as_float(s[h][2 * j]), __uint_as_float(s[h][2 * j + 1])), make_float2(f, f), make_float2(base, base));
+            const float2 x = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+            part4[j & 3] = add2(part4[j & 3], x);
+            hi[j] = as_u32(__floats2half2_rn(x.x, x.y));
+          }
+          tmem_st16(place_s + b * kPosTile + 16 * h, hi);  // over the thread's own scores, which are read
+        }
+        const float2 part = add2(add2(part4[0], part4[1]), add2(part4[2], part4[3]));
+        sum = fmaf(part.x + part.y, v_inv, sum);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&B.pair_p[g][b]);
+      }
+      if (ok && nt > 0) {
+        ok = products_done(c - 1);
+        if (nt > 1) note_bad(n + nt - 2);
+        note_bad(n + nt - 1);
+      }
+      const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {  // a block of dims
+        uint32_t r[32];
+        if (ok && nt > 0) {
+          tmem_ld32(place_o + d, r);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = 0;
+        }
+        const float factor = nan_blocks >> (d >> 5) & 1 ? NAN : inv;
+        if (live) {
+          uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (long long)(it.start + col_k) * a.out_stride + elem + d);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * k]) * factor, __uint_as_float(r[8 * j + 2 * k + 1]) * factor);
+              u[k] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            out[j] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+        __syncwarp();  // the next block's TMEM read is the whole warp's
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Launches one of the kernels, one CTA per SM at most.
+template <typename Kernel>
+cudaError_t launch_items(Kernel* kern, int smem, int rows, const Kv4AttnArgs& a, int dtype, std::atomic<uint64_t>& ready, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {  // once per device
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
-  const long long items = (cols + kRowsTile - 1) / kRowsTile * a.c.n_kv_heads * a.n_seqs;
-  const int grid = (int)min(items, (long long)sm_count());
-  kern<<<grid, kChunkThreads, smem, st>>>(a, dtype);
+  const long long items = (cols + rows - 1) / rows * a.c.n_kv_heads * a.n_seqs;
+  kern<<<(int)min(items, (long long)sm_count()), kChunkThreads, smem, st>>>(a, dtype);
   return cudaGetLastError();
+}
+
+template <int D, int NQ, int NKV, int NP>
+cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
+  constexpr int smem = ChunkLayout<D, NKV, 2, 0>::bytes;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  static std::atomic<uint64_t> ready{0};
+  return launch_items(kv4_chunk_kernel<D, NQ, NKV, NP>, smem, kRowsTile, a, dtype, ready, st);
+}
+
+template <int D>
+cudaError_t launch_pair(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
+  constexpr int smem = ChunkLayout<D, 1, 3, 2 * kRowsTile * D * 2>::bytes;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  static std::atomic<uint64_t> ready{0};
+  return launch_items(kv4_pair_kernel<D>, smem, 2 * kRowsTile, a, dtype, ready, st);
 }
 
 }  // namespace
@@ -813,11 +1170,11 @@ cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cuda
   if (head_dim == 128) {
     if (dtype == KV4_F32) return launch_chunk<128, 2, 2, 2>(a, dtype, st);
     if (dtype == KV4_F16) return launch_chunk<128, 1, 2, 1>(a, dtype, st);
-    return launch_chunk<128, 1, 1, 1>(a, dtype, st);
+    return launch_pair<128>(a, dtype, st);
   }
   if (dtype == KV4_F32) return launch_chunk<64, 2, 2, 2>(a, dtype, st);
   if (dtype == KV4_F16) return launch_chunk<64, 1, 2, 1>(a, dtype, st);
-  return launch_chunk<64, 1, 1, 1>(a, dtype, st);
+  return launch_pair<64>(a, dtype, st);
 }
 
 }  // namespace lrs
