@@ -30,7 +30,7 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kUnitTiles = kWarps;  // a unit: one tile of 16 positions per warp
 constexpr int kStages = 4;          // tiles in flight per warp, less one
 constexpr int kFlush = 16;          // tiles between two flushes of the accumulators
-constexpr int kMaxCtas = 512;
+constexpr int kMaxCtas = kKv4MaxCtas;
 constexpr int kRowCost = 4;  // 64 ragged sequences (64/8 heads): 91 us with 0, 74 with 2, 68 with 3, 69 with 5
 constexpr int kSlack = 4;           // r is raised when a score passes it by 2^kSlack
 constexpr float kTop = 11.f;
@@ -584,8 +584,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
   }
 }
 
-constexpr size_t kCounterBytes = kMaxCtas * sizeof(unsigned);
-
 template <int D, int NC>
 cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
   constexpr size_t smem = sizeof(AttnSmem<D, NC>);
@@ -609,20 +607,35 @@ cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
                          ((len + kUnitTiles * kKv4Tile - 1) / (kUnitTiles * kKv4Tile));
   const int grid = (int)min(min(most, 2ll * sm_count()), (long long)kMaxCtas);
   unsigned* counters = (unsigned*)a.ws;
-  kern<<<grid, kThreads, smem, st>>>(a, dtype, counters, (float*)((char*)a.ws + kCounterBytes), Quotient(group),
+  kern<<<grid, kThreads, smem, st>>>(a, dtype, counters, (float*)((char*)a.ws + kKv4CounterBytes), Quotient(group),
                                      Quotient(a.c.page_len / kKv4Tile));
   return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv4_attention_ws_bytes(int, int, int, int head_dim, int, int) {
-  return kCounterBytes + (size_t)2 * kMaxCtas * slot_floats(head_dim) * sizeof(float);
+// Few columns (query tokens of a sequence times heads of a group) run on the kernel above, which reads the cache again for
+// every eight of them; many on the tiles of kernels_kv4_chunk.cu.  Measured (32/8 heads, head_dim 128, us), with z =
+// n_seqs * n_kv_heads * max_len in millions: here 10 + 43 z per eight columns; there 18 + 195 z per 128 rows (float32),
+// 18 + 155 z per 256 (bfloat16; float16, 128 rows with two products each, lies between).  E.g. 16 sequences of 4096:
+// 64 columns 182 here and 123 there, 32 columns 97 and 122; one sequence of 512: 256 columns 20 and 27.
+constexpr int kFewColumns = 32;
+
+bool many_columns(int n_seqs, int n_kv_heads, long long cols, int max_len, int dtype) {
+  if (cols <= kFewColumns) return false;
+  const double z = 1e-6 * n_seqs * n_kv_heads * max_len;
+  const double there = dtype == KV4_BF16 ? 155. * ((cols + 255) / 256) : (dtype == KV4_F32 ? 195. : 175.) * ((cols + 127) / 128);
+  return (43. * ((cols + 7) / 8) - there) * z > 8.;
+}
+
+size_t kv4_attention_ws_bytes(int, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int) {
+  const size_t few = kKv4CounterBytes + (size_t)2 * kMaxCtas * slot_floats(head_dim) * sizeof(float);
+  return (long long)max_q * (n_q_heads / n_kv_heads) > kFewColumns ? max(few, kv4_chunk_ws_bytes(head_dim)) : few;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st) {
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
-  if (cols > 32) return launch_kv4_chunk(a, head_dim, dtype, st);
+  if (many_columns(a.n_seqs, a.c.n_kv_heads, cols, a.max_len, dtype)) return launch_kv4_chunk(a, head_dim, dtype, st);
   if (head_dim == 128) return cols <= 4 ? launch<128, 4>(a, dtype, st) : launch<128, 8>(a, dtype, st);
   return cols <= 4 ? launch<64, 4>(a, dtype, st) : launch<64, 8>(a, dtype, st);
 }

@@ -62,6 +62,62 @@ struct ChunkBars {
   uint64_t pair_q[2], pair_s[2][2], pair_p[2][2], pair_o[2][2];  // of the kernel with two row tiles: [tile][buffer]
 };
 
+struct ChunkItem {
+  long long number, count;         // of this item, and of all
+  int group, row_tiles;            // query heads per KV head; row tiles of a sequence at the call's bounds
+  int seq, head, row0;             // sequence, KV head, first row
+  int start, tokens, len, ncols;   // first query token of the sequence, its tokens, its positions, its rows
+  int lim_hi, t0, nt;              // positions that some row sees; the first of the item's tiles and how many they are
+};
+
+// Items of ROWS rows: row tiles from the last (which sees most) down, then KV heads, then sequences, then the parts of
+// their positions; a CTA has every gridDim.x-th.  Every warp goes through them for itself.  SPLIT: whether
+// there are parts; without them the loops keep their registers for their work.
+template <int ROWS, bool SPLIT>
+struct ChunkItems {
+  const Kv4AttnArgs& a;
+  const int parts;
+  ChunkItem it;
+  __device__ __forceinline__ ChunkItems(const Kv4AttnArgs& args, int parts_of_row) : a(args), parts(SPLIT ? parts_of_row : 1) {
+    it.group = a.n_q_heads / a.c.n_kv_heads;
+    it.row_tiles = (int)(((long long)a.max_q * it.group + ROWS - 1) / ROWS);
+    it.count = (long long)it.row_tiles * a.c.n_kv_heads * a.n_seqs * parts;
+  }
+  // Takes number w apart; false if its sequence has no such rows.
+  __device__ __forceinline__ bool at(long long w) {
+    const long long per = (long long)a.c.n_kv_heads * a.n_seqs * parts;
+    const int row_tile = it.row_tiles - 1 - (int)(w / per), rest = (int)(w % per), part = rest % parts, row = rest / parts;
+    const int seq = row / a.c.n_kv_heads, row0 = row_tile * ROWS;
+    int start;
+    const int tokens = seq_tokens(a, seq, &start), ncols = min(tokens, a.max_q) * it.group;
+    if (row0 >= ncols) return false;
+    it.number = w;
+    it.seq = seq;
+    it.head = row % a.c.n_kv_heads;
+    it.row0 = row0;
+    it.start = start;
+    it.tokens = tokens;
+    it.len = seq_positions(a, seq);
+    it.ncols = ncols;
+    it.lim_hi = seen(min(ncols, row0 + ROWS) - 1);
+    const long long nt = (it.lim_hi + kPosTile - 1) / kPosTile;
+    it.t0 = (int)(nt * part / parts);
+    it.nt = (int)(nt * (part + 1) / parts) - it.t0;
+    return true;
+  }
+  // The next item from number w on; false behind the last.
+  __device__ __forceinline__ bool next(long long& w) {
+    for (; w < it.count; w += gridDim.x)
+      if (at(w)) {
+        w += gridDim.x;
+        return true;
+      }
+    return false;
+  }
+  // Positions that the item's sequence shows to row r.
+  __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.tokens + r / it.group + 1); }
+};
+
 struct alignas(16) ChunkMisc {
   ChunkBars bar;
   float k_pow[kInfo], v_exp[kInfo], v_inv[kInfo];  // 2^E_k; E_v; 2^-E_v
@@ -104,45 +160,14 @@ __device__ __forceinline__ bool cwait(uint64_t* bar, uint32_t parity, volatile i
   return true;
 }
 
-struct ChunkItem {
-  int seq, head, row0;             // sequence, KV head, first row
-  int start, count, len, ncols;    // first query token of the sequence, its tokens, its positions, its rows
-  int lim_hi, nt;                  // positions that some row sees, tiles
-};
-
-// Items: row tiles from the last (which sees most) down, then KV heads, then sequences; a CTA has every gridDim.x-th.
-struct ChunkItems {
-  const Kv4AttnArgs& a;
-  int group, rows, row_tiles;
-  long long count;
-  ChunkItem it;
-  __device__ __forceinline__ ChunkItems(const Kv4AttnArgs& args, int rows_of_item) : a(args), rows(rows_of_item) {
-    group = a.n_q_heads / a.c.n_kv_heads;
-    row_tiles = (int)(((long long)a.max_q * group + rows - 1) / rows);
-    count = (long long)row_tiles * a.c.n_kv_heads * a.n_seqs;
-  }
-  // The next item from number w on; false behind the last.
-  __device__ __forceinline__ bool next(long long& w) {
-    const long long per = (long long)a.c.n_kv_heads * a.n_seqs;
-    for (; w < count; w += gridDim.x) {
-      const int row_tile = row_tiles - 1 - (int)(w / per), rest = (int)(w % per);
-      it.seq = rest / a.c.n_kv_heads;
-      it.head = rest % a.c.n_kv_heads;
-      it.row0 = row_tile * rows;
-      it.count = seq_tokens(a, it.seq, &it.start);
-      it.len = seq_positions(a, it.seq);
-      it.ncols = min(it.count, a.max_q) * group;
-      if (it.row0 >= it.ncols) continue;
-      it.lim_hi = seen(min(it.ncols, it.row0 + rows) - 1);
-      it.nt = (it.lim_hi + kPosTile - 1) / kPosTile;
-      w += gridDim.x;
-      return true;
-    }
-    return false;
-  }
-  // Positions that the item's sequence shows to row r.
-  __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.count + r / group + 1); }
-};
+// Partial results, where a row tile's positions are shared out: per item and row the sums (float32, not divided), and
+// the reference and the sum that divides them.
+__device__ __forceinline__ float* part_row(const Kv4AttnArgs& a, long long number, int rows, int row, int D) {
+  return reinterpret_cast<float*>((char*)a.ws + kKv4CounterBytes) + (number * rows + row) * D;
+}
+__device__ __forceinline__ float2* part_ml(const Kv4AttnArgs& a, long long count, long long number, int rows, int row, int D) {
+  return reinterpret_cast<float2*>(part_row(a, count, rows, 0, D)) + number * rows + row;
+}
 
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -203,8 +228,8 @@ __device__ void chunk_init(ChunkMisc& M) {
 }
 
 // Expansion, by two groups of four warps: group g has the tiles n with n % 2 = g, in KS stages of operands.
-template <int D, int NKV, int NP, int KS, typename L>
-__device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, ChunkItems& items) {
+template <int D, int NKV, int NP, int KS, typename L, int ROWS, bool SPLIT>
+__device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, ChunkItems<ROWS, SPLIT>& items) {
   constexpr int NB = D / 32, HALF = kv4_half(D), CODES = kv4_codes(D);
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
@@ -221,13 +246,14 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
     if (!ok) break;
     const int absent = M.absent[inf];
     const unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
-    const bool ragged = absent || (i + 1) * kPosTile > lim_hi;  // some positions do not count: their scales read as 0
+    const int pos0 = (it.t0 + i) * kPosTile;
+    const bool ragged = absent || pos0 + kPosTile > lim_hi;  // some positions do not count: their scales read as 0
 
     // the largest scales (every warp for itself)
     int e_k, e_v;
     bool v_bad = false;
     {
-      const int s = lane >> 3, at = i * kPosTile + s * kKv4Tile + 2 * (lane & 7);
+      const int s = lane >> 3, at = pos0 + s * kKv4Tile + 2 * (lane & 7);
       const bool ok0 = !(absent >> s & 1) && at < lim_hi, ok1 = !(absent >> s & 1) && at + 1 < lim_hi;
       const unsigned char* base = raw + s * L::sub_stride + (lane & 7) * (4 * NB);
       uint32_t top[2];
@@ -302,7 +328,7 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
         w[0] = u.x, w[1] = u.y;
         sc[0] = *reinterpret_cast<const uint32_t*>(src + CODES + (pos & 15) * (2 * NB));
       }
-      if (ragged && ((absent >> s & 1) || i * kPosTile + pos >= lim_hi)) {
+      if (ragged && ((absent >> s & 1) || pos0 + pos >= lim_hi)) {
 #pragma unroll
         for (int b = 0; b < NB / 2; ++b) sc[b] = 0;
       }
@@ -364,7 +390,7 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
         if (ragged || v_bad) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int at = i * kPosTile + chunk * 8 + 2 * tig + e;
+            const int at = pos0 + chunk * 8 + 2 * tig + e;
             const bool off = (absent >> s & 1) || at >= lim_hi;
 #pragma unroll
             for (int b = 0; b < VB; ++b) {
@@ -409,8 +435,8 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
 }
 
 // Copies of the packed tiles, by one thread.
-template <int D, typename L>
-__device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, ChunkItems& items) {
+template <int D, typename L, int ROWS, bool SPLIT>
+__device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, ChunkItems<ROWS, SPLIT>& items) {
   constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
@@ -423,7 +449,7 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
     const int n16 = (it.lim_hi + kKv4Tile - 1) / kKv4Tile;
     const int* trow = a.table + (long long)it.seq * a.table_stride;
     // the pages of a tile are asked for a tile ahead; places go on without a division
-    int ids[kSub], places[kSub], next_t = 0, next_page = 0, next_place = 0;
+    int ids[kSub], places[kSub], next_t = it.t0 * kSub, next_page = next_t / tpp, next_place = next_t - next_page * tpp;
     auto ask = [&]() {
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
@@ -469,8 +495,8 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
     for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
 }
 
-template <int D, int NQ, int NKV, int NP>
-__global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a, int dtype) {
+template <int D, int NQ, int NKV, int NP, bool SPLIT>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a, int dtype, int parts_of_row) {
   using L = ChunkLayout<D, NKV, 2, 0>;
   constexpr int HD = D / 2;  // dims of a softmax thread
   extern __shared__ unsigned char chunk_raw[];
@@ -480,9 +506,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  ChunkItems items(a, kRowsTile);
+  ChunkItems<kRowsTile, SPLIT> items(a, parts_of_row);
+  const int parts = items.parts;
   const ChunkItem& it = items.it;
-  const int group = items.group;
 
   if (tid == 0) chunk_init(M);
   if (warp == 0) {
@@ -587,9 +613,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     const int nt = it.nt, lim_lo = items.seen(it.row0);  // positions that every row sees
     const int col = it.row0 + row;
     const bool live = col < it.ncols;
-    const int col_k = col / group;
+    const int col_k = col / it.group;
     const int lim = live ? items.seen(col) : 0;
-    const long long elem = live ? (long long)(it.head * group + col % group) * D + half * HD : 0;
+    const long long elem = live ? (long long)(it.head * it.group + col - col_k * it.group) * D + half * HD : 0;
     // ---- q into TMEM: scaled by a power of two per row, high and low part; within eight dims in the order of the unpacked
     // codes (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with its q: this thread has waited for them
     float zscale;
@@ -680,7 +706,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       const int absent = M.absent[inf] >> (2 * half) & 3;
       if (i >= 2) note_bad(ni - 2);
       tmem_wait_ld();
-      const int pos0 = i * kPosTile + 32 * half;
+      const int pos0 = (it.t0 + i) * kPosTile + 32 * half;
       if (pos0 + 32 > lim_lo || absent) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
@@ -777,7 +803,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     named_bar(1 + (warp & 3), 64);
     sum += M.top[(n + nt) & 1][half ^ 1][row];
     named_bar(1 + (warp & 3), 64);  // read before the next item writes there
-    const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+    const float inv = !ok ? NAN : parts > 1 ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+    if (parts > 1 && half == 0) *part_ml(a, it.count, it.number, kRowsTile, row, D) = make_float2(ref, sum);
 #pragma unroll
     for (int c = 0; c < HD; c += 32) {  // 32 dims: a block
       float v[32];
@@ -801,8 +828,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       for (int j = 0; j < 32; ++j) v[j] *= factor;
       const long long at = (long long)(it.start + col_k) * a.out_stride + elem + c;
       if (!live) {
-      } else if (dtype == KV4_F32) {
-        float4* out = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at);
+      } else if (dtype == KV4_F32 || parts > 1) {
+        float4* out = reinterpret_cast<float4*>(
+            parts > 1 ? part_row(a, it.number, kRowsTile, row, D) + half * HD + c : reinterpret_cast<float*>(a.out) + at);
 #pragma unroll
         for (int j = 0; j < 8; ++j) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       } else {
@@ -843,11 +871,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 // scores that are written there wait for the product that reads P.  q lies in shared memory: TMEM holds the two tiles'
 // S and P, two of each, and O.
 constexpr uint32_t kColPairS = 0, kColPairO = 256;
-constexpr int kRegsPairSoft = 144, kRegsPairRest = 48;  // a whole row of scores per thread
-static_assert(32 * (kSoftWarps * kRegsPairSoft + kProdWarps * kRegsProd + 4 * kRegsPairRest) <= kChunkThreads * kRegsStart, "the trade adds up");
+constexpr int kRegsPairSoft = 144, kRegsPairProd = 72, kRegsPairRest = 48;  // a whole row of scores per thread
+static_assert(32 * (kSoftWarps * kRegsPairSoft + kProdWarps * kRegsPairProd + 4 * kRegsPairRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 
-template <int D>
-__global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4AttnArgs a, int /* STAGE_BF16 */) {
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4AttnArgs a, int /* STAGE_BF16 */, int parts_of_row) {
   constexpr int KS = 3, q_tile = kRowsTile * D * 2;
   using L = ChunkLayout<D, 1, KS, 2 * q_tile>;
   extern __shared__ unsigned char chunk_raw[];
@@ -856,13 +884,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  ChunkItems items(a, 2 * kRowsTile);
+  ChunkItems<2 * kRowsTile, SPLIT> items(a, parts_of_row);
+  const int parts = items.parts;
   const ChunkItem& it = items.it;
-  const int group = items.group;
-  // tiles of positions that row tile g of the item sees (0: it has no rows)
+  // the item's tiles of positions that its row tile g sees
   auto tiles_of = [&](int g) {
     const int r0 = it.row0 + g * kRowsTile;
-    return r0 < it.ncols ? (items.seen(min(it.ncols, r0 + kRowsTile) - 1) + kPosTile - 1) / kPosTile : 0;
+    const int all = r0 < it.ncols ? (items.seen(min(it.ncols, r0 + kRowsTile) - 1) + kPosTile - 1) / kPosTile : 0;
+    return min(max(all - it.t0, 0), it.nt);
   };
 
   if (tid == 0) chunk_init(M);
@@ -876,7 +905,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
   const uint32_t tmem = M.tmem;
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
-    regs_down<kRegsProd>();
+    regs_down<kRegsPairProd>();
     chunk_expand<D, 1, 1, KS, L>(sm, M, items);
   } else if (warp >= kSoftWarps + kProdWarps) {
     regs_down<kRegsPairRest>();
@@ -967,10 +996,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
     for (long long w_item = blockIdx.x; items.next(w_item); n += it.nt) {
       const int r0 = it.row0 + g * kRowsTile, nt = tiles_of(g);
       if (r0 >= it.ncols) continue;
-      const int lim_lo = items.seen(r0), col = r0 + row, col_k = col / group;
+      const int lim_lo = items.seen(r0), col = r0 + row, col_k = col / it.group;
       const bool live = col < it.ncols;
       const int lim = live ? items.seen(col) : 0;
-      const long long elem = live ? (long long)(it.head * group + col % group) * D : 0;
+      const long long elem = live ? (long long)(it.head * it.group + col - col_k * it.group) * D : 0;
       // ---- q into shared memory: fp16, scaled by a power of two per row, eight dims in the order of the unpacked codes
       // (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with their q: this thread has waited for them
       float zscale;
@@ -1035,7 +1064,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
         const int absent = M.absent[inf];
         if (i >= 2) note_bad(ni - 2);
         tmem_wait_ld();
-        const int pos0 = i * kPosTile;
+        const int pos0 = (it.t0 + i) * kPosTile;
         if (pos0 + kPosTile > lim_lo || absent) {
 #pragma unroll
           for (int j = 0; j < kPosTile; ++j)
@@ -1093,7 +1122,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
         if (nt > 1) note_bad(n + nt - 2);
         note_bad(n + nt - 1);
       }
-      const float inv = !ok ? NAN : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+      const float inv = !ok ? NAN : parts > 1 ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+      if (parts > 1) *part_ml(a, it.count, it.number, 2 * kRowsTile, g * kRowsTile + row, D) = make_float2(ref, sum);
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {  // a block of dims
         uint32_t r[32];
@@ -1105,7 +1135,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
         const float factor = nan_blocks >> (d >> 5) & 1 ? NAN : inv;
-        if (live) {
+        if (live && parts > 1) {
+          float4* out = reinterpret_cast<float4*>(part_row(a, it.number, 2 * kRowsTile, g * kRowsTile + row, D) + d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            out[j] = make_float4(__uint_as_float(r[4 * j]) * factor, __uint_as_float(r[4 * j + 1]) * factor,
+                                 __uint_as_float(r[4 * j + 2]) * factor, __uint_as_float(r[4 * j + 3]) * factor);
+        } else if (live) {
           uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + (long long)(it.start + col_k) * a.out_stride + elem + d);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1131,9 +1167,61 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
   }
 }
 
-// Launches one of the kernels, one CTA per SM at most.
+// Joins the parts of a row, in their order: a warp per row.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4AttnArgs a, int dtype, int parts) {
+  constexpr int rows = ROWS;
+  constexpr int N = D / 32;  // dims of a lane
+  ChunkItems<ROWS, true> items(a, parts);
+  const ChunkItem& it = items.it;
+  const long long first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // row, counted over all row tiles
+  const int lane = threadIdx.x & 31, row = (int)(first % rows);
+  const long long number = first / rows * parts;
+  if (number >= it.count || !items.at(number) || it.row0 + row >= it.ncols) return;
+  float top = -INFINITY, sum = 0.f, v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (int p = 0; p < parts; ++p) top = fmaxf(top, part_ml(a, it.count, number + p, rows, row, D)->x);
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = *part_ml(a, it.count, number + p, rows, row, D);
+    const float k = ml.x == top ? 1.f : exp2_approx(ml.x - top);
+    const float* src = part_row(a, number + p, rows, row, D) + lane * N;
+    sum = fmaf(ml.y, k, sum);
+    if constexpr (N == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      v[0] = fmaf(x.x, k, v[0]), v[1] = fmaf(x.y, k, v[1]), v[2] = fmaf(x.z, k, v[2]), v[3] = fmaf(x.w, k, v[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      v[0] = fmaf(x.x, k, v[0]), v[1] = fmaf(x.y, k, v[1]);
+    }
+  }
+  const int at = it.row0 + row, k = at / it.group;
+  const long long out = (long long)(it.start + k) * a.out_stride + (it.head * it.group + at % it.group) * D + lane * N;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) store_elem(a.out, dtype, out + i, v[i] * inv);
+}
+
+// Where the row tiles alone leave SMs without work, the positions of each are shared out over `parts` items, of four
+// tiles at least.
+int chunk_parts(long long row_tiles, int max_len, int sms) {
+  const long long tiles = (max_len + kPosTile - 1) / kPosTile;
+  const long long most = min((long long)min(sms, kKv4ChunkParts) / max(row_tiles, 1ll), tiles / 4);
+  return (int)max(1ll, most);
+}
+
+// Row tiles of ROWS rows at the call's bounds, and the parts of each.
+template <int ROWS>
+long long chunk_tiles(const Kv4AttnArgs& a) {
+  const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
+  return (cols + ROWS - 1) / ROWS * a.c.n_kv_heads * a.n_seqs;
+}
+
+// Launches a kernel, one CTA per SM at most.
 template <typename Kernel>
-cudaError_t launch_items(Kernel* kern, int smem, int rows, const Kv4AttnArgs& a, int dtype, std::atomic<uint64_t>& ready, cudaStream_t st) {
+cudaError_t launch_items(Kernel* kern, int smem, long long items, const Kv4AttnArgs& a, int dtype, int parts, std::atomic<uint64_t>& ready,
+                         cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1142,39 +1230,48 @@ cudaError_t launch_items(Kernel* kern, int smem, int rows, const Kv4AttnArgs& a,
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
-  const long long items = (cols + rows - 1) / rows * a.c.n_kv_heads * a.n_seqs;
-  kern<<<(int)min(items, (long long)sm_count()), kChunkThreads, smem, st>>>(a, dtype);
+  kern<<<(int)min(items, (long long)sm_count()), kChunkThreads, smem, st>>>(a, dtype, parts);
   return cudaGetLastError();
 }
 
-template <int D, int NQ, int NKV, int NP>
-cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
-  constexpr int smem = ChunkLayout<D, NKV, 2, 0>::bytes;
+// The kernel for one row tile per item, or (PAIR) for two.
+template <int D, int NQ, int NKV, int NP, bool PAIR, bool SPLIT>
+cudaError_t launch_split(const Kv4AttnArgs& a, int dtype, long long tiles, int parts, cudaStream_t st) {
+  constexpr int ROWS = (PAIR ? 2 : 1) * kRowsTile;
+  constexpr int smem = PAIR ? ChunkLayout<D, 1, 3, 2 * kRowsTile * D * 2>::bytes : ChunkLayout<D, NKV, 2, 0>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<uint64_t> ready{0};
-  return launch_items(kv4_chunk_kernel<D, NQ, NKV, NP>, smem, kRowsTile, a, dtype, ready, st);
+  cudaError_t e;
+  if constexpr (PAIR) e = launch_items(kv4_pair_kernel<D, SPLIT>, smem, tiles * parts, a, dtype, parts, ready, st);
+  else e = launch_items(kv4_chunk_kernel<D, NQ, NKV, NP, SPLIT>, smem, tiles * parts, a, dtype, parts, ready, st);
+  if (!SPLIT || e != cudaSuccess) return e;
+  kv4_join_kernel<D, ROWS><<<(unsigned)((tiles * ROWS + 7) / 8), 256, 0, st>>>(a, dtype, parts);
+  return cudaGetLastError();
 }
 
-template <int D>
-cudaError_t launch_pair(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
-  constexpr int smem = ChunkLayout<D, 1, 3, 2 * kRowsTile * D * 2>::bytes;
-  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  static std::atomic<uint64_t> ready{0};
-  return launch_items(kv4_pair_kernel<D>, smem, 2 * kRowsTile, a, dtype, ready, st);
+template <int D, int NQ, int NKV, int NP, bool PAIR>
+cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
+  const long long tiles = chunk_tiles<(PAIR ? 2 : 1) * kRowsTile>(a);
+  const int parts = chunk_parts(tiles, a.max_len, sm_count());
+  return parts > 1 ? launch_split<D, NQ, NKV, NP, PAIR, true>(a, dtype, tiles, parts, st)
+                   : launch_split<D, NQ, NKV, NP, PAIR, false>(a, dtype, tiles, 1, st);
 }
 
 }  // namespace
 
+size_t kv4_chunk_ws_bytes(int head_dim) {
+  return kKv4CounterBytes + (size_t)kKv4ChunkParts * 2 * kRowsTile * (head_dim + 2) * sizeof(float);
+}
+
 cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st) {
   if (head_dim == 128) {
-    if (dtype == KV4_F32) return launch_chunk<128, 2, 2, 2>(a, dtype, st);
-    if (dtype == KV4_F16) return launch_chunk<128, 1, 2, 1>(a, dtype, st);
-    return launch_pair<128>(a, dtype, st);
+    if (dtype == KV4_F32) return launch_chunk<128, 2, 2, 2, false>(a, dtype, st);
+    if (dtype == KV4_F16) return launch_chunk<128, 1, 2, 1, false>(a, dtype, st);
+    return launch_chunk<128, 1, 1, 1, true>(a, dtype, st);
   }
-  if (dtype == KV4_F32) return launch_chunk<64, 2, 2, 2>(a, dtype, st);
-  if (dtype == KV4_F16) return launch_chunk<64, 1, 2, 1>(a, dtype, st);
-  return launch_pair<64>(a, dtype, st);
+  if (dtype == KV4_F32) return launch_chunk<64, 2, 2, 2, false>(a, dtype, st);
+  if (dtype == KV4_F16) return launch_chunk<64, 1, 2, 1, false>(a, dtype, st);
+  return launch_chunk<64, 1, 1, 1, true>(a, dtype, st);
 }
 
 }  // namespace lrs

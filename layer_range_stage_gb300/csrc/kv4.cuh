@@ -80,6 +80,12 @@ struct Kv4AttnArgs {
   void* ws = nullptr;
 };
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
+// Workspace: arrival counters, zero between calls, which calls of many columns leave alone; then partial results.
+constexpr int kKv4MaxCtas = 512;
+constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(unsigned);
+// Row tiles times parts that the workspace of a chunk call holds.
+constexpr int kKv4ChunkParts = 192;
+size_t kv4_chunk_ws_bytes(int head_dim);
 cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
 size_t kv4_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int max_len);
 

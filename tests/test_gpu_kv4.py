@@ -458,6 +458,39 @@ def test_two_streams_with_a_workspace_each(B):
         check_attention(out, kv4.attention(cache, q, cu, length, table), "f32")
 
 
+def test_one_workspace_for_chunks_and_decode_in_turn(B):
+    """A workspace of the larger size serves calls of both sizes one after another: each leaves it ready for the next."""
+    rng = np.random.default_rng(75)
+    few = attention_case(rng, 2, 4, 128, 32, [(1, 3000)], "f32", extra=0)
+    many = attention_case(rng, 2, 4, 128, 32, [(60, 2100)], "f32", extra=0)
+    size = max(B.stage_op_kv4_attention_workspace_bytes(1, 8, 2, 128, q, 3000) for q in (1, 60))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for cache, table, cu, length, q in (few, many, few, many, many, few):
+        out = run_attention(B, cache, table, cu, length, q, "f32", ws=ws)
+        check_attention(out, kv4.attention(cache, q, cu, length, table), "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("hkv,group,d,rows", [(1, 4, 128, [(70, 1500)]), (2, 1, 64, [(40, 2000), (0, 7), (36, 500)]), (1, 8, 128, [(40, 40), (33, 3000)])])
+def test_few_row_tiles_share_their_positions_out(B, hkv, group, d, rows, dtype):
+    """Few row tiles over long contexts: the positions of a tile are shared out, some parts are empty for short sequences,
+    and a NaN in V reaches the rows and dims that it reaches otherwise."""
+    rng = np.random.default_rng(77 + d)
+    cache, table, cu, length, q = attention_case(rng, hkv, group, d, 16, rows, dtype)
+    out = run_attention(B, cache, table, cu, length, q, dtype)
+    want = kv4.attention(cache, q, cu, length, table)
+    check_attention(out, want, dtype)
+    at = int(length[0]) // 2
+    vs = int(kv4.scale_place(at % 16, 0, d, True))
+    cache[table[0, at // 16], 0, 0, vs:vs + 2] = [0xFF, 0x7F]
+    got = run_attention(B, cache, table, cu, length, q, dtype).double().cpu().numpy()
+    hit = np.zeros(q.shape, bool)
+    first = max(0, at - (int(length[0]) - rows[0][0]))
+    hit[first:rows[0][0], :group, :32] = True
+    assert np.isnan(got[hit]).all()
+    check_attention(torch.from_numpy(got), want, dtype, ~np.isnan(want[0]) & ~hit)
+
+
 # ------------------------------------------------------------------------------------------- refusals through the binding
 
 def test_binding_refusals(B):
