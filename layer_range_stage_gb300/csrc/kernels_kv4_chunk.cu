@@ -1,7 +1,7 @@
 // Attention of many query tokens per sequence (prompt chunks) over the paged 4-bit KV cache (sm_103a): tcgen05 tiles.
 //
 // A work item is 128 rows -- (token, head of the group) pairs of one sequence and KV head -- against the positions they
-// see, in tiles of 64.  One CTA per SM goes through its items (the longest first, dealt in turn) without a barrier
+// see, in tiles of 64.  One CTA per SM goes through its items (the longest first, dealt forth and back) without a barrier
 // between them: a tile's number n runs on over the items, and the copies and the expansion of the next item's first
 // tiles go on while the last item's results are put down.  Roles, joined by mbarriers:
 //   warps 0-7   softmax: warp w has the rows 32 (w % 4) .. + 31 (the TMEM lanes it may read), w / 4 the half of a tile's
@@ -41,8 +41,9 @@ namespace {
 constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
 constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 16 * kProdWarps;  // kProd: threads of a group of four warps
 constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpgroups
-// Registers per thread: the block starts with kRegsStart and its warpgroups trade them.
-constexpr int kRegsStart = 96, kRegsSoft = 136, kRegsProd = 72, kRegsRest = 64;
+// Registers per thread: the block starts with kRegsStart and its warpgroups trade them (4 x 512 rows, STAGE_F32: 64 us with
+// 136, 72, 64; 61 with these, 71 with 128, 80, 64; 2 x 1024 rows, STAGE_BF16: 377, 355, 369).
+constexpr int kRegsStart = 96, kRegsSoft = 152, kRegsProd = 64, kRegsRest = 48;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
 constexpr int kInfo = 16;  // ring of what the tiles' producers tell the softmax
@@ -62,38 +63,44 @@ struct ChunkBars {
   uint64_t pair_q[2], pair_s[2][2], pair_p[2][2], pair_o[2][2];  // of the kernel with two row tiles: [tile][buffer]
 };
 
+// What a call has, the same for all its items: read from the kernel's parameters, so that it takes no registers.
+struct ChunkArgs : Kv4AttnArgs {
+  long long count;       // items
+  int group, row_tiles;  // query heads per KV head; row tiles of a sequence at the call's bounds
+  int parts;             // of a row tile's positions
+};
+
 struct ChunkItem {
-  long long number, count;         // of this item, and of all
-  int group, row_tiles;            // query heads per KV head; row tiles of a sequence at the call's bounds
+  long long number;
   int seq, head, row0;             // sequence, KV head, first row
   int start, tokens, len, ncols;   // first query token of the sequence, its tokens, its positions, its rows
   int lim_hi, t0, nt;              // positions that some row sees; the first of the item's tiles and how many they are
 };
 
 // Items of ROWS rows: row tiles from the last (which sees most) down, then KV heads, then sequences, then the parts of
-// their positions; a CTA has every gridDim.x-th.  Every warp goes through them for itself.  SPLIT: whether
-// there are parts; without them the loops keep their registers for their work.
+// their positions, dealt to the CTAs forth and back: c, 2 G - 1 - c, 2 G + c, ... of G, so that nobody has the longest of
+// every round (4 x 512 rows, STAGE_F32: 64 us, 66 dealt forth alone).  Every warp goes through them for itself.
+// SPLIT: whether there are parts.  What a loop over tiles has to keep counts: the kernels live off their last registers.
 template <int ROWS, bool SPLIT>
 struct ChunkItems {
-  const Kv4AttnArgs& a;
-  const int parts;
+  const ChunkArgs& a;
   ChunkItem it;
-  __device__ __forceinline__ ChunkItems(const Kv4AttnArgs& args, int parts_of_row) : a(args), parts(SPLIT ? parts_of_row : 1) {
-    it.group = a.n_q_heads / a.c.n_kv_heads;
-    it.row_tiles = (int)(((long long)a.max_q * it.group + ROWS - 1) / ROWS);
-    it.count = (long long)it.row_tiles * a.c.n_kv_heads * a.n_seqs * parts;
-  }
+  int round = 0;
+  __device__ __forceinline__ explicit ChunkItems(const ChunkArgs& args) : a(args) {}
   // Takes number w apart; false if its sequence has no such rows.
   __device__ __forceinline__ bool at(long long w) {
+    const int parts = SPLIT ? a.parts : 1;
     const long long per = (long long)a.c.n_kv_heads * a.n_seqs * parts;
-    const int row_tile = it.row_tiles - 1 - (int)(w / per), rest = (int)(w % per), part = rest % parts, row = rest / parts;
+    // counts rarely need 64 bits
+    const long long back = a.count >> 32 ? w / per : (long long)((uint32_t)w / (uint32_t)per);
+    const int row_tile = a.row_tiles - 1 - (int)back, rest = (int)(w - back * per), part = rest % parts, row = rest / parts;
     const int seq = row / a.c.n_kv_heads, row0 = row_tile * ROWS;
     int start;
-    const int tokens = seq_tokens(a, seq, &start), ncols = min(tokens, a.max_q) * it.group;
+    const int tokens = seq_tokens(a, seq, &start), ncols = min(tokens, a.max_q) * a.group;
     if (row0 >= ncols) return false;
     it.number = w;
     it.seq = seq;
-    it.head = row % a.c.n_kv_heads;
+    it.head = row - seq * a.c.n_kv_heads;
     it.row0 = row0;
     it.start = start;
     it.tokens = tokens;
@@ -105,17 +112,17 @@ struct ChunkItems {
     it.nt = (int)(nt * (part + 1) / parts) - it.t0;
     return true;
   }
-  // The next item from number w on; false behind the last.
-  __device__ __forceinline__ bool next(long long& w) {
-    for (; w < it.count; w += gridDim.x)
-      if (at(w)) {
-        w += gridDim.x;
-        return true;
-      }
-    return false;
+  // The CTA's next item; false behind the last.
+  __device__ __forceinline__ bool next() {
+    while (true) {
+      const long long w = (long long)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (w >= a.count) return false;
+      ++round;
+      if (at(w)) return true;
+    }
   }
   // Positions that the item's sequence shows to row r.
-  __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.tokens + r / it.group + 1); }
+  __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.tokens + r / a.group + 1); }
 };
 
 struct alignas(16) ChunkMisc {
@@ -134,7 +141,8 @@ struct alignas(16) ChunkMisc {
 
 static_assert(offsetof(ChunkMisc, v_pos_exp) % 16 == 0 && offsetof(ChunkMisc, v_pos_inv) % 16 == 0, "vector reads");
 
-// Shared memory: KS stages of K and of V operands behind QB bytes of q.
+// Shared memory: KS stages of K and of V operands behind QB bytes of q, or of the warps' places to turn rows (kTurn each).
+constexpr int kTurn = 32 * 128;
 template <int D, int NKV, int KS, int QB>
 struct ChunkLayout {
   static constexpr int k_part = kPosTile * D * 2, v_part = D * kPosTile * 2;
@@ -158,6 +166,52 @@ __device__ __forceinline__ bool cwait(uint64_t* bar, uint32_t parity, volatile i
     }
   }
   return true;
+}
+
+// A softmax thread works on a row, but 32 rows in one access are 32 lines: rows go between global memory and their
+// threads through kTurn bytes of the warp's shared memory, CH 16-byte pieces of a row at a time, swizzled, and a line is
+// touched once (4 x 512 rows, STAGE_F32: 66 us, 71 with a row per lane).  `off`: where the lane's row begins behind `base`, in
+// bytes; below 0: it is none.  The kernel for STAGE_BF16, whose items are longer, does without: there it cost registers, and
+// 397 us became 355 without it (2 x 1024 rows).
+template <int CH>
+__device__ __forceinline__ unsigned char* turn_place(unsigned char* turn, int row, int piece) {
+  return turn + (row * CH + (piece ^ (CH == 8 ? row & 7 : (row >> 1) & 3))) * 16;
+}
+template <int CH, int PASSES>
+__device__ __forceinline__ void rows_in(unsigned char* turn, const void* base, long long off, uint4 (&own)[PASSES * CH]) {
+  const int lane = threadIdx.x & 31;
+  uint4 v[PASSES][CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const long long at = __shfl_sync(0xffffffffu, off, i * (32 / CH) + lane / CH);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+      v[p][i] = at >= 0 ? *reinterpret_cast<const uint4*>((const char*)base + at + p * (16 * CH) + lane % CH * 16) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) *reinterpret_cast<uint4*>(turn_place<CH>(turn, i * (32 / CH) + lane / CH, lane % CH)) = v[p][i];
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < CH; ++j) own[p * CH + j] = *reinterpret_cast<const uint4*>(turn_place<CH>(turn, lane, j));
+    __syncwarp();
+  }
+}
+template <int CH>
+__device__ __forceinline__ void rows_out(unsigned char* turn, void* base, long long off, const uint4* own) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) *reinterpret_cast<uint4*>(turn_place<CH>(turn, lane, j)) = own[j];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int row = i * (32 / CH) + lane / CH;
+    const long long at = __shfl_sync(0xffffffffu, off, row);
+    const uint4 v = *reinterpret_cast<const uint4*>(turn_place<CH>(turn, row, lane % CH));
+    if (at >= 0) *reinterpret_cast<uint4*>((char*)base + at + lane % CH * 16) = v;
+  }
+  __syncwarp();
 }
 
 // Partial results, where a row tile's positions are shared out: per item and row the sums (float32, not divided), and
@@ -239,7 +293,7 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
   const uint32_t ex = exponent_bits();
   bool ok = true;  // a warp in which a wait has run out leaves as a whole
   int n = 0;
-  for (long long w = blockIdx.x; ok && items.next(w); n += it.nt)
+  for (; ok && items.next(); n += it.nt)
   for (int i = (n & 1) == group_of ? 0 : 1; i < it.nt; i += 2) {
     const int ni = n + i, st = ni % KS, rs = ni & (kRaw - 1), inf = ni & (kInfo - 1), lim_hi = it.lim_hi;
     ok = __all_sync(0xffffffffu, cwait(&B.raw_full[rs], (uint32_t)(ni / kRaw) & 1u, abort_flag));
@@ -440,12 +494,12 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
   constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
-  const Kv4AttnArgs& a = items.a;
+  const ChunkArgs& a = items.a;
   const ChunkItem& it = items.it;
   const int tpp = a.c.page_len / kKv4Tile;
   bool ok = true;
   int n = 0;
-  for (long long w = blockIdx.x; ok && items.next(w);) {
+  for (; ok && items.next();) {
     const int n16 = (it.lim_hi + kKv4Tile - 1) / kKv4Tile;
     const int* trow = a.table + (long long)it.seq * a.table_stride;
     // the pages of a tile are asked for a tile ahead; places go on without a division
@@ -496,9 +550,10 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
 }
 
 template <int D, int NQ, int NKV, int NP, bool SPLIT>
-__global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4AttnArgs a, int dtype, int parts_of_row) {
-  using L = ChunkLayout<D, NKV, 2, 0>;
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const ChunkArgs a) {
+  using L = ChunkLayout<D, NKV, 2, kSoftWarps * kTurn>;
   constexpr int HD = D / 2;  // dims of a softmax thread
+  constexpr bool F32 = NP == 2;
   extern __shared__ unsigned char chunk_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)chunk_raw + 1023) & ~(uintptr_t)1023);
   ChunkMisc& M = *reinterpret_cast<ChunkMisc*>(sm + L::off_misc);
@@ -506,8 +561,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  ChunkItems<kRowsTile, SPLIT> items(a, parts_of_row);
-  const int parts = items.parts;
+  ChunkItems<kRowsTile, SPLIT> items(a);
   const ChunkItem& it = items.it;
 
   if (tid == 0) chunk_init(M);
@@ -563,7 +617,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       };
       bool ok = true;
       uint32_t q_ph = 0;
-      for (long long w = blockIdx.x; ok && items.next(w);) {
+      for (; ok && items.next();) {
         if (it.nt == 0) continue;  // its q is not waited for, and not announced
         ok = __all_sync(0xffffffffu, cwait(&B.q_full, q_ph, abort_flag));
         q_ph ^= 1;
@@ -607,27 +661,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     regs_up<kRegsSoft>();
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const int row = 32 * (warp & 3) + lane, half = (warp >> 2) & 1;
+    unsigned char* turn = sm + warp * kTurn;
     bool ok = true;
     int n = 0;
-    for (long long w_item = blockIdx.x; items.next(w_item); n += it.nt) {
+    for (; items.next(); n += it.nt) {
     const int nt = it.nt, lim_lo = items.seen(it.row0);  // positions that every row sees
     const int col = it.row0 + row;
     const bool live = col < it.ncols;
-    const int col_k = col / it.group;
+    const int col_k = col / a.group;
     const int lim = live ? items.seen(col) : 0;
-    const long long elem = live ? (long long)(it.head * it.group + col - col_k * it.group) * D + half * HD : 0;
+    const long long elem = (long long)(it.head * a.group + col - col_k * a.group) * D + half * HD;
     // ---- q into TMEM: scaled by a power of two per row, high and low part; within eight dims in the order of the unpacked
     // codes (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with its q: this thread has waited for them
     float zscale;
     {
       float q[HD / 8][8], top = 0.f;
+      constexpr int W = HD * (F32 ? 4 : 2) / 16;  // 16-byte pieces of the thread's dims
+      uint4 own[W];
+      rows_in<W < 8 ? W : 8, W < 8 ? 1 : W / 8>(turn, a.q, live ? ((long long)(it.start + col_k) * a.q_stride + elem) * (F32 ? 4 : 2) : -1, own);
 #pragma unroll
       for (int g = 0; g < HD / 8; ++g) {
-        if (live) {
-          load8(a.q, dtype, (long long)(it.start + col_k) * a.q_stride + elem + 8 * g, q[g]);
-        } else {
+        if constexpr (F32) {
+          const uint4 lo = own[2 * g], hi = own[2 * g + 1];
+          const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[g][i] = 0.f;
+          for (int i = 0; i < 8; ++i) q[g][i] = __uint_as_float(u[i]);
+        } else {
+          const uint32_t u[4] = {own[g].x, own[g].y, own[g].z, own[g].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = h2_to_f2(u[i]);
+            q[g][2 * i] = f.x, q[g][2 * i + 1] = f.y;
+          }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[g][i]));
@@ -803,8 +868,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
     named_bar(1 + (warp & 3), 64);
     sum += M.top[(n + nt) & 1][half ^ 1][row];
     named_bar(1 + (warp & 3), 64);  // read before the next item writes there
-    const float inv = !ok ? NAN : parts > 1 ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
-    if (parts > 1 && half == 0) *part_ml(a, it.count, it.number, kRowsTile, row, D) = make_float2(ref, sum);
+    const float inv = !ok ? NAN : SPLIT ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+    if (SPLIT && half == 0) *part_ml(a, a.count, it.number, kRowsTile, row, D) = make_float2(ref, sum);
+    // where the results go: the output, or (float32) the part's place
+    void* out = SPLIT ? (void*)part_row(a, it.number, kRowsTile, 0, D) : a.out;
+    const long long to = SPLIT ? ((long long)row * D + half * HD) * 4 : ((long long)(it.start + col_k) * a.out_stride + elem) * (F32 ? 4 : 2);
+    uint4 narrow[HD / 8];
 #pragma unroll
     for (int c = 0; c < HD; c += 32) {  // 32 dims: a block
       float v[32];
@@ -826,33 +895,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
       const float factor = nan_blocks >> (c >> 5) & 1 ? NAN : inv;
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] *= factor;
-      const long long at = (long long)(it.start + col_k) * a.out_stride + elem + c;
-      if (!live) {
-      } else if (dtype == KV4_F32 || parts > 1) {
-        float4* out = reinterpret_cast<float4*>(
-            parts > 1 ? part_row(a, it.number, kRowsTile, row, D) + half * HD + c : reinterpret_cast<float*>(a.out) + at);
+      if constexpr (F32 || SPLIT) {
+        uint4 own[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) out[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        for (int j = 0; j < 8; ++j)
+          own[j] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+        rows_out<8>(turn, out, live ? to + c * 4 : -1, own);
       } else {
-        uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t u[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = v[8 * j + 2 * k], y = v[8 * j + 2 * k + 1];
-            if (dtype == KV4_F16) {
-              u[k] = as_u32(__floats2half2_rn(x, y));
-            } else {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-              u[k] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-          }
-          out[j] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
+        for (int j = 0; j < 4; ++j)
+          narrow[c / 8 + j] = make_uint4(as_u32(__floats2half2_rn(v[8 * j], v[8 * j + 1])), as_u32(__floats2half2_rn(v[8 * j + 2], v[8 * j + 3])),
+                                         as_u32(__floats2half2_rn(v[8 * j + 4], v[8 * j + 5])), as_u32(__floats2half2_rn(v[8 * j + 6], v[8 * j + 7])));
       }
-      __syncwarp();  // the next block's TMEM read is the whole warp's
     }
+    if constexpr (!F32 && !SPLIT) rows_out<HD / 8>(turn, out, live ? to : -1, narrow);
     tc_fence_before();
     }
   }
@@ -871,11 +927,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Kv4At
 // scores that are written there wait for the product that reads P.  q lies in shared memory: TMEM holds the two tiles'
 // S and P, two of each, and O.
 constexpr uint32_t kColPairS = 0, kColPairO = 256;
-constexpr int kRegsPairSoft = 144, kRegsPairProd = 72, kRegsPairRest = 48;  // a whole row of scores per thread
-static_assert(32 * (kSoftWarps * kRegsPairSoft + kProdWarps * kRegsPairProd + 4 * kRegsPairRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4AttnArgs a, int /* STAGE_BF16 */, int parts_of_row) {
+__global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkArgs a) {
   constexpr int KS = 3, q_tile = kRowsTile * D * 2;
   using L = ChunkLayout<D, 1, KS, 2 * q_tile>;
   extern __shared__ unsigned char chunk_raw[];
@@ -884,8 +938,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  ChunkItems<2 * kRowsTile, SPLIT> items(a, parts_of_row);
-  const int parts = items.parts;
+  ChunkItems<2 * kRowsTile, SPLIT> items(a);
   const ChunkItem& it = items.it;
   // the item's tiles of positions that its row tile g sees
   auto tiles_of = [&](int g) {
@@ -905,10 +958,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
   const uint32_t tmem = M.tmem;
 
   if (warp >= kSoftWarps && warp < kSoftWarps + kProdWarps) {
-    regs_down<kRegsPairProd>();
+    regs_down<kRegsProd>();
     chunk_expand<D, 1, 1, KS, L>(sm, M, items);
   } else if (warp >= kSoftWarps + kProdWarps) {
-    regs_down<kRegsPairRest>();
+    regs_down<kRegsRest>();
     if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) chunk_copy<D, L>(sm, M, items);
     if (warp == kSoftWarps + kProdWarps) {
       // ---------------- products (as in the kernel with one row tile: one elected thread of a converged warp) ----------------
@@ -960,7 +1013,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
       };
       bool ok = true;
       int n = 0;
-      for (long long w = blockIdx.x; ok && items.next(w); n += it.nt) {
+      for (; ok && items.next(); n += it.nt) {
         const int nt0 = tiles_of(0), nt1 = tiles_of(1);
         for (int g = 0; g < 2; ++g)
           if (ok && (g ? nt1 : nt0) > 0) {
@@ -986,20 +1039,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
     }
   } else {
     // ---------------- softmax ----------------
-    regs_up<kRegsPairSoft>();
+    regs_up<kRegsSoft>();
     const int g = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t place_s = lanes + kColPairS + g * 128, place_o = lanes + kColPairO + g * 128;
     bool ok = true;
     int n = 0;
     uint32_t c = 0;  // tiles of this row tile so far
-    for (long long w_item = blockIdx.x; items.next(w_item); n += it.nt) {
+    for (; items.next(); n += it.nt) {
       const int r0 = it.row0 + g * kRowsTile, nt = tiles_of(g);
       if (r0 >= it.ncols) continue;
-      const int lim_lo = items.seen(r0), col = r0 + row, col_k = col / it.group;
+      const int lim_lo = items.seen(r0), col = r0 + row, col_k = col / a.group;
       const bool live = col < it.ncols;
       const int lim = live ? items.seen(col) : 0;
-      const long long elem = live ? (long long)(it.head * it.group + col - col_k * it.group) * D : 0;
+      const long long elem = live ? (long long)(it.head * a.group + col - col_k * a.group) * D : 0;
       // ---- q into shared memory: fp16, scaled by a power of two per row, eight dims in the order of the unpacked codes
       // (0, 4, 1, 5, 2, 6, 3, 7).  The last item's scores are done with their q: this thread has waited for them
       float zscale;
@@ -1122,8 +1175,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
         if (nt > 1) note_bad(n + nt - 2);
         note_bad(n + nt - 1);
       }
-      const float inv = !ok ? NAN : parts > 1 ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
-      if (parts > 1) *part_ml(a, it.count, it.number, 2 * kRowsTile, g * kRowsTile + row, D) = make_float2(ref, sum);
+      const float inv = !ok ? NAN : SPLIT ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
+      if (SPLIT) *part_ml(a, a.count, it.number, 2 * kRowsTile, g * kRowsTile + row, D) = make_float2(ref, sum);
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {  // a block of dims
         uint32_t r[32];
@@ -1135,7 +1188,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
         const float factor = nan_blocks >> (d >> 5) & 1 ? NAN : inv;
-        if (live && parts > 1) {
+        if (live && SPLIT) {
           float4* out = reinterpret_cast<float4*>(part_row(a, it.number, 2 * kRowsTile, g * kRowsTile + row, D) + d);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -1169,22 +1222,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const Kv4Att
 
 // Joins the parts of a row, in their order: a warp per row.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4AttnArgs a, int dtype, int parts) {
+__global__ void __launch_bounds__(256) kv4_join_kernel(const ChunkArgs a, int dtype) {
   constexpr int rows = ROWS;
   constexpr int N = D / 32;  // dims of a lane
-  ChunkItems<ROWS, true> items(a, parts);
+  const int parts = a.parts;
+  ChunkItems<ROWS, true> items(a);
   const ChunkItem& it = items.it;
   const long long first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // row, counted over all row tiles
   const int lane = threadIdx.x & 31, row = (int)(first % rows);
   const long long number = first / rows * parts;
-  if (number >= it.count || !items.at(number) || it.row0 + row >= it.ncols) return;
+  if (number >= a.count || !items.at(number) || it.row0 + row >= it.ncols) return;
   float top = -INFINITY, sum = 0.f, v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int p = 0; p < parts; ++p) top = fmaxf(top, part_ml(a, it.count, number + p, rows, row, D)->x);
+  for (int p = 0; p < parts; ++p) top = fmaxf(top, part_ml(a, a.count, number + p, rows, row, D)->x);
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    const float2 ml = *part_ml(a, it.count, number + p, rows, row, D);
+    const float2 ml = *part_ml(a, a.count, number + p, rows, row, D);
     const float k = ml.x == top ? 1.f : exp2_approx(ml.x - top);
     const float* src = part_row(a, number + p, rows, row, D) + lane * N;
     sum = fmaf(ml.y, k, sum);
@@ -1196,8 +1250,8 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const Kv4AttnArgs a, int 
       v[0] = fmaf(x.x, k, v[0]), v[1] = fmaf(x.y, k, v[1]);
     }
   }
-  const int at = it.row0 + row, k = at / it.group;
-  const long long out = (long long)(it.start + k) * a.out_stride + (it.head * it.group + at % it.group) * D + lane * N;
+  const int at = it.row0 + row, k = at / a.group;
+  const long long out = (long long)(it.start + k) * a.out_stride + (it.head * a.group + at % a.group) * D + lane * N;
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) store_elem(a.out, dtype, out + i, v[i] * inv);
@@ -1211,17 +1265,9 @@ int chunk_parts(long long row_tiles, int max_len, int sms) {
   return (int)max(1ll, most);
 }
 
-// Row tiles of ROWS rows at the call's bounds, and the parts of each.
-template <int ROWS>
-long long chunk_tiles(const Kv4AttnArgs& a) {
-  const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
-  return (cols + ROWS - 1) / ROWS * a.c.n_kv_heads * a.n_seqs;
-}
-
 // Launches a kernel, one CTA per SM at most.
 template <typename Kernel>
-cudaError_t launch_items(Kernel* kern, int smem, long long items, const Kv4AttnArgs& a, int dtype, int parts, std::atomic<uint64_t>& ready,
-                         cudaStream_t st) {
+cudaError_t launch_items(Kernel* kern, int smem, const ChunkArgs& a, std::atomic<uint64_t>& ready, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1230,31 +1276,36 @@ cudaError_t launch_items(Kernel* kern, int smem, long long items, const Kv4AttnA
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  kern<<<(int)min(items, (long long)sm_count()), kChunkThreads, smem, st>>>(a, dtype, parts);
+  kern<<<(int)min(a.count, (long long)sm_count()), kChunkThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 // The kernel for one row tile per item, or (PAIR) for two.
 template <int D, int NQ, int NKV, int NP, bool PAIR, bool SPLIT>
-cudaError_t launch_split(const Kv4AttnArgs& a, int dtype, long long tiles, int parts, cudaStream_t st) {
+cudaError_t launch_split(const ChunkArgs& a, int dtype, cudaStream_t st) {
   constexpr int ROWS = (PAIR ? 2 : 1) * kRowsTile;
-  constexpr int smem = PAIR ? ChunkLayout<D, 1, 3, 2 * kRowsTile * D * 2>::bytes : ChunkLayout<D, NKV, 2, 0>::bytes;
+  constexpr int smem = PAIR ? ChunkLayout<D, 1, 3, 2 * kRowsTile * D * 2>::bytes : ChunkLayout<D, NKV, 2, kSoftWarps * kTurn>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<uint64_t> ready{0};
   cudaError_t e;
-  if constexpr (PAIR) e = launch_items(kv4_pair_kernel<D, SPLIT>, smem, tiles * parts, a, dtype, parts, ready, st);
-  else e = launch_items(kv4_chunk_kernel<D, NQ, NKV, NP, SPLIT>, smem, tiles * parts, a, dtype, parts, ready, st);
+  if constexpr (PAIR) e = launch_items(kv4_pair_kernel<D, SPLIT>, smem, a, ready, st);
+  else e = launch_items(kv4_chunk_kernel<D, NQ, NKV, NP, SPLIT>, smem, a, ready, st);
   if (!SPLIT || e != cudaSuccess) return e;
-  kv4_join_kernel<D, ROWS><<<(unsigned)((tiles * ROWS + 7) / 8), 256, 0, st>>>(a, dtype, parts);
+  kv4_join_kernel<D, ROWS><<<(unsigned)((a.count / a.parts * ROWS + 7) / 8), 256, 0, st>>>(a, dtype);
   return cudaGetLastError();
 }
 
 template <int D, int NQ, int NKV, int NP, bool PAIR>
-cudaError_t launch_chunk(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
-  const long long tiles = chunk_tiles<(PAIR ? 2 : 1) * kRowsTile>(a);
-  const int parts = chunk_parts(tiles, a.max_len, sm_count());
-  return parts > 1 ? launch_split<D, NQ, NKV, NP, PAIR, true>(a, dtype, tiles, parts, st)
-                   : launch_split<D, NQ, NKV, NP, PAIR, false>(a, dtype, tiles, 1, st);
+cudaError_t launch_chunk(const Kv4AttnArgs& args, int dtype, cudaStream_t st) {
+  constexpr int ROWS = (PAIR ? 2 : 1) * kRowsTile;
+  ChunkArgs a;
+  static_cast<Kv4AttnArgs&>(a) = args;
+  a.group = a.n_q_heads / a.c.n_kv_heads;
+  a.row_tiles = (int)(((long long)a.max_q * a.group + ROWS - 1) / ROWS);
+  const long long tiles = (long long)a.row_tiles * a.c.n_kv_heads * a.n_seqs;
+  a.parts = chunk_parts(tiles, a.max_len, sm_count());
+  a.count = tiles * a.parts;
+  return a.parts > 1 ? launch_split<D, NQ, NKV, NP, PAIR, true>(a, dtype, st) : launch_split<D, NQ, NKV, NP, PAIR, false>(a, dtype, st);
 }
 
 }  // namespace
