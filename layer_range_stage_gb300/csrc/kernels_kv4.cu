@@ -241,9 +241,10 @@ template <typename T>
 struct Row8;
 template <>
 struct Row8<float> {
-  static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  static constexpr int kWords = 8;
+  static __device__ __forceinline__ void values(const uint32_t (&w)[kWords], float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   }
   // Neighbouring lanes swap halves, so that each of the two stores fills whole 32-byte sectors (`live` is the same in both).
   static __device__ __forceinline__ void store(float* p, const float (&v)[8], bool live) {
@@ -261,9 +262,8 @@ struct Row8<float> {
 };
 template <>
 struct Row8<__half> {
-  static __device__ __forceinline__ void load(const __half* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  static constexpr int kWords = 4;
+  static __device__ __forceinline__ void values(const uint32_t (&w)[kWords], float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -282,9 +282,8 @@ struct Row8<__half> {
 };
 template <>
 struct Row8<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  static constexpr int kWords = 4;
+  static __device__ __forceinline__ void values(const uint32_t (&w)[kWords], float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
@@ -310,6 +309,23 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return y;
 }
 
+// Of three.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return y;
+}
+
 // Quantise the eight values of this lane with the block's four lanes: the codes, eight to a word, and the scale's bits.
 // Code of x for the scale s (finite, not 0): the nearest integer to x / s, ties to even, plus 8, in [0, 15].  Adding
 // 1.5 * 2^23 to the product with the reciprocal leaves the integer n in the sum's low bits.  The product is off by less
@@ -317,11 +333,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 // (s has 11 bits, n four), is compared with s / 2.  The sums' bits, shifted four apart and added up, are the eight
 // codes and a constant.
 __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], int lane, uint16_t* scale) {
-  float high = x[0], low = x[0];
+  float high = max_nan(x[0], x[1]), low = min_nan(x[0], x[1]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    high = max_nan(high, x[i]);
-    low = min_nan(low, x[i]);
+  for (int i = 2; i < 8; i += 2) {
+    high = max_nan(high, x[i], x[i + 1]);
+    low = min_nan(low, x[i], x[i + 1]);
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
@@ -350,31 +366,33 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], int lane, 
   constexpr float kMagic = 12582912.f;
   float t[8], far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; i += 2) {
     t[i] = fmaf(x[i], inv, kMagic);
-    far = fmaxf(far, fabsf(fmaf(kMagic - t[i], s, x[i])));
+    t[i + 1] = fmaf(x[i + 1], inv, kMagic);
+    far = max_abs(far, fmaf(kMagic - t[i], s, x[i]), fmaf(kMagic - t[i + 1], s, x[i + 1]));
   }
   const float h = 0.5f * fabsf(s);
-  if (far > 0.9998f * h && s != 0.f) {
+  // A normal scale is m / -8 to 2^-11 of itself, so no integer lies below -8; a subnormal one may be further off
+  if (!(far <= 0.9998f * h && fabsf(s) >= 6.103515625e-5f)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float n = t[i] - kMagic, r = fmaf(-n, s, x[i]);
       const bool odd = __float_as_uint(t[i]) & 1;
       if (fabsf(r) > h || (fabsf(r) == h && odd)) t[i] += (r > 0.f) == (s > 0.f) ? 1.f : -1.f;
+      // all values count as 0 for the scale 0, and for none (NaN and infinities among them)
+      t[i] = s == 0.f ? kMagic : fmaxf(t[i], kMagic - 8.f);
     }
   }
   uint32_t c = 0;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
-    // NaN and infinities were taken care of by the scale: their product with inv = 0 counts as 0
-    const float v = s == 0.f ? kMagic : fminf(fmaxf(t[i], kMagic - 8.f), kMagic + 7.f);
-    c = c * 16u + __float_as_uint(v);
+    c = c * 16u + __float_as_uint(fminf(t[i], kMagic + 7.f));
   }
   constexpr uint32_t kOnes = 0x11111111u;
   return c - (0x4B400000u - 8u) * kOnes;
 }
 
-constexpr int kRowsThreads = 256;
+constexpr int kRowsThreads = 128;
 
 // Where a warp's token lies: its tile of KV head 0 and its position there; the tiles of a page's next KV head are
 // `stride` bytes on.  Null for a slot outside the cache.
@@ -400,31 +418,33 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_append_kernel(const Kv4RowsA
   const int l8 = lane % LPR, block = l8 >> 2, tig = l8 & 3;
   const int first = blockIdx.y * passes * RPP + lane / LPR;
   const long long at = t * a.row_stride + 8 * l8;
-  for (int i = 0; i < passes; i += 2) {
-    float x[2][2][8];
+  constexpr int W = Row8<T>::kWords, AHEAD = 16 / W;  // rows of either side that are asked for at once
+  for (int i = 0; i < passes; i += AHEAD) {
+    uint32_t w[AHEAD][2][W];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       const int h = first + (i + j) * RPP;
       const bool live = i + j < passes && h < a.c.n_kv_heads;
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
-        const T* in = reinterpret_cast<const T*>(side ? a.v_in : a.k_in) + at + (long long)h * D;
-        if (live) {
-          Row8<T>::load(in, x[j][side]);
-        } else {
+        const uint4* in = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(side ? a.v_in : a.k_in) + at + (long long)h * D);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[j][side][k] = 0.f;
+        for (int k = 0; k < W; k += 4) {
+          const uint4 u = live ? in[k / 4] : make_uint4(0, 0, 0, 0);
+          w[j][side][k] = u.x, w[j][side][k + 1] = u.y, w[j][side][k + 2] = u.z, w[j][side][k + 3] = u.w;
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       if (i + j >= passes) break;  // the same for the whole warp
       const int h = first + (i + j) * RPP;
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
+        float x[8];
+        Row8<T>::values(w[j][side], x);
         uint16_t scale;
-        const uint32_t c = kv4_quantise(x[j][side], lane, &scale);
+        const uint32_t c = kv4_quantise(x, lane, &scale);
         if (h < a.c.n_kv_heads) {
           uint8_t* part = tile + h * stride + side * kv4_half(D);
           if (side == 0) {
