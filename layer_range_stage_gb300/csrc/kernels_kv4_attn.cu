@@ -615,11 +615,12 @@ cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
 }  // namespace
 
 // Few columns (query tokens of a sequence times heads of a group) run on the kernel above, which reads the cache again for
-// every eight of them; many on the tiles of kernels_kv4_chunk.cu.  Measured (32/8 heads, head_dim 128, us), with z =
-// n_seqs * n_kv_heads * max_len in millions: here 10 + 43 z per eight columns; there 18 + 195 z per 128 rows (float32),
-// 18 + 155 z per 256 (bfloat16; float16, 128 rows with two products each, lies between).  E.g. 16 sequences of 4096:
-// 64 columns 182 here and 123 there, 32 columns 97 and 122; one sequence of 512: 256 columns 20 and 27.
-constexpr int kFewColumns = 32;
+// every eight of them; many on the tiles of kernels_kv4_chunk.cu.  Measured (4 heads per group, head_dim 128, us), with
+// z = n_seqs * n_kv_heads * max_len in millions: here 12 + 43 z per eight columns; there 20 + 195 z per 128 rows (float32),
+// 17 + 155 z per 256 (bfloat16; float16, 128 rows with two products each, lies between).  E.g. 16 sequences of 4096 with 8 KV
+// heads: 64 columns 183 here and 120 (float32) or 78 (bfloat16) there, 32 columns 97 and 119 or 78, 24 columns 77 and 78;
+// 4 of 512: 64 columns 19 and 23, 256 columns 44 and 27.
+constexpr int kFewColumns = 24;
 
 bool many_columns(int n_seqs, int n_kv_heads, long long cols, int max_len, int dtype) {
   if (cols <= kFewColumns) return false;
