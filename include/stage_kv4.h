@@ -47,7 +47,7 @@ enum {
   STAGE_PLAN_OK = 0,
   STAGE_PLAN_NO_PAGES = 1, /* the requests need more pages than are free */
   STAGE_PLAN_BAD_LEN = 2,  /* a length that is negative, a kept length above the cached one, a request beyond
-                              its table row, or a ring whose state does not fit its size */
+                              its table row or 2^31 - 1 positions, or a ring whose state does not fit its size */
   STAGE_PLAN_NO_ROOM = 3   /* more new tokens than the slot map holds */
 };
 
@@ -114,7 +114,8 @@ STAGE_API size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_head
 
 /* Attention over the paged 4-bit cache.
  *   q_dev: [n_tok] rows of n_q_heads * head_dim elements of `dtype` (already rotated), row t at
- *     t * q_stride elements; out_dev the same with out_stride.  Query head j reads KV head
+ *     t * q_stride elements; out_dev the same with out_stride (it may be q_dev, with the same stride, and else
+ *     overlaps no input).  Query head j reads KV head
  *     j / (n_q_heads / n_kv_heads); any ratio.
  *   cu_q_dev [n_seqs + 1]: sequence i has the query tokens cu_q[i] .. cu_q[i + 1] - 1, not decreasing, at most n_tok;
  *   seq_len_dev [n_seqs]: its positions in the cache, those of its query tokens included: with
@@ -128,11 +129,16 @@ STAGE_API size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_head
  *   out: sum_j p_j v_j with p = softmax(q k^T / sqrt(head_dim)); a token with no position gets zeros.
  *     Rows behind cu_q[n_seqs] are left as they were.  Positions whose table entry is no page id count as absent;
  *     what the cache holds behind seq_len never matters.
- *   Arithmetic: the codes enter the tensor cores as exact integers; sums, maxima and the softmax are
- *     float32.  STAGE_F32: q and the probabilities are each held as two fp16 values (22 bits), for
- *     an error of the order of float32's.  The 16-bit types round out once to nearest.
+ *   Arithmetic: sums, maxima and the softmax are float32.  STAGE_F32: q and the probabilities are each
+ *     held as two fp16 values (22 bits) and meet exact integers or exact values, for an error of the
+ *     order of float32's; what lies 2^34 or more below a row's largest p_j v_j, or 2^25 below the largest
+ *     scale of a position, counts as 0.  The 16-bit types round out once to nearest, and a probability
+ *     may be rounded once to fp16; STAGE_BF16 may also round K and V once to fp16 (11 bits, where the
+ *     output has 8).
+ *     A chunk's row is NaN where the GPU did not finish a copy or a product within two seconds.
  *   workspace_dev: stage_op_kv4_attention_workspace_bytes(...) bytes whose contents must be zero
- *     before the first call (each call leaves it ready for the next); two calls that may run at the
+ *     before the first call (each call leaves it ready for the next, of any sizes it is large enough
+ *     for); two calls that may run at the
  *     same time (on two streams, or in two graphs) need one each.
  * Every sum has a fixed order: the same inputs give the same bits.  Runs on `stream`.  n_seqs = 0 or
  * n_tok = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned pointers, cache sizes, dtype, strides below

@@ -38,7 +38,7 @@ __device__ __forceinline__ PlanReq plan_request(const Kv4PlanArgs& a, int i) {
   const int some = min(fresh, a.n_tok + 1);  // more is refused by the total; the sums below fit 32 bits
   const unsigned pl = (unsigned)a.page_len, stride = (unsigned)a.table_stride;
   const unsigned have = ((unsigned)len + pl - 1) / pl, need = ((unsigned)keep + (unsigned)some + pl - 1) / pl;
-  if (have > stride || (need > stride && fresh <= a.n_tok)) return r;
+  if (have > stride || (need > stride && fresh <= a.n_tok) || (unsigned)keep + (unsigned)some > 0x7fffffffu) return r;
   r.bad = false;
   r.have = (int)have;
   r.need = (int)(need > stride ? have : need);
@@ -217,7 +217,8 @@ cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  // one CTA where it has a few dozen steps at most: a cluster's launch and barrier cost more than they save
+  // one CTA where it has a few dozen steps at most: a cluster's launch and barrier cost more than they save (64 requests with a
+  // token each: 3.8 us, 7.7 in a cluster; 512 with 2048 tokens: 9.6 and 8.4; 1024 with 49 thousand: 128 and 14)
   const int ncta = a.n_seqs > 2 * kPlanFew || a.n_tok > 8 * kPlanFew ? kPlanCluster : 1;
   cfg.gridDim = dim3(ncta);
   cfg.blockDim = dim3(ncta > 1 ? kPlanThreads : kPlanFew);
@@ -405,6 +406,9 @@ __device__ __forceinline__ uint8_t* kv4_place(const Kv4Cache& c, int slot, int* 
   return c.data + (long long)page * c.n_kv_heads * *stride + (in / kKv4Tile) * kv4_tile_bytes(D);
 }
 
+// A warp per token, eight dims per lane: a row of a KV head is one access, a block's maximum two shuffles.  Bound by the
+// quantiser's instructions (20 per value; 70 % of the issue slots): 16411 tokens of 8 heads of 128, bfloat16, 28.6 us for 86 MB,
+// 3.0 TB/s.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowsThreads) kv4_append_kernel(const Kv4RowsArgs a, int passes) {
   constexpr int NB = D / 32, LPR = D / 8, RPP = 32 / LPR;  // lanes per row, rows per pass
@@ -460,6 +464,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_append_kernel(const Kv4RowsA
   }
 }
 
+// The same split.  Bound by the writes: 16411 tokens of 8 heads of 128 to float32, 27.3 us for 153 MB, 5.6 TB/s.
 template <int D, typename T>
 __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const Kv4RowsArgs a, int passes) {
   constexpr int NB = D / 32, LPR = D / 8, RPP = 32 / LPR;

@@ -195,7 +195,7 @@ int stage_op_kv4_attention(const void* cache_dev, int64_t n_pages, int page_len,
   a.n_q_heads = n_q_heads;
   a.n_seqs = n_seqs;
   a.table_stride = table_stride;
-  a.max_q = max_q;
+  a.max_q = max_q < n_tok ? max_q : n_tok;  // no sequence has more: a loose bound launches no empty work
   a.max_len = max_len;
   a.cu_q = cu_q_dev;
   a.seq_len = seq_len_dev;

@@ -132,7 +132,7 @@ def plan(page_len, seq_len, new_len, table, ring, free_state, n_tok, n_pages, ke
         ok = length >= 0 and 0 <= keep <= length and new >= 0
         have.append(-(-length // page_len) if ok else 0)
         need.append(-(-(keep + new) // page_len) if ok else 0)
-        bad |= not ok or have[-1] > stride or (need[-1] > stride and new <= n_tok)
+        bad |= not ok or have[-1] > stride or (need[-1] > stride and new <= n_tok) or keep + min(new, n_tok + 1) >= 2 ** 31
     give = sum(max(0, h - w) for h, w in zip(have, need))
     if bad or count + give > len(ring):
         r["status"] = 2

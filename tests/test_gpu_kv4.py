@@ -241,6 +241,17 @@ def test_plan_refuses_a_step_as_a_whole(B):
     assert seen == [0, 2, 2, 2, 2, 2, 3, 3, 1, 0, 2, 2, 2, 0, 2, 0, 0]
 
 
+def test_plan_refuses_positions_beyond_31_bits(B):
+    """Table rows may be wider than positions can be counted."""
+    page, stride = 4096, (1 << 31) // 4096 + 1
+    table, ring = np.zeros((1, stride), np.int32), np.arange(2, dtype=np.int32)
+    for new, status in ((1, 0), (2, 2), (5, 2)):
+        length = np.array([2 ** 31 - 2], np.int32)
+        want = kv4.plan(page, length, [new], table, ring, np.array([0, 2], np.int32), 8, 2)
+        assert want["status"] == status
+        check_plan(run_plan(B, page, length, [new], table, ring, [0, 2], 8, 2), want)
+
+
 def test_plan_gives_no_slot_of_a_page_outside_the_cache(B):
     table = np.array([[5, 99, -3, 7]], np.int32)
     length, new = np.array([10], np.int32), [50]
@@ -489,6 +500,69 @@ def test_few_row_tiles_share_their_positions_out(B, hkv, group, d, rows, dtype):
     hit[first:rows[0][0], :group, :32] = True
     assert np.isnan(got[hit]).all()
     check_attention(torch.from_numpy(got), want, dtype, ~np.isnan(want[0]) & ~hit)
+
+
+def with_loose_bounds(monkeypatch, empty):
+    """Attention called with a bound on the lengths far above them, and with `empty` sequences more that have no token: the
+    launch is chosen by the bounds, so chunks of any length run on the tiles for many columns -- their positions shared out
+    over the GPU without empty sequences, in one part each with many."""
+    tight = run_attention
+
+    def loose(B, cache, table, cu, length, q, dtype, max_q=None, max_len=None, **kw):
+        max_q = max_q or max(1, int(np.diff(cu).max()))
+        cu = np.concatenate([cu, np.full(empty, cu[-1], np.int32)])
+        length = np.concatenate([length, np.zeros(empty, np.int32)])
+        table = np.concatenate([table, np.full((empty, table.shape[1]), -1, np.int32)])
+        return tight(B, cache, table, cu, length, q, dtype, max_q=max_q, max_len=max_len or 1 << 28, **kw)
+
+    monkeypatch.setitem(globals(), "run_attention", loose)
+
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("hkv,group,d,page,rows", CHUNKS)
+def test_chunks_match_oracle_under_loose_bounds(B, monkeypatch, hkv, group, d, page, rows, dtype, empty):
+    rng = np.random.default_rng(hkv * 1000 + group * 10 + d + 9)
+    cache, table, cu, length, q = attention_case(rng, hkv, group, d, page, rows, dtype)
+    with_loose_bounds(monkeypatch, empty)
+    out = run_attention(B, cache, table, cu, length, q, dtype)
+    check_attention(out, kv4.attention(cache, q, cu, length, table), dtype, chunk=True)
+
+
+@pytest.mark.parametrize("empty", [0, 160])
+def test_hard_chunks_under_loose_bounds(B, monkeypatch, empty):
+    """Wide ranges, NaN rows and bad pages, on the tiles for many columns."""
+    with_loose_bounds(monkeypatch, empty)
+    test_scales_and_scores_over_a_wide_range(B, 1, 4, 128, [(40, 600)])
+    test_scales_and_scores_over_a_wide_range(B, 1, 8, 64, [(40, 600)])
+    test_nan_rows_stay_where_they_belong(B, 33)
+    test_bad_page_ids_count_as_absent(B)
+    for dtype in DT:
+        test_few_row_tiles_share_their_positions_out(B, 1, 4, 128, [(70, 1500)], dtype)
+        test_few_row_tiles_share_their_positions_out(B, 2, 1, 64, [(40, 2000), (0, 7), (36, 500)], dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,max_len", [([(1, 3000), (2, 40)], 3000), ([(40, 900), (33, 33)], 1 << 28)])
+def test_the_output_in_the_place_of_q(B, rows, max_len, dtype):
+    """Rows that several CTAs share (long, and chunks in parts) read their q before any of it is written."""
+    rng = np.random.default_rng(91)
+    cache, table, cu, length, q = attention_case(rng, 2, 4, 128, 16, rows, dtype)
+    apart = run_attention(B, cache, table, cu, length, q, dtype, max_len=max_len)
+    qd, most = torch.as_tensor(q).to(DT[dtype]).cuda(), max(c for c, _ in rows)
+    ws = torch.zeros(B.stage_op_kv4_attention_workspace_bytes(2, 8, 2, 128, most, max_len), dtype=torch.uint8, device="cuda")
+    B.stage_op_kv4_attention(torch.from_numpy(cache).cuda(), qd, i32(cu), i32(length), i32(table), qd, most, max_len, ws)
+    same(qd[:int(cu[-1])].float().cpu().numpy(), apart[:int(cu[-1])].float().cpu().numpy())
+
+
+@pytest.mark.parametrize("max_q", [1, 1 << 20])
+def test_a_loose_bound_on_the_tokens(B, max_q):
+    """Each of 200 sequences has one token, whatever the bound says: at most the call's tokens count."""
+    rng = np.random.default_rng(81)
+    rows = [(1, int(n)) for n in rng.integers(1, 90, 200)]
+    cache, table, cu, length, q = attention_case(rng, 2, 4, 64, 16, rows, "f32")
+    out = run_attention(B, cache, table, cu, length, q, "f32", max_q=max_q)
+    check_attention(out, kv4.attention(cache, q, cu, length, table), "f32", chunk=True)
 
 
 # ------------------------------------------------------------------------------------------- refusals through the binding
