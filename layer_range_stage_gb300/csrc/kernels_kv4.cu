@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "kernels.cuh"
 #include "kv4.cuh"
+#include "kv4_attn.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -17,13 +18,14 @@ namespace lrs {
 // the requests before each one (exclusive prefix sums), which places every page taken, every
 // page given back and every token.  A step is bound by the latency of its few dependent reads.  One cluster of CTAs does
 // it in one launch: every CTA computes the sums of all requests for itself, in shared memory, and then they share out
-// the page moves and the tokens one by one, each of which looks its request up by a binary search -- so a request of
-// thousands of pages or tokens is no longer work than as many small ones (1021 requests with 49 thousand tokens: 20 us,
-// 47 us when a warp moved a request's pages).  The lengths are read before the cluster's barrier and written after it, so
+// the page moves and the tokens, in warps' shares of neighbours that look their request up once and go on from there -- so
+// a request of thousands of pages or tokens is no longer work than as many small ones (1021 requests with 58 thousand
+// tokens: 12 us; 16 with a cluster of eight, 20 when every token was searched for by itself and every thread added up all
+// warps' sums, 47 when a warp moved a request's pages).  The lengths are read before the cluster's barrier and written after it, so
 // in and out may be the same arrays; nothing is kept between calls.
 
 constexpr int kPlanThreads = 1024, kPlanFew = 256;  // threads of a CTA, and of a lone one
-constexpr int kPlanCluster = 8;
+constexpr int kPlanCluster = 16;
 constexpr int kPlanBatch = 4096;  // requests whose sums lie in shared memory at a time
 
 struct PlanReq {
@@ -51,10 +53,11 @@ struct PlanSmem {
   // per request of the batch: the first of its page moves and of its tokens (batch-wide numbers; one more entry), where
   // its pages lie in the ring, the first table column that moves (negative, less one: given back), its positions
   int move[kPlanBatch + 1], token[kPlanBatch + 1], ring[kPlanBatch], col[kPlanBatch], end[kPlanBatch];
-  long long part[3][kPlanThreads / 32];
+  long long part[3][kPlanThreads / 32], all[3];
 };
 
-// Sums of v over the block, and over the threads before this one.
+// Sums of v over the block, and over the threads before this one: within warps, then over the warps by each thread, or by
+// the first warp where they are many (32 warps' sums, added up by each thread: 8000 cycles; eight: fewer than a barrier).
 __device__ __forceinline__ void plan_scan(PlanSmem& sm, const long long (&v)[3], long long (&before)[3], long long (&sum)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   __syncthreads();  // the last scan's parts are read
@@ -70,14 +73,37 @@ __device__ __forceinline__ void plan_scan(PlanSmem& sm, const long long (&v)[3],
     if (lane == 31) sm.part[k][warp] = s;
   }
   __syncthreads();
+  if (warps <= 8) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      sum[k] = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w == warp) before[k] += sum[k];
+        if (w < warps) sum[k] += sm.part[k][w];
+      }
+    }
+    return;
+  }
+  if (warp == 0) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const long long mine = lane < warps ? sm.part[k][lane] : 0;
+      long long s = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+      }
+      if (lane < warps) sm.part[k][lane] = s - mine;
+      if (lane == 31) sm.all[k] = s;
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    sum[k] = 0;
-#pragma unroll 8
-    for (int w = 0; w < warps; ++w) {
-      if (w == warp) before[k] += sum[k];
-      sum[k] += sm.part[k][w];
-    }
+    before[k] += sm.part[k][warp];
+    sum[k] = sm.all[k];
   }
 }
 
@@ -92,7 +118,17 @@ __device__ __forceinline__ int plan_find(const int* first, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArgs a) {
+// The same from an i with first[i] <= x on, where it is near (first[n] > x).
+__device__ __forceinline__ int plan_next(const int* first, int n, int i, int x) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (first[i + 1] > x) return i;
+    ++i;
+  }
+  return first[i + 1] > x ? i : i + plan_find(first + i, n - i, x);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArgs a, const Quotient by_page) {
   extern __shared__ __align__(16) unsigned char plan_raw[];
   PlanSmem& sm = *reinterpret_cast<PlanSmem*>(plan_raw);
   cg::cluster_group cluster = cg::this_cluster();
@@ -105,7 +141,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
   long long total[3] = {0, 0, 0};
   bool bad = head < 0 || head >= R || count < 0 || count > R;
   int status = 0;
-  auto judge = [&]() {
+  auto decide = [&]() {
     if (__syncthreads_or(bad) || count + total[1] > R) status = 2;
     else if (total[2] > a.n_tok) status = 3;
     else if (total[0] > count) status = 1;
@@ -121,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
       v[2] += r.fresh;
     }
     plan_scan(sm, v, before, total);
-    judge();
+    decide();
   }
 
   int done[3] = {0, 0, 0};  // takes, gives and tokens of the batches before
@@ -142,7 +178,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
     if (one) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) total[k] = sum[k];
-      judge();
+      decide();
     }
     if (status) {
 #pragma unroll
@@ -172,9 +208,18 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
       a.seq_len_out[b + i] = sm.end[i];
       a.cu_new[b + i] = done[2] + sm.token[i];
     }
-#pragma unroll 2
-    for (int x = g; x < moves; x += nthr) {
-      const int i = plan_find(sm.move, m, x), j = x - sm.move[i], col = sm.col[i];
+    // Every warp has neighbouring moves, and neighbouring tokens, and goes on from request to request
+    const int lane = tid & 31;
+    auto share = [&](int n, int* begin, int* end) {
+      const int per = (n + nthr - 1) / nthr * 32;
+      *begin = (int)min((long long)n, (long long)(g >> 5) * per);
+      *end = min(n, *begin + per);
+    };
+    int x0, x1;
+    share(moves, &x0, &x1);
+    for (int x = x0 + lane, i = x < x1 ? plan_find(sm.move, m, x) : 0; x < x1; x += 32) {
+      i = plan_next(sm.move, m, i, x);
+      const int j = x - sm.move[i], col = sm.col[i];
       int* ring = a.ring + wrap(sm.ring[i] + j);
       int* entry = a.table + (long long)(b + i) * a.table_stride + (col < 0 ? -1 - col : col) + j;
       if (col < 0) *ring = *entry;
@@ -182,9 +227,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
     }
     // a token's page: of the columns that stay, or the ring's (which nobody writes in this step: what is given back goes
     // behind its last page)
-#pragma unroll 2
-    for (int x = g; x < tokens; x += nthr) {
-      const int i = plan_find(sm.token, m, x), pos = sm.end[i] - (sm.token[i + 1] - x), c = pos / a.page_len, col = sm.col[i];
+    share(tokens, &x0, &x1);
+    for (int x = x0 + lane, i = x < x1 ? plan_find(sm.token, m, x) : 0; x < x1; x += 32) {
+      i = plan_next(sm.token, m, i, x);
+      const int pos = sm.end[i] - (sm.token[i + 1] - x), c = by_page(pos), col = sm.col[i];
       const int page = col < 0 || c < col ? a.table[(long long)(b + i) * a.table_stride + c]
                                           : a.ring[wrap(sm.ring[i] + c - col)];
       const int t = done[2] + x;
@@ -213,13 +259,15 @@ cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, cudaStream_t st) {
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
     e = cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PlanSmem));
     if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  // one CTA where it has a few dozen steps at most: a cluster's launch and barrier cost more than they save (64 requests with a
-  // token each: 3.8 us, 7.7 in a cluster; 512 with 2048 tokens: 9.6 and 8.4; 1024 with 49 thousand: 128 and 14)
-  const int ncta = a.n_seqs > 2 * kPlanFew || a.n_tok > 8 * kPlanFew ? kPlanCluster : 1;
+  // one CTA where it has a few steps at most: a cluster's launch and barrier cost more than they save (64 requests with a token
+  // each: 4.1 us, 5.5 in a cluster; 512 tokens: 4.6 and 5.5; 256 with 2048 tokens: 9.3 and 6.0; 1024 with 49 thousand: 58 and 7)
+  const int ncta = a.n_seqs > 2 * kPlanFew || a.n_tok > 3 * kPlanFew ? kPlanCluster : 1;
   cfg.gridDim = dim3(ncta);
   cfg.blockDim = dim3(ncta > 1 ? kPlanThreads : kPlanFew);
   cfg.dynamicSmemBytes = sizeof(PlanSmem);
@@ -229,7 +277,7 @@ cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kv4_plan_kernel, a, Quotient(a.page_len));
 }
 
 // ------------------------------------------------------------------------------------------

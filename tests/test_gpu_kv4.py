@@ -241,6 +241,29 @@ def test_plan_refuses_a_step_as_a_whole(B):
     assert seen == [0, 2, 2, 2, 2, 2, 3, 3, 1, 0, 2, 2, 2, 0, 2, 0, 0]
 
 
+@pytest.mark.parametrize("n", [40, 3000, 9000])
+def test_plan_with_long_runs_of_idle_requests(B, n):
+    """A few requests with hundreds of tokens and pages each, among thousands without any."""
+    rng = np.random.default_rng(n)
+    page, stride = 16, 64
+    length = np.where(rng.random(n) < 0.5, rng.integers(0, 200, n), 0).astype(np.int32)
+    have = -(-length // page)
+    table = np.full((n, stride), -1, np.int32)
+    ids = rng.permutation(int(have.sum()) + 600).astype(np.int32)
+    at = np.concatenate([[0], np.cumsum(have)])
+    for i in range(n):
+        table[i, :have[i]] = ids[at[i]:at[i + 1]]
+    ring = np.full(len(ids), -9, np.int32)
+    ring[5:605] = ids[at[-1]:]
+    new, keep = np.zeros(n, np.int32), length.copy()
+    busy = rng.choice(n, 12, replace=False)
+    new[busy[:8]] = rng.integers(300, 800, 8)
+    keep[busy[6:]] = 0
+    want = kv4.plan(page, length, new, table, ring, np.array([5, 600], np.int32), 7000, len(ids), keep)
+    assert want["status"] == 0
+    check_plan(run_plan(B, page, length, new, table, ring, [5, 600], 7000, len(ids), keep), want)
+
+
 def test_plan_refuses_positions_beyond_31_bits(B):
     """Table rows may be wider than positions can be counted."""
     page, stride = 4096, (1 << 31) // 4096 + 1
