@@ -13,8 +13,8 @@
 //               memory would be read again by every product);
 //   warp 17     copies the packed tiles in (bulk copies, up to four tiles ahead).
 // What bounds it: the latency of a tile's chain (scores, softmax, probabilities, outputs) and of an item's ends (its q, its
-// results); the tensor cores are busy for 23 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 60 us) and 33 % (2 x 1024
-// rows on 8192 positions, STAGE_BF16, the second kernel below: 355 us, 656 TFLOP/s), the schedulers for 40 and 48 %.
+// results); the tensor cores are busy for 23 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 60 us) and 35 % (2 x 1024
+// rows on 8192 positions, STAGE_BF16, the second kernel below: 343 us, 680 TFLOP/s), the schedulers for 40 and 48 %.
 // The tensor cores' additions truncate: over a long sum the result shrinks (by 1e-4 of itself at 32768 positions).  So in
 // STAGE_F32 every tile's O is added to float32 registers, rounded to nearest, and the products with low parts come
 // first, where the sums they truncate are still small: 2e-6 of error became 5e-7.  The 16-bit types keep the whole sum
@@ -45,7 +45,8 @@ constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
 constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 16 * kProdWarps;  // kProd: threads of a group of four warps
 constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpgroups
 // Registers per thread: the block starts with kRegsStart and its warpgroups trade them (4 x 512 rows, STAGE_F32: 64 us with
-// 136, 72, 64; 61 with these, 71 with 128, 80, 64; 2 x 1024 rows, STAGE_BF16: 377, 355, 369).
+// 136, 72, 64; 61 with these, 71 with 128, 80, 64; 2 x 1024 rows, STAGE_BF16: 343 with these, 353 with 144, 72, 48, 355 with
+// 160, 56, 48, 359 with 152, 56, 64).
 constexpr int kRegsStart = 96, kRegsSoft = 152, kRegsProd = 64, kRegsRest = 48;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
@@ -928,7 +929,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
 // K and V, and their softmaxes, four warps each with a whole row per thread, are independent, so one's chain of
 // reads, maxima, exponentials and writes runs beside the other's.  P takes the place of its S in TMEM; the next
 // scores that are written there wait for the product that reads P.  q lies in shared memory: TMEM holds the two tiles'
-// S and P, two of each, and O.
+// S and P, two of each, and O.  The products' warp is the narrow place: each of its waits costs a hundred cycles though the
+// barrier has long been passed, so K and V are waited for once per tile, not once per row tile (355 -> 343 us).
 constexpr uint32_t kColPairS = 0, kColPairO = 256;
 
 template <int D, bool SPLIT>
@@ -972,10 +974,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
       constexpr uint32_t id_s = idesc_f16_f32(kRowsTile, kPosTile), id_o = idesc_f16_f32(kRowsTile, D);
       const uint64_t qd = desc_sw128(smem_u32(sm)), kd = desc_sw128(smem_u32(sm + L::off_k)), vd = desc_sw128(smem_u32(sm + L::off_v));
       uint32_t s_count[2] = {0, 0}, o_count[2] = {0, 0}, q_ph[2] = {0, 0};  // of each row tile: scores and outputs so far
-      // scores of row tile g and tile number ni; `last`: nobody reads this K after
-      auto scores = [&](int g, int ni, bool last) {
+      // scores of row tile g and tile number ni; `last`: nobody reads this K after; `there`: it has been waited for
+      auto scores = [&](int g, int ni, bool last, bool there) {
         const uint32_t c = s_count[g], b = c & 1, st = (uint32_t)ni % KS;
-        bool ok = cwait(&B.k_full[st], (uint32_t)ni / KS & 1u, abort_flag);
+        bool ok = there || cwait(&B.k_full[st], (uint32_t)ni / KS & 1u, abort_flag);
         if (c >= 2) ok = ok && cwait(&B.pair_o[g][b], (c / 2 + 1) & 1u, abort_flag);  // the product that read this place's P
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
@@ -995,9 +997,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
         return true;
       };
       // its output; `more`: added to the last tile's
-      auto outputs = [&](int g, int ni, bool more, bool last) {
+      auto outputs = [&](int g, int ni, bool more, bool last, bool there) {
         const uint32_t c = o_count[g], b = c & 1, st = (uint32_t)ni % KS;
-        const bool ok = cwait(&B.v_full[st], (uint32_t)ni / KS & 1u, abort_flag) && cwait(&B.pair_p[g][b], c / 2 & 1u, abort_flag);
+        const bool ok = (there || cwait(&B.v_full[st], (uint32_t)ni / KS & 1u, abort_flag)) && cwait(&B.pair_p[g][b], c / 2 & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         const uint64_t vb = vd + st * (uint32_t)(L::v_part >> 4);
@@ -1025,14 +1027,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
           }
         if (!ok) break;
         tc_fence_after();
-        if (nt0 > 0) ok = scores(0, n, nt1 <= 0);
-        if (ok && nt1 > 0) ok = scores(1, n, true);
-        if (ok && nt0 > 1) ok = scores(0, n + 1, nt1 <= 1);
+        if (nt0 > 0) ok = scores(0, n, nt1 <= 0, false);
+        if (ok && nt1 > 0) ok = scores(1, n, true, nt0 > 0);
+        if (ok && nt0 > 1) ok = scores(0, n + 1, nt1 <= 1, false);
         for (int i = 0; ok && i < it.nt; ++i) {
-          if (i < nt0) ok = outputs(0, n + i, i > 0, i >= nt1);
-          if (ok && i + 1 < nt1) ok = scores(1, n + i + 1, true);
-          if (ok && i < nt1) ok = outputs(1, n + i, i > 0, true);
-          if (ok && i + 2 < nt0) ok = scores(0, n + i + 2, i + 2 >= nt1);
+          if (i < nt0) ok = outputs(0, n + i, i > 0, i >= nt1, false);
+          if (ok && i + 1 < nt1) ok = scores(1, n + i + 1, true, i + 1 < nt0);
+          if (ok && i < nt1) ok = outputs(1, n + i, i > 0, true, i < nt0);
+          if (ok && i + 2 < nt0) ok = scores(0, n + i + 2, i + 2 >= nt1, false);
         }
       }
       if (!ok && leader) {  // given up: the products already issued finish before TMEM is released
