@@ -583,6 +583,8 @@ def stage_op_kv4_plan(page_len: int, seq_len, new_len, table, free_ring, free_st
     """Block tables and slot maps of one step (include/stage_kv4.h).  Device int32 tensors: seq_len, keep_len,
     new_len, seq_len_out [n]; table [n, stride]; free_ring; free_state, free_state_out [2]; cu_new [n + 1];
     slot, pos, seq [n_tok]; status [1].  n_pages: the cache's pages (default: as many as the ring holds)."""
+    if not 16 <= page_len <= 4096:  # a C int would drop what lies above its bits
+        _invalid("page_len must lie in [16, 4096]")
     tensors = (seq_len, new_len, table, free_ring, free_state, seq_len_out, free_state_out, cu_new, slot, pos, seq, status)
     stream = _kv4_launch(stream, *tensors) if keep_len is None else _kv4_launch(stream, *tensors, keep_len)
     n, n_tok, ring_len = seq_len.numel(), slot.numel(), free_ring.numel()
@@ -644,6 +646,8 @@ def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_
     """q, out [n_tok, n_q_heads, head_dim] of one type; cu_q int32 [n_seqs + 1], seq_len int32 [n_seqs], table int32
     [n_seqs, stride]; max_q, max_len bound the query tokens and the length of a sequence; workspace: a tensor of
     stage_op_kv4_attention_workspace_bytes(...) bytes, zero before its first use."""
+    if not (0 < max_q <= 1 << 20 and 0 < max_len <= 1 << 30):  # a C int would drop what lies above its bits
+        _invalid("max_q must lie in [1, 2^20] and max_len in [1, 2^30]")
     ptr, n_pages, page_len, hkv, d = _kv4_cache(cache)
     stream = _kv4_launch(stream, cache, q, cu_q, seq_len, table, out, workspace)
     if q.dim() != 3 or out.shape != q.shape:

@@ -185,3 +185,14 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         assert e.value.code == L.STAGE_E_INVALID
     with pytest.raises(L.StageError, match="device tensors"):
         L.stage_op_kv4_append(cache, k, k, slot)
+
+
+def test_binding_refuses_sizes_that_a_c_int_would_cut_off():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, dtype=torch.int32)
+    for max_q, max_len in ((0, 5), ((1 << 32) + 1, 5), (1, 0), (1, (1 << 32) + 5), (-1, 5), ((1 << 20) + 1, 5)):
+        with pytest.raises(L.StageError, match="max_q"):
+            L.stage_op_kv4_attention(x, x, x, x, x, x, max_q, max_len, x)
+    for page_len in (0, -16, 8192, (1 << 32) + 16):
+        with pytest.raises(L.StageError, match="page_len"):
+            L.stage_op_kv4_plan(page_len, *[x] * 12)
