@@ -264,6 +264,40 @@ def test_plan_with_long_runs_of_idle_requests(B, n):
     check_plan(run_plan(B, page, length, new, table, ring, [5, 600], 7000, len(ids), keep), want)
 
 
+def test_a_large_plan_captured_and_replayed(B):
+    """A cluster launch in a graph; lengths and ring go on from replay to replay."""
+    rng = np.random.default_rng(17)
+    n, page, stride, n_tok = 1500, 16, 8, 3000
+    length = rng.integers(0, 60, n).astype(np.int32)
+    have = -(-length // page)
+    ids = rng.permutation(n * stride).astype(np.int32)
+    table, at = np.full((n, stride), -1, np.int32), np.concatenate([[0], np.cumsum(have)])
+    for i in range(n):
+        table[i, :have[i]] = ids[at[i]:at[i + 1]]
+    ring, free = np.resize(ids[at[-1]:], n * stride).astype(np.int32), np.array([0, n * stride - at[-1]], np.int32)
+    new = rng.integers(0, 4, n).astype(np.int32)
+    new[np.cumsum(new) > n_tok] = 0
+    t = {k: i32(x) for k, x in (("len", length), ("new", new), ("table", table), ("ring", ring), ("free", free), ("cu", np.zeros(n + 1)),
+                                ("slot", np.zeros(n_tok)), ("pos", np.zeros(n_tok)), ("seq", np.zeros(n_tok)), ("status", np.full(1, -1)))}
+
+    def step():
+        B.stage_op_kv4_plan(page, t["len"], t["new"], t["table"], t["ring"], t["free"], t["len"], t["free"], t["cu"], t["slot"], t["pos"], t["seq"],
+                            t["status"])
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        want = kv4.plan(page, length, new, table, ring, free, n_tok, n * stride)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: x.cpu().numpy() for k, x in t.items()}
+        check_plan({**got, "status": int(got["status"][0])}, want)
+        length, table, ring, free = want["len"], want["table"], want["ring"], want["free"]
+    assert want["status"] == 0
+
+
 def test_plan_refuses_positions_beyond_31_bits(B):
     """Table rows may be wider than positions can be counted."""
     page, stride = 4096, (1 << 31) // 4096 + 1
