@@ -129,6 +129,8 @@ STAGE_API size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_head
  *   out: sum_j p_j v_j with p = softmax(q k^T / sqrt(head_dim)); a token with no position gets zeros.
  *     Rows behind cu_q[n_seqs] are left as they were.  Positions whose table entry is no page id count as absent;
  *     what the cache holds behind seq_len never matters.
+ *     A scale that is no finite number (append writes NaN; another writer may leave infinities, which count as NaN): in K it
+ *     makes NaN of the KV head's outputs of every token that sees the position, in V of its own block of dims in them.
  *   Arithmetic: sums, maxima and the softmax are float32.  STAGE_F32: q and the probabilities are each
  *     held as two fp16 values (22 bits) and meet exact integers or exact values, for an error of the
  *     order of float32's; what lies 2^34 or more below a row's largest p_j v_j, or 2^25 below the largest

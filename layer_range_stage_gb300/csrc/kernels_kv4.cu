@@ -369,11 +369,6 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {
   asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
-  return y;
-}
 
 // Quantise the eight values of this lane with the block's four lanes: the codes, eight to a word, and the scale's bits.
 // Code of x for the scale s (finite, not 0): the nearest integer to x / s, ties to even, plus 8, in [0, 15].  Adding

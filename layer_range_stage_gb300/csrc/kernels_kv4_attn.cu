@@ -476,6 +476,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           vs[n][2 * b + 1] = make_float2(first.y, second.y);
         }
       }
+      // An infinite scale of K counts as NaN: a score of -infinity would drop its position without a word
+#pragma unroll
+      for (int n = 0; n < 2; ++n) z[n] = fma2(z[n], make_float2(0.f, 0.f), z[n]);
       if (pos0 + kKv4Tile > lim_lo) {
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -489,18 +492,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attn_kernel(const Kv4AttnArgs
           }
         }
       }
-      // the largest z + log2 of a position's largest scale (at least fp16's smallest; NaN loses)
+      // the largest z + log2 of a position's largest scale (at least fp16's smallest; NaN loses; an infinity counts as fp16's
+      // largest, so that it makes its own block NaN, through its product, and nothing of the others)
       float most = -INFINITY;
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         float2 top = make_float2(5.9604645e-8f, 5.9604645e-8f);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          top.x = fmaxf(top.x, fabsf(vs[n][b].x));
-          top.y = fmaxf(top.y, fabsf(vs[n][b].y));
+        for (int b = 0; b < NB; b += 2) {
+          top.x = max_abs(top.x, vs[n][b].x, vs[n][b + 1].x);
+          top.y = max_abs(top.y, vs[n][b].y, vs[n][b + 1].y);
         }
-        most = fmaxf(most, fmaf(z[n].x, zscale, log2_approx(top.x)));
-        most = fmaxf(most, fmaf(z[n].y, zscale, log2_approx(top.y)));
+        most = fmaxf(most, fmaf(z[n].x, zscale, log2_approx(fminf(top.x, 65504.f))));
+        most = fmaxf(most, fmaf(z[n].y, zscale, log2_approx(fminf(top.y, 65504.f))));
       }
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
