@@ -23,10 +23,14 @@
 // Precision: a value s (c - 8) has 15 significant bits, so two fp16 numbers hold it exactly; q and the probabilities are
 // float32 and two fp16 numbers hold 22 bits.  STAGE_F32 multiplies high by high, low by high and high by low (three
 // products each for S and O); STAGE_F16 has an exact q in one number and keeps K and V exact (two); STAGE_BF16, whose
-// output keeps 8 bits, rounds K, V and the probabilities to fp16 once (one).  Scales are divided by a power of two
+// output keeps 8 bits, rounds K, V and the probabilities to fp16 once (one).
+// Values of K are multiples of 2^-24 and, with scales below 4096, at most 2^15: fp16's range holds them as they are (a
+// subnormal one exactly, in one number).  In the rare tile with a scale from 4096 on (rows of 32768), each position
+// has a power of its own, 1 where its own scales are below, which its score is multiplied by: what other positions hold,
+// those that a row does not see among them, changes nothing, and the position's own values lose 2^-33 of its largest.
+// V's scales are divided by a power of two
 // above the largest one, so that fp16's range holds them whatever they are, and what lies below 2^-25 of the largest is
-// lost: of a tile's K scales, where it moves a score by 2^-24 of the largest one; of a position's V scales in
-// STAGE_F32, of a tile's in the 16-bit types.  The power goes into the score's factor (K) and the probabilities (V).
+// lost: of a position's in STAGE_F32, of a tile's in the 16-bit types.  The power goes into the probabilities.
 
 #include <atomic>
 #include <cfloat>
@@ -129,13 +133,21 @@ struct ChunkItems {
   __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.tokens + r / a.group + 1); }
 };
 
+// Prepared scales of a tile: [position][block] fp16, each eight positions a padding further, for the banks.
+__host__ __device__ constexpr int scale_place(int D, int pos) { return pos * (D / 16) + (pos >> 3) * (D / 8); }
+constexpr int kWide = 16;
+constexpr int kScaleBytes = scale_place(128, kPosTile);
+
 struct alignas(16) ChunkMisc {
   ChunkBars bar;
-  float k_pow[kInfo], v_exp[kInfo], v_inv[kInfo];  // 2^E_k; E_v; 2^-E_v
+  float v_exp[kInfo], v_inv[kInfo];  // E_v; 2^-E_v
+  alignas(16) float k_pos_pow[kInfo][kPosTile];
   alignas(16) float v_pos_exp[kInfo][kPosTile];  // read in 16-byte pieces
   alignas(16) float v_pos_inv[kInfo][kPosTile];  // STAGE_F32: E_v and 2^-E_v of each position
   uint32_t v_norm[kProdWarps][kPosTile / 2];                     // and 2^-E_v of two positions in fp16, one copy per warp
+  alignas(16) unsigned char k_scale[kProdWarps][kScaleBytes];  // a tile's scales as the products take them, one copy per warp
   int absent[kInfo];                               // bit i: the tile's i-th 16 positions are not there
+  int odd[kInfo];                                  // the same, and kWide: its positions have powers of K of their own
   int bad[kInfo];                                  // whether some V scale is no number
   int first_bad[kInfo][4];                         // per block of dims: the first such position
   float top[2][2][kRowsTile], q_top[2][kRowsTile]; // [tile parity][half][row]
@@ -250,6 +262,11 @@ __device__ __forceinline__ __half2 code_high(uint32_t x, uint32_t ex) {
 // 2^-e as fp16, e in [-14, 16].
 __device__ __forceinline__ uint16_t half_power(int e) { return (uint16_t)(e <= 14 ? (15 - e) << 10 : 0x400 >> (e - 14)); }
 
+// K's scales from 4096 on (fp16 bits from here on) are divided by a power of two: e of a position with the largest scale `top`.
+constexpr uint32_t kBigScale = 27u << 10;
+__device__ __forceinline__ int k_power(uint32_t top) { return max(0, (int)min(top >> 10, 30u) - 26); }
+__device__ __forceinline__ uint32_t larger_half(__half2 m) { return max(as_u32(m) >> 16, as_u32(m) & 0xffffu); }
+
 // ---------------- what both kernels have ----------------
 
 __device__ void chunk_init(ChunkMisc& M) {
@@ -307,60 +324,73 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
     const int pos0 = (it.t0 + i) * kPosTile;
     const bool ragged = absent || pos0 + kPosTile > lim_hi;  // some positions do not count: their scales read as 0
 
-    // the largest scales (every warp for itself)
-    int e_k, e_v;
-    bool v_bad = false;
+    // the scales, every warp for itself: a lane has two neighbouring positions.  Those that do not count read as 0
+    int e_v;
+    bool v_bad = false, k_big;
+    unsigned char* k_scale = M.k_scale[warp - kSoftWarps];
     {
       const int s = lane >> 3, at = pos0 + s * kKv4Tile + 2 * (lane & 7);
       const bool ok0 = !(absent >> s & 1) && at < lim_hi, ok1 = !(absent >> s & 1) && at + 1 < lim_hi;
       const unsigned char* base = raw + s * L::sub_stride + (lane & 7) * (4 * NB);
-      uint32_t top[2];
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const unsigned char* sc = base + (side ? HALF + CODES + 16 + ((lane & 4) << 2) : CODES);
-        uint32_t w[NB];
+      uint32_t w[NB];  // words 0 .. NB / 2 - 1: the first position's
+      auto load = [&](const unsigned char* from) {
         if constexpr (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sc);
+          const uint4 u = *reinterpret_cast<const uint4*>(from);
           w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
         } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sc);
+          const uint2 u = *reinterpret_cast<const uint2*>(from);
           w[0] = u.x, w[1] = u.y;
         }
-        __half2 m = __floats2half2_rn(0.f, 0.f), first = m;  // first: of the first position alone
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t u = (b < NB / 2 ? ok0 : ok1) ? w[b] & 0x7fff7fffu : 0u;
-          if (side) v_bad |= (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
-          if (NP == 2 && side && b == NB / 2) {
-            first = m;
-            m = __floats2half2_rn(0.f, 0.f);
-          }
-          m = __hmax2(m, as_h2(u));  // NaN loses
-        }
-        top[side] = max(as_u32(m) >> 16, as_u32(m) & 0xffffu);
-        if (NP == 2 && side) {
-          const int e0 = (int)min(max(as_u32(first) >> 16, as_u32(first) & 0xffffu) >> 10, 30u) - 14;
-          const int e1 = (int)min(top[1] >> 10, 30u) - 14;
-          M.v_norm[warp - kSoftWarps][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
-          if (pw == 0) {
-            *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
-            *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
-                make_float2(__uint_as_float((uint32_t)(127 - e0) << 23), __uint_as_float((uint32_t)(127 - e1) << 23));
-          }
+        for (int b = 0; b < NB; ++b)
+          if (!(b < NB / 2 ? ok0 : ok1)) w[b] = 0;
+      };
+      auto largest = [&](int i) {  // of the first or the second position; NaN loses
+        __half2 m = as_h2(w[i * (NB / 2)] & 0x7fff7fffu);
+        if (NB == 4) m = __hmax2(m, as_h2(w[i * (NB / 2) + NB / 2 - 1] & 0x7fff7fffu));
+        m = __hmax2(m, __floats2half2_rn(0.f, 0.f));
+        return larger_half(m);
+      };
+      load(base + CODES);
+      k_big = __reduce_max_sync(0xffffffffu, max(largest(0), largest(1))) >= kBigScale;
+      if (k_big) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e = k_power(largest(i));
+          if (pw == 0) M.k_pos_pow[inf][2 * lane + i] = __uint_as_float((uint32_t)(127 + e) << 23);
+          const __half2 norm = __half2half2(__ushort_as_half(half_power(e)));
+#pragma unroll
+          for (int b = i * (NB / 2); b < (i + 1) * (NB / 2); ++b)  // an infinity becomes NaN: a score of -infinity would drop its position
+            w[b] = as_u32(__hmul2(__hfma2(as_h2(w[b]), __floats2half2_rn(0.f, 0.f), as_h2(w[b])), norm));
         }
       }
-      e_k = (int)min(__reduce_max_sync(0xffffffffu, top[0]) >> 10, 30u) - 14;
-      e_v = NP == 2 ? 0 : (int)min(__reduce_max_sync(0xffffffffu, top[1]) >> 10, 30u) - 14;
+      __syncwarp();  // the last tile's are read
+      if constexpr (D == 128) *reinterpret_cast<uint4*>(k_scale + scale_place(D, 2 * lane)) = make_uint4(w[0], w[1], w[2], w[3]);
+      else *reinterpret_cast<uint2*>(k_scale + scale_place(D, 2 * lane)) = make_uint2(w[0], w[1]);
+
+      load(base + HALF + CODES + 16 + ((lane & 4) << 2));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) v_bad |= (w[b] & 0x7c00u) == 0x7c00u || (w[b] & 0x7c000000u) == 0x7c000000u;
+      const uint32_t top0 = largest(0), top1 = largest(1);
+      if (NP == 2) {
+        const int e0 = (int)min(top0 >> 10, 30u) - 14, e1 = (int)min(top1 >> 10, 30u) - 14;
+        M.v_norm[warp - kSoftWarps][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
+        if (pw == 0) {
+          *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
+          *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
+              make_float2(__uint_as_float((uint32_t)(127 - e0) << 23), __uint_as_float((uint32_t)(127 - e1) << 23));
+        }
+      }
+      e_v = NP == 2 ? 0 : (int)min(__reduce_max_sync(0xffffffffu, max(top0, top1)) >> 10, 30u) - 14;
       v_bad = __any_sync(0xffffffffu, v_bad);
     }
-    const __half2 norm_k = __half2half2(__ushort_as_half(half_power(e_k)));
     const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
-    if (NP == 2) __syncwarp();  // v_norm
+    __syncwarp();  // the prepared scales
     // K: 64 positions x 4 x (the word of eight dims of every block)
     if (ni >= KS) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)(ni / KS + 1) & 1u, abort_flag));
     if (!ok) break;
     if (p == 0) {
-      M.k_pow[inf] = __uint_as_float((uint32_t)(e_k + 127) << 23);
+      M.odd[inf] = absent | (k_big ? kWide : 0);
       M.v_exp[inf] = (float)e_v;
       M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
       M.bad[inf] = v_bad;
@@ -379,20 +409,16 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
       if constexpr (D == 128) {
         const uint4 u = *reinterpret_cast<const uint4*>(src + (pos & 15) * (D / 2) + tig * 16);
         w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        const uint2 v = *reinterpret_cast<const uint2*>(src + CODES + (pos & 15) * (2 * NB));
+        const uint2 v = *reinterpret_cast<const uint2*>(k_scale + scale_place(D, pos));
         sc[0] = v.x, sc[1] = v.y;
       } else {
         const uint2 u = *reinterpret_cast<const uint2*>(src + (pos & 15) * (D / 2) + tig * 8);
         w[0] = u.x, w[1] = u.y;
-        sc[0] = *reinterpret_cast<const uint32_t*>(src + CODES + (pos & 15) * (2 * NB));
-      }
-      if (ragged && ((absent >> s & 1) || pos0 + pos >= lim_hi)) {
-#pragma unroll
-        for (int b = 0; b < NB / 2; ++b) sc[b] = 0;
+        sc[0] = *reinterpret_cast<const uint32_t*>(k_scale + scale_place(D, pos));
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[b / 2], 0, b & 1 ? 0x3232 : 0x1010)), norm_k);
+        const __half2 s2 = as_h2(__byte_perm(sc[b / 2], 0, b & 1 ? 0x3232 : 0x1010));
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -771,15 +797,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
       tc_fence_after();
       uint32_t s[32];
       tmem_ld32(lanes + kColS + st * kPosTile + half * 32, s);
-      const float f = zscale * M.k_pow[inf], ev = M.v_exp[inf], v_inv = M.v_inv[inf];
-      const int absent = M.absent[inf] >> (2 * half) & 3;
+      const float f = zscale, ev = M.v_exp[inf], v_inv = M.v_inv[inf];
+      const int odd = M.odd[inf];
       if (i >= 2) note_bad(ni - 2);
       tmem_wait_ld();
       const int pos0 = (it.t0 + i) * kPosTile + 32 * half;
-      if (pos0 + 32 > lim_lo || absent) {
+      if (pos0 + 32 > lim_lo || odd) {
+        if (odd & kWide) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * M.k_pos_pow[inf][32 * half + j]);
+        }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (pos0 + j >= lim || (absent >> (j >> 4) & 1)) s[j] = 0xff800000u;
+          if (pos0 + j >= lim || (odd >> (2 * half + (j >> 4)) & 1)) s[j] = 0xff800000u;
       }
       // exponents in base 2; STAGE_F32: with each position's power of V
       float most = -INFINITY;
@@ -1118,15 +1148,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
         uint32_t s[2][32];
         tmem_ld32(place_s + b * kPosTile, s[0]);
         tmem_ld32(place_s + b * kPosTile + 32, s[1]);
-        const float f = zscale * M.k_pow[inf], ev = M.v_exp[inf], v_inv = M.v_inv[inf];
-        const int absent = M.absent[inf];
+        const float f = zscale, ev = M.v_exp[inf], v_inv = M.v_inv[inf];
+        const int odd = M.odd[inf];
         if (i >= 2) note_bad(ni - 2);
         tmem_wait_ld();
         const int pos0 = (it.t0 + i) * kPosTile;
-        if (pos0 + kPosTile > lim_lo || absent) {
+        if (pos0 + kPosTile > lim_lo || odd) {
+          if (odd & kWide) {
+#pragma unroll
+            for (int j = 0; j < kPosTile; ++j)
+              s[j >> 5][j & 31] = __float_as_uint(__uint_as_float(s[j >> 5][j & 31]) * M.k_pos_pow[inf][j]);
+          }
 #pragma unroll
           for (int j = 0; j < kPosTile; ++j)
-            if (pos0 + j >= lim || (absent >> (j >> 4) & 1)) s[j >> 5][j & 31] = 0xff800000u;
+            if (pos0 + j >= lim || (odd >> (j >> 4) & 1)) s[j >> 5][j & 31] = 0xff800000u;
         }
         float m4[4];  // four chains
 #pragma unroll

@@ -124,3 +124,26 @@ def test_infinite_scales_count_as_nan(B, bits, dtype, qtok, n, empty):
     hit[qtok:2 * qtok, :group, 64:96] = True
     assert np.isnan(got[hit]).all()
     check(got, clean, dtype, ~np.isnan(clean[0]) & ~hit)
+
+
+# ------------------------------------------------------------------------------------------- positions that a row does not see
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d,size", [(128, 2e-3), (64, 0.08), (128, 0.4)])
+def test_large_keys_of_later_positions(B, dtype, d, size, empty):
+    """The last tokens of a chunk have keys near the largest that the cache holds; the tokens before them, in the same tile of
+    positions, do not see them and get what they get without them."""
+    rng = np.random.default_rng(101)
+    hkv, group, page, rows = 2, 4, 16, [(40, 61), (33, 126)]
+    cache, table, cu, length, q = attention_case(rng, hkv, group, d, page, rows, dtype, extra=0)
+    for i, (c, n) in enumerate(rows):
+        k = rng.standard_normal((n, hkv, d)) * size
+        k[n - 3:] = rng.standard_normal((3, hkv, d)) * 1e5
+        k = np.clip(k, -5e5, 5e5)
+        v = rng.standard_normal((n, hkv, d))
+        at = np.arange(n)
+        kv4.append(cache, k.astype(np.float32), v.astype(np.float32), table[i][at // page] * page + at % page)
+    q = as_given(q * (0.5 / size), dtype)      # scores of order 1 before the large keys
+    out = tiled(B, cache, table, cu, length, q, dtype, empty=empty)
+    check(out, reference(cache, q, cu, length, table), dtype)
