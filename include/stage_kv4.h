@@ -133,10 +133,12 @@ STAGE_API size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_head
  *     makes NaN of the KV head's outputs of every token that sees the position, in V of its own block of dims in them.
  *   Arithmetic: sums, maxima and the softmax are float32.  STAGE_F32: q and the probabilities are each
  *     held as two fp16 values (22 bits) and meet exact integers or exact values, for an error of the
- *     order of float32's; what lies 2^34 or more below a row's largest p_j v_j, or 2^25 below the largest
- *     scale of a position, counts as 0.  The 16-bit types round out once to nearest, and a probability
- *     may be rounded once to fp16; STAGE_BF16 may also round K and V once to fp16 (11 bits, where the
- *     output has 8).
+ *     order of float32's; what lies 2^34 or more below a row's largest p_j v_j counts as 0.  The 16-bit types round out
+ *     once to nearest, and a probability may be rounded once to fp16; what lies 2^27 or more below a row's largest p_j v_j
+ *     counts as 0.  STAGE_BF16 may also round K and V once to fp16 (11 bits, where the output has 8).  In all types an
+ *     element of q 2^34 or more below its row's largest counts as 0 (and from 2^27 below on has fewer bits), and where a
+ *     position's largest scale in K or V is 4096 or more, its values may be off by 2^-33 of its largest.  What a token
+ *     does not see has no part in any of this.
  *     A chunk's row is NaN where the GPU did not finish a copy or a product within two seconds.
  *   workspace_dev: stage_op_kv4_attention_workspace_bytes(...) bytes whose contents must be zero
  *     before the first call (each call leaves it ready for the next, of any sizes it is large enough

@@ -13,8 +13,8 @@
 //               memory would be read again by every product);
 //   warp 17     copies the packed tiles in (bulk copies, up to four tiles ahead).
 // What bounds it: the latency of a tile's chain (scores, softmax, probabilities, outputs) and of an item's ends (its q, its
-// results); the tensor cores are busy for 23 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 60 us) and 35 % (2 x 1024
-// rows on 8192 positions, STAGE_BF16, the second kernel below: 343 us, 680 TFLOP/s), the schedulers for 40 and 48 %.
+// results); the tensor cores are busy for 23 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 58 us) and 34 % (2 x 1024
+// rows on 8192 positions, STAGE_BF16, the second kernel below: 348 us, 669 TFLOP/s), the schedulers for 40 and 48 %.
 // The tensor cores' additions truncate: over a long sum the result shrinks (by 1e-4 of itself at 32768 positions).  So in
 // STAGE_F32 every tile's O is added to float32 registers, rounded to nearest, and the products with low parts come
 // first, where the sums they truncate are still small: 2e-6 of error became 5e-7.  The 16-bit types keep the whole sum
@@ -28,9 +28,12 @@
 // subnormal one exactly, in one number).  In the rare tile with a scale from 4096 on (rows of 32768), each position
 // has a power of its own, 1 where its own scales are below, which its score is multiplied by: what other positions hold,
 // those that a row does not see among them, changes nothing, and the position's own values lose 2^-33 of its largest.
-// V's scales are divided by a power of two
-// above the largest one, so that fp16's range holds them whatever they are, and what lies below 2^-25 of the largest is
-// lost: of a position's in STAGE_F32, of a tile's in the 16-bit types.  The power goes into the probabilities.
+// V's scales are multiplied by a power of two that brings the largest to 2^10 .. 2^12, and the probabilities by its inverse: so
+// the largest p_j |v_j| of a row, whatever the scales, has a probability near fp16's top, and what lies
+// 2^27 (STAGE_F32: 2^34) or more below it is lost.  Multiplied by powers of two up (from scales below 4096), multiples of 2^-24
+// stay what they are, so values of V are exact like K's.  In STAGE_F32 each position has its power.  In the 16-bit types a tile's
+// positions share one where their largest scales lie within a factor of 16, which rows of a model mostly do and which saves
+// a multiplication and an addition per score; in other tiles each has its own.
 
 #include <atomic>
 #include <cfloat>
@@ -48,10 +51,9 @@ namespace {
 constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
 constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 16 * kProdWarps;  // kProd: threads of a group of four warps
 constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpgroups
-// Registers per thread: the block starts with kRegsStart and its warpgroups trade them (4 x 512 rows, STAGE_F32: 64 us with
-// 136, 72, 64; 61 with these, 71 with 128, 80, 64; 2 x 1024 rows, STAGE_BF16: 343 with these, 353 with 144, 72, 48, 355 with
-// 160, 56, 48, 359 with 152, 56, 64).
-constexpr int kRegsStart = 96, kRegsSoft = 152, kRegsProd = 64, kRegsRest = 48;
+// Registers per thread: the block starts with kRegsStart and its warpgroups trade them (4 x 512 rows, STAGE_F32: 58.2 us with
+// these, 58.8 with 152, 64, 48, 59.8 with 136, 80, 48; 2 x 1024 rows, STAGE_BF16: 352, 360, 350, at the time).
+constexpr int kRegsStart = 96, kRegsSoft = 144, kRegsProd = 72, kRegsRest = 48;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
 constexpr int kInfo = 16;  // ring of what the tiles' producers tell the softmax
@@ -135,19 +137,19 @@ struct ChunkItems {
 
 // Prepared scales of a tile: [position][block] fp16, each eight positions a padding further, for the banks.
 __host__ __device__ constexpr int scale_place(int D, int pos) { return pos * (D / 16) + (pos >> 3) * (D / 8); }
-constexpr int kWide = 16;
+constexpr int kWide = 16, kSpread = 32;
 constexpr int kScaleBytes = scale_place(128, kPosTile);
 
 struct alignas(16) ChunkMisc {
   ChunkBars bar;
-  float v_exp[kInfo], v_inv[kInfo];  // E_v; 2^-E_v
+  float v_exp[kInfo], v_inv[kInfo];  // E_v; 2^-E_v (0 and 0 where each position has its own)
   alignas(16) float k_pos_pow[kInfo][kPosTile];
   alignas(16) float v_pos_exp[kInfo][kPosTile];  // read in 16-byte pieces
-  alignas(16) float v_pos_inv[kInfo][kPosTile];  // STAGE_F32: E_v and 2^-E_v of each position
-  uint32_t v_norm[kProdWarps][kPosTile / 2];                     // and 2^-E_v of two positions in fp16, one copy per warp
-  alignas(16) unsigned char k_scale[kProdWarps][kScaleBytes];  // a tile's scales as the products take them, one copy per warp
+  alignas(16) float v_pos_inv[kInfo][kPosTile];  // E_v and 2^-E_v of each position
+  alignas(16) unsigned char k_scale[kProdWarps][kScaleBytes], v_scale[kProdWarps][kScaleBytes];  // a tile's scales as the products
+                                                                                                 // take them, one copy per warp
   int absent[kInfo];                               // bit i: the tile's i-th 16 positions are not there
-  int odd[kInfo];                                  // the same, and kWide: its positions have powers of K of their own
+  int odd[kInfo];                                  // the same, and kWide, kSpread: its positions have powers of K, of V of their own
   int bad[kInfo];                                  // whether some V scale is no number
   int first_bad[kInfo][4];                         // per block of dims: the first such position
   float top[2][2][kRowsTile], q_top[2][kRowsTile]; // [tile parity][half][row]
@@ -259,12 +261,14 @@ __device__ __forceinline__ __half2 code_high(uint32_t x, uint32_t ex) {
   return __hfma2(as_h2(and_or(x, 0x00f000f0u, ex)), __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-72.f, -72.f));
 }
 
-// 2^-e as fp16, e in [-14, 16].
-__device__ __forceinline__ uint16_t half_power(int e) { return (uint16_t)(e <= 14 ? (15 - e) << 10 : 0x400 >> (e - 14)); }
+// 2^k in both halves, k in [-14, 15].
+__device__ __forceinline__ __half2 half_power(int k) { return __half2half2(__ushort_as_half((uint16_t)((15 + k) << 10))); }
 
 // K's scales from 4096 on (fp16 bits from here on) are divided by a power of two: e of a position with the largest scale `top`.
 constexpr uint32_t kBigScale = 27u << 10;
 __device__ __forceinline__ int k_power(uint32_t top) { return max(0, (int)min(top >> 10, 30u) - 26); }
+// V's are multiplied by 2^k twice (once would not reach: 2^26 for subnormal ones): k of the largest scale `top`, for 2^10 .. 2^12.
+__device__ __forceinline__ int v_power(uint32_t top) { return (26 - (int)(top >> 10)) >> 1; }
 __device__ __forceinline__ uint32_t larger_half(__half2 m) { return max(as_u32(m) >> 16, as_u32(m) & 0xffffu); }
 
 // ---------------- what both kernels have ----------------
@@ -322,12 +326,11 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
     const int absent = M.absent[inf];
     const unsigned char* raw = sm + L::off_raw + rs * L::stage_bytes;
     const int pos0 = (it.t0 + i) * kPosTile;
-    const bool ragged = absent || pos0 + kPosTile > lim_hi;  // some positions do not count: their scales read as 0
 
     // the scales, every warp for itself: a lane has two neighbouring positions.  Those that do not count read as 0
-    int e_v;
-    bool v_bad = false, k_big;
-    unsigned char* k_scale = M.k_scale[warp - kSoftWarps];
+    int k_tile = 0;
+    bool v_bad = false, k_big, v_spread = false;
+    unsigned char *k_scale = M.k_scale[warp - kSoftWarps], *v_scale = M.v_scale[warp - kSoftWarps];
     {
       const int s = lane >> 3, at = pos0 + s * kKv4Tile + 2 * (lane & 7);
       const bool ok0 = !(absent >> s & 1) && at < lim_hi, ok1 = !(absent >> s & 1) && at + 1 < lim_hi;
@@ -351,6 +354,48 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
         m = __hmax2(m, __floats2half2_rn(0.f, 0.f));
         return larger_half(m);
       };
+      auto put = [&](unsigned char* to) {
+        if constexpr (D == 128) *reinterpret_cast<uint4*>(to + scale_place(D, 2 * lane)) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2*>(to + scale_place(D, 2 * lane)) = make_uint2(w[0], w[1]);
+      };
+      __syncwarp();  // the last tile's are read
+      load(base + HALF + CODES + 16 + ((lane & 4) << 2));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) v_bad |= (w[b] & 0x7c00u) == 0x7c00u || (w[b] & 0x7c000000u) == 0x7c000000u;
+      v_bad = __any_sync(0xffffffffu, v_bad);
+      if (v_bad) {  // noted, and taken for 0
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t ones = h ? 0x7c000000u : 0x7c00u;
+            if ((w[b] & ones) == ones) {
+              if (pw == 0) atomicMin(&M.first_bad[inf][2 * b % NB + h], at + (b >= NB / 2));
+              w[b] &= h ? 0xffffu : 0xffff0000u;
+            }
+          }
+      }
+      const uint32_t top0 = largest(0), top1 = largest(1);
+      int k0 = v_power(top0), k1 = v_power(top1);
+      if (NP == 1) {
+        const uint32_t high = __reduce_max_sync(0xffffffffu, max(top0, top1));
+        const uint32_t low = __reduce_min_sync(0xffffffffu, min(top0 ? top0 : 0x7c00u, top1 ? top1 : 0x7c00u));  // 0 is of any size
+        v_spread = (low >> 10) + 3 < high >> 10;
+        k_tile = v_power(high);
+        if (!v_spread) k0 = k1 = k_tile;
+      }
+      if ((NP == 2 || v_spread) && pw == 0) {
+        *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)(-2 * k0), (float)(-2 * k1));
+        *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
+            make_float2(__uint_as_float((uint32_t)(127 + 2 * k0) << 23), __uint_as_float((uint32_t)(127 + 2 * k1) << 23));
+      }
+      const __half2 up0 = half_power(k0), up1 = half_power(k1);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const __half2 up = b < NB / 2 ? up0 : up1;
+        w[b] = as_u32(__hmul2(__hmul2(as_h2(w[b]), up), up));
+      }
+      put(v_scale);
       load(base + CODES);
       k_big = __reduce_max_sync(0xffffffffu, max(largest(0), largest(1))) >= kBigScale;
       if (k_big) {
@@ -358,41 +403,25 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
         for (int i = 0; i < 2; ++i) {
           const int e = k_power(largest(i));
           if (pw == 0) M.k_pos_pow[inf][2 * lane + i] = __uint_as_float((uint32_t)(127 + e) << 23);
-          const __half2 norm = __half2half2(__ushort_as_half(half_power(e)));
+          const __half2 norm = half_power(-e);
 #pragma unroll
           for (int b = i * (NB / 2); b < (i + 1) * (NB / 2); ++b)  // an infinity becomes NaN: a score of -infinity would drop its position
             w[b] = as_u32(__hmul2(__hfma2(as_h2(w[b]), __floats2half2_rn(0.f, 0.f), as_h2(w[b])), norm));
         }
       }
-      __syncwarp();  // the last tile's are read
-      if constexpr (D == 128) *reinterpret_cast<uint4*>(k_scale + scale_place(D, 2 * lane)) = make_uint4(w[0], w[1], w[2], w[3]);
-      else *reinterpret_cast<uint2*>(k_scale + scale_place(D, 2 * lane)) = make_uint2(w[0], w[1]);
+      put(k_scale);
 
-      load(base + HALF + CODES + 16 + ((lane & 4) << 2));
-#pragma unroll
-      for (int b = 0; b < NB; ++b) v_bad |= (w[b] & 0x7c00u) == 0x7c00u || (w[b] & 0x7c000000u) == 0x7c000000u;
-      const uint32_t top0 = largest(0), top1 = largest(1);
-      if (NP == 2) {
-        const int e0 = (int)min(top0 >> 10, 30u) - 14, e1 = (int)min(top1 >> 10, 30u) - 14;
-        M.v_norm[warp - kSoftWarps][lane] = (uint32_t)half_power(e0) | (uint32_t)half_power(e1) << 16;
-        if (pw == 0) {
-          *reinterpret_cast<float2*>(&M.v_pos_exp[inf][2 * lane]) = make_float2((float)e0, (float)e1);
-          *reinterpret_cast<float2*>(&M.v_pos_inv[inf][2 * lane]) =
-              make_float2(__uint_as_float((uint32_t)(127 - e0) << 23), __uint_as_float((uint32_t)(127 - e1) << 23));
-        }
-      }
-      e_v = NP == 2 ? 0 : (int)min(__reduce_max_sync(0xffffffffu, max(top0, top1)) >> 10, 30u) - 14;
-      v_bad = __any_sync(0xffffffffu, v_bad);
     }
-    const __half2 norm_v = __half2half2(__ushort_as_half(half_power(e_v)));
     __syncwarp();  // the prepared scales
     // K: 64 positions x 4 x (the word of eight dims of every block)
     if (ni >= KS) ok = __all_sync(0xffffffffu, cwait(&B.k_empty[st], (uint32_t)(ni / KS + 1) & 1u, abort_flag));
     if (!ok) break;
     if (p == 0) {
-      M.odd[inf] = absent | (k_big ? kWide : 0);
-      M.v_exp[inf] = (float)e_v;
-      M.v_inv[inf] = __uint_as_float((uint32_t)(127 - e_v) << 23);
+      M.odd[inf] = absent | (k_big ? kWide : 0) | (v_spread ? kSpread : 0);
+      if (NP == 1) {
+        M.v_exp[inf] = v_spread ? 0.f : (float)(-2 * k_tile);
+        M.v_inv[inf] = v_spread ? 0.f : __uint_as_float((uint32_t)(127 + 2 * k_tile) << 23);
+      }
       M.bad[inf] = v_bad;
       // For tile n + kRaw, which no warp has begun: its copy waits until every warp of the group has read tile n.  The
       // entry's last tile, n + kRaw - kInfo, was read by the softmax before it handed on the probabilities of a tile whose
@@ -447,7 +476,7 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
       const int chunk = lane & 7, dsel = (lane >> 3) & 1, gid = pw * 2 + (lane >> 4), s = chunk >> 1, h = chunk & 1;
       const unsigned char* src = raw + s * L::sub_stride + HALF;
       const unsigned char* codes = src + h * (CODES / 2 + 16) + gid * (D / 2);
-      const unsigned char* scales = src + CODES + 16 + h * (8 * 2 * NB + 16);
+      const unsigned char* scales = v_scale + scale_place(D, 8 * chunk);
 #pragma unroll 1
       for (int b0 = 0; b0 < NB; b0 += VB) {
       uint32_t hi[VB][2][4], lo[VB][2][4];
@@ -471,24 +500,9 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
           const uint2 v = *reinterpret_cast<const uint2*>(scales + tig * 8);
           sc[0][0] = v.x >> (16 * b0), sc[1][0] = v.y >> (16 * b0);
         }
-        if (ragged || v_bad) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = pos0 + chunk * 8 + 2 * tig + e;
-            const bool off = (absent >> s & 1) || at >= lim_hi;
-#pragma unroll
-            for (int b = 0; b < VB; ++b) {
-              const uint32_t mask = b & 1 ? 0xffff0000u : 0xffffu;
-              const bool bad = (sc[e][b / 2] & mask & 0x7c007c00u) == (mask & 0x7c007c00u);
-              if (bad && !off) atomicMin(&M.first_bad[inf][b0 + b], at);
-              if (bad || off) sc[e][b / 2] &= ~mask;
-            }
-          }
-        }
 #pragma unroll
         for (int b = 0; b < VB; ++b) {
-          const __half2 s2 = __hmul2(as_h2(__byte_perm(sc[0][b / 2], sc[1][b / 2], b & 1 ? 0x7632 : 0x5410)),
-                                     NP == 2 ? as_h2(M.v_norm[warp - kSoftWarps][4 * chunk + tig]) : norm_v);
+          const __half2 s2 = as_h2(__byte_perm(sc[0][b / 2], sc[1][b / 2], b & 1 ? 0x7632 : 0x5410));
           // byte dsel of the block's two bytes, of both positions
           const uint32_t x = __byte_perm(w[0][b / 2], w[1][b / 2], (b & 1 ? 0x6622 : 0x4400) + dsel * 0x1111);
           const __half2 n0 = code_low(x, ex), n1 = code_high(x, ex);
@@ -797,7 +811,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
       tc_fence_after();
       uint32_t s[32];
       tmem_ld32(lanes + kColS + st * kPosTile + half * 32, s);
-      const float f = zscale, ev = M.v_exp[inf], v_inv = M.v_inv[inf];
+      float f = zscale;
+      const float ev = NP == 2 ? 0.f : M.v_exp[inf], v_inv = NP == 2 ? 1.f : M.v_inv[inf];
       const int odd = M.odd[inf];
       if (i >= 2) note_bad(ni - 2);
       tmem_wait_ld();
@@ -806,6 +821,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
         if (odd & kWide) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * M.k_pos_pow[inf][32 * half + j]);
+        }
+        if (NP == 1 && (odd & kSpread)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(fmaf(__uint_as_float(s[j]), f, M.v_pos_exp[inf][32 * half + j]));
+          f = 1.f;
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j)
@@ -865,6 +885,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
         }
       }
       const float c = ev - (ref == -INFINITY ? 0.f : ref);
+      if (NP == 1 && (odd & kSpread)) {  // the sum by each position's power; the one below counts for 0 (v_inv)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum += exp2_approx(__uint_as_float(s[j]) - M.v_pos_exp[inf][32 * half + j] + c);
+      }
       float2 part4[4];  // four chains
 #pragma unroll
       for (int j = 0; j < 4; ++j) part4[j] = make_float2(0.f, 0.f);
@@ -1148,7 +1172,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
         uint32_t s[2][32];
         tmem_ld32(place_s + b * kPosTile, s[0]);
         tmem_ld32(place_s + b * kPosTile + 32, s[1]);
-        const float f = zscale, ev = M.v_exp[inf], v_inv = M.v_inv[inf];
+        float f = zscale;
+        const float ev = M.v_exp[inf], v_inv = M.v_inv[inf];
         const int odd = M.odd[inf];
         if (i >= 2) note_bad(ni - 2);
         tmem_wait_ld();
@@ -1158,6 +1183,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
 #pragma unroll
             for (int j = 0; j < kPosTile; ++j)
               s[j >> 5][j & 31] = __float_as_uint(__uint_as_float(s[j >> 5][j & 31]) * M.k_pos_pow[inf][j]);
+          }
+          if (odd & kSpread) {
+#pragma unroll
+            for (int j = 0; j < kPosTile; ++j)
+              s[j >> 5][j & 31] = __float_as_uint(fmaf(__uint_as_float(s[j >> 5][j & 31]), f, M.v_pos_exp[inf][j]));
+            f = 1.f;
           }
 #pragma unroll
           for (int j = 0; j < kPosTile; ++j)
@@ -1175,20 +1206,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
           ref = most - kChunkTop<1>;
           sum *= keep;
         }
-        if (__any_sync(0xffffffffu, keep != 1.f) && i > 0) {
-          ok = products_done(c - 1);
-          if (!ok) break;
-#pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            uint32_t r[16];
-            tmem_ld16(place_o + d, r);
-            tmem_wait_ld();
+        const float base = ev - (ref == -INFINITY ? 0.f : ref);
+        const bool moved = __any_sync(0xffffffffu, keep != 1.f) && i > 0;
+        if (moved || (odd & kSpread)) {
+          if (odd & kSpread) {  // the sum by each position's power; the one below counts for 0 (v_inv)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * keep);
-            tmem_st16(place_o + d, r);
+            for (int j = 0; j < kPosTile; ++j) sum += exp2_approx(__uint_as_float(s[j >> 5][j & 31]) - M.v_pos_exp[inf][j] + base);
+          }
+          if (moved) {
+            ok = products_done(c - 1);
+            if (!ok) break;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 16) {
+              uint32_t r[16];
+              tmem_ld16(place_o + d, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * keep);
+              tmem_st16(place_o + d, r);
+            }
           }
         }
-        const float base = ev - (ref == -INFINITY ? 0.f : ref);
         float2 part4[4];  // four chains
 #pragma unroll
         for (int j = 0; j < 4; ++j) part4[j] = make_float2(0.f, 0.f);

@@ -1,6 +1,15 @@
-"""Attention over the paged 4-bit cache at the edges of its range, against a float64 reference.
+"""Attention over the paged 4-bit cache where scales are infinite or spread far, where positions that a row does not see
+hold large values, and where a CTA of the tiles for many columns goes from item to item.
 
-The tolerances are those of tests/test_gpu_kv4.py, derived there; `small` bounds what fp16's smallest step takes from a probability.
+The tolerances are those of tests/test_gpu_kv4.py, derived there, with two changes for the tiles for many columns.  K and V
+are exact there (STAGE_BF16: rounded once to fp16, 2^-11 of themselves), whatever the block's scale, unless a scale of 4096 or
+more shares the position; then a value is off by at most 2^-33 of the position's largest.  And the fp16 probabilities end at
+2^-25 (half of the smallest step): with T_j the largest scale of position j (at least 2^-14), a probability stands as
+x_j = 2^(z_j - r + e_j) against values v_j 2^-(e_j), where T_j is in 2^(e_j) * [2^10, 2^12) if each position has its own power and in
+2^(e_j) * [2^7, 2^12) if a tile's positions share one.  The largest x_j is at least 2^11 (two fp16 values) or 2^7 (one), at a position
+m, and divides by p_m 2^(e_m) / x_m at most, so dim d is off by at most
+    sum_j 2^-25 |v_jd| 2^-(e_j) p_m 2^(e_m) / x_m <= 2^-34 max_j(p_j T_j) sum_j |v_jd| / T_j          (two)
+                                                  <= 2^-27 max_j(p_j T_j) sum_j |v_jd| / T_j          (one).
 """
 import numpy as np
 import pytest
@@ -105,7 +114,7 @@ def put_scale(cache, table, i, pos, head, block, is_v, bits):
 
 @pytest.mark.parametrize("bits", [0x7C00, 0xFC00])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("qtok,n,empty", [(1, 100, None), (1, 3000, None), (3, 200, None)])
+@pytest.mark.parametrize("qtok,n,empty", [(1, 100, None), (1, 3000, None), (3, 200, None), (40, 200, 0), (40, 200, 160)])
 def test_infinite_scales_count_as_nan(B, bits, dtype, qtok, n, empty):
     """An infinite scale in K makes NaN of the outputs that see it, of its KV head; one in V of its block's dims; other heads,
     sequences, dims and tokens keep their values, and the sign does not matter."""
@@ -145,5 +154,65 @@ def test_large_keys_of_later_positions(B, dtype, d, size, empty):
         at = np.arange(n)
         kv4.append(cache, k.astype(np.float32), v.astype(np.float32), table[i][at // page] * page + at % page)
     q = as_given(q * (0.5 / size), dtype)      # scores of order 1 before the large keys
+    out = tiled(B, cache, table, cu, length, q, dtype, empty=empty)
+    check(out, reference(cache, q, cu, length, table), dtype)
+
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_of_later_positions(B, dtype, d, empty):
+    """The same for values: 1e-4 beside 4e5 that only the last tokens see."""
+    rng = np.random.default_rng(103)
+    hkv, group, page, rows = 2, 4, 16, [(40, 61), (33, 126)]
+    cache, table, cu, length, q = attention_case(rng, hkv, group, d, page, rows, dtype, extra=0)
+    for i, (c, n) in enumerate(rows):
+        v = rng.standard_normal((n, hkv, d)) * 1e-4
+        v[n - 3:] = np.clip(rng.standard_normal((3, hkv, d)) * 1e5, -4e5, 4e5)
+        if dtype == "f16":
+            v[n - 3:] /= 16        # outputs that float16 holds
+        at = np.arange(n)
+        kv4.append(cache, rng.standard_normal((n, hkv, d)).astype(np.float32), v.astype(np.float32), table[i][at // page] * page + at % page)
+    out = tiled(B, cache, table, cu, length, q, dtype, empty=empty)
+    check(out, reference(cache, q, cu, length, table), dtype)
+
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d,by", [(128, "position"), (64, "position"), (128, "block"), (64, "block"), (128, "tile")])
+def test_values_over_a_wide_range(B, dtype, d, by, empty):
+    """V from 1e-6 to 1e4 from position to position, block to block or tile to tile, with scores that single positions out."""
+    rng = np.random.default_rng(105)
+    hkv, group, page, rows = 2, 4, 32, [(40, 300), (35, 130)]
+    cache, table, cu, length, q = attention_case(rng, hkv, group, d, page, rows, dtype, extra=0)
+    for i, (c, n) in enumerate(rows):
+        shape = {"position": (n, hkv, 1, 1), "block": (n, hkv, d // 32, 1), "tile": (n, hkv, 1, 1)}[by]
+        power = rng.integers(-6, 4, shape)
+        if by == "tile":
+            power = power[np.arange(n) // 64 * 64]
+        v = rng.standard_normal((n, hkv, d // 32, 32)) * 10.0 ** power
+        v = np.clip(v, -3e4, 3e4).reshape(n, hkv, d)
+        at = np.arange(n)
+        kv4.append(cache, (2 * rng.standard_normal((n, hkv, d))).astype(np.float32), v.astype(np.float32), table[i][at // page] * page + at % page)
+    q = as_given(q * 10.0 ** rng.integers(-2, 2, q.shape[:2] + (1,)), dtype)
+    out = tiled(B, cache, table, cu, length, q, dtype, empty=empty)
+    check(out, reference(cache, q, cu, length, table), dtype)
+
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_keys_and_values_of_many_sizes(B, dtype, empty):
+    """Keys and values from 1e-6 to 1e5: scores far beyond float32's exponentials, rows of zeros, subnormal scales."""
+    rng = np.random.default_rng(107)
+    hkv, group, d, page, rows = 2, 4, 128, 16, [(40, 300), (50, 64)]
+    cache, table, cu, length, q = attention_case(rng, hkv, group, d, page, rows, dtype, extra=0)
+    for i, (c, n) in enumerate(rows):
+        k, v = (rng.standard_normal((n, hkv, d)) * 10.0 ** rng.integers(-6, 5, (n, hkv, 1)) for _ in range(2))
+        k[n // 3], v[n // 2] = 0, 0
+        if dtype == "f16":
+            v = np.clip(v, -3e4, 3e4)
+        at = np.arange(n)
+        kv4.append(cache, k.astype(np.float32), v.astype(np.float32), table[i][at // page] * page + at % page)
+    q = as_given(q * 10.0 ** rng.integers(-4, 1, q.shape[:2] + (1,)), dtype)
     out = tiled(B, cache, table, cu, length, q, dtype, empty=empty)
     check(out, reference(cache, q, cu, length, table), dtype)
