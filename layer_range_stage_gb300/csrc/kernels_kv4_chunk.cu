@@ -15,10 +15,11 @@
 // What bounds it: the latency of a tile's chain (scores, softmax, probabilities, outputs) and of an item's ends (its q, its
 // results); the tensor cores are busy for 23 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 58 us) and 34 % (2 x 1024
 // rows on 8192 positions, STAGE_BF16, the second kernel below: 348 us, 669 TFLOP/s), the schedulers for 40 and 48 %.
-// The tensor cores' additions truncate: over a long sum the result shrinks (by 1e-4 of itself at 32768 positions).  So in
-// STAGE_F32 every tile's O is added to float32 registers, rounded to nearest, and the products with low parts come
-// first, where the sums they truncate are still small: 2e-6 of error became 5e-7.  The 16-bit types keep the whole sum
-// in TMEM; there a row's change of reference, which is rare, rescales its sums.
+// The tensor cores' additions truncate: over a long sum the result shrinks (by 6e-7 of itself per tile of 64 positions, 15 %
+// over 16 million).  So in STAGE_F32 every tile's O is added to float32 registers, rounded to nearest, and the products with
+// low parts come first, where the sums they truncate are still small: 2e-6 of error became 5e-7.  The 16-bit types keep
+// the sum in TMEM, where a row's change of reference, which is rare, rescales it, for a chain of kChain tiles (7e-5 of the
+// sum); then it is added to float32 sums in the workspace and begins again.
 //
 // Precision: a value s (c - 8) has 15 significant bits, so two fp16 numbers hold it exactly; q and the probabilities are
 // float32 and two fp16 numbers hold 22 bits.  STAGE_F32 multiplies high by high, low by high and high by low (three
@@ -56,6 +57,7 @@ constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpg
 constexpr int kRegsStart = 96, kRegsSoft = 144, kRegsProd = 72, kRegsRest = 48;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");
+constexpr int kChain = 128;  // tiles, a power of two
 constexpr int kInfo = 16;  // ring of what the tiles' producers tell the softmax
 // The largest probability (times its power of V) lies at 2^top when the reference is set, and may grow by 2^slack before
 // it is set again: fp16 ends at 2^16.  With one fp16 value per probability fewer changes count more than the range below.
@@ -233,12 +235,42 @@ __device__ __forceinline__ void rows_out(unsigned char* turn, void* base, long l
 }
 
 // Partial results, where a row tile's positions are shared out: per item and row the sums (float32, not divided), and
-// the reference and the sum that divides them.
-__device__ __forceinline__ float* part_row(const Kv4AttnArgs& a, long long number, int rows, int row, int D) {
-  return reinterpret_cast<float*>((char*)a.ws + kKv4CounterBytes) + (number * rows + row) * D;
+// the reference and the sum that divides them.  Before these, and without parts, the chains' sums lie there.
+__device__ __forceinline__ float* part_row(void* ws, long long number, int rows, int row, int D) {
+  return reinterpret_cast<float*>((char*)ws + kKv4CounterBytes) + (number * rows + row) * D;
 }
-__device__ __forceinline__ float2* part_ml(const Kv4AttnArgs& a, long long count, long long number, int rows, int row, int D) {
-  return reinterpret_cast<float2*>(part_row(a, count, rows, 0, D)) + number * rows + row;
+__device__ __forceinline__ float2* part_ml(void* ws, long long count, long long number, int rows, int row, int D) {
+  return reinterpret_cast<float2*>(part_row(ws, count, rows, 0, D)) + number * rows + row;
+}
+
+// END: the sums of a row's dims from `place` (TMEM) on are added to those of the chains that are done (`first`: there are none
+// yet), and set to 0; else those are added to them.  They lie at the partial results' place `number` of `count`, the reference
+// that they are of beside them, one for each half of the row's dims.  The whole warp.  A function of its own: inside the
+// kernels, which live off their last registers, it made 2 x 1024 rows of STAGE_BF16 take 398 us instead of 349.
+template <int D, int ROWS, int DIMS, bool END>
+__device__ __noinline__ void chain_sums(void* ws, long long number, long long count, int row, int half, uint32_t place, float ref, bool first) {
+  float* done = part_row(ws, number, ROWS, row, D) + half * DIMS;
+  float* done_ref = &part_ml(ws, count, number, ROWS, row, D)->x + half;
+  const float old = first ? 0.f : *done_ref, factor = first ? 0.f : old == ref ? 1.f : exp2_approx(old - ref);
+#pragma unroll 1
+  for (int d = 0; d < DIMS; d += 16) {
+    uint32_t r[16];
+    tmem_ld16(place + d, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      float4* at = reinterpret_cast<float4*>(done + d + j);
+      float4 v = factor != 0.f ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+      v = make_float4(fmaf(v.x, factor, __uint_as_float(r[j])), fmaf(v.y, factor, __uint_as_float(r[j + 1])),
+                      fmaf(v.z, factor, __uint_as_float(r[j + 2])), fmaf(v.w, factor, __uint_as_float(r[j + 3])));
+      if (END) *at = v;
+      r[j] = END ? 0 : __float_as_uint(v.x), r[j + 1] = END ? 0 : __float_as_uint(v.y);
+      r[j + 2] = END ? 0 : __float_as_uint(v.z), r[j + 3] = END ? 0 : __float_as_uint(v.w);
+    }
+    tmem_st16(place + d, r);
+  }
+  tmem_wait_st();
+  if (END) *done_ref = ref;
 }
 
 template <int N>
@@ -799,7 +831,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
         }
       }
     };
-    for (int i = 0; i < nt; ++i) {
+    for (int i = 0; i < nt;) {  // STAGE_F16: chains of tiles
+    if (NP == 1 && i > 0) {
+      ok = ok && products_done(n + i - 1);
+      if (ok) chain_sums<D, kRowsTile, HD, true>(a.ws, SPLIT ? it.number : (long long)blockIdx.x, SPLIT ? a.count : (long long)gridDim.x, row, half, lanes + kColO + half * HD, ref, i == kChain);
+    }
+    for (const int end = NP == 1 ? min(nt, i + kChain) : nt; i < end; ++i) {
       const int ni = n + i, st = ni & 1, inf = ni & (kInfo - 1);
       // S of tile i is there, and so is the product of tile i - 2, issued before it: P's place is free.  When a wait has run
       // out every thread still goes through the barriers, and does nothing else
@@ -916,9 +953,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
       tc_fence_before();
       mbar_arrive(&B.p_full[st]);
     }
+    }
     if (ok && nt > 0) {
       ok = products_done(n + nt - 1);
       if (ok && NP == 2) collect();
+      if (ok && NP == 1 && nt > kChain) chain_sums<D, kRowsTile, HD, false>(a.ws, SPLIT ? it.number : (long long)blockIdx.x, SPLIT ? a.count : (long long)gridDim.x, row, half, lanes + kColO + half * HD, ref, false);
       if (nt > 1) note_bad(n + nt - 2);
       note_bad(n + nt - 1);
     }
@@ -927,9 +966,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
     sum += M.top[(n + nt) & 1][half ^ 1][row];
     named_bar(1 + (warp & 3), 64);  // read before the next item writes there
     const float inv = !ok ? NAN : SPLIT ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
-    if (SPLIT && half == 0) *part_ml(a, a.count, it.number, kRowsTile, row, D) = make_float2(ref, sum);
+    if (SPLIT && half == 0) *part_ml(a.ws, a.count, it.number, kRowsTile, row, D) = make_float2(ref, sum);
     // where the results go: the output, or (float32) the part's place
-    void* out = SPLIT ? (void*)part_row(a, it.number, kRowsTile, 0, D) : a.out;
+    void* out = SPLIT ? (void*)part_row(a.ws, it.number, kRowsTile, 0, D) : a.out;
     const long long to = SPLIT ? ((long long)row * D + half * HD) * 4 : ((long long)(it.start + col_k) * a.out_stride + elem) * (F32 ? 4 : 2);
     uint4 narrow[HD / 8];
 #pragma unroll
@@ -1163,7 +1202,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
             if (M.first_bad[i & (kInfo - 1)][b] < lim) nan_blocks |= 1 << b;
         }
       };
-      for (int i = 0; ok && i < nt; ++i, ++c) {
+      for (int i = 0; ok && i < nt;) {  // chains of tiles
+      if (i > 0) {
+        ok = products_done(c - 1);
+        if (!ok) break;
+        chain_sums<D, 2 * kRowsTile, D, true>(a.ws, SPLIT ? it.number : (long long)blockIdx.x, SPLIT ? a.count : (long long)gridDim.x, g * kRowsTile + row, 0, place_o, ref, i == kChain);
+      }
+      for (const int end = min(nt, i + kChain); i < end; ++i, ++c) {
         const int ni = n + i, inf = ni & (kInfo - 1);
         const uint32_t b = c & 1;
         ok = __all_sync(0xffffffffu, cwait(&B.pair_s[g][b], c / 2 & 1u, abort_flag));
@@ -1248,13 +1293,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
         tc_fence_before();
         mbar_arrive(&B.pair_p[g][b]);
       }
+      }
       if (ok && nt > 0) {
         ok = products_done(c - 1);
+        if (ok && nt > kChain) chain_sums<D, 2 * kRowsTile, D, false>(a.ws, SPLIT ? it.number : (long long)blockIdx.x, SPLIT ? a.count : (long long)gridDim.x, g * kRowsTile + row, 0, place_o, ref, false);
         if (nt > 1) note_bad(n + nt - 2);
         note_bad(n + nt - 1);
       }
       const float inv = !ok ? NAN : SPLIT ? 1.f : sum != 0.f ? 1.f / sum : 0.f;  // rows that could not be finished are NaN
-      if (SPLIT) *part_ml(a, a.count, it.number, 2 * kRowsTile, g * kRowsTile + row, D) = make_float2(ref, sum);
+      if (SPLIT) *part_ml(a.ws, a.count, it.number, 2 * kRowsTile, g * kRowsTile + row, D) = make_float2(ref, sum);
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {  // a block of dims
         uint32_t r[32];
@@ -1267,7 +1314,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
         }
         const float factor = nan_blocks >> (d >> 5) & 1 ? NAN : inv;
         if (live && SPLIT) {
-          float4* out = reinterpret_cast<float4*>(part_row(a, it.number, 2 * kRowsTile, g * kRowsTile + row, D) + d);
+          float4* out = reinterpret_cast<float4*>(part_row(a.ws, it.number, 2 * kRowsTile, g * kRowsTile + row, D) + d);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             out[j] = make_float4(__uint_as_float(r[4 * j]) * factor, __uint_as_float(r[4 * j + 1]) * factor,
@@ -1313,12 +1360,12 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const ChunkArgs a, int dt
   float top = -INFINITY, sum = 0.f, v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0.f;
-  for (int p = 0; p < parts; ++p) top = fmaxf(top, part_ml(a, a.count, number + p, rows, row, D)->x);
+  for (int p = 0; p < parts; ++p) top = fmaxf(top, part_ml(a.ws, a.count, number + p, rows, row, D)->x);
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    const float2 ml = *part_ml(a, a.count, number + p, rows, row, D);
+    const float2 ml = *part_ml(a.ws, a.count, number + p, rows, row, D);
     const float k = ml.x == top ? 1.f : exp2_approx(ml.x - top);
-    const float* src = part_row(a, number + p, rows, row, D) + lane * N;
+    const float* src = part_row(a.ws, number + p, rows, row, D) + lane * N;
     sum = fmaf(ml.y, k, sum);
     if constexpr (N == 4) {
       const float4 x = *reinterpret_cast<const float4*>(src);
@@ -1355,7 +1402,8 @@ cudaError_t launch_items(Kernel* kern, int smem, const ChunkArgs& a, std::atomic
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  kern<<<(int)min(a.count, (long long)sm_count()), kChunkThreads, smem, st>>>(a);
+  // the workspace has places for kKv4ChunkParts CTAs' chains
+  kern<<<(int)min(a.count, (long long)min(sm_count(), kKv4ChunkParts)), kChunkThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

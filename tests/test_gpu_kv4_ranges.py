@@ -216,3 +216,27 @@ def test_keys_and_values_of_many_sizes(B, dtype, empty):
     q = as_given(q * 10.0 ** rng.integers(-4, 1, q.shape[:2] + (1,)), dtype)
     out = tiled(B, cache, table, cu, length, q, dtype, empty=empty)
     check(out, reference(cache, q, cu, length, table), dtype)
+
+
+# ------------------------------------------------------------------------------------------- long sums
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_over_millions_of_positions(B, dtype, d, empty):
+    """One page of values between 0.5 and 1, 4096 times in the table: with q = 0 every position weighs the same (an exact
+    probability), so the output is the page's mean.  The tensor cores' additions drop 6e-7 of the sum per tile of 64 positions (as
+    measured: 15 % over these when a chain of them had no end), 128 tiles 2^-13; the chains' sums are then added up in float32,
+    2048 additions of 2^-24 each: 2^-13.  64 more tokens or fewer than the whole page move the mean by less than
+    2^-18; bfloat16 rounds V to fp16, 2^-12 of itself; 2^-14 for the probabilities' sum and the division.  The output's rounding
+    comes on top."""
+    page, n = 4096, 4096 * 4096
+    rng = np.random.default_rng(127)
+    cache = kv4.cache_array(1, page, 1, d)
+    kv4.append(cache, np.zeros((page, 1, d), np.float32), rng.uniform(0.5, 1, (page, 1, d)).astype(np.float32), np.arange(page))
+    want = kv4.rows(cache, np.arange(page), True).mean(0)
+    table = np.zeros((1, n // page), np.int32)
+    out = tiled(B, cache, table, np.array([0, 40], np.int32), np.array([n], np.int32), np.zeros((40, 1, d)), dtype, empty=empty)
+    got = out.double().cpu().numpy()
+    tol = 2.0 ** -12 + 2.0 ** -14 + 2.0 ** -18 + (2.0 ** -12 if dtype == "bf16" else 0) + torch.finfo(DT[dtype]).eps / 2
+    assert (np.abs(got - want) <= tol * want).all(), (np.abs(got - want) / want).max()
