@@ -218,6 +218,44 @@ def test_keys_and_values_of_many_sizes(B, dtype, empty):
     check(out, reference(cache, q, cu, length, table), dtype)
 
 
+# ------------------------------------------------------------------------------------------- from item to item
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_items_on_every_cta(B, dtype, d):
+    """40 sequences of 8 KV heads, several hundred items: items without a tile, of one, two and more than sixteen follow one another
+    on a CTA, with NaN in V, a K scale far above the others and absent pages in some of them."""
+    rng = np.random.default_rng(109 + d)
+    rows = [(int(rng.integers(40, 131)), int(rng.integers(60, 701))) for _ in range(36)]
+    rows += [(100, 30), (0, 50), (1, 1300), (70, 1400)]
+    rows = [rows[i] for i in rng.permutation(len(rows))]
+    cache, table, cu, length, q = attention_case(rng, 8, 4, d, 16, rows, dtype)
+    put_scale(cache, table, 3, int(length[3]) // 2, 2, 1, False, 0x7800)       # 32768
+    at = rows.index((70, 1400))
+    table[at, 40:44] = [-1, cache.shape[0], 2 ** 31 - 1, -2 ** 31]
+    bad, block = next(i for i in range(15, 40) if rows[i][0] > 60 and rows[i][1] > 200), 1
+    want = reference(cache, q, cu, length, table)
+    pos = rows[bad][1] - 30
+    put_scale(cache, table, bad, pos, 5, block, True, 0x7FFF)
+    out = run_attention(B, cache, table, cu, length, q, dtype).double().cpu().numpy()
+    hit = np.zeros(q.shape, bool)
+    hit[int(cu[bad]) + pos - (rows[bad][1] - rows[bad][0]):int(cu[bad + 1]), 20:24, 32 * block:32 * block + 32] = True
+    assert np.isnan(out[hit]).all()
+    check(out, want, dtype, ~np.isnan(want[0]) & ~hit)
+    again = run_attention(B, cache, table, cu, length, q, dtype).double().cpu().numpy()
+    same(out, again)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_long_items_follow_one_another(B, dtype):
+    """Fewer sequences with long contexts: each CTA has a few items of dozens of tiles."""
+    rng = np.random.default_rng(113)
+    rows = [(300, 2500), (420, 420), (333, 1111), (512, 2000)]
+    cache, table, cu, length, q = attention_case(rng, 8, 4, 128, 64, rows, dtype)
+    out = run_attention(B, cache, table, cu, length, q, dtype)
+    check(out, reference(cache, q, cu, length, table), dtype)
+
+
 # ------------------------------------------------------------------------------------------- long sums
 
 @pytest.mark.parametrize("empty", [0, 160])
