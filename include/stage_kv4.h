@@ -112,6 +112,12 @@ STAGE_API size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_head
                                                         int max_q, int max_len);
 #define STAGE_KV4_SCRATCH_MAX (64u << 20)
 
+/* Which kernel a call of stage_op_kv4_attention with these sizes runs on: 1, the one for many columns (query tokens of a
+ * sequence times query heads per KV head; a chunk of a prompt), whose precision is stated below as that of chunks; 0, the one
+ * for few.  It goes by the bounds alone.  Host only.  Errors: STAGE_E_INVALID (sizes that no call accepts). */
+STAGE_API int stage_op_kv4_attention_many(int n_seqs, int n_tok, int n_q_heads, int n_kv_heads, int head_dim, int dtype, int max_q,
+                                          int max_len);
+
 /* Attention over the paged 4-bit cache.
  *   q_dev: [n_tok] rows of n_q_heads * head_dim elements of `dtype` (already rotated), row t at
  *     t * q_stride elements; out_dev the same with out_stride (it may be q_dev, with the same stride, and else

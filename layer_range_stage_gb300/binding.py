@@ -124,6 +124,7 @@ _SIGS = {
     "stage_op_kv4_read": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
                                     C.c_void_p, C.c_int, C.c_int64, C.c_void_p]),
     "stage_op_kv4_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 6),
+    "stage_op_kv4_attention_many": (C.c_int, [C.c_int] * 8),
     "stage_op_kv4_attention": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_int64,
                                          C.c_int, C.c_int] + [C.c_void_p] * 3 + [C.c_int] * 4 +
                                [C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]),
@@ -567,7 +568,13 @@ def _rows(t, heads: int, head_dim: int, what: str):
     return t.data_ptr(), dt, s0 if shape[0] > 1 else heads * head_dim
 
 
+def _beyond_c_int(*sizes) -> bool:  # it would drop what lies above its bits
+    return any(not -1 << 31 <= s < 1 << 31 for s in sizes)
+
+
 def stage_op_kv4_cache_bytes(n_pages: int, page_len: int, n_kv_heads: int, head_dim: int) -> int:
+    if not 0 < n_pages < 1 << 31 or _beyond_c_int(page_len, n_kv_heads, head_dim):
+        return 0
     return int(lib().stage_op_kv4_cache_bytes(n_pages, page_len, n_kv_heads, head_dim))
 
 
@@ -639,7 +646,21 @@ def stage_op_kv4_read(cache, slot, k_out, v_out, stream=None) -> None:
 
 def stage_op_kv4_attention_workspace_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int,
                                            max_len: int) -> int:
+    if _beyond_c_int(n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_len):
+        return 0
     return int(lib().stage_op_kv4_attention_workspace_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_len))
+
+
+def stage_op_kv4_attention_many(n_seqs: int, n_tok: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype, max_q: int,
+                                max_len: int) -> bool:
+    """Whether a call with these sizes (dtype: a torch type) runs on the kernel for many columns."""
+    _torch or _load_torch()
+    if _beyond_c_int(n_seqs, n_tok, n_q_heads, n_kv_heads, head_dim, max_q, max_len):
+        _invalid("no attention of these sizes")
+    rc = lib().stage_op_kv4_attention_many(n_seqs, n_tok, n_q_heads, n_kv_heads, head_dim, _KV4_DTYPE.get(dtype, -1), max_q, max_len)
+    if rc < 0:
+        _opcheck(rc)
+    return bool(rc)
 
 
 def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_len: int, workspace, stream=None) -> None:

@@ -632,9 +632,10 @@ cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
 // 4 of 512: 64 columns 19 and 23, 256 columns 44 and 27.
 constexpr int kFewColumns = 24;
 
-bool many_columns(int n_seqs, int n_kv_heads, long long cols, int max_len, int dtype) {
+bool kv4_many_columns(const Kv4AttnArgs& a, int dtype) {
+  const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
   if (cols <= kFewColumns) return false;
-  const double z = 1e-6 * n_seqs * n_kv_heads * max_len;
+  const double z = 1e-6 * a.n_seqs * a.c.n_kv_heads * a.max_len;
   const double there = dtype == KV4_BF16 ? 155. * ((cols + 255) / 256) : (dtype == KV4_F32 ? 195. : 175.) * ((cols + 127) / 128);
   return (43. * ((cols + 7) / 8) - there) * z > 8.;
 }
@@ -645,8 +646,8 @@ size_t kv4_attention_ws_bytes(int, int n_q_heads, int n_kv_heads, int head_dim, 
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st) {
+  if (kv4_many_columns(a, dtype)) return launch_kv4_chunk(a, head_dim, dtype, st);
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
-  if (many_columns(a.n_seqs, a.c.n_kv_heads, cols, a.max_len, dtype)) return launch_kv4_chunk(a, head_dim, dtype, st);
   if (head_dim == 128) return cols <= 4 ? launch<128, 4>(a, dtype, st) : launch<128, 8>(a, dtype, st);
   return cols <= 4 ? launch<64, 4>(a, dtype, st) : launch<64, 8>(a, dtype, st);
 }

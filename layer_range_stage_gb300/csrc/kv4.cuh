@@ -87,6 +87,8 @@ constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(unsigned);
 constexpr int kKv4ChunkParts = 192;
 size_t kv4_chunk_ws_bytes(int head_dim);
 cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
+// Whether a call runs on the kernel for many columns.
+bool kv4_many_columns(const Kv4AttnArgs& a, int dtype);
 size_t kv4_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int max_len);
 
 }  // namespace lrs

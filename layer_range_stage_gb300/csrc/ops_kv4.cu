@@ -21,12 +21,22 @@ bool cache_sizes_ok(int64_t n_pages, int page_len, int n_kv_heads, int head_dim)
          n_kv_heads >= 1 && n_kv_heads <= 1024 && (head_dim == 64 || head_dim == 128);
 }
 
+bool known_dtype(int dtype) { return dtype == STAGE_F32 || dtype == STAGE_F16 || dtype == STAGE_BF16; }
+
+bool attention_sizes_ok(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int max_len) {
+  return n_seqs >= 0 && n_seqs <= 65535 && n_kv_heads >= 1 && n_q_heads >= 1 && n_q_heads <= 1024 && n_q_heads % n_kv_heads == 0 &&
+         (head_dim == 64 || head_dim == 128) && max_q >= 1 && max_q <= (1 << 20) && max_len >= 1 && max_len <= (1 << 30);
+}
+
+// A sequence has no more tokens than the call.
+int bounded_q(int max_q, int n_tok) { return max_q < n_tok ? max_q : n_tok; }
+
 int check_cache(const void* cache, int64_t n_pages, int page_len, int n_kv_heads, int head_dim, int dtype, int n_tok) {
   if (!cache_sizes_ok(n_pages, page_len, n_kv_heads, head_dim))
     return op_err(STAGE_E_INVALID,
                   "cache sizes: n_pages >= 1, page_len a multiple of 16 up to 4096, n_pages * page_len < 2^31, "
                   "1 to 1024 KV heads, head_dim 64 or 128");
-  if (dtype != STAGE_F32 && dtype != STAGE_F16 && dtype != STAGE_BF16) return op_err(STAGE_E_INVALID, "unknown dtype %d", dtype);
+  if (!known_dtype(dtype)) return op_err(STAGE_E_INVALID, "unknown dtype %d", dtype);
   if (n_tok < 0 || n_tok > (1 << 24)) return op_err(STAGE_E_INVALID, "n_tok outside [0, 2^24]");
   if (!cache) return op_err(STAGE_E_INVALID, "null cache");
   if (!aligned(cache, 16)) return op_err(STAGE_E_INVALID, "the cache must be 16-byte aligned");
@@ -157,11 +167,27 @@ int stage_op_kv4_read(const void* cache_dev, int64_t n_pages, int page_len, int 
   return op_host_failure("unknown exception");
 }
 
+int stage_op_kv4_attention_many(int n_seqs, int n_tok, int n_q_heads, int n_kv_heads, int head_dim, int dtype, int max_q,
+                                int max_len) try {
+  if (!attention_sizes_ok(n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_len) || n_kv_heads > 1024 || !known_dtype(dtype) ||
+      n_tok < 0 || n_tok > (1 << 24))
+    return op_err(STAGE_E_INVALID, "no attention of these sizes");
+  lrs::Kv4AttnArgs a;
+  a.c.n_kv_heads = n_kv_heads;
+  a.n_q_heads = n_q_heads;
+  a.n_seqs = n_seqs;
+  a.max_q = bounded_q(max_q, n_tok);
+  a.max_len = max_len;
+  return n_tok && n_seqs && lrs::kv4_many_columns(a, dtype);
+} catch (const std::exception& ex) {
+  return op_host_failure(ex.what());
+} catch (...) {
+  return op_host_failure("unknown exception");
+}
+
 size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int max_q,
                                               int max_len) {
-  if (n_seqs < 0 || n_seqs > 65535 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads > 1024 || n_q_heads % n_kv_heads ||
-      (head_dim != 64 && head_dim != 128) || max_q < 1 || max_q > (1 << 20) || max_len < 1 || max_len > (1 << 30))
-    return 0;
+  if (!attention_sizes_ok(n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_len)) return 0;
   return lrs::kv4_attention_ws_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_len);
 }
 
@@ -195,7 +221,7 @@ int stage_op_kv4_attention(const void* cache_dev, int64_t n_pages, int page_len,
   a.n_q_heads = n_q_heads;
   a.n_seqs = n_seqs;
   a.table_stride = table_stride;
-  a.max_q = max_q < n_tok ? max_q : n_tok;  // no sequence has more: a loose bound launches no empty work
+  a.max_q = bounded_q(max_q, n_tok);
   a.max_len = max_len;
   a.cu_q = cu_q_dev;
   a.seq_len = seq_len_dev;

@@ -278,3 +278,112 @@ def test_sums_over_millions_of_positions(B, dtype, d, empty):
     got = out.double().cpu().numpy()
     tol = 2.0 ** -12 + 2.0 ** -14 + 2.0 ** -18 + (2.0 ** -12 if dtype == "bf16" else 0) + torch.finfo(DT[dtype]).eps / 2
     assert (np.abs(got - want) <= tol * want).all(), (np.abs(got - want) / want).max()
+
+
+# ------------------------------------------------------------------------------------------- one after another, captured, together
+
+def on_tiles(B, n, n_tok, hq, hkv, d, dtype, max_q, max_len):
+    return B.stage_op_kv4_attention_many(n, n_tok, hq, hkv, d, DT[dtype], max_q, max_len)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_one_workspace_for_both_kernels_in_turn(B, dtype):
+    """Decode rows cut over the GPU, chunks in parts and chunks of many items one after another on one workspace: each leaves the
+    arrival counters zero, and each call's rows are right."""
+    rng = np.random.default_rng(131)
+    few = attention_case(rng, 2, 4, 128, 32, [(1, 3000)], dtype, extra=0)
+    parts = attention_case(rng, 2, 4, 128, 32, [(60, 2100)], dtype, extra=0)
+    items = attention_case(rng, 2, 4, 128, 32, [(60, 300 + i) for i in range(160)], dtype, extra=0)
+    size = max(B.stage_op_kv4_attention_workspace_bytes(160, 8, 2, 128, q, WIDE_BOUND) for q in (1, 60))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = {id(c): reference(c[0], c[4], c[2], c[3], c[1]) for c in (few, parts, items)}
+    for case in (few, parts, few, items, few, items, parts, few):
+        cache, table, cu, length, q = case
+        bound = 3000 if case is few else WIDE_BOUND
+        assert on_tiles(B, len(length), len(q), 8, 2, 128, dtype, int(np.diff(cu).max()), bound) == (case is not few)
+        out = run_attention(B, cache, table, cu, length, q, dtype, ws=ws, max_len=bound)
+        check(out, want[id(case)], dtype)
+        assert (ws[:2048] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_captured_chunks_with_their_own_workspaces_on_two_streams(B, dtype):
+    """Chunk calls in two graphs, one in parts with its join, replayed at the same time; then with other lengths and queries."""
+    rng = np.random.default_rng(137)
+    graphs = []
+    for rows in ([(60, 2000)], [(50, 300 + i) for i in range(90)]):
+        cache, table, cu, length, q = attention_case(rng, 2, 4, 128, 32, rows, dtype, extra=0)
+        n, most = len(rows), rows[0][0]
+        assert on_tiles(B, n, len(q), 8, 2, 128, dtype, most, WIDE_BOUND)
+        dev, qd, args = torch.from_numpy(cache).cuda(), torch.as_tensor(q).to(DT[dtype]).cuda(), (i32(cu), i32(length), i32(table))
+        out = torch.zeros_like(qd)
+        ws = torch.zeros(B.stage_op_kv4_attention_workspace_bytes(n, 8, 2, 128, most, WIDE_BOUND), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            B.stage_op_kv4_attention(dev, qd, *args, out, most, WIDE_BOUND, ws)
+        graphs.append((g, out, (cache, table, cu, length, q), (dev, qd, args, ws), torch.cuda.Stream()))
+    for shorter in (0, 7):
+        for g, out, (cache, table, cu, length, q), (dev, qd, args, ws), st in graphs:
+            args[1].copy_(i32(length - shorter))
+            qd.copy_(torch.as_tensor(np.roll(q, shorter, 0)))
+            out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, out, case, held, st in graphs:
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for g, out, (cache, table, cu, length, q), held, st in graphs:
+            check(out, reference(cache, np.roll(q, shorter, 0), cu, length - shorter, table), dtype)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("dtype,hkv,group,d,page", [("f32", 2, 4, 128, 32), ("f16", 2, 4, 64, 16), ("bf16", 1, 8, 64, 16)])
+def test_a_serving_loop_of_chunks(B, graph, dtype, hkv, group, d, page):
+    """plan, append and attention on the tiles for many columns: prompts enter in chunks beside tokens and rolled-back drafts, eagerly
+    and as one captured graph.  The expected output comes from lists of rows per request."""
+    n, stride, n_tok, max_q = 4, 12, 200, 90
+    s = Server(B, n, page, hkv, group, d, n * stride, stride, n_tok, dtype, max_q, 139)
+    s.max_len = WIDE_BOUND
+    s.ws = torch.zeros(B.stage_op_kv4_attention_workspace_bytes(n, hkv * group, hkv, d, max_q, s.max_len), dtype=torch.uint8, device="cuda")
+    assert on_tiles(B, n, n_tok, hkv * group, hkv, d, dtype, max_q, s.max_len)
+    s.launch()
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.launch()
+    rng = np.random.default_rng(149)
+    rows = [[] for _ in range(n)]
+    for step in range(10):
+        keep = np.array([len(r) for r in rows])
+        new = np.ones(n, int)
+        for i in range(n):
+            what = rng.random()
+            if what < 0.15:
+                keep[i], new[i] = 0, 0                                   # leaves
+            elif what < 0.6 or not rows[i]:
+                new[i] = rng.integers(20, 50)                            # a prompt's next chunk
+            elif what < 0.8:
+                keep[i], new[i] = max(0, keep[i] - 3), rng.integers(1, 6)
+            new[i] = min(new[i], stride * page - keep[i])
+        total = int(new.sum())
+        assert total <= n_tok
+        k, v, q = (as_given(rng.standard_normal((n_tok, h, d)), dtype) for h in (hkv, hkv, hkv * group))
+        s.k.copy_(torch.as_tensor(k)), s.v.copy_(torch.as_tensor(v)), s.q.copy_(torch.as_tensor(q))
+        s.keep.copy_(i32(keep)), s.new.copy_(i32(new))
+        s.out.fill_(5)
+        g.replay() if graph else s.launch()
+        torch.cuda.synchronize()
+        assert s.status.item() == 0
+        cu = np.concatenate([[0], np.cumsum(new)])
+        for i in range(n):
+            rows[i] = rows[i][:keep[i]] + [(k[t], v[t]) for t in range(cu[i], cu[i + 1])]
+        flat = kv4.cache_array(n * stride, page, hkv, d)
+        table = np.arange(n * stride, dtype=np.int32).reshape(n, stride)
+        for i in range(n):
+            if rows[i]:
+                kv4.append(flat, np.stack([r[0] for r in rows[i]]), np.stack([r[1] for r in rows[i]]), i * stride * page + np.arange(len(rows[i])))
+        check(s.out[:total], reference(flat, q[:total], cu, [len(r) for r in rows], table), dtype)
+        assert (s.out[total:] == 5).all()
