@@ -621,8 +621,8 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
       ask();
     }
   }
-  if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
-    for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
+  // Nothing may still be landing in shared memory when the CTA leaves, whoever has given up, be it after this
+  for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
 }
 
 template <int D, int NQ, int NKV, int NP, bool SPLIT>
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
           if (i + 2 < it.nt) ok = scores();
         }
       }
-      if (!ok && leader) {  // given up: the products already issued finish before TMEM is released
+      if (leader) {  // the products finish before TMEM is released, whoever has given up waiting for them
         umma_commit(&B.drain);
         mbar_wait(&B.drain, 0u, kDrainNs);
       }
@@ -1130,7 +1130,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
           if (ok && i + 2 < nt0) ok = scores(0, n + i + 2, i + 2 >= nt1, false);
         }
       }
-      if (!ok && leader) {  // given up: the products already issued finish before TMEM is released
+      if (leader) {  // the products finish before TMEM is released, whoever has given up waiting for them
         umma_commit(&B.drain);
         mbar_wait(&B.drain, 0u, kDrainNs);
       }
