@@ -111,6 +111,7 @@ STAGE_API int stage_op_kv4_read(const void* cache_dev, int64_t n_pages, int page
 STAGE_API size_t stage_op_kv4_attention_workspace_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
                                                         int max_q, int max_len);
 #define STAGE_KV4_SCRATCH_MAX (64u << 20)
+#define STAGE_KV4_ERROR_AT 2048
 
 /* Which kernel a call of stage_op_kv4_attention with these sizes runs on: 1, the one for many columns (query tokens of a
  * sequence times query heads per KV head; a chunk of a prompt), whose precision is stated below as that of chunks; 0, the one
@@ -145,7 +146,9 @@ STAGE_API int stage_op_kv4_attention_many(int n_seqs, int n_tok, int n_q_heads, 
  *     element of q 2^34 or more below its row's largest counts as 0 (and from 2^27 below on has fewer bits), and where a
  *     position's largest scale in K or V is 4096 or more, its values may be off by 2^-33 of its largest.  What a token
  *     does not see has no part in any of this.
- *     A chunk's row is NaN where the GPU did not finish a copy or a product within two seconds.
+ *     Where the GPU does not finish a copy or a product of a chunk within a second, the rows that miss it are NaN, and the
+ *     32-bit word STAGE_KV4_ERROR_AT bytes into the workspace is set to 1; no call clears it (it is read, and cleared, where
+ *     results are read: nothing here synchronises).
  *   workspace_dev: stage_op_kv4_attention_workspace_bytes(...) bytes whose contents must be zero
  *     before the first call (each call leaves it ready for the next, of any sizes it is large enough
  *     for); two calls that may run at the
@@ -161,6 +164,12 @@ STAGE_API int stage_op_kv4_attention(const void* cache_dev, int64_t n_pages, int
                                      const int32_t* table_dev, int table_stride, int n_seqs, int max_q, int max_len,
                                      void* out_dev, int64_t out_stride, void* workspace_dev, size_t workspace_bytes,
                                      void* stream);
+
+/* For tests: the next `calls` calls of stage_op_kv4_attention by this thread that run on the kernel for many columns copy
+ * nothing of the cache, so that the waits for it run out: every row is NaN, the error word is set, and the workspace is ready for
+ * the next call.  Nothing faults, traps or hangs.  calls = 0 takes it back.  Host only.  Errors: STAGE_E_INVALID (calls outside
+ * [0, 16]). */
+STAGE_API int stage_op_kv4_debug_stall(int calls);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,7 @@ STAGE_E_INJECTED = -9
 STAGE_E_HOST = -10
 STAGE_F32, STAGE_F16, STAGE_BF16 = 0, 1, 2
 STAGE_KV4_SCRATCH_MAX = 64 << 20
+STAGE_KV4_ERROR_AT = 2048
 STAGE_PLAN_OK, STAGE_PLAN_NO_PAGES, STAGE_PLAN_BAD_LEN, STAGE_PLAN_NO_ROOM = 0, 1, 2, 3
 ERROR_NAMES = {0: "STAGE_OK", -1: "STAGE_E_INVALID", -2: "STAGE_E_DOES_NOT_FIT", -3: "STAGE_E_HANDOFF",
                -4: "STAGE_E_POSITION", -5: "STAGE_E_BUSY", -6: "STAGE_E_NOT_LAST", -7: "STAGE_E_CUDA",
@@ -125,6 +126,7 @@ _SIGS = {
                                     C.c_void_p, C.c_int, C.c_int64, C.c_void_p]),
     "stage_op_kv4_attention_workspace_bytes": (C.c_size_t, [C.c_int] * 6),
     "stage_op_kv4_attention_many": (C.c_int, [C.c_int] * 8),
+    "stage_op_kv4_debug_stall": (C.c_int, [C.c_int]),
     "stage_op_kv4_attention": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_int64,
                                          C.c_int, C.c_int] + [C.c_void_p] * 3 + [C.c_int] * 4 +
                                [C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]),
@@ -663,10 +665,16 @@ def stage_op_kv4_attention_many(n_seqs: int, n_tok: int, n_q_heads: int, n_kv_he
     return bool(rc)
 
 
+def stage_op_kv4_debug_stall(calls: int) -> None:
+    """The next calls of this thread on the kernel for many columns run out of time (tests of that path)."""
+    _opcheck(lib().stage_op_kv4_debug_stall(calls))
+
+
 def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_len: int, workspace, stream=None) -> None:
     """q, out [n_tok, n_q_heads, head_dim] of one type; cu_q int32 [n_seqs + 1], seq_len int32 [n_seqs], table int32
     [n_seqs, stride]; max_q, max_len bound the query tokens and the length of a sequence; workspace: a tensor of
-    stage_op_kv4_attention_workspace_bytes(...) bytes, zero before its first use."""
+    stage_op_kv4_attention_workspace_bytes(...) bytes, zero before its first use; the 32-bit word STAGE_KV4_ERROR_AT bytes into
+    it is 1 once a call has given up waiting (its rows are NaN)."""
     if not (0 < max_q <= 1 << 20 and 0 < max_len <= 1 << 30):  # a C int would drop what lies above its bits
         _invalid("max_q must lie in [1, 2^20] and max_len in [1, 2^30]")
     ptr, n_pages, page_len, hkv, d = _kv4_cache(cache)

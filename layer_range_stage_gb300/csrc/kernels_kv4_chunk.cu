@@ -65,7 +65,7 @@ template <int NP>
 constexpr float kChunkTop = NP == 2 ? 11.f : 7.f;
 template <int NP>
 constexpr float kChunkSlack = 15.f - kChunkTop<NP>;
-constexpr uint64_t kWaitNs = 2000000000ull, kDrainNs = 200000000ull;
+constexpr uint64_t kWaitNs = 1000000000ull, kDrainNs = 200000000ull;
 constexpr int kRaw = 4;    // packed tiles in shared memory
 constexpr uint32_t kTmemCols = 512, kColQ = 0, kColS = 128, kColP = 256, kColO = 384;
 
@@ -80,6 +80,7 @@ struct ChunkArgs : Kv4AttnArgs {
   long long count;       // items
   int group, row_tiles;  // query heads per KV head; row tiles of a sequence at the call's bounds
   int parts;             // of a row tile's positions
+  int stall;             // copy no tile: the waits run out
 };
 
 struct ChunkItem {
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
     regs_down<kRegsRest>();
     if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) {
       // ---------------- copies ----------------
-      chunk_copy<D, L>(sm, M, items);
+      if (!a.stall) chunk_copy<D, L>(sm, M, items);
     }
     if (warp == kSoftWarps + kProdWarps) {
       // ---------------- products ----------------
@@ -1015,6 +1016,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (tid == 0 && M.abort) *kv4_error_word(a.ws) = 1;
 }
 
 // ---------------- two row tiles per item ----------------
@@ -1060,7 +1062,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
     chunk_expand<D, 1, 1, KS, L>(sm, M, items);
   } else if (warp >= kSoftWarps + kProdWarps) {
     regs_down<kRegsRest>();
-    if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) chunk_copy<D, L>(sm, M, items);
+    if (warp == kSoftWarps + kProdWarps + 1 && lane == 0 && !a.stall) chunk_copy<D, L>(sm, M, items);
     if (warp == kSoftWarps + kProdWarps) {
       // ---------------- products (as in the kernel with one row tile: one elected thread of a converged warp) ----------------
       const bool leader = elect_one();
@@ -1343,6 +1345,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (tid == 0 && M.abort) *kv4_error_word(a.ws) = 1;
 }
 
 // Joins the parts of a row, in their order: a warp per row.
@@ -1422,6 +1425,8 @@ cudaError_t launch_split(const ChunkArgs& a, int dtype, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+thread_local int g_stalls = 0;  // calls of this thread still to be stalled
+
 template <int D, int NQ, int NKV, int NP, bool PAIR>
 cudaError_t launch_chunk(const Kv4AttnArgs& args, int dtype, cudaStream_t st) {
   constexpr int ROWS = (PAIR ? 2 : 1) * kRowsTile;
@@ -1432,10 +1437,13 @@ cudaError_t launch_chunk(const Kv4AttnArgs& args, int dtype, cudaStream_t st) {
   const long long tiles = (long long)a.row_tiles * a.c.n_kv_heads * a.n_seqs;
   a.parts = chunk_parts(tiles, a.max_len, sm_count());
   a.count = tiles * a.parts;
+  a.stall = g_stalls > 0 ? g_stalls-- > 0 : 0;
   return a.parts > 1 ? launch_split<D, NQ, NKV, NP, PAIR, true>(a, dtype, st) : launch_split<D, NQ, NKV, NP, PAIR, false>(a, dtype, st);
 }
 
 }  // namespace
+
+void kv4_stall(int calls) { g_stalls = calls; }
 
 size_t kv4_chunk_ws_bytes(int head_dim) {
   return kKv4CounterBytes + (size_t)kKv4ChunkParts * 2 * kRowsTile * (head_dim + 2) * sizeof(float);

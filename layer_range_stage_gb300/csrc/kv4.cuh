@@ -80,12 +80,15 @@ struct Kv4AttnArgs {
   void* ws = nullptr;
 };
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
-// Workspace: arrival counters, zero between calls, which calls of many columns leave alone; then partial results.
+// Workspace: arrival counters, zero between calls, which calls of many columns leave alone; the error word, in a
+// line of its own; then partial results.
 constexpr int kKv4MaxCtas = 512;
-constexpr size_t kKv4CounterBytes = kKv4MaxCtas * sizeof(unsigned);
+constexpr size_t kKv4ErrorAt = kKv4MaxCtas * sizeof(unsigned), kKv4CounterBytes = kKv4ErrorAt + 128;
+__device__ __forceinline__ int* kv4_error_word(void* ws) { return reinterpret_cast<int*>((char*)ws + kKv4ErrorAt); }
 // Row tiles times parts that the workspace of a chunk call holds.
 constexpr int kKv4ChunkParts = 192;
 size_t kv4_chunk_ws_bytes(int head_dim);
+void kv4_stall(int calls);  // the thread's next calls of many columns copy nothing of the cache
 cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st);
 // Whether a call runs on the kernel for many columns.
 bool kv4_many_columns(const Kv4AttnArgs& a, int dtype);

@@ -12,6 +12,8 @@ using lrs::op_cuda;
 using lrs::op_err;
 using lrs::op_host_failure;
 
+static_assert(lrs::kKv4ErrorAt == STAGE_KV4_ERROR_AT, "stage_kv4.h says where the error word lies");
+
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -230,6 +232,16 @@ int stage_op_kv4_attention(const void* cache_dev, int64_t n_pages, int page_len,
   a.ws = workspace_dev;
   const cudaError_t e = lrs::launch_kv4_attention(a, head_dim, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? STAGE_OK : op_cuda(e, "kv4 attention");
+} catch (const std::exception& ex) {
+  return op_host_failure(ex.what());
+} catch (...) {
+  return op_host_failure("unknown exception");
+}
+
+int stage_op_kv4_debug_stall(int calls) try {
+  if (calls < 0 || calls > 16) return op_err(STAGE_E_INVALID, "calls outside [0, 16]");
+  lrs::kv4_stall(calls);
+  return STAGE_OK;
 } catch (const std::exception& ex) {
   return op_host_failure(ex.what());
 } catch (...) {

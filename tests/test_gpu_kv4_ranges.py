@@ -387,3 +387,39 @@ def test_a_serving_loop_of_chunks(B, graph, dtype, hkv, group, d, page):
                 kv4.append(flat, np.stack([r[0] for r in rows[i]]), np.stack([r[1] for r in rows[i]]), i * stride * page + np.arange(len(rows[i])))
         check(s.out[:total], reference(flat, q[:total], cu, [len(r) for r in rows], table), dtype)
         assert (s.out[total:] == 5).all()
+
+
+# ------------------------------------------------------------------------------------------- a wait that runs out
+
+@pytest.mark.parametrize("dtype,rows", [("f32", [(60, 2000)]), ("f32", [(60, 300 + i) for i in range(160)]), ("f16", [(60, 2000)]),
+                                        ("bf16", [(60, 2000)]), ("bf16", [(60, 300 + i) for i in range(160)])])
+def test_a_wait_that_runs_out_gives_nan_and_the_error_word(B, dtype, rows):
+    """The next call copies nothing of the cache: every wait for it runs out.  Its rows are NaN and the error word is set, the rows behind
+    the last sequence stay, and the call after it is right on the same workspace."""
+    rng = np.random.default_rng(151)
+    cache, table, cu, length, q = attention_case(rng, 2, 4, 128, 32, rows, dtype)
+    n = len(rows)
+    assert on_tiles(B, n, len(q), 8, 2, 128, dtype, 60, WIDE_BOUND)
+    ws = torch.zeros(B.stage_op_kv4_attention_workspace_bytes(n, 8, 2, 128, 60, WIDE_BOUND), dtype=torch.uint8, device="cuda")
+    word = ws[B.STAGE_KV4_ERROR_AT:B.STAGE_KV4_ERROR_AT + 4].view(torch.int32)
+    want = reference(cache, q, cu, length, table)
+    B.stage_op_kv4_debug_stall(1)
+    out = run_attention(B, cache, table, cu, length, q, dtype, ws=ws, max_len=WIDE_BOUND)
+    assert torch.isnan(out[:int(cu[-1])].float()).all() and word.item() == 1
+    for _ in range(2):
+        out = run_attention(B, cache, table, cu, length, q, dtype, ws=ws, max_len=WIDE_BOUND)
+        check(out, want, dtype)
+        assert word.item() == 1                    # no call clears it
+    word.zero_()
+    out = run_attention(B, cache, table, cu, length, q, dtype, ws=ws, max_len=WIDE_BOUND)
+    check(out, want, dtype)
+    assert word.item() == 0
+
+
+def test_stall_refuses_other_counts(B):
+    for calls in (-1, 17):
+        with pytest.raises(B.StageError) as e:
+            B.stage_op_kv4_debug_stall(calls)
+        assert e.value.code == B.STAGE_E_INVALID
+    B.stage_op_kv4_debug_stall(3)
+    B.stage_op_kv4_debug_stall(0)
