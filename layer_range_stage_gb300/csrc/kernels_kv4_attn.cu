@@ -635,6 +635,8 @@ constexpr int kFewColumns = 24;
 bool kv4_many_columns(const Kv4AttnArgs& a, int dtype) {
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
   if (cols <= kFewColumns) return false;
+  // Bounds so loose that looking through the row tiles alone would take a tenth of a second
+  if ((cols + 127) / 128 * a.c.n_kv_heads * a.n_seqs > kKv4ChunkItems) return false;
   const double z = 1e-6 * a.n_seqs * a.c.n_kv_heads * a.max_len;
   const double there = dtype == KV4_BF16 ? 155. * ((cols + 255) / 256) : (dtype == KV4_F32 ? 195. : 175.) * ((cols + 127) / 128);
   return (43. * ((cols + 7) / 8) - there) * z > 8.;

@@ -93,9 +93,14 @@ struct ChunkItem {
 // Items of ROWS rows: row tiles from the last (which sees most) down, then KV heads, then sequences, then the parts of
 // their positions, dealt to the CTAs forth and back: c, 2 G - 1 - c, 2 G + c, ... of G, so that nobody has the longest of
 // every round (4 x 512 rows, STAGE_F32: 64 us, 66 dealt forth alone).  Every warp goes through them for itself.
-// SPLIT: whether there are parts.  What a loop over tiles has to keep counts: the kernels live off their last registers.
-template <int ROWS, bool SPLIT>
+// kParts: there are parts.  kLoose: at the call's bounds most numbers are no items, because the bounds are loose or one sequence of
+// many has most of the tokens; then a warp looks for its next item 32 numbers at a time (1 sequence of 2000 tokens among 4096 of
+// one, STAGE_F32: 1.7 ms, 6.0 one by one; 1 of 512 among 64: 49 us, 62).  As kernels of their own: what a loop over tiles has to keep
+// counts, the kernels live off their last registers (2 x 1024 rows of STAGE_BF16: 346 us, 391 with this search, which they do not need).
+enum { kTight, kParts, kLoose };
+template <int ROWS, int MODE>
 struct ChunkItems {
+  static constexpr bool SPLIT = MODE == kParts;
   const ChunkArgs& a;
   ChunkItem it;
   int round = 0;
@@ -103,10 +108,8 @@ struct ChunkItems {
   // Takes number w apart; false if its sequence has no such rows.
   __device__ __forceinline__ bool at(long long w) {
     const int parts = SPLIT ? a.parts : 1;
-    const long long per = (long long)a.c.n_kv_heads * a.n_seqs * parts;
-    // counts rarely need 64 bits
-    const long long back = a.count >> 32 ? w / per : (long long)((uint32_t)w / (uint32_t)per);
-    const int row_tile = a.row_tiles - 1 - (int)back, rest = (int)(w - back * per), part = rest % parts, row = rest / parts;
+    const uint32_t per = (uint32_t)a.c.n_kv_heads * a.n_seqs * parts, back = (uint32_t)w / per;  // kKv4ChunkItems bounds them
+    const int row_tile = a.row_tiles - 1 - (int)back, rest = (int)((uint32_t)w - back * per), part = rest % parts, row = rest / parts;
     const int seq = row / a.c.n_kv_heads, row0 = row_tile * ROWS;
     int start;
     const int tokens = seq_tokens(a, seq, &start), ncols = min(tokens, a.max_q) * a.group;
@@ -125,14 +128,30 @@ struct ChunkItems {
     it.nt = (int)(nt * (part + 1) / parts) - it.t0;
     return true;
   }
-  // The CTA's next item; false behind the last.
+  __device__ __forceinline__ long long dealt(int r) const {
+    return (long long)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  }
+  // The CTA's next item; false behind the last.  kLoose: the whole warp.
   __device__ __forceinline__ bool next() {
     while (true) {
-      const long long w = (long long)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const long long w = dealt(round);
       if (w >= a.count) return false;
       ++round;
       if (at(w)) return true;
+      if constexpr (MODE == kLoose)
+        for (uint32_t found = 0; !found && dealt(round) < a.count;) {
+          const long long mine = dealt(round + (int)(threadIdx.x & 31));
+          found = __ballot_sync(0xffffffffu, mine < a.count && live((uint32_t)mine));
+          round += found ? __ffs(found) - 1 : 32;
+        }
     }
+  }
+  // Whether number w is an item (of a sequence that has such rows).
+  __device__ __forceinline__ bool live(uint32_t w) const {
+    const uint32_t per = (uint32_t)a.c.n_kv_heads * a.n_seqs, back = w / per;
+    int start;
+    const int tokens = seq_tokens(a, (int)((w - back * per) / (uint32_t)a.c.n_kv_heads), &start);
+    return (a.row_tiles - 1 - (int)back) * ROWS < min(tokens, a.max_q) * a.group;
   }
   // Positions that the item's sequence shows to row r.
   __device__ __forceinline__ int seen(int r) const { return max(0, it.len - it.tokens + r / a.group + 1); }
@@ -340,8 +359,8 @@ __device__ void chunk_init(ChunkMisc& M) {
 }
 
 // Expansion, by two groups of four warps: group g has the tiles n with n % 2 = g, in KS stages of operands.
-template <int D, int NKV, int NP, int KS, typename L, int ROWS, bool SPLIT>
-__device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, ChunkItems<ROWS, SPLIT>& items) {
+template <int D, int NKV, int NP, int KS, typename L, int ROWS, int MODE>
+__device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, ChunkItems<ROWS, MODE>& items) {
   constexpr int NB = D / 32, HALF = kv4_half(D), CODES = kv4_codes(D);
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
@@ -565,9 +584,9 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
   }
 }
 
-// Copies of the packed tiles, by one thread.
-template <int D, typename L, int ROWS, bool SPLIT>
-__device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, ChunkItems<ROWS, SPLIT>& items) {
+// Copies of the packed tiles, by one thread (kLoose: of a whole warp, which looks for the items).
+template <int D, typename L, int ROWS, int MODE>
+__device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, ChunkItems<ROWS, MODE>& items) {
   constexpr int TILE = kv4_tile_bytes(D), HALF = kv4_half(D), CODES = kv4_codes(D);
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
@@ -576,7 +595,8 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
   const int tpp = a.c.page_len / kKv4Tile;
   bool ok = true;
   int n = 0;
-  for (; ok && items.next();) {
+  for (; (MODE == kLoose ? __all_sync(0xffffffffu, ok) : ok) && items.next();) {
+    if (MODE == kLoose && (threadIdx.x & 31)) continue;
     const int n16 = (it.lim_hi + kKv4Tile - 1) / kKv4Tile;
     const int* trow = a.table + (long long)it.seq * a.table_stride;
     // the pages of a tile are asked for a tile ahead; places go on without a division
@@ -622,12 +642,13 @@ __device__ __forceinline__ void chunk_copy(unsigned char* sm, ChunkMisc& M, Chun
       ask();
     }
   }
-  // Nothing may still be landing in shared memory when the CTA leaves, whoever has given up, be it after this
+  // Nothing may still be landing in shared memory when the CTA leaves, whoever has given up, be it after this (n: the copying thread's)
   for (int i = max(0, n - kRaw); i < n; ++i) mbar_wait(&B.raw_full[i & (kRaw - 1)], (uint32_t)(i / kRaw) & 1u, kDrainNs);
 }
 
-template <int D, int NQ, int NKV, int NP, bool SPLIT>
+template <int D, int NQ, int NKV, int NP, int MODE>
 __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const ChunkArgs a) {
+  constexpr bool SPLIT = MODE == kParts;
   using L = ChunkLayout<D, NKV, 2, kSoftWarps * kTurn>;
   constexpr int HD = D / 2;  // dims of a softmax thread
   constexpr bool F32 = NP == 2;
@@ -638,7 +659,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  ChunkItems<kRowsTile, SPLIT> items(a);
+  ChunkItems<kRowsTile, MODE> items(a);
   const ChunkItem& it = items.it;
 
   if (tid == 0) chunk_init(M);
@@ -658,7 +679,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
     chunk_expand<D, NKV, NP, 2, L>(sm, M, items);
   } else if (warp >= kSoftWarps + kProdWarps) {
     regs_down<kRegsRest>();
-    if (warp == kSoftWarps + kProdWarps + 1 && lane == 0) {
+    if (warp == kSoftWarps + kProdWarps + 1 && (MODE == kLoose || lane == 0)) {
       // ---------------- copies ----------------
       if (!a.stall) chunk_copy<D, L>(sm, M, items);
     }
@@ -1028,8 +1049,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_chunk_kernel(const Chunk
 // barrier has long been passed, so K and V are waited for once per tile, not once per row tile (355 -> 343 us).
 constexpr uint32_t kColPairS = 0, kColPairO = 256;
 
-template <int D, bool SPLIT>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkArgs a) {
+  constexpr bool SPLIT = MODE == kParts;
   constexpr int KS = 3, q_tile = kRowsTile * D * 2;
   using L = ChunkLayout<D, 1, KS, 2 * q_tile>;
   extern __shared__ unsigned char chunk_raw[];
@@ -1038,7 +1060,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
   ChunkBars& B = M.bar;
   volatile int* abort_flag = &M.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  ChunkItems<2 * kRowsTile, SPLIT> items(a);
+  ChunkItems<2 * kRowsTile, MODE> items(a);
   const ChunkItem& it = items.it;
   // the item's tiles of positions that its row tile g sees
   auto tiles_of = [&](int g) {
@@ -1062,7 +1084,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) kv4_pair_kernel(const ChunkA
     chunk_expand<D, 1, 1, KS, L>(sm, M, items);
   } else if (warp >= kSoftWarps + kProdWarps) {
     regs_down<kRegsRest>();
-    if (warp == kSoftWarps + kProdWarps + 1 && lane == 0 && !a.stall) chunk_copy<D, L>(sm, M, items);
+    if (warp == kSoftWarps + kProdWarps + 1 && (MODE == kLoose || lane == 0) && !a.stall) chunk_copy<D, L>(sm, M, items);
     if (warp == kSoftWarps + kProdWarps) {
       // ---------------- products (as in the kernel with one row tile: one elected thread of a converged warp) ----------------
       const bool leader = elect_one();
@@ -1354,7 +1376,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const ChunkArgs a, int dt
   constexpr int rows = ROWS;
   constexpr int N = D / 32;  // dims of a lane
   const int parts = a.parts;
-  ChunkItems<ROWS, true> items(a);
+  ChunkItems<ROWS, kParts> items(a);
   const ChunkItem& it = items.it;
   const long long first = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // row, counted over all row tiles
   const int lane = threadIdx.x & 31, row = (int)(first % rows);
@@ -1411,16 +1433,16 @@ cudaError_t launch_items(Kernel* kern, int smem, const ChunkArgs& a, std::atomic
 }
 
 // The kernel for one row tile per item, or (PAIR) for two.
-template <int D, int NQ, int NKV, int NP, bool PAIR, bool SPLIT>
-cudaError_t launch_split(const ChunkArgs& a, int dtype, cudaStream_t st) {
+template <int D, int NQ, int NKV, int NP, bool PAIR, int MODE>
+cudaError_t launch_mode(const ChunkArgs& a, int dtype, cudaStream_t st) {
   constexpr int ROWS = (PAIR ? 2 : 1) * kRowsTile;
   constexpr int smem = PAIR ? ChunkLayout<D, 1, 3, 2 * kRowsTile * D * 2>::bytes : ChunkLayout<D, NKV, 2, kSoftWarps * kTurn>::bytes;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<uint64_t> ready{0};
   cudaError_t e;
-  if constexpr (PAIR) e = launch_items(kv4_pair_kernel<D, SPLIT>, smem, a, ready, st);
-  else e = launch_items(kv4_chunk_kernel<D, NQ, NKV, NP, SPLIT>, smem, a, ready, st);
-  if (!SPLIT || e != cudaSuccess) return e;
+  if constexpr (PAIR) e = launch_items(kv4_pair_kernel<D, MODE>, smem, a, ready, st);
+  else e = launch_items(kv4_chunk_kernel<D, NQ, NKV, NP, MODE>, smem, a, ready, st);
+  if (MODE != kParts || e != cudaSuccess) return e;
   kv4_join_kernel<D, ROWS><<<(unsigned)((a.count / a.parts * ROWS + 7) / 8), 256, 0, st>>>(a, dtype);
   return cudaGetLastError();
 }
@@ -1438,7 +1460,10 @@ cudaError_t launch_chunk(const Kv4AttnArgs& args, int dtype, cudaStream_t st) {
   a.parts = chunk_parts(tiles, a.max_len, sm_count());
   a.count = tiles * a.parts;
   a.stall = g_stalls > 0 ? g_stalls-- > 0 : 0;
-  return a.parts > 1 ? launch_split<D, NQ, NKV, NP, PAIR, true>(a, dtype, st) : launch_split<D, NQ, NKV, NP, PAIR, false>(a, dtype, st);
+  if (a.parts > 1) return launch_mode<D, NQ, NKV, NP, PAIR, kParts>(a, dtype, st);
+  // no more items than this, however the tokens are spread over the sequences
+  const long long items = ((long long)a.n_tok * a.group / ROWS + a.n_seqs) * a.c.n_kv_heads;
+  return tiles > 2 * items ? launch_mode<D, NQ, NKV, NP, PAIR, kLoose>(a, dtype, st) : launch_mode<D, NQ, NKV, NP, PAIR, kTight>(a, dtype, st);
 }
 
 }  // namespace

@@ -423,3 +423,35 @@ def test_stall_refuses_other_counts(B):
         assert e.value.code == B.STAGE_E_INVALID
     B.stage_op_kv4_debug_stall(3)
     B.stage_op_kv4_debug_stall(0)
+
+
+# ------------------------------------------------------------------------------------------- one prompt among many tokens
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d,bound", [(128, None), (64, None), (128, 1 << 20)])
+def test_one_prompt_among_many_decoding_sequences(B, dtype, d, bound):
+    """One bound for a prompt's chunk and single tokens: of the row tiles that it allows for, few are there.  `bound`: far above even the
+    chunk's tokens.  NaN in V in one of the sequences, another without positions for its token."""
+    rng = np.random.default_rng(157)
+    rows = [(1, int(n)) for n in rng.integers(1, 150, 300)]
+    rows[171], rows[40], rows[41], rows[299] = (260, 500), (1, 0), (0, 30), (9, 80)
+    cache, table, cu, length, q = attention_case(rng, 2, 4, d, 16, rows, dtype)
+    assert on_tiles(B, len(rows), len(q), 8, 2, d, dtype, bound or 260, WIDE_BOUND)
+    want = reference(cache, q, cu, length, table)
+    put_scale(cache, table, 171, 300, 1, 0, True, 0x7FFF)
+    out = run_attention(B, cache, table, cu, length, q, dtype, max_q=bound, max_len=WIDE_BOUND).double().cpu().numpy()
+    hit = np.zeros(q.shape, bool)
+    hit[int(cu[171]) + 60:int(cu[172]), 4:, :32] = True
+    assert np.isnan(out[hit]).all()
+    check(out, want, dtype, ~np.isnan(want[0]) & ~hit)
+
+
+def test_thousands_of_sequences(B):
+    """3000 sequences of a token and one prompt: 375 thousand places for items of which 6 thousand are there."""
+    rng = np.random.default_rng(163)
+    rows = [(1, 1 + i % 20) for i in range(3000)]
+    rows[2000] = (1000, 1000)
+    cache, table, cu, length, q = attention_case(rng, 1, 8, 64, 16, rows, "bf16")
+    assert on_tiles(B, len(rows), len(q), 8, 1, 64, "bf16", 1000, WIDE_BOUND)
+    out = run_attention(B, cache, table, cu, length, q, "bf16", max_len=WIDE_BOUND)
+    check(out, reference(cache, q, cu, length, table), "bf16")

@@ -47,3 +47,10 @@ def test_sizes_that_a_c_int_would_cut_off_give_no_bytes():
     assert L.stage_op_kv4_attention_workspace_bytes(4, 8, 2, 64, 3, (1 << 32) + 100) == 0
     assert L.stage_op_kv4_attention_workspace_bytes(4, 8, 2, 64, (1 << 32) + 3, 100) == 0
     assert L.stage_op_kv4_cache_bytes(4, (1 << 32) + 16, 2, 64) == 0 and L.stage_op_kv4_cache_bytes((1 << 64) + 4, 16, 2, 64) == 0
+
+
+def test_bounds_too_loose_to_look_through_run_on_the_kernel_for_few():
+    """2^30 row tiles at the bounds: their places alone would take a tenth of a second to look through."""
+    assert many(65535, 1 << 17, 64, 8, 1 << 14, 1 << 16)              # 2^14 * 8 / 128 row tiles * 8 heads * 65535
+    assert not many(65535, 1 << 20, 64, 8, 1 << 20, 1 << 16)
+    assert not many(65535, 1 << 24, 1024, 8, 1 << 20, 1 << 20, torch.bfloat16)
