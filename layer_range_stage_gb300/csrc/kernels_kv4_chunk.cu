@@ -1423,6 +1423,12 @@ cudaError_t launch_items(Kernel* kern, int smem, const ChunkArgs& a, std::atomic
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {  // once per device
+    // The warpgroups share out kRegsStart registers a thread: from a compiler that gave the kernel fewer, the one that asks for more
+    // would wait forever
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < kRegsStart) return cudaErrorLaunchOutOfResources;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
