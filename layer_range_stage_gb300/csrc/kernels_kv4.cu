@@ -25,7 +25,7 @@ namespace lrs {
 // in and out may be the same arrays; nothing is kept between calls.
 
 constexpr int kPlanThreads = 1024, kPlanFew = 256;  // threads of a CTA, and of a lone one
-constexpr int kPlanCluster = 16;
+constexpr int kPlanCluster = 16, kPlanPortable = 8;  // CTAs; the smaller one where the GPU (or the part of it that is there) has no room
 constexpr int kPlanBatch = 4096;  // requests whose sums lie in shared memory at a time
 
 struct PlanReq {
@@ -252,31 +252,45 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const Kv4PlanArg
 }
 
 cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, cudaStream_t st) {
-  static std::atomic<uint64_t> ready{0};  // one bit per device
+  static std::atomic<uint64_t> ready{0}, small{0};  // one bit per device; small: a cluster of kPlanCluster never gets its CTAs
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+  const bool first = dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1);
+  if (first) {
     e = cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(PlanSmem));
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  // one CTA where it has a few steps at most: a cluster's launch and barrier cost more than they save (64 requests with a token
-  // each: 4.1 us, 5.5 in a cluster; 512 tokens: 4.6 and 5.5; 256 with 2048 tokens: 9.3 and 6.0; 1024 with 49 thousand: 58 and 7)
-  const int ncta = a.n_seqs > 2 * kPlanFew || a.n_tok > 3 * kPlanFew ? kPlanCluster : 1;
-  cfg.gridDim = dim3(ncta);
-  cfg.blockDim = dim3(ncta > 1 ? kPlanThreads : kPlanFew);
   cfg.dynamicSmemBytes = sizeof(PlanSmem);
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ncta;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  bool fits = !(small.load(std::memory_order_relaxed) >> (dev & 63) & 1);
+  if (first) {
+    int clusters = 0;
+    cfg.gridDim = dim3(kPlanCluster);
+    cfg.blockDim = dim3(kPlanThreads);
+    attr[0].val.clusterDim.x = kPlanCluster;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kv4_plan_kernel, &cfg);
+    if (e != cudaSuccess) cudaGetLastError();
+    fits = e == cudaSuccess && clusters > 0;
+    if (dev < 64) {
+      if (!fits) small.fetch_or(1ull << dev, std::memory_order_relaxed);
+      ready.fetch_or(1ull << dev, std::memory_order_release);
+    }
+  }
+  // one CTA where it has a few steps at most: a cluster's launch and barrier cost more than they save (64 requests with a token
+  // each: 4.1 us, 5.5 in a cluster; 512 tokens: 4.6 and 5.5; 256 with 2048 tokens: 9.3 and 6.0; 1024 with 49 thousand: 58 and 7)
+  const int ncta = a.n_seqs > 2 * kPlanFew || a.n_tok > 3 * kPlanFew ? (fits ? kPlanCluster : kPlanPortable) : 1;
+  cfg.gridDim = dim3(ncta);
+  cfg.blockDim = dim3(ncta > 1 ? kPlanThreads : kPlanFew);
+  attr[0].val.clusterDim.x = ncta;
   return cudaLaunchKernelEx(&cfg, kv4_plan_kernel, a, Quotient(a.page_len));
 }
 
