@@ -455,3 +455,55 @@ def test_thousands_of_sequences(B):
     assert on_tiles(B, len(rows), len(q), 8, 1, 64, "bf16", 1000, WIDE_BOUND)
     out = run_attention(B, cache, table, cu, length, q, "bf16", max_len=WIDE_BOUND)
     check(out, reference(cache, q, cu, length, table), "bf16")
+
+
+# ------------------------------------------------------------------------------------------- bounds, and rows by the thousand
+
+@pytest.mark.parametrize("empty", [0, 160])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_chunks_beyond_the_stated_bounds(B, dtype, empty):
+    """On the tiles for many columns too, tokens behind max_q get no output and keep their positions, seq_len counts as at most the
+    table's positions, and one below zero as none."""
+    rng = np.random.default_rng(167)
+    cache, table, cu, length, q = attention_case(rng, 2, 4, 64, 16, [(70, 150), (40, 300), (33, 40)], dtype)
+    out = tiled(B, cache, table, cu, length, q, dtype, empty=empty, max_q=45)
+    ref = reference(cache, q, cu, length, table)
+    done = np.zeros(q.shape, bool)
+    for i in range(3):
+        done[cu[i]:min(cu[i] + 45, cu[i + 1])] = True
+    check(out, ref, dtype, done)
+    assert (out[45:70] == 3).all()
+    short = table[:, :5].copy()
+    out = tiled(B, cache, short, cu, np.array([10 ** 9, 2 ** 31 - 1, -7], np.int32), q, dtype, empty=empty)
+    ref = reference(cache, q, cu, [80, 80, 0], short)
+    check(out, ref, dtype)
+    assert (out[int(cu[2]):int(cu[3])] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d,hkv", [(128, 8), (128, 3), (128, 1), (64, 8), (64, 5), (64, 1)])
+def test_thousands_of_rows_are_written_and_read_as_few_are(B, dtype, d, hkv):
+    """From 4096 rows on a warp goes through all heads of its row, below through some: the same bytes, and the same values back.  The calls
+    of few rows are those that tests/test_gpu_kv4.py holds against the oracle."""
+    g = torch.Generator(device="cuda").manual_seed(d + hkv)
+    n, page = 4099, 32
+    pages = n // page + 20
+    slot = torch.randperm(pages * page, device="cuda", generator=g)[:n].to(torch.int32)
+    slot[::17] = -1
+    slot[5] = pages * page
+    power = torch.randint(-30, 18, (n, hkv, 1), device="cuda", generator=g)
+    k, v = ((torch.randn(n, hkv, d, device="cuda", generator=g) * 2.0 ** power).to(DT[dtype]) for _ in range(2))
+    k[7, 0, 3], v[9, -1, 40] = float("inf"), float("nan")
+    start = torch.randint(0, 256, B.stage_op_kv4_cache_shape(pages, page, hkv, d), device="cuda", generator=g).to(torch.uint8)
+    one, some = start.clone(), start.clone()
+    B.stage_op_kv4_append(one, k, v, slot)
+    for a in range(0, n, 1000):
+        B.stage_op_kv4_append(some, k[a:a + 1000], v[a:a + 1000], slot[a:a + 1000])
+    assert torch.equal(one, some) and not torch.equal(one, start)
+    got = [torch.full((n, hkv, d), 7.0, dtype=DT[dtype], device="cuda") for _ in range(4)]
+    B.stage_op_kv4_read(one, slot, got[0], got[1])
+    for a in range(0, n, 1000):
+        B.stage_op_kv4_read(one, slot[a:a + 1000], got[2][a:a + 1000], got[3][a:a + 1000])
+    for x, y in ((got[0], got[2]), (got[1], got[3])):
+        same(x.double().cpu().numpy(), y.double().cpu().numpy())
+    assert (got[0][::17] == 7).all()
