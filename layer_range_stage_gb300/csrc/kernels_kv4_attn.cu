@@ -15,10 +15,10 @@
 // a row costs by itself (its q, the merge of the warps, its output).  A row cut by piece borders is merged by the last
 // of its CTAs to arrive, in the order of the positions.
 //
-// What bounds it: instructions, not bytes.  A tile of 16 positions is 2304 bytes and 490 instructions of a warp (unpacking
+// What bounds it: instructions, not bytes.  A tile of 16 positions is 2304 bytes and 496 instructions of a warp (unpacking
 // 4096 codes alone takes 130), which the four schedulers of an SM issue at about three quarters of their rate.  One token on
-// 131001 positions (32/8 heads of 128): 56 us for 151 MB, 2.7 TB/s; 64 ragged sequences of 128 .. 4096: 65 us for 166 MB; up
-// to 5 drafts of 16 sequences: 26 us, where every eight columns read the cache again.  Two tiles a round, for more
+// 131001 positions (32/8 heads of 128): 56 us for 151 MB, 2.7 TB/s; 64 ragged sequences of 128 .. 4096: 66 us for 166 MB; up
+// to 5 drafts of 16 sequences: 27 us, where every eight columns read the cache again.  Two tiles a round, for more
 // independent work, spilled and took 58, 68 and 30 us.
 
 #include <atomic>
@@ -625,21 +625,24 @@ cudaError_t launch(const Kv4AttnArgs& a, int dtype, cudaStream_t st) {
 }  // namespace
 
 // Few columns (query tokens of a sequence times heads of a group) run on the kernel above, which reads the cache again for
-// every eight of them; many on the tiles of kernels_kv4_chunk.cu.  Measured (4 heads per group, head_dim 128, us), with
-// z = n_seqs * n_kv_heads * max_len in millions: here 12 + 43 z per eight columns; there 20 + 195 z per 128 rows (float32),
-// 17 + 155 z per 256 (bfloat16; float16, 128 rows with two products each, lies between).  E.g. 16 sequences of 4096 with 8 KV
-// heads: 64 columns 183 here and 120 (float32) or 78 (bfloat16) there, 32 columns 97 and 119 or 78, 24 columns 77 and 78;
-// 4 of 512: 64 columns 19 and 23, 256 columns 44 and 27.
+// every eight of them; many on the tiles of kernels_kv4_chunk.cu.  Measured (us), with z = n_seqs * n_kv_heads * max_len in
+// millions: here 12 + `few` z per eight columns; there about 20 + `many` z per 128 rows, STAGE_BF16 per 256.  16 sequences of 4096 with
+// 8 KV heads (z = 0.52), head_dim 128, float32, float16, bfloat16: 32 columns 99 here and 111, 82, 76 there, 64 columns 185
+// and the same; head_dim 64: 32 columns 64 and 93, 78, 70, 64 columns 117 and the same.  4 of 512 (z = 0.016), head_dim 128: 64
+// columns 20 and 23, 21, 21, 256 columns 43 and 23, 21, 27.
 constexpr int kFewColumns = 24;
 
-bool kv4_many_columns(const Kv4AttnArgs& a, int dtype) {
+bool kv4_many_columns(const Kv4AttnArgs& a, int head_dim, int dtype) {
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
   if (cols <= kFewColumns) return false;
   // Bounds so loose that looking through the row tiles alone would take a tenth of a second
   if ((cols + 127) / 128 * a.c.n_kv_heads * a.n_seqs > kKv4ChunkItems) return false;
   const double z = 1e-6 * a.n_seqs * a.c.n_kv_heads * a.max_len;
-  const double there = dtype == KV4_BF16 ? 155. * ((cols + 255) / 256) : (dtype == KV4_F32 ? 195. : 175.) * ((cols + 127) / 128);
-  return (43. * ((cols + 7) / 8) - there) * z > 8.;
+  const bool wide = head_dim == 128;
+  const double few = wide ? 43. : 25.;
+  const double many = dtype == KV4_F32 ? (wide ? 175. : 139.) : dtype == KV4_F16 ? (wide ? 118. : 111.) : (wide ? 155. : 126.);
+  const int rows = dtype == KV4_BF16 ? 256 : 128;
+  return (few * ((cols + 7) / 8) - many * ((cols + rows - 1) / rows)) * z > 8.;
 }
 
 size_t kv4_attention_ws_bytes(int, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int) {
@@ -648,7 +651,7 @@ size_t kv4_attention_ws_bytes(int, int n_q_heads, int n_kv_heads, int head_dim, 
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, int head_dim, int dtype, cudaStream_t st) {
-  if (kv4_many_columns(a, dtype)) return launch_kv4_chunk(a, head_dim, dtype, st);
+  if (kv4_many_columns(a, head_dim, dtype)) return launch_kv4_chunk(a, head_dim, dtype, st);
   const long long cols = (long long)a.max_q * (a.n_q_heads / a.c.n_kv_heads);
   if (head_dim == 128) return cols <= 4 ? launch<128, 4>(a, dtype, st) : launch<128, 8>(a, dtype, st);
   return cols <= 4 ? launch<64, 4>(a, dtype, st) : launch<64, 8>(a, dtype, st);

@@ -13,8 +13,8 @@
 //               memory would be read again by every product);
 //   warp 17     copies the packed tiles in (bulk copies, up to four tiles ahead).
 // What bounds it: the latency of a tile's chain (scores, softmax, probabilities, outputs) and of an item's ends (its q, its
-// results); the tensor cores are busy for 23 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 58 us) and 34 % (2 x 1024
-// rows on 8192 positions, STAGE_BF16, the second kernel below: 348 us, 669 TFLOP/s), the schedulers for 40 and 48 %.
+// results); the tensor cores are busy for 25 % of the time (4 x 512 rows of 32/8 heads, STAGE_F32: 57 us) and 34 % (2 x 1024
+// rows on 8192 positions, STAGE_BF16, the second kernel below: 342 us, 682 TFLOP/s), the schedulers for 41 and 48 %.
 // The tensor cores' additions truncate: over a long sum the result shrinks (by 6e-7 of itself per tile of 64 positions, 15 %
 // over 16 million).  So in STAGE_F32 every tile's O is added to float32 registers, rounded to nearest, and the products with
 // low parts come first, where the sums they truncate are still small: 2e-6 of error became 5e-7.  The 16-bit types keep
@@ -52,8 +52,8 @@ namespace {
 constexpr int kRowsTile = 128, kPosTile = 64, kSub = kPosTile / kKv4Tile;
 constexpr int kSoftWarps = 8, kProdWarps = 8, kProd = 16 * kProdWarps;  // kProd: threads of a group of four warps
 constexpr int kChunkThreads = 32 * (kSoftWarps + kProdWarps + 4);  // five warpgroups
-// Registers per thread: the block starts with kRegsStart and its warpgroups trade them (4 x 512 rows, STAGE_F32: 58.2 us with
-// these, 58.8 with 152, 64, 48, 59.8 with 136, 80, 48; 2 x 1024 rows, STAGE_BF16: 352, 360, 350, at the time).
+// Registers per thread: the block starts with kRegsStart and its warpgroups trade them (4 x 512 rows, STAGE_F32: 57.6 us with
+// these, 57.4 with 152, 64, 48, 59.4 with 136, 80, 48; 2 x 1024 rows, STAGE_BF16: 342, 348, 350).
 constexpr int kRegsStart = 96, kRegsSoft = 144, kRegsProd = 72, kRegsRest = 48;
 static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsRest) <= kChunkThreads * kRegsStart, "the trade adds up");
 static_assert(kChunkThreads * kRegsStart <= 65536 && kSoftWarps % 4 == 0 && kProdWarps % 4 == 0, "whole warpgroups");

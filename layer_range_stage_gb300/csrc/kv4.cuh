@@ -93,7 +93,7 @@ cudaError_t launch_kv4_chunk(const Kv4AttnArgs& a, int head_dim, int dtype, cuda
 // Row tiles at a call's bounds times KV heads times sequences, at most, for the kernel for many columns, whose CTAs look through them.
 constexpr long long kKv4ChunkItems = 1ll << 30;
 // Whether a call runs on the kernel for many columns.
-bool kv4_many_columns(const Kv4AttnArgs& a, int dtype);
+bool kv4_many_columns(const Kv4AttnArgs& a, int head_dim, int dtype);
 size_t kv4_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim, int max_q, int max_len);
 
 }  // namespace lrs

@@ -180,7 +180,7 @@ int stage_op_kv4_attention_many(int n_seqs, int n_tok, int n_q_heads, int n_kv_h
   a.n_seqs = n_seqs;
   a.max_q = bounded_q(max_q, n_tok);
   a.max_len = max_len;
-  return n_tok && n_seqs && lrs::kv4_many_columns(a, dtype);
+  return n_tok && n_seqs && lrs::kv4_many_columns(a, head_dim, dtype);
 } catch (const std::exception& ex) {
   return op_host_failure(ex.what());
 } catch (...) {
