@@ -77,7 +77,7 @@ struct ChunkBars {
 
 // What a call has, the same for all its items: read from the kernel's parameters, so that it takes no registers.
 struct ChunkArgs : Kv4AttnArgs {
-  long long count;       // items
+  long long count;       // numbers of items, at most kKv4ChunkItems; those of sequences without such rows are none
   int group, row_tiles;  // query heads per KV head; row tiles of a sequence at the call's bounds
   int parts;             // of a row tile's positions
   int stall;             // copy no tile: the waits run out
@@ -448,6 +448,7 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
         w[b] = as_u32(__hmul2(__hmul2(as_h2(w[b]), up), up));
       }
       put(v_scale);
+
       load(base + CODES);
       k_big = __reduce_max_sync(0xffffffffu, max(largest(0), largest(1))) >= kBigScale;
       if (k_big) {
@@ -462,7 +463,6 @@ __device__ __forceinline__ void chunk_expand(unsigned char* sm, ChunkMisc& M, Ch
         }
       }
       put(k_scale);
-
     }
     __syncwarp();  // the prepared scales
     // K: 64 positions x 4 x (the word of eight dims of every block)
