@@ -39,9 +39,6 @@
 extern "C" {
 #endif
 
-/* Types of the rows that append, read and attention take and give. */
-enum { STAGE_F32 = 0, STAGE_F16 = 1, STAGE_BF16 = 2 };
-
 /* What stage_op_kv4_plan writes to its status word. */
 enum {
   STAGE_PLAN_OK = 0,

@@ -17,6 +17,9 @@
 extern "C" {
 #endif
 
+/* Types of the rows that an op takes and gives, where it has a choice. */
+enum { STAGE_F32 = 0, STAGE_F16 = 1, STAGE_BF16 = 2 };
+
 /* Device bytes of a packed [rows x cols] int8 block-32 matrix: the weight bytes (biased,
  * rows padded to a multiple of 256 weights) and the fp16 scale bytes.  STAGE_E_INVALID for
  * rows < 1, cols outside [1, 2^30] or null pointers. */

@@ -27,6 +27,8 @@ STAGE_E_STATE = -8
 STAGE_E_INJECTED = -9
 STAGE_E_HOST = -10
 STAGE_F32, STAGE_F16, STAGE_BF16 = 0, 1, 2
+STAGE_ROPE_PLAIN, STAGE_ROPE_LINEAR, STAGE_ROPE_BASE, STAGE_ROPE_BANDS, STAGE_ROPE_PARTS = 0, 1, 2, 3, 4
+STAGE_LOGPROBS_MAX_TOP = 32
 STAGE_KV4_SCRATCH_MAX = 64 << 20
 STAGE_KV4_ERROR_AT = 2048
 STAGE_PLAN_OK, STAGE_PLAN_NO_PAGES, STAGE_PLAN_BAD_LEN, STAGE_PLAN_NO_ROOM = 0, 1, 2, 3
@@ -130,6 +132,19 @@ _SIGS = {
     "stage_op_kv4_attention": (C.c_int, [C.c_void_p, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_int64,
                                          C.c_int, C.c_int] + [C.c_void_p] * 3 + [C.c_int] * 4 +
                                [C.c_void_p, C.c_int64, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "stage_op_norm_f8": (C.c_int, [C.c_void_p, C.c_int, C.c_int64] * 2 + [C.c_void_p, C.c_int64, C.c_void_p, C.c_float,
+                                                                         C.c_int, C.c_int] +
+                         [C.c_void_p, C.c_int64] * 3 + [C.c_void_p]),
+    "stage_op_f8_gemm": (C.c_int, [C.c_void_p, C.c_int64] * 3 + [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int,
+                                                                 C.c_int64, C.c_void_p, C.c_void_p]),
+    "stage_op_f8_debug_stall": (C.c_int, [C.c_int]),
+    "stage_op_rope_freqs": (C.c_int, [C.c_int, C.c_double, C.c_int] + [C.c_double] * 4 + [C.POINTER(C.c_double),
+                                                                                        C.POINTER(C.c_float)]),
+    "stage_op_rope": (C.c_int, [C.c_void_p, C.c_int64, C.c_int] * 2 + [C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
+                                                                      C.c_int, C.c_int, C.c_float] +
+                      [C.c_void_p, C.c_int64] * 2 + [C.c_void_p]),
+    "stage_op_logprobs": (C.c_int, [C.c_void_p, C.c_int, C.c_int64, C.c_int, C.c_int] + [C.c_void_p] * 4 +
+                          [C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]),
 }
 
 
@@ -694,5 +709,181 @@ def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_
         ptr, n_pages, page_len, hkv, d, qp, qt, qs, n_tok, hq, _i32dev(cu_q, "cu_q", n + 1),
         _i32dev(seq_len, "seq_len", n), _i32dev(table, "table", n * stride), stride, n, max_q, max_len, op, os_,
         workspace.data_ptr(), workspace.nbytes, stream)
+    if rc:
+        _opcheck(rc)
+
+
+# ----------------------------------------------------------------------------- a step's operators around the projections
+# include/stage_step.h.  8-bit rows are torch.float8_e4m3fn tensors (or uint8 codes); like the 4-bit cache's entry points
+# these check types, shapes and devices.
+
+def _f8(t, what: str):
+    """(pointer, rows, columns, row stride) of 8-bit rows, which may lie apart."""
+    if t.dtype is not _torch.float8_e4m3fn and t.dtype is not _torch.uint8:
+        _invalid(f"{what} must be float8_e4m3fn (or uint8 codes)")
+    if t.dim() != 2:
+        _invalid(f"{what} must be a matrix")
+    n, k = t.shape
+    s0, s1 = t.stride()
+    if k > 1 and s1 != 1:
+        _invalid(f"the columns of {what} must lie side by side")
+    return t.data_ptr(), n, k, s0 if n > 1 else -(-k // 16) * 16
+
+
+def _matrix(t, n: int, k: int, what: str):
+    """(pointer, dtype, row stride) of rows [n, k] of a float type, which may lie apart."""
+    dt = _KV4_DTYPE.get(t.dtype)
+    if dt is None:
+        _invalid(f"{what} must be float32, float16 or bfloat16")
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != k:
+        _invalid(f"{what} must be [{n}, {k}]")
+    s0, s1 = t.stride()
+    if k > 1 and s1 != 1:
+        _invalid(f"the columns of {what} must lie side by side")
+    return t.data_ptr(), dt, s0 if n > 1 else k
+
+
+def _scales(t, blocks: int, n: int, what: str):
+    """(pointer, stride) of float32 scales [blocks, n]."""
+    if t.dtype is not _torch.float32 or t.dim() != 2 or t.shape[0] != blocks or t.shape[1] != n:
+        _invalid(f"{what} must be float32 [{blocks}, {n}]")
+    s0, s1 = t.stride()
+    if n > 1 and s1 != 1:
+        _invalid(f"the columns of {what} must lie side by side")
+    return t.data_ptr(), s0 if blocks > 1 else n
+
+
+def stage_op_norm_f8(x, q=None, scale=None, gamma=None, eps: float = 1e-5, resid=None, resid_out=None, y=None, stream=None) -> None:
+    """Rows x [n_tok, n] plus resid (if given; the sum goes to resid_out, which may be resid), RMS norm with gamma (float32 [n]; None:
+    no norm), as 8-bit rows q [n_tok, n] with scales [ceil(n / 128), n_tok] and/or as rows y of x's type."""
+    _torch or _load_torch()
+    if x.dim() != 2:
+        _invalid("x must be [n_tok, n]")
+    if (resid is None) != (resid_out is None) or (q is None) != (scale is None):
+        _invalid("resid and resid_out go together, and so do q and scale")
+    stream = _kv4_launch(stream, x, *[t for t in (q, scale, gamma, resid, resid_out, y) if t is not None])
+    n_tok, n = x.shape
+    xp, xt, xs = _matrix(x, n_tok, n, "x")
+    rp = rt = rs = op = os_ = qp = qs = sp = ss = yp = ys = 0
+    if resid is not None:
+        rp, rt, rs = _matrix(resid, n_tok, n, "resid")
+        op, ot, os_ = _matrix(resid_out, n_tok, n, "resid_out")
+        if ot != rt:
+            _invalid("resid and resid_out must have one type")
+    if gamma is not None and (gamma.dtype is not _torch.float32 or gamma.numel() != n or not gamma.is_contiguous()):
+        _invalid(f"gamma must be a contiguous float32 tensor of {n} entries")
+    if q is not None:
+        qp, qn, qk, qs = _f8(q, "q")
+        if qn != n_tok or qk != n:
+            _invalid(f"q must be [{n_tok}, {n}]")
+        sp, ss = _scales(scale, (n + 127) // 128, n_tok, "scale")
+    if y is not None:
+        yp, yt, ys = _matrix(y, n_tok, n, "y")
+        if yt != xt:
+            _invalid("y must have x's type")
+    rc = (_lib or lib()).stage_op_norm_f8(xp, xt, xs, rp, rt, rs, op, os_, None if gamma is None else gamma.data_ptr(), eps, n_tok, n,
+                                          qp, qs, sp, ss, yp, ys, stream)
+    if rc:
+        _opcheck(rc)
+
+
+def stage_op_f8_gemm(a, a_scale, w, w_scale, out, error=None, stream=None) -> None:
+    """out [M, N] (float32, float16 or bfloat16) = a w^T of 8-bit rows a [M, K] and w [N, K] (row strides of multiples of 16 bytes) with
+    scales a_scale [ceil(K / 128), M] and w_scale [ceil(N / 128), ceil(K / 128)]; error: int32 [1], set to 1 once a call has
+    given up waiting (what misses something is NaN)."""
+    torch = _torch or _load_torch()
+    stream = _kv4_launch(stream, a, a_scale, w, w_scale, out) if error is None else _kv4_launch(stream, a, a_scale, w, w_scale, out, error)
+    ap, m, k, as_ = _f8(a, "a")
+    wp, n, wk, ws = _f8(w, "w")
+    if wk != k:
+        _invalid("a and w must have one number of columns")
+    kb = (k + 127) // 128
+    sp, ss = _scales(a_scale, kb, m, "a_scale")
+    if w_scale.dtype is not torch.float32 or w_scale.shape != ((n + 127) // 128, kb) or not w_scale.is_contiguous():
+        _invalid(f"w_scale must be contiguous float32 [{(n + 127) // 128}, {kb}]")
+    yp, yt, ys = _matrix(out, m, n, "out")
+    rc = (_lib or lib()).stage_op_f8_gemm(ap, as_, sp, ss, wp, ws, w_scale.data_ptr(), m, n, k, yp, yt, ys,
+                                          None if error is None else _i32dev(error, "error", 1), stream)
+    if rc:
+        _opcheck(rc)
+
+
+def stage_op_f8_debug_stall(calls: int) -> None:
+    """The next calls of stage_op_f8_gemm by this thread run out of time (tests of that path)."""
+    _opcheck(lib().stage_op_f8_debug_stall(calls))
+
+
+def stage_op_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = STAGE_ROPE_PLAIN, factor: float = 1.0,
+                        first_len: float = 1.0, low: float = 1.0, high: float = 32.0):
+    """(frequencies float64 [rot_dim / 2] on the host, scale) for stage_op_rope."""
+    if _beyond_c_int(rot_dim, scaling):
+        _invalid("rot_dim or scaling out of range")
+    f, scale = np.zeros(max(1, min(rot_dim, 1024) // 2), dtype=np.float64), C.c_float()
+    _opcheck(lib().stage_op_rope_freqs(rot_dim, theta, scaling, factor, first_len, low, high, f.ctypes.data_as(C.POINTER(C.c_double)),
+                                       C.byref(scale)))
+    return f, scale.value
+
+
+def stage_op_rope(q, k, pos, freqs, q_out=None, k_out=None, interleaved: bool = False, scale: float = 1.0, stream=None) -> None:
+    """Rotary positions of the heads q [n_tok, n_q_heads, head_dim] and k [n_tok, n_k_heads, head_dim] (or None) at pos (int32 [n_tok];
+    negative: padding, not written) with freqs (float64 [rot_dim / 2], radians per position), into q_out and k_out (default: in
+    place).  Rows may lie apart; the heads of a row lie side by side."""
+    torch = _torch or _load_torch()
+    if q_out is None:
+        q_out = q
+    if k_out is None:
+        k_out = k
+    if (k is None) != (k_out is None):
+        _invalid("k_out without k")
+    stream = _kv4_launch(stream, q, q_out, pos, freqs) if k is None else _kv4_launch(stream, q, q_out, pos, freqs, k, k_out)
+    if q.dim() != 3:
+        _invalid("q must be [n_tok, n_q_heads, head_dim]")
+    n_tok, hq, d = q.shape
+    qp, qt, qs = _rows(q, hq, d, "q")
+    qop, qot, qos = _rows(q_out, hq, d, "q_out")
+    kp = ks = kop = kos = hk = 0
+    kt = kot = qt
+    if k is not None:
+        if k.dim() != 3:
+            _invalid("k must be [n_tok, n_k_heads, head_dim]")
+        hk = k.shape[1]
+        kp, kt, ks = _rows(k, hk, d, "k")
+        kop, kot, kos = _rows(k_out, hk, d, "k_out")
+        if k.shape[0] != n_tok or k_out.shape[0] != n_tok:
+            _invalid("q and k must have one number of tokens")
+    if q_out.shape[0] != n_tok or not qt == qot == kt == kot:
+        _invalid("q, k and their outputs must have one type and number of tokens")
+    if freqs.dtype is not torch.float64 or not freqs.is_contiguous():
+        _invalid("freqs must be a contiguous float64 tensor")
+    rc = (_lib or lib()).stage_op_rope(qp, qs, hq, kp, ks, hk, d, qt, _i32dev(pos, "pos", n_tok), n_tok, freqs.data_ptr(),
+                                       2 * freqs.numel(), int(bool(interleaved)), scale, qop, qos, kop, kos, stream)
+    if rc:
+        _opcheck(rc)
+
+
+def stage_op_logprobs(logits, tokens=None, logprob=None, entropy=None, rank=None, top_ids=None, top_logprobs=None, stream=None) -> None:
+    """From rows of logits [n, vocab] (which may lie apart): logprob (float32 [n]) and rank (int32 [n]) of tokens (int32 [n]), entropy
+    (float32 [n]), and the k likeliest tokens top_ids (int32 [n, k]) with top_logprobs (float32 [n, k]); each may be None."""
+    torch = _torch or _load_torch()
+    stream = _kv4_launch(stream, logits, *[t for t in (tokens, logprob, entropy, rank, top_ids, top_logprobs) if t is not None])
+    if logits.dim() != 2:
+        _invalid("logits must be [n, vocab]")
+    n, vocab = logits.shape
+    zp, zt, zs = _matrix(logits, n, vocab, "logits")
+    i32, f32 = torch.int32, torch.float32
+    for t, dt, what in ((tokens, i32, "tokens"), (logprob, f32, "logprob"), (entropy, f32, "entropy"), (rank, i32, "rank")):
+        if t is not None and (t.dtype is not dt or t.numel() != n or not t.is_contiguous()):
+            _invalid(f"{what} must be a contiguous {dt} tensor of {n} entries")
+    top = 0
+    for t, dt, what in ((top_ids, i32, "top_ids"), (top_logprobs, f32, "top_logprobs")):
+        if t is None:
+            continue
+        if t.dtype is not dt or t.dim() != 2 or t.shape[0] != n or not t.is_contiguous():
+            _invalid(f"{what} must be a contiguous {dt} tensor [{n}, k]")
+        if t is top_logprobs and top_ids is not None and t.shape[1] != top:
+            _invalid("top_ids and top_logprobs must have one shape")
+        top = t.shape[1]
+    p = [None if t is None else t.data_ptr() for t in (tokens, logprob, entropy, rank, top_ids, top_logprobs)]
+    rc = (_lib or lib()).stage_op_logprobs(zp, zt, zs, n, vocab, p[0], p[1], p[2], p[3], top, p[4], p[5], stream)
     if rc:
         _opcheck(rc)

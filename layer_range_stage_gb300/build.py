@@ -19,7 +19,8 @@ LIB = os.path.join(LIB_DIR, "libstage.so")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["kernels_decode.cu", "kernels_prefill.cu", "kernels_mega.cu", "kernels_mega_moe.cu", "kernels_kv4.cu",
-           "kernels_kv4_attn.cu", "kernels_kv4_chunk.cu", "stage.cu", "ops.cu", "ops_kv4.cu"]
+           "kernels_kv4_attn.cu", "kernels_kv4_chunk.cu", "kernels_norm_f8.cu", "kernels_f8_gemm.cu", "kernels_rope.cu",
+           "kernels_logprobs.cu", "stage.cu", "ops.cu", "ops_kv4.cu", "ops_step.cu"]
 
 
 def nvcc() -> str:

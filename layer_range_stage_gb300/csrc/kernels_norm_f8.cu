@@ -1,0 +1,239 @@
+// The residual's addition, an RMS norm, and 8-bit rows with scales (include/stage_step.h: stage_op_norm_f8).
+//
+// One pass: a row's values stay in registers between the sum of squares and the codes.  A warp takes a
+// block of 128 columns at a time, four neighbouring columns a lane, so that a block's largest value is one warp
+// reduction and its codes are one store of 128 bytes.  The bytes in and out bound it.
+//
+// The codes are defined by float32 roundings, so two machines agree if they agree on r = fl(1 / sqrt(mean + eps)).  A float32
+// sum would not do: its last bits depend on its order, and where r differs by one unit so does a code now and then.
+// The sum is held as an unevaluated pair of float32 (every addition's error is caught exactly and added up: Knuth's
+// two-sum), about 2^-45 of it, and r comes from the reciprocal square root by one Newton step whose residual
+// 1 - m r^2 is formed in pairs as well, so that its only rounding that counts is the last.
+#include <algorithm>
+#include <type_traits>
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "step.cuh"
+
+namespace lrs {
+
+namespace {
+
+struct Pair {  // an unevaluated sum hi + lo
+  float hi, lo;
+};
+
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair r;
+  float e;
+  two_sum(a.hi, b.hi, r.hi, e);
+  r.lo = __fadd_rn(__fadd_rn(a.lo, b.lo), e);
+  return r;
+}
+
+// fl(1 / sqrt(sum / n + eps))
+__device__ __forceinline__ float recip_root(Pair sum, float n, float eps) {
+  const float q = __fdiv_rn(sum.hi, n);
+  const float rem = __fadd_rn(__fmaf_rn(-q, n, sum.hi), sum.lo);
+  Pair m;
+  float e;
+  two_sum(q, eps, m.hi, e);
+  m.lo = __fadd_rn(__fdiv_rn(rem, n), e);
+  two_sum(m.hi, m.lo, m.hi, m.lo);
+  const float r = rsqrtf(m.hi);
+  const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
+  const float t = __fmul_rn(m.hi, p), te = __fmaf_rn(m.hi, p, -t);
+  // 1 - (m.hi + m.lo) (p + pe), t being next to 1
+  float d = __fsub_rn(1.f, t);
+  d = __fsub_rn(d, te);
+  d = __fmaf_rn(-m.hi, pe, d);
+  d = __fmaf_rn(-m.lo, p, d);
+  return __fmaf_rn(__fmul_rn(0.5f, r), d, r);
+}
+
+template <typename T>
+struct alignas(sizeof(T) * 4) Four {
+  T v[4];
+};
+
+// Columns of lane's four values in a block: 4 lane + i side by side, or lane + 32 i where rows are not aligned for that.
+__device__ __forceinline__ int col_of(int vec, int lane, int i) { return vec ? 4 * lane + i : lane + 32 * i; }
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* row, int c0, int lane, int n, int vec, float (&f)[4]) {
+  if (vec && c0 + 4 * lane + 4 <= n) {
+    const Four<T> p = *reinterpret_cast<const Four<T>*>(row + c0 + 4 * lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = to_f32(p.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + col_of(vec, lane, i);
+      f[i] = c < n ? to_f32(row[c]) : 0.f;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* row, int c0, int lane, int n, int vec, const Four<T>& p) {
+  if (vec && c0 + 4 * lane + 4 <= n) {
+    *reinterpret_cast<Four<T>*>(row + c0 + 4 * lane) = p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + col_of(vec, lane, i);
+      if (c < n) row[c] = p.v[i];
+    }
+  }
+}
+
+// TR: the residual's type, or void.  W warps of a row (blockDim.x / 32), blockDim.y rows per CTA, CH blocks of 128 per warp.
+template <typename TX, typename TR, int CH>
+__global__ void __launch_bounds__(512) norm_f8_kernel(const NormF8Args a) {
+  __shared__ Pair part[16];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live = row < a.n_tok;
+  const int nb = (a.n + 127) >> 7;
+  constexpr bool kResid = !std::is_void<TR>::value;
+  using TRv = typename std::conditional<kResid, TR, float>::type;
+
+  float h[CH][4];
+  const TX* x = static_cast<const TX*>(a.x) + (int64_t)row * a.x_stride;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int b = c * W + w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[c][i] = 0.f;
+    if (live && b < nb) load4(x, b * 128, lane, a.n, a.vec, h[c]);
+  }
+  if (kResid) {
+    const TRv* res = static_cast<const TRv*>(a.resid) + (int64_t)row * a.resid_stride;
+    TRv* out = static_cast<TRv*>(a.resid_out) + (int64_t)row * a.resid_out_stride;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int b = c * W + w;
+      if (!live || b >= nb) continue;
+      float f[4];
+      load4(res, b * 128, lane, a.n, a.vec, f);
+      Four<TRv> p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p.v[i] = from_f32<TRv>(__fadd_rn(h[c][i], f[i]));
+        h[c][i] = to_f32(p.v[i]);  // the norm is of what the next block will read
+      }
+      store4(out, b * 128, lane, a.n, a.vec, p);
+    }
+  }
+  if (a.gamma) {
+    Pair s{0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p = __fmul_rn(h[c][i], h[c][i]);
+        float e;
+        two_sum(s.hi, p, s.hi, e);
+        s.lo = __fadd_rn(s.lo, __fadd_rn(e, __fmaf_rn(h[c][i], h[c][i], -p)));
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Pair t;
+      t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+      t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+      s = add(s, t);
+    }
+    if (W > 1) {  // one row per CTA then
+      if (lane == 0) part[w] = s;
+      __syncthreads();
+      s = part[0];
+      for (int i = 1; i < W; ++i) s = add(s, part[i]);
+    }
+    const float r = recip_root(s, (float)a.n, a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int b = c * W + w;
+      if (b >= nb) continue;
+      float g[4];
+      load4(a.gamma, b * 128, lane, a.n, a.vec, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[c][i] = __fmul_rn(__fmul_rn(h[c][i], r), g[i]);
+    }
+  }
+  if (!live) return;
+  if (a.y) {
+    TX* y = static_cast<TX*>(a.y) + (int64_t)row * a.y_stride;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int b = c * W + w;
+      if (b >= nb) continue;
+      Four<TX> p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.v[i] = from_f32<TX>(h[c][i]);
+      store4(y, b * 128, lane, a.n, a.vec, p);
+    }
+  }
+  if (a.q) {
+    uint8_t* q = a.q + (int64_t)row * a.q_stride;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int b = c * W + w;
+      if (b >= nb) continue;
+      // magnitudes compare like their bits, and a NaN above all of them: it is not lost
+      uint32_t m = 0x0D800000u;  // 2^-100
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(h[c][i]) & 0x7FFFFFFFu);
+      const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, m));
+      const float t = __fdiv_rn(448.f, top);
+      Four<uint8_t> p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.v[i] = __nv_cvt_float_to_fp8(__fmul_rn(h[c][i], t), __NV_SATFINITE, __NV_E4M3);
+      store4(q, b * 128, lane, a.n, a.vec, p);
+      if (lane == 0) a.scale[(int64_t)b * a.scale_stride + row] = __fdiv_rn(top, 448.f);
+    }
+  }
+}
+
+template <typename TX, typename TR, int CH>
+cudaError_t launch_ch(const NormF8Args& a, int warps, int rows, cudaStream_t st) {
+  norm_f8_kernel<TX, TR, CH><<<(unsigned)((a.n_tok + rows - 1) / rows), dim3(32 * warps, rows), 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename TX, typename TR>
+cudaError_t launch_t(const NormF8Args& a, cudaStream_t st) {
+  const int nb = (a.n + 127) / 128;
+  // blocks per warp: 16 at the widest rows (16 warps), else few enough for a warp to have its loads in flight together
+  int ch = nb > 128 ? 16 : nb > 64 ? 8 : nb > 2 ? 4 : 2;
+  const int warps = (nb + ch - 1) / ch;
+  const int rows = warps == 1 ? 4 : 1;
+  if (ch == 16) return launch_ch<TX, TR, 16>(a, warps, rows, st);
+  if (ch == 8) return launch_ch<TX, TR, 8>(a, warps, rows, st);
+  if (ch == 4) return launch_ch<TX, TR, 4>(a, warps, rows, st);
+  return launch_ch<TX, TR, 2>(a, warps, rows, st);
+}
+
+template <typename TX>
+cudaError_t launch_x(const NormF8Args& a, int resid_dtype, cudaStream_t st) {
+  if (!a.resid) return launch_t<TX, void>(a, st);
+  if (resid_dtype == kTypeF32) return launch_t<TX, float>(a, st);
+  return launch_t<TX, TX>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_f8(const NormF8Args& a, int x_dtype, int resid_dtype, cudaStream_t st) {
+  if (x_dtype == kTypeF32) return launch_x<float>(a, resid_dtype, st);
+  if (x_dtype == kTypeF16) return launch_x<__half>(a, resid_dtype, st);
+  return launch_x<__nv_bfloat16>(a, resid_dtype, st);
+}
+
+}  // namespace lrs

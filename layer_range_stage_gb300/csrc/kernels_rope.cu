@@ -1,0 +1,181 @@
+// Rotary positions of query and key heads (include/stage_step.h: stage_op_rope).
+//
+// Angles.  A position's angle is pos * f radians; only its fraction of a turn matters.  f / 2 pi is taken as a 64-bit
+// fraction of a turn (its rounding is f's own, 2^-53 of it), and the product with pos wraps around at whole turns by itself: one
+// integer multiplication reduces the angle exactly, at any position.  The top two bits of the fraction (plus an eighth)
+// are the quadrant, the rest lies within an eighth of a turn of zero, where float32 holds it to 2^-28 of a turn.
+//
+// A row is read and written once: the bytes bound it.  A CTA makes its tokens' table of cos and sin in
+// shared memory while its first loads are in flight, and every head of the token uses it.
+#include <algorithm>
+
+#include "common.cuh"
+#include "step.cuh"
+
+namespace lrs {
+
+namespace {
+
+constexpr int kThreads = 256, kItems = 4;  // items of a thread, all loaded before the table is waited for
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+  T v[VEC];
+};
+
+__device__ __forceinline__ float2 cos_sin_of(int pos, double f, float scale) {
+  constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+  double t = f * kTurn;
+  t -= floor(t);
+  const uint64_t frac = (uint64_t)pos * __double2ull_rn(t * 18446744073709551616.0);
+  const uint32_t top = (uint32_t)(frac >> 32) + (1u << 29);  // an eighth of a turn up: the quadrant is in the two top bits
+  const float x = (float)((int)(top & 0x3FFFFFFFu) - (1 << 29)) * (1.0f / 2147483648.0f);  // in half turns, within +-1/4
+  float s, c;
+  sincospif(x, &s, &c);
+  const uint32_t quad = top >> 30;
+  if (quad & 1) {
+    const float h = c;
+    c = -s;
+    s = h;
+  }
+  if (quad & 2) {
+    c = -c;
+    s = -s;
+  }
+  return make_float2(c * scale, s * scale);
+}
+
+// An item is two vectors of VEC elements of one head: the halves' parts of VEC pairs, or (interleaved, and dims that are
+// only copied) two neighbouring vectors.
+template <typename T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tok_per_cta, int splits, int rot_items,
+                                                        int head_items) {
+  extern __shared__ float2 table[];  // [token][rot / 2]
+  using P = Pack<T, VEC>;
+  const int t0 = (int)(blockIdx.x / splits) * tok_per_cta, nt = min(tok_per_cta, a.n_tok - t0);
+  const int split = (int)(blockIdx.x % splits);
+  const int heads = a.hq + a.hk, half = a.rot >> 1;
+  const int h0 = (int)((int64_t)heads * split / splits), nh = (int)((int64_t)heads * (split + 1) / splits) - h0;
+  const int per_tok = nh * head_items, total = nt * per_tok;
+  bool have_table = false;
+
+  for (int base = 0; base < total; base += kThreads * kItems) {
+    P u[kItems], v[kItems];
+    T* out[kItems];
+    int d0[kItems], d1[kItems], tok[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int it = base + i * kThreads + (int)threadIdx.x;
+      tok[i] = -1;
+      if (it >= total) continue;
+      const int tl = it / per_tok, rest = it - tl * per_tok, hl = rest / head_items, j = rest - hl * head_items;
+      const int t = t0 + tl, h = h0 + hl;
+      const bool is_k = h >= a.hq;
+      const int64_t in_off = is_k ? t * a.k_stride + (int64_t)(h - a.hq) * a.head_dim : t * a.q_stride + (int64_t)h * a.head_dim;
+      const T* in = static_cast<const T*>(is_k ? a.k : a.q) + in_off;
+      const int64_t out_off =
+          is_k ? t * a.k_out_stride + (int64_t)(h - a.hq) * a.head_dim : t * a.q_out_stride + (int64_t)h * a.head_dim;
+      out[i] = static_cast<T*>(is_k ? a.k_out : a.q_out) + out_off;
+      tok[i] = a.pos[t] < 0 ? -1 : tl;  // padding is read like the rest, but not written
+      if (INTER) {
+        d0[i] = 2 * j * VEC;
+        d1[i] = d0[i] + VEC;
+      } else if (j < rot_items) {
+        d0[i] = j * VEC;
+        d1[i] = half + d0[i];
+      } else {
+        d0[i] = a.rot + 2 * (j - rot_items) * VEC;
+        d1[i] = d0[i] + VEC;
+      }
+      u[i] = *reinterpret_cast<const P*>(in + d0[i]);
+      if (d1[i] < a.head_dim) v[i] = *reinterpret_cast<const P*>(in + d1[i]);
+    }
+    if (!have_table) {
+      for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+        const int tl = i / half, p = a.pos[t0 + tl];
+        if (p >= 0) table[i] = cos_sin_of(p, a.freqs[i - tl * half], a.scale);
+      }
+      __syncthreads();
+      have_table = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      if (tok[i] < 0) continue;
+      const float2* cs = table + tok[i] * half;
+      if (!INTER) {
+        if (d0[i] < half) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float2 w = cs[d0[i] + e];
+            const float x = to_f32(u[i].v[e]), y = to_f32(v[i].v[e]);
+            u[i].v[e] = from_f32<T>(x * w.x - y * w.y);
+            v[i].v[e] = from_f32<T>(y * w.x + x * w.y);
+          }
+        }
+      } else if (VEC == 1) {  // a pair is the two vectors
+        if (d0[i] < a.rot) {
+          const float2 w = cs[d0[i] >> 1];
+          const float x = to_f32(u[i].v[0]), y = to_f32(v[i].v[0]);
+          u[i].v[0] = from_f32<T>(x * w.x - y * w.y);
+          v[i].v[0] = from_f32<T>(y * w.x + x * w.y);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          constexpr int kHi = VEC > 1 ? 1 : 0;
+          if (d0[i] < a.rot) {
+            const float2 w = cs[(d0[i] + e) >> 1];
+            const float x = to_f32(u[i].v[e]), y = to_f32(u[i].v[e + kHi]);
+            u[i].v[e] = from_f32<T>(x * w.x - y * w.y);
+            u[i].v[e + kHi] = from_f32<T>(y * w.x + x * w.y);
+          }
+          if (d1[i] < a.rot) {
+            const float2 w = cs[(d1[i] + e) >> 1];
+            const float x = to_f32(v[i].v[e]), y = to_f32(v[i].v[e + kHi]);
+            v[i].v[e] = from_f32<T>(x * w.x - y * w.y);
+            v[i].v[e + kHi] = from_f32<T>(y * w.x + x * w.y);
+          }
+        }
+      }
+      *reinterpret_cast<P*>(out[i] + d0[i]) = u[i];
+      if (d1[i] < a.head_dim) *reinterpret_cast<P*>(out[i] + d1[i]) = v[i];
+    }
+  }
+}
+
+template <typename T, int VEC, bool INTER>
+cudaError_t launch_t(const RopeArgs& a, cudaStream_t st) {
+  // items of a head: those that turn, and behind them those that are only copied (where something is copied at all)
+  const int rot_items = INTER ? (a.rot + 2 * VEC - 1) / (2 * VEC) : a.rot / (2 * VEC);
+  const int rest = a.copy ? a.head_dim - a.rot : 0;
+  const int head_items = INTER ? ((a.copy ? a.head_dim : a.rot) + 2 * VEC - 1) / (2 * VEC) : rot_items + (rest + 2 * VEC - 1) / (2 * VEC);
+  const int heads = a.hq + a.hk, per_tok = heads * head_items;
+  // A CTA takes whole tokens, about a round of items, as long as there are some CTAs for each SM; else a token's heads are
+  // shared out (each share makes the table for itself).
+  const int round = kThreads * kItems;
+  int tok_per_cta = std::max(1, std::min(round / std::max(1, per_tok), a.n_tok / 608));
+  tok_per_cta = std::min(tok_per_cta, std::max(1, 16384 / (a.rot * 4)));
+  int splits = 1;
+  if (a.n_tok < 304) splits = std::max(1, std::min({heads, 304 / a.n_tok, (per_tok + kThreads - 1) / kThreads}));
+  const size_t smem = (size_t)tok_per_cta * (a.rot / 2) * sizeof(float2);
+  const int64_t grid = (int64_t)((a.n_tok + tok_per_cta - 1) / tok_per_cta) * splits;
+  rope_kernel<T, VEC, INTER><<<(unsigned)grid, kThreads, smem, st>>>(a, tok_per_cta, splits, rot_items, head_items);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_d(const RopeArgs& a, cudaStream_t st) {
+  constexpr int kVec = 16 / sizeof(T);
+  if (a.interleaved) return a.vec ? launch_t<T, kVec, true>(a, st) : launch_t<T, 1, true>(a, st);
+  return a.vec ? launch_t<T, kVec, false>(a, st) : launch_t<T, 1, false>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st) {
+  if (dtype == kTypeF32) return launch_d<float>(a, st);
+  if (dtype == kTypeF16) return launch_d<__half>(a, st);
+  return launch_d<__nv_bfloat16>(a, st);
+}
+
+}  // namespace lrs

@@ -1,0 +1,89 @@
+// Launch interface of the step's operators (include/stage_step.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace lrs {
+
+// The types of stage_ops.h: STAGE_F32, STAGE_F16, STAGE_BF16 are 0, 1, 2.
+constexpr int kTypeF32 = 0, kTypeF16 = 1, kTypeBf16 = 2;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+struct NormF8Args {
+  const void* x = nullptr;
+  const void* resid = nullptr;
+  void* resid_out = nullptr;
+  const float* gamma = nullptr;
+  uint8_t* q = nullptr;
+  float* scale = nullptr;
+  void* y = nullptr;
+  int64_t x_stride = 0, resid_stride = 0, resid_out_stride = 0, q_stride = 0, scale_stride = 0, y_stride = 0;
+  int n_tok = 0, n = 0;
+  float eps = 0.f;
+  int vec = 0;  // every row and base at a multiple of four elements
+};
+cudaError_t launch_norm_f8(const NormF8Args& a, int x_dtype, int resid_dtype, cudaStream_t st);
+
+struct F8GemmArgs {
+  const uint8_t* a = nullptr;
+  const uint8_t* w = nullptr;
+  const float* sa = nullptr;  // [nkb] rows at sa_stride
+  const float* sw = nullptr;  // [ceil(N / 128)][nkb]
+  void* y = nullptr;
+  int* error = nullptr;
+  int64_t a_stride = 0, w_stride = 0, sa_stride = 0, y_stride = 0;
+  int M = 0, N = 0, K = 0, nkb = 0;
+  int vec = 0;  // y's base and rows at multiples of 16 bytes
+  int stall = 0;  // tests: nothing is copied, so that the waits run out
+};
+cudaError_t launch_f8_gemm(const F8GemmArgs& a, int y_dtype, cudaStream_t st);
+
+struct RopeArgs {
+  const void* q = nullptr;
+  const void* k = nullptr;
+  void* q_out = nullptr;
+  void* k_out = nullptr;
+  const int* pos = nullptr;
+  const double* freqs = nullptr;
+  int64_t q_stride = 0, k_stride = 0, q_out_stride = 0, k_out_stride = 0;
+  int hq = 0, hk = 0, head_dim = 0, rot = 0, n_tok = 0, interleaved = 0;
+  float scale = 1.f;
+  int vec = 0;   // bases, strides, heads and pairs allow accesses of 16 bytes
+  int copy = 0;  // dims from rot on are to be copied (some output is not in place)
+};
+cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st);
+
+struct LogprobsArgs {
+  const void* z = nullptr;
+  const int* tokens = nullptr;
+  float* logprob = nullptr;
+  float* entropy = nullptr;
+  int* rank = nullptr;
+  int* top_ids = nullptr;
+  float* top_lp = nullptr;
+  int64_t stride = 0;
+  int rows = 0, vocab = 0, top = 0;
+};
+cudaError_t launch_logprobs(const LogprobsArgs& a, int dtype, cudaStream_t st);
+
+}  // namespace lrs
