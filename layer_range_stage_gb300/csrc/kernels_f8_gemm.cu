@@ -7,12 +7,15 @@
 #include <algorithm>
 #include <atomic>
 
+#include <cooperative_groups.h>
 #include <cuda.h>
 
 #include "common.cuh"
 #include "kernels.cuh"
 #include "step.cuh"
 #include "tc.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace lrs {
 
@@ -21,10 +24,21 @@ namespace {
 constexpr uint64_t kWaitNs = 1000000000ull;  // a wait's limit; what misses it is NaN
 constexpr uint64_t kDrainNs = 200000000ull;
 
+// A wait with a limit, which also ends as soon as another role of the CTA has given up.  The thread sleeps on the mbarrier (up to the
+// hint): one that keeps asking takes shared-memory cycles from the products' operands.
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (sleep_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!sleep_wait(bar, parity)) {
     if (*abort_flag) return false;
     if (global_ns() - t0 > kWaitNs) {
       *abort_flag = 1;
@@ -35,31 +49,39 @@ __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, volatile i
   return true;
 }
 
-// acc += s * d for two neighbouring columns
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
+// acc += s * d for two neighbouring columns.  (The same in inline PTX costs a move for each operand: 231 us for 2048 x 28672 x 4096 where
+// this takes 202, and single multiply-adds 233.)
+__device__ __forceinline__ void fma2(float2& acc, uint32_t d0, uint32_t d1, float2 s) {
+  acc = __ffma2_rn(make_float2(__uint_as_float(d0), __uint_as_float(d1)), s, acc);
 }
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+__device__ __forceinline__ float2 unpack2(float2 v) { return v; }
+
+// ---- many rows: tiles of 256 rows x 256 columns, one persistent pair of CTAs per two SMs ----
+// A product of a pair reads from each SM's shared memory its 128 rows of a and half of the weights' 256, where two CTAs on their
+// own would read all 256 each: with copies coming in at the same time that is more than shared memory gives (and half again
+// as much from L2).  Both CTAs: warp 0 copies, warps 4-11 read TMEM and hold the sums (warp w: rows 32 (w % 4) .. + 31 of the CTA's
+// 128, columns of half w / 4 - 1).  Warp 1 of the first CTA issues the products.  The first warpgroup gives its registers to the two that
+// hold the sums.
+constexpr int kBM = 256, kBN = 256, kBK = 128, kThreads = 384;
+constexpr int kRegsStart = 168, kRegsRoles = 56, kRegsSums = 224;
+static_assert(128 * kRegsRoles + 256 * kRegsSums <= kThreads * kRegsStart, "the warpgroups share out what the block is launched with");
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ---- many rows: tiles of 128 rows x BN columns, one persistent CTA per SM ----
-// Warps 0-7 read TMEM and hold the sums (warp w: rows 32 (w % 4) .. + 31, columns of half w / 4), warp 8 copies, warp 9 issues
-// the products.
-constexpr int kBM = 128, kBK = 128, kThreads = 320;
-
-template <int BN>
 struct Big {
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr uint32_t kTileA = kBM * kBK, kTileB = BN * kBK, kStage = kTileA + kTileB;
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kTileA = 128 * kBK, kTileB = 128 * kBK, kStage = kTileA + kTileB;  // of one CTA
   static constexpr uint32_t kOffOut = kStages * kStage;       // 8 warps x 4 KB: rows on their way out
   static constexpr uint32_t kOffBar = kOffOut + 8 * 4096;
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
-  static constexpr uint32_t kCols = 2 * BN;
+  static constexpr uint32_t kCols = 2 * kBN;
   struct Bars {
     uint64_t full[kStages], empty[kStages], done[2], free_[2], drain;
   };
@@ -67,7 +89,7 @@ struct Big {
 
 // A warp's 32 rows x COLS columns (row = lane) through 4 KB of shared memory, so that rows leave in whole lines.
 template <int COLS, typename T>
-__device__ __forceinline__ void store_rows(const uint64_t (&acc)[COLS / 2], unsigned char* stg, const F8GemmArgs& a, int row0, int col0,
+__device__ __forceinline__ void store_rows(const float2 (&acc)[COLS / 2], unsigned char* stg, const F8GemmArgs& a, int row0, int col0,
                                            bool ok) {
   constexpr int kPiece = 128 / sizeof(T), kUnit = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
@@ -124,18 +146,21 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[COLS / 2], unsi
   }
 }
 
-template <int BN, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     f8_gemm_kernel(const F8GemmArgs a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB) {
-  using G = Big<BN>;
-  constexpr int kHalf = BN / 2;
+  using G = Big;
+  constexpr int kHalf = kBN / 2;
   extern __shared__ unsigned char raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  typename G::Bars* B = reinterpret_cast<typename G::Bars*>(sm + G::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + G::kOffBar + sizeof(typename G::Bars));
+  G::Bars* B = reinterpret_cast<G::Bars*>(sm + G::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + G::kOffBar + sizeof(G::Bars));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tiles_m = (a.M + kBM - 1) / kBM, tiles = tiles_m * ((a.N + BN - 1) / BN), nkb = a.nkb;
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles_m = (a.M + kBM - 1) / kBM, tiles = tiles_m * ((a.N + kBN - 1) / kBN), nkb = a.nkb;
 
   if (tid == 0) {
     for (int i = 0; i < G::kStages; ++i) {
@@ -144,7 +169,173 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B->done[i], 1);
-      mbar_init(&B->free_[i], 8);
+      mbar_init(&B->free_[i], 16);
+    }
+    mbar_init(&B->drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(tmem_slot, G::kCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster.sync();  // both CTAs' barriers and TMEM are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+    regs_down<kRegsRoles>();
+    if (warp == 0 && lane == 0 && !a.stall) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        const int m0 = tile % tiles_m * kBM + 128 * rank, n0 = tile / tiles_m * kBN + 128 * rank;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % G::kStages;
+          if (it >= G::kStages && !(ok = fwait(&B->empty[s], (uint32_t)(it / G::kStages + 1) & 1u, abort_flag, a.error))) break;
+          const uint32_t bar = at_rank(&B->full[s], 0);  // the first CTA's counts both CTAs' bytes
+          if (rank == 0) mbar_arrive_expect_tx(&B->full[s], 2 * G::kStage);
+          tma_load_2d_pair(sm + s * G::kStage, &tA, kb * kBK, m0, bar);
+          tma_load_2d_pair(sm + s * G::kStage + G::kTileA, &tB, kb * kBK, n0, bar);
+        }
+      }
+      if (*abort_flag) {  // nothing may still be landing in shared memory when the CTA leaves
+        if (rank == 0) {
+          for (int k = max(0, it - G::kStages); k < it; ++k)
+            mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
+        } else {  // only the first CTA can see these land: a time in which they have
+          const uint64_t t0 = global_ns();
+          while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
+        }
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_f8_f32(kBM, kBN);
+      int it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += pairs)
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % G::kStages, d = it & 1;
+          if (!(ok = fwait(&B->full[s], (uint32_t)(it / G::kStages) & 1u, abort_flag, a.error))) break;
+          if (it >= 2 && !(ok = fwait(&B->free_[d], (uint32_t)(it / 2 + 1) & 1u, abort_flag, a.error))) break;
+          tc_fence_after();
+          const uint32_t pa = smem_u32(sm + s * G::kStage), pb = pa + G::kTileA;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            umma_f8_pair(tmem + d * kBN, desc_sw128(pa + kk * 32), desc_sw128(pb + kk * 32), idesc, kk > 0);
+          umma_commit_pair(&B->empty[s]);
+          umma_commit_pair(&B->done[d]);
+        }
+      if (!ok && it > 0) {  // given up: the products already issued finish before TMEM is released
+        umma_commit_pair(&B->drain);
+        mbar_wait(&B->drain, 0u, kDrainNs);
+      }
+    }
+  } else {
+    regs_up<kRegsSums>();
+    const int quarter = warp & 3, half = (warp >> 2) - 1;
+    const uint32_t lane_tmem = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(half * kHalf);
+    unsigned char* stg = sm + G::kOffOut + (warp - 4) * 4096;
+    const uint32_t free0 = at_rank(&B->free_[0], 0), free1 = at_rank(&B->free_[1], 0);
+    int it = 0;
+    bool ok = true;
+    for (int tile = pair; tile < tiles; tile += pairs) {
+      const int m0 = tile % tiles_m * kBM + 128 * rank, n0 = tile / tiles_m * kBN;
+      const int row0 = m0 + 32 * quarter, col0 = n0 + half * kHalf;
+      const float* sa = a.sa + min(row0 + lane, a.M - 1);
+      const float* sw = a.sw + (int64_t)min(col0 >> 7, (a.N - 1) >> 7) * nkb;
+      float2 acc[kHalf / 2];
+#pragma unroll
+      for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      // the factors of two blocks ahead, multiplied only when they are needed: nothing waits for a load that has just been made
+      float fa[2], fw[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fa[i] = i < nkb ? sa[(int64_t)i * a.sa_stride] : 0.f;
+        fw[i] = i < nkb ? sw[i] : 0.f;
+      }
+#pragma unroll 2
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int d = it & 1;
+        ok = __all_sync(0xffffffffu, fwait(&B->done[d], (uint32_t)(it / 2) & 1u, abort_flag, a.error));
+        if (!ok) break;
+        tc_fence_after();
+        const float f1 = fa[kb & 1] * fw[kb & 1];
+        const float2 f = make_float2(f1, f1);
+        if (kb + 2 < nkb) {
+          fa[kb & 1] = sa[(int64_t)(kb + 2) * a.sa_stride];
+          fw[kb & 1] = sw[kb + 2];
+        }
+        // 16 columns on their way while the 16 before them are added
+        uint32_t r[2][16];
+        tmem_ld16(lane_tmem + d * kBN, r[0]);
+#pragma unroll
+        for (int c = 0; c < kHalf / 16; ++c) {
+          tmem_wait_ld16(r[c & 1]);
+          if (c + 1 < kHalf / 16) {
+            tmem_ld16(lane_tmem + d * kBN + (c + 1) * 16, r[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(d ? free1 : free0);
+          }
+#pragma unroll
+          for (int i = 0; i < 16 / 2; ++i) fma2(acc[c * (16 / 2) + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], f);
+        }
+      }
+      store_rows<kHalf, T>(acc, stg, a, row0, col0, ok);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster.sync();  // the other CTA's products, copies and arrivals are done with this one's memory
+  if (warp == 0) tmem_dealloc_pair(tmem, G::kCols);
+}
+
+// ---- few rows: 128 weight rows x NT rows of a, the K blocks shared out over a cluster ----
+// The weights are what is read, so they are the 128 lanes of the products, once, and the rows of a their columns.  A CTA takes
+// a tile of 128 weight rows and its rank's K blocks; the ranks' sums meet in shared memory, added in the order of the ranks.
+// Warps 0-3 hold the sums (a weight row per thread), warp 4 copies, warp 5 issues the products.
+constexpr int kSmallThreads = 192;
+
+template <int NT>
+struct Small {
+  static constexpr int kStages = NT >= 128 ? 3 : NT == 64 ? 4 : 6;
+  static constexpr uint32_t kTileW = 128 * kBK, kTileA = NT * kBK, kStage = kTileW + kTileA;
+  static constexpr uint32_t kOffScale = kStages * kStage;             // 4 warps x 2 blocks x NT products of scales
+  static constexpr uint32_t kOffBar = kOffScale + 4 * 2 * NT * 4;
+  static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+  static constexpr uint32_t kCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static_assert(kStages * kStage >= 128 * NT * 4, "the sums take the stages' place");
+  struct Bars {
+    uint64_t full[kStages], empty[kStages], done[2], free_[2], drain;
+  };
+};
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(kSmallThreads)
+    f8_gemm_small_kernel(const F8GemmArgs a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tW) {
+  using G = Small<NT>;
+  extern __shared__ unsigned char raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  typename G::Bars* B = reinterpret_cast<typename G::Bars*>(sm + G::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + G::kOffBar + sizeof(typename G::Bars));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tile = blockIdx.x / C, n0 = tile * 128;
+  const int k0 = (int)((int64_t)a.nkb * rank / C), nk = (int)((int64_t)a.nkb * (rank + 1) / C) - k0;
+
+  if (tid == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->done[i], 1);
+      mbar_init(&B->free_[i], 4);
     }
     mbar_init(&B->drain, 1);
     *abort_flag = 0;
@@ -159,126 +350,197 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
+  float2 acc[NT / 2];
+#pragma unroll
+  for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+  bool ok = true;
+  if (warp == 4) {
     if (lane == 0 && !a.stall) {
       int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int m0 = tile % tiles_m * kBM, n0 = tile / tiles_m * BN;
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % G::kStages;
-          if (it >= G::kStages && !(ok = fwait(&B->empty[s], (uint32_t)(it / G::kStages + 1) & 1u, abort_flag, a.error))) break;
-          mbar_arrive_expect_tx(&B->full[s], G::kStage);
-          tma_load_2d(sm + s * G::kStage, &tA, kb * kBK, m0, &B->full[s]);
-          tma_load_2d(sm + s * G::kStage + G::kTileA, &tB, kb * kBK, n0, &B->full[s]);
-        }
+      for (; it < nk; ++it) {
+        const int s = it % G::kStages;
+        if (it >= G::kStages && !fwait(&B->empty[s], (uint32_t)(it / G::kStages + 1) & 1u, abort_flag, a.error)) break;
+        mbar_arrive_expect_tx(&B->full[s], G::kStage);
+        tma_load_2d(sm + s * G::kStage, &tW, (k0 + it) * kBK, n0, &B->full[s]);
+        tma_load_2d(sm + s * G::kStage + G::kTileW, &tA, (k0 + it) * kBK, 0, &B->full[s]);
       }
       if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
         for (int k = max(0, it - G::kStages); k < it; ++k)
           mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
     }
-  } else if (warp == 9) {
+  } else if (warp == 5) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f8_f32(kBM, BN);
+      constexpr uint32_t idesc = idesc_f8_f32(128, NT);
       int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x)
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % G::kStages, d = it & 1;
-          if (!(ok = fwait(&B->full[s], (uint32_t)(it / G::kStages) & 1u, abort_flag, a.error))) break;
-          if (it >= 2 && !(ok = fwait(&B->free_[d], (uint32_t)(it / 2 + 1) & 1u, abort_flag, a.error))) break;
-          tc_fence_after();
-          const uint32_t pa = smem_u32(sm + s * G::kStage), pb = pa + G::kTileA;
+      for (; it < nk; ++it) {
+        const int s = it % G::kStages, d = it & 1;
+        if (!fwait(&B->full[s], (uint32_t)(it / G::kStages) & 1u, abort_flag, a.error)) break;
+        if (it >= 2 && !fwait(&B->free_[d], (uint32_t)(it / 2 + 1) & 1u, abort_flag, a.error)) break;
+        tc_fence_after();
+        const uint32_t pw = smem_u32(sm + s * G::kStage), pa = pw + G::kTileW;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 32; ++kk)
-            umma_f8(tmem + d * BN, desc_sw128(pa + kk * 32), desc_sw128(pb + kk * 32), idesc, kk > 0);
-          umma_commit(&B->empty[s]);
-          umma_commit(&B->done[d]);
-        }
-      if (!ok && it > 0) {  // given up: the products already issued finish before TMEM is released
+        for (int kk = 0; kk < kBK / 32; ++kk)
+          umma_f8(tmem + d * NT, desc_sw128(pw + kk * 32), desc_sw128(pa + kk * 32), idesc, kk > 0);
+        umma_commit(&B->empty[s]);
+        umma_commit(&B->done[d]);
+      }
+      if (it < nk && it > 0) {  // given up: the products already issued finish before TMEM is released
         umma_commit(&B->drain);
         mbar_wait(&B->drain, 0u, kDrainNs);
       }
     }
   } else {
-    const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t lane_tmem = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(half * kHalf);
-    unsigned char* stg = sm + G::kOffOut + warp * 4096;
-    int it = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const int m0 = tile % tiles_m * kBM, n0 = tile / tiles_m * BN;
-      const int row0 = m0 + 32 * quarter, col0 = n0 + half * kHalf;
-      const float* sa = a.sa + min(row0 + lane, a.M - 1);
-      const float* sw = a.sw + (int64_t)min(col0 >> 7, (a.N - 1) >> 7) * nkb;
-      uint64_t acc[kHalf / 2];
+    const uint32_t lane_tmem = tmem + ((uint32_t)(32 * warp) << 16);
+    const float* sw = a.sw + (int64_t)tile * a.nkb + k0;
+    const float* sa = a.sa + (int64_t)k0 * a.sa_stride;
+    float* scales = reinterpret_cast<float*>(sm + G::kOffScale) + warp * 2 * NT;
+    constexpr int kPer = (NT + 31) / 32;
+    // the next block's factors of columns lane, lane + 32, ..., multiplied only when they are needed
+    float next[kPer], next_w = nk > 0 ? sw[0] : 0.f;
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
-      float s = sa[0] * sw[0];
-      for (int kb = 0; kb < nkb && ok; ++kb, ++it) {
-        const float cur = s;
-        if (kb + 1 < nkb) s = sa[(int64_t)(kb + 1) * a.sa_stride] * sw[kb + 1];
-        const int d = it & 1;
-        ok = __all_sync(0xffffffffu, fwait(&B->done[d], (uint32_t)(it / 2) & 1u, abort_flag, a.error));
-        if (!ok) break;
-        tc_fence_after();
-        uint64_t f;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(cur)));
+    for (int j = 0; j < kPer; ++j) next[j] = nk > 0 ? sa[min(lane + 32 * j, a.M - 1)] : 0.f;
+    for (int it = 0; it < nk; ++it) {
+      const int d = it & 1;
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(lane_tmem + d * BN + c * 32, r);
-          tmem_wait_ld();
+      for (int j = 0; j < kPer; ++j)
+        if (lane + 32 * j < NT) scales[d * NT + lane + 32 * j] = next[j] * next_w;
+      if (it + 1 < nk) {
+        next_w = sw[it + 1];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], r[2 * i], r[2 * i + 1], f);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&B->free_[d]);
+        for (int j = 0; j < kPer; ++j) next[j] = sa[(int64_t)(it + 1) * a.sa_stride + min(lane + 32 * j, a.M - 1)];
       }
-      store_rows<kHalf, T>(acc, stg, a, row0, col0, ok);
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, fwait(&B->done[d], (uint32_t)(it / 2) & 1u, abort_flag, a.error));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        uint32_t r[16];
+        tmem_ld16(lane_tmem + d * NT + c * 16, r);
+        tmem_wait_ld16(r);
+        const float4* f = reinterpret_cast<const float4*>(scales + d * NT + c * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 g = f[i];
+          fma2(acc[c * 8 + 2 * i], r[4 * i], r[4 * i + 1], make_float2(g.x, g.y));
+          fma2(acc[c * 8 + 2 * i + 1], r[4 * i + 2], r[4 * i + 3], make_float2(g.z, g.w));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->free_[d]);
     }
+  }
+  const float bad = __int_as_float(0x7FC00000);
+  T* y = static_cast<T*>(a.y);
+  const bool whole = !*abort_flag;
+  if (C == 1) {
+    if (warp < 4 && n0 + tid < a.N) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float2 p = unpack2(acc[i / 2]);
+        if (i < a.M) y[(int64_t)i * a.y_stride + n0 + tid] = from_f32<T>(ok && whole ? (i & 1 ? p.y : p.x) : bad);
+      }
+    }
+  } else {
+    __syncthreads();  // a CTA that has given up has waited for its copies
+    float* sums = reinterpret_cast<float*>(sm);  // [row of a][weight row]
+    if (warp < 4) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float2 p = unpack2(acc[i / 2]);
+        if (i < a.M) sums[i * 128 + tid] = ok ? (i & 1 ? p.y : p.x) : bad;
+      }
+    }
+    cluster.sync();
+    const int total = a.M * 128, e1 = (int)((int64_t)total * (rank + 1) / C);
+    for (int e = (int)((int64_t)total * rank / C) + tid; e < e1; e += kSmallThreads) {
+      float v = 0.f;
+      for (int r = 0; r < C; ++r) v += cluster.map_shared_rank(sums, r)[e];
+      const int n = n0 + (e & 127);
+      if (n < a.N) y[(int64_t)(e >> 7) * a.y_stride + n] = from_f32<T>(v);
+    }
+    cluster.sync();  // the others read these sums until here
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, G::kCols);
 }
 
-// Once per device: the kernel's shared memory.
+// Once per device: the kernel's shared memory, and whether it has the registers that its warpgroups share out (from a kernel
+// with fewer, the one that asks for more would wait forever).
 template <typename K>
-cudaError_t ready_once(K kernel, size_t smem, std::atomic<uint64_t>& done) {
+cudaError_t ready_once(K kernel, size_t smem, int regs, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < regs) return cudaErrorLaunchOutOfResources;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
   return e;
 }
 
-template <int BN, typename T>
+template <typename T>
 cudaError_t launch_big(const F8GemmArgs& a, cudaStream_t st) {
-  using G = Big<BN>;
+  using G = Big;
+  static_assert(sizeof(G::Bars) + 8 <= 256, "barrier block");
+  static_assert(G::kSmem <= 227 * 1024, "shared memory");
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = ready_once(f8_gemm_kernel<T>, G::kSmem, kRegsStart, done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap tA, tB;
+  if (!encode_2d(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.a_stride, kBK, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.w_stride, kBK, 128,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
+  const int grid = 2 * (int)std::min<int64_t>(tiles, std::max(1, sm_count() / 2));
+  f8_gemm_kernel<T><<<grid, kThreads, G::kSmem, st>>>(a, tA, tB);
+  return cudaGetLastError();
+}
+
+template <int NT, typename T>
+cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
+  using G = Small<NT>;
   static_assert(sizeof(typename G::Bars) + 8 <= 256, "barrier block");
   static_assert(G::kSmem <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = ready_once(f8_gemm_kernel<BN, T>, G::kSmem, done);
+  cudaError_t e = ready_once(f8_gemm_small_kernel<NT, T>, G::kSmem, 0, done);
   if (e != cudaSuccess) return e;
-  CUtensorMap tA, tB;
-  if (!encode_2d(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.a_stride, kBK, kBM,
+  CUtensorMap tA, tW;
+  if (!encode_2d(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.a_stride, kBK, NT,
                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_2d(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.w_stride, kBK, BN,
+      !encode_2d(&tW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.w_stride, kBK, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int64_t tiles = (int64_t)((a.M + kBM - 1) / kBM) * ((a.N + BN - 1) / BN);
-  const int grid = (int)std::min<int64_t>(tiles, std::max(1, sm_count()));
-  f8_gemm_kernel<BN, T><<<grid, kThreads, G::kSmem, st>>>(a, tA, tB);
-  return cudaGetLastError();
+  const int tiles = (a.N + 127) / 128;
+  const int C = std::max(1, std::min({8, 2 * sm_count() / tiles, a.nkb / 2}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * C));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = G::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f8_gemm_small_kernel<NT, T>, a, tA, tW);
 }
 
 template <typename T>
 cudaError_t launch_t(const F8GemmArgs& a, cudaStream_t st) {
-  return launch_big<256, T>(a, st);
+  if (a.M <= 16) return launch_small<16, T>(a, st);
+  if (a.M <= 32) return launch_small<32, T>(a, st);
+  if (a.M <= 64) return launch_small<64, T>(a, st);
+  if (a.M <= 128) return launch_small<128, T>(a, st);
+  return launch_big<T>(a, st);
 }
 
 }  // namespace

@@ -5,7 +5,9 @@
 //
 // The likeliest tokens: the row is cut into chunks of 32 bytes, a thread's load, and a chunk's largest logit (which the running
 // maximum needs anyway) is kept in shared memory.  The n_top first tokens lie in the n_top chunks that come first in the same order
-// by their largest logit, so a warp picks those chunks, and only they are read again.
+// by their largest logit, and those in the n_top threads that come first by theirs: a search over the bits of a threshold, a
+// barrier that counts per bit, finds a bound that few threads reach; their chunks above it are ranked by counting, and only
+// the n_top first are read again.
 //
 // Few rows are split over a cluster's CTAs, whose parts meet in the first one's shared memory.
 #include <algorithm>
@@ -22,8 +24,9 @@ namespace lrs {
 
 namespace {
 
-constexpr int kThreads = 256, kTop = 32, kMaxCluster = 8;
+constexpr int kTop = 32, kMaxCluster = 8;
 constexpr int kMaxChunks = 16384;  // of a CTA: their maxima take 64 KB
+constexpr int kSlack = 8;          // threads above the bound beyond the n_top that are needed, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN wins
@@ -65,17 +68,18 @@ struct alignas(32) Chunk {
   T v[32 / sizeof(T)];
 };
 
+template <int NT>
 struct Shared {
-  Sums sums[kThreads / 32];
-  int above[kThreads / 32];
+  Sums sums[NT / 32];
+  int above[NT / 32];
   Sums all;
   int above_all;
-  int n_best;
+  int n_chunks, n_cand;
   uint32_t best_chunk[kTop];
-  int n_cand;
-  uint64_t cand[kTop * 16];
-  uint64_t list[kTop];  // this CTA's first tokens in order: (ordered logit, ~index)
+  float bound;             // the last of these chunks' largest logit
+  uint64_t list[kTop];     // this CTA's first tokens in order: (ordered logit, ~index)
   uint64_t merged[kTop];
+  uint64_t cand[kTop * 16];
 };
 
 // Elements of chunk c (of the row's grid of 32-byte chunks, whose first element is -off), -inf outside the row.
@@ -94,11 +98,41 @@ __device__ __forceinline__ void load_chunk(const T* z, int off, int vocab, int c
   }
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a, int chunks_per_cta) {
+__device__ __forceinline__ float max_of(const Chunk<float>& p) {
+  float top = p.v[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = max_nan(top, p.v[i]);
+  return top;
+}
+__device__ __forceinline__ float max_of(const Chunk<__half>& p) {
+  const __half2* h = reinterpret_cast<const __half2*>(p.v);
+  __half2 top = h[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = __hmax2_nan(top, h[i]);
+  return max_nan(__low2float(top), __high2float(top));
+}
+__device__ __forceinline__ float max_of(const Chunk<__nv_bfloat16>& p) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(p.v);
+  __nv_bfloat162 top = h[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = __hmax2_nan(top, h[i]);
+  return max_nan(__low2float(top), __high2float(top));
+}
+__device__ __forceinline__ float2 two_of(const Chunk<float>& p, int i) { return make_float2(p.v[2 * i], p.v[2 * i + 1]); }
+__device__ __forceinline__ float2 two_of(const Chunk<__half>& p, int i) {
+  return __half22float2(reinterpret_cast<const __half2*>(p.v)[i]);
+}
+__device__ __forceinline__ float2 two_of(const Chunk<__nv_bfloat16>& p, int i) {
+  const uint32_t u = reinterpret_cast<const uint32_t*>(p.v)[i];
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+
+// NT threads, U chunks of each on their way at once.
+template <typename T, bool TOP, int NT, int U>
+__global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int chunks_per_cta) {
   constexpr int E = 32 / sizeof(T);
-  extern __shared__ uint32_t maxima[];  // [chunks_per_cta], ordered; 0: taken
-  __shared__ Shared sh;
+  extern __shared__ uint32_t maxima[];  // [chunks_per_cta] ordered, then (8-byte aligned) the chunks above the bound
+  __shared__ Shared<NT> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -114,38 +148,50 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
   int above = 0;
   uint64_t mine = 0;  // the thread's best chunk: (ordered maximum, ~chunk)
 
-  for (int c = tid; c < nc; c += kThreads) {
-    Chunk<T> p;
-    load_chunk(z, off, a.vocab, c0 + c, p);
-    float f[E];
+  for (int base = tid; base < nc; base += NT * U) {
+    Chunk<T> p[U];
 #pragma unroll
-    for (int i = 0; i < E; ++i) f[i] = to_f32(p.v[i]);
-    float top = f[0];
+    for (int u = 0; u < U; ++u)
+      if (base + u * NT < nc) load_chunk(z, off, a.vocab, c0 + base + u * NT, p[u]);
 #pragma unroll
-    for (int i = 1; i < E; ++i) top = max_nan(top, f[i]);
-    if (TOP) {
-      const uint32_t k = ordered(top);
-      maxima[c] = k;
-      mine = max(mine, (uint64_t)k << 32 | (uint32_t)~c);
-    }
-    if (top >= zt) {
-      const int e0 = (c0 + c) * E - off;
+    for (int u = 0; u < U; ++u) {
+      const int c = base + u * NT;
+      if (c >= nc) break;
+      const float top = max_of(p[u]);
+      if (TOP) {
+        const uint32_t k = ordered(top);
+        maxima[c] = k;
+        mine = max(mine, (uint64_t)k << 32 | (uint32_t)~c);
+      }
+      if (top >= zt) {
+        const int e0 = (c0 + c) * E - off;
 #pragma unroll
-      for (int i = 0; i < E; ++i) above += f[i] > zt || (f[i] == zt && e0 + i >= 0 && e0 + i < t) ? 1 : 0;
-    }
-    if (top == -INFINITY) continue;
-    if (!(top <= m.ref)) {  // above, or NaN (which then reaches the sums)
-      const float ref = top == top ? top : 0.f, d = (m.ref - ref) * kLog2e, g = ex2(d);
-      m.t = m.ref == -INFINITY ? 0.f : g * (m.t + fmaxf(d, -1000.f) * m.s);
-      m.s = m.ref == -INFINITY ? 0.f : g * m.s;
-      m.ref = ref;
-    }
+        for (int i = 0; i < E; ++i) {
+          const float f = to_f32(p[u].v[i]);
+          above += f > zt || (f == zt && e0 + i >= 0 && e0 + i < t) ? 1 : 0;
+        }
+      }
+      if (top == -INFINITY) continue;
+      if (!(top <= m.ref)) {  // above, or NaN (which then reaches the sums)
+        const float ref = top == top ? top : 0.f, d = (m.ref - ref) * kLog2e, g = ex2(d);
+        m.t = m.ref == -INFINITY ? 0.f : g * (m.t + fmaxf(d, -1000.f) * m.s);
+        m.s = m.ref == -INFINITY ? 0.f : g * m.s;
+        m.ref = ref;
+      }
+      const float2 down = make_float2(-m.ref, -m.ref), l2 = make_float2(kLog2e, kLog2e);
+      float2 s = make_float2(m.s, 0.f), td = make_float2(m.t, 0.f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float d = max_nan((f[i] - m.ref) * kLog2e, -1000.f);  // 2^-1000 is 0 here, and 0 * -1000 too
-      const float e = ex2(d);
-      m.s += e;
-      m.t = fmaf(e, d, m.t);
+      for (int i = 0; i < E / 2; ++i) {
+        float2 d = __fmul2_rn(__fadd2_rn(two_of(p[u], i), down), l2), e;
+        d.x = max_nan(d.x, -1000.f);  // 2^-1000 is 0 here, and 0 * -1000 too
+        d.y = max_nan(d.y, -1000.f);
+        e.x = ex2(d.x);
+        e.y = ex2(d.y);
+        s = __fadd2_rn(s, e);
+        td = __ffma2_rn(e, d, td);
+      }
+      m.s = s.x + s.y;
+      m.t = td.x + td.y;
     }
   }
 #pragma unroll
@@ -161,81 +207,88 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
     sh.sums[warp] = m;
     sh.above[warp] = above;
   }
-  uint64_t* entries = reinterpret_cast<uint64_t*>(sh.cand);  // the threads' best chunks, before the candidates take the place
-  if (TOP) entries[tid] = mine;
+  if (tid == 0) sh.n_chunks = sh.n_cand = 0;
+  if (tid < kTop) sh.list[tid] = 0;
   __syncthreads();
-  if (tid == 0) {
-    Sums s = sh.sums[0];
-    int n = sh.above[0];
-    for (int w = 1; w < kThreads / 32; ++w) {
-      s = merge(s, sh.sums[w]);
-      n += sh.above[w];
+  if (warp == 0) {
+    Sums s{-INFINITY, 0.f, 0.f};
+    int n = 0;
+    if (lane < NT / 32) {
+      s = sh.sums[lane];
+      n = sh.above[lane];
     }
-    sh.all = s;
-    sh.above_all = n;
+#pragma unroll
+    for (int o = NT / 64; o > 0; o >>= 1) {
+      Sums b;
+      b.ref = __shfl_down_sync(0xffffffffu, s.ref, o);
+      b.s = __shfl_down_sync(0xffffffffu, s.s, o);
+      b.t = __shfl_down_sync(0xffffffffu, s.t, o);
+      s = merge(s, b);
+      n += __shfl_down_sync(0xffffffffu, n, o);
+    }
+    if (lane == 0) {
+      sh.all = s;
+      sh.above_all = n;
+    }
   }
-  if (TOP) {
-    if (warp == 0) {  // the first a.top chunks, one after another
-      uint64_t e[kThreads / 32];
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) e[i] = entries[i * 32 + lane];
-      int n = 0;
-      for (; n < min(a.top, nc); ++n) {
-        uint64_t best = e[0];
-#pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) best = max(best, e[i]);
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        const int c = (int)~lo, owner = c % kThreads;
-        if (lane == 0) {
-          sh.best_chunk[n] = (uint32_t)c;
-          maxima[c] = 0;
-        }
-        __syncwarp();
-        uint64_t next = 0;  // the owner's best chunk that is left
-        for (int j = owner + lane * kThreads; j < nc; j += 32 * kThreads) {
-          const uint32_t k = maxima[j];
-          if (k) next = max(next, (uint64_t)k << 32 | (uint32_t)~j);
-        }
-        const uint32_t nhi = __reduce_max_sync(0xffffffffu, (uint32_t)(next >> 32));
-        const uint32_t nlo = __reduce_max_sync(0xffffffffu, (uint32_t)(next >> 32) == nhi ? (uint32_t)next : 0u);
-        if (lane == (owner & 31)) {
-#pragma unroll
-          for (int i = 0; i < kThreads / 32; ++i)
-            if (i == owner >> 5) e[i] = (uint64_t)nhi << 32 | nlo;
-        }
+  if (TOP && nc > 0) {
+    uint64_t* chunk_list = reinterpret_cast<uint64_t*>(maxima + (chunks_per_cta + 1) / 2 * 2);
+    // a bound that at least min(n_top, threads with a chunk) threads' best chunks reach, and few more
+    const int want = min(a.top, min(nc, NT));
+    uint64_t bound = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const uint64_t b = bound | 1ull << bit;
+      const int n = __syncthreads_count(mine >= b);
+      if (n >= want) {
+        bound = b;
+        if (n <= want + kSlack) break;
       }
-      if (lane == 0) {
-        sh.n_best = n;
-        sh.n_cand = 0;
+    }
+    if (mine && mine >= bound) {
+      for (int c = tid; c < nc; c += NT) {
+        const uint64_t k = (uint64_t)maxima[c] << 32 | (uint32_t)~c;
+        if (k >= bound) chunk_list[atomicAdd(&sh.n_chunks, 1)] = k;
       }
     }
     __syncthreads();
-    // their elements: all of them are candidates
-    const int n_el = sh.n_best * E;
-    for (int i = tid; i < n_el; i += kThreads) {
-      const int e = (c0 + (int)sh.best_chunk[i / E]) * E - off + i % E;
-      if (e >= 0 && e < a.vocab) sh.cand[atomicAdd(&sh.n_cand, 1)] = (uint64_t)ordered(to_f32(z[e])) << 32 | (uint32_t)~e;
+    const int n_chunks = sh.n_chunks, n_best = min(a.top, n_chunks);
+    for (int i = tid; i < n_chunks; i += NT) {
+      const uint64_t key = chunk_list[i];
+      int before = 0;
+      for (int j = 0; j < n_chunks; ++j) before += chunk_list[j] > key;
+      if (before < n_best) sh.best_chunk[before] = ~(uint32_t)key;
+      if (before == n_best - 1) sh.bound = unordered((uint32_t)(key >> 32));
     }
-    if (tid < kTop) sh.list[tid] = 0;
+    __syncthreads();
+    // the first of their elements are all among those that reach the last chunk's largest (where there are n_top chunks)
+    const float least = n_best == a.top ? sh.bound : -INFINITY;
+    for (int i = tid; i < n_best * E; i += NT) {
+      const int e = (c0 + (int)sh.best_chunk[i / E]) * E - off + i % E;
+      const float f = e >= 0 && e < a.vocab ? to_f32(z[e]) : 0.f;
+      if (e >= 0 && e < a.vocab && !(f < least)) sh.cand[atomicAdd(&sh.n_cand, 1)] = (uint64_t)ordered(f) << 32 | (uint32_t)~e;
+    }
     __syncthreads();
     const int n_cand = sh.n_cand;
-    for (int i = tid; i < n_cand; i += kThreads) {
+    for (int i = tid; i < n_cand; i += NT) {
       const uint64_t key = sh.cand[i];
       int before = 0;
       for (int j = 0; j < n_cand; ++j) before += sh.cand[j] > key;
       if (before < a.top) sh.list[before] = key;
     }
   }
-  cluster.sync();
+  if (C > 1)
+    cluster.sync();
+  else
+    __syncthreads();
   if (rank == 0) {
     if (TOP && C > 1) {
-      for (int i = tid; i < C * kTop; i += kThreads) sh.cand[i] = cluster.map_shared_rank(&sh, i / kTop)->list[i % kTop];
+      const int n = C * a.top;
+      for (int i = tid; i < n; i += NT) sh.cand[i] = cluster.map_shared_rank(&sh, i / a.top)->list[i % a.top];
       __syncthreads();
-      for (int i = tid; i < C * kTop; i += kThreads) {
+      for (int i = tid; i < n; i += NT) {
         const uint64_t key = sh.cand[i];
         int before = 0;
-        for (int j = 0; j < C * kTop; ++j) before += sh.cand[j] > key;
+        for (int j = 0; j < n; ++j) before += sh.cand[j] > key;
         if (key && before < a.top) sh.merged[before] = key;
       }
       __syncthreads();
@@ -243,10 +296,27 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
     if (tid < 32) {
       Sums s = sh.all;
       int n = sh.above_all;
-      for (int r = 1; r < C; ++r) {
-        const Shared* o = cluster.map_shared_rank(&sh, r);
-        s = merge(s, o->all);
-        n += o->above_all;
+      if (C > 1) {  // a lane for each CTA, merged in one order
+        Sums o{-INFINITY, 0.f, 0.f};
+        int k = 0;
+        if (lane < C) {
+          const Shared<NT>* at = cluster.map_shared_rank(&sh, lane);
+          o = at->all;
+          k = at->above_all;
+        }
+#pragma unroll
+        for (int d = kMaxCluster / 2; d > 0; d >>= 1) {
+          Sums b;
+          b.ref = __shfl_down_sync(0xffffffffu, o.ref, d);
+          b.s = __shfl_down_sync(0xffffffffu, o.s, d);
+          b.t = __shfl_down_sync(0xffffffffu, o.t, d);
+          o = merge(o, b);
+          k += __shfl_down_sync(0xffffffffu, k, d);
+        }
+        s.ref = __shfl_sync(0xffffffffu, o.ref, 0);
+        s.s = __shfl_sync(0xffffffffu, o.s, 0);
+        s.t = __shfl_sync(0xffffffffu, o.t, 0);
+        n = __shfl_sync(0xffffffffu, k, 0);
       }
       const float ls = log2f(s.s);
       const bool bad = !(s.s > 0.f) || !(s.ref < INFINITY);
@@ -265,7 +335,34 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsArgs a
       }
     }
   }
-  cluster.sync();  // the others' shared memory is read until here
+  if (C > 1) cluster.sync();  // the others' shared memory is read until here
+}
+
+template <typename T, bool TOP, int NT, int U>
+cudaError_t launch_k(const LogprobsArgs& a, int C, int per, cudaStream_t st) {
+  // the bound's threads hold (per + NT - 1) / NT chunks each
+  const size_t smem = TOP ? ((size_t)per + 1) / 2 * 8 + (size_t)(a.top + kSlack) * ((per + NT - 1) / NT) * 8 : 0;
+  static std::atomic<uint64_t> ready{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(logprobs_kernel<T, TOP, NT, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunks * 4 + (kTop + kSlack) * (kMaxChunks / NT) * 8);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.rows * C));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, TOP, NT, U>, a, per);
 }
 
 template <typename T, bool TOP>
@@ -275,28 +372,9 @@ cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t st) {
   int C = 1;
   while (C < kMaxCluster && ((chunks + C - 1) / C > kMaxChunks || (a.rows * (int64_t)C < 304 && chunks / C >= 1024))) C *= 2;
   const int per = (chunks + C - 1) / C;
-  const size_t smem = TOP ? (size_t)per * 4 : 0;
-  static std::atomic<uint64_t> ready{0};  // one bit per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxChunks * 4);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.rows * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, TOP>, a, per);
+  // one row's latency counts where a cluster shares it: more threads, each with fewer loads after one another
+  if (C > 1) return launch_k<T, TOP, 512, 4>(a, C, per, st);
+  return launch_k<T, TOP, 256, 2>(a, C, per, st);
 }
 
 template <typename T>

@@ -59,6 +59,14 @@ __device__ __forceinline__ float recip_root(Pair sum, float n, float eps) {
   return __fmaf_rn(__fmul_rn(0.5f, r), d, r);
 }
 
+// The same for two sums side by side.
+__device__ __forceinline__ float2 neg(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ void two_sum2(float2 a, float2 b, float2& s, float2& e) {
+  s = __fadd2_rn(a, b);
+  const float2 t = __fadd2_rn(s, neg(a));
+  e = __fadd2_rn(__fadd2_rn(a, neg(__fadd2_rn(s, neg(t)))), __fadd2_rn(b, neg(t)));
+}
+
 template <typename T>
 struct alignas(sizeof(T) * 4) Four {
   T v[4];
@@ -106,6 +114,8 @@ __global__ void __launch_bounds__(512) norm_f8_kernel(const NormF8Args a) {
   constexpr bool kResid = !std::is_void<TR>::value;
   using TRv = typename std::conditional<kResid, TR, float>::type;
 
+  // all of the row is asked for before anything of it is used; the widest rows' residual (its registers) four blocks at a time
+  constexpr int kBatch = CH > 8 ? 4 : CH;
   float h[CH][4];
   const TX* x = static_cast<const TX*>(a.x) + (int64_t)row * a.x_stride;
 #pragma unroll
@@ -119,31 +129,43 @@ __global__ void __launch_bounds__(512) norm_f8_kernel(const NormF8Args a) {
     const TRv* res = static_cast<const TRv*>(a.resid) + (int64_t)row * a.resid_stride;
     TRv* out = static_cast<TRv*>(a.resid_out) + (int64_t)row * a.resid_out_stride;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int b = c * W + w;
-      if (!live || b >= nb) continue;
-      float f[4];
-      load4(res, b * 128, lane, a.n, a.vec, f);
-      Four<TRv> p;
+    for (int c0 = 0; c0 < CH; c0 += kBatch) {
+      float f[kBatch][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p.v[i] = from_f32<TRv>(__fadd_rn(h[c][i], f[i]));
-        h[c][i] = to_f32(p.v[i]);  // the norm is of what the next block will read
+      for (int j = 0; j < kBatch; ++j) {
+        const int b = (c0 + j) * W + w;
+        if (live && b < nb) load4(res, b * 128, lane, a.n, a.vec, f[j]);
       }
-      store4(out, b * 128, lane, a.n, a.vec, p);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int b = (c0 + j) * W + w;
+        if (!live || b >= nb) continue;
+        Four<TRv> p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p.v[i] = from_f32<TRv>(__fadd_rn(h[c0 + j][i], f[j][i]));
+          h[c0 + j][i] = to_f32(p.v[i]);  // the norm is of what the next block will read
+        }
+        store4(out, b * 128, lane, a.n, a.vec, p);
+      }
     }
   }
   if (a.gamma) {
-    Pair s{0.f, 0.f};
+    float2 hi = make_float2(0.f, 0.f), lo = hi;
+    // a square of 12 bits or fewer is a float32
+    constexpr bool kExact = sizeof(TRv) == 2 || (!kResid && sizeof(TX) == 2);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __fmul_rn(h[c][i], h[c][i]);
-        float e;
-        two_sum(s.hi, p, s.hi, e);
-        s.lo = __fadd_rn(s.lo, __fadd_rn(e, __fmaf_rn(h[c][i], h[c][i], -p)));
+      for (int i = 0; i < 4; i += 2) {
+        const float2 v = make_float2(h[c][i], h[c][i + 1]);
+        const float2 p = __fmul2_rn(v, v);
+        float2 e;
+        two_sum2(hi, p, hi, e);
+        if (!kExact) e = __fadd2_rn(e, __ffma2_rn(v, v, neg(p)));
+        lo = __fadd2_rn(lo, e);
       }
+    Pair s = add(Pair{hi.x, lo.x}, Pair{hi.y, lo.y});
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       Pair t;
@@ -154,8 +176,16 @@ __global__ void __launch_bounds__(512) norm_f8_kernel(const NormF8Args a) {
     if (W > 1) {  // one row per CTA then
       if (lane == 0) part[w] = s;
       __syncthreads();
-      s = part[0];
-      for (int i = 1; i < W; ++i) s = add(s, part[i]);
+      s = lane < W ? part[lane] : Pair{0.f, 0.f};
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        Pair t;
+        t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+        t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+        s = add(s, t);
+      }
+      s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+      s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
     }
     const float r = recip_root(s, (float)a.n, a.eps);
 #pragma unroll
@@ -183,21 +213,32 @@ __global__ void __launch_bounds__(512) norm_f8_kernel(const NormF8Args a) {
   }
   if (a.q) {
     uint8_t* q = a.q + (int64_t)row * a.q_stride;
+    // lane c divides for the warp's block c
+    float top = 1.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int b = c * W + w;
-      if (b >= nb) continue;
       // magnitudes compare like their bits, and a NaN above all of them: it is not lost
       uint32_t m = 0x0D800000u;  // 2^-100
 #pragma unroll
       for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(h[c][i]) & 0x7FFFFFFFu);
-      const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, m));
-      const float t = __fdiv_rn(448.f, top);
-      Four<uint8_t> p;
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == c) top = __uint_as_float(m);
+    }
+    const float up = __fdiv_rn(448.f, top);
+    if (lane < CH && lane * W + w < nb) a.scale[(int64_t)(lane * W + w) * a.scale_stride + row] = __fdiv_rn(top, 448.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p.v[i] = __nv_cvt_float_to_fp8(__fmul_rn(h[c][i], t), __NV_SATFINITE, __NV_E4M3);
+    for (int c = 0; c < CH; ++c) {
+      const int b = c * W + w;
+      const float t = __shfl_sync(0xffffffffu, up, c);
+      if (b >= nb) continue;
+      const __nv_fp8x2_storage_t q0 = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[c][0], t), __fmul_rn(h[c][1], t)), __NV_SATFINITE, __NV_E4M3);
+      const __nv_fp8x2_storage_t q1 = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[c][2], t), __fmul_rn(h[c][3], t)), __NV_SATFINITE, __NV_E4M3);
+      Four<uint8_t> p;
+      p.v[0] = (uint8_t)q0;
+      p.v[1] = (uint8_t)(q0 >> 8);
+      p.v[2] = (uint8_t)q1;
+      p.v[3] = (uint8_t)(q1 >> 8);
       store4(q, b * 128, lane, a.n, a.vec, p);
-      if (lane == 0) a.scale[(int64_t)b * a.scale_stride + row] = __fdiv_rn(top, 448.f);
     }
   }
 }

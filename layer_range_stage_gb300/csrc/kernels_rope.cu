@@ -23,11 +23,16 @@ struct alignas(sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 
-__device__ __forceinline__ float2 cos_sin_of(int pos, double f, float scale) {
+// f / 2 pi as a 64-bit fraction of a turn
+__device__ __forceinline__ uint64_t turn_of(double f) {
   constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
   double t = f * kTurn;
   t -= floor(t);
-  const uint64_t frac = (uint64_t)pos * __double2ull_rn(t * 18446744073709551616.0);
+  return __double2ull_rn(t * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ float2 cos_sin_of(int pos, uint64_t turn, float scale) {
+  const uint64_t frac = (uint64_t)pos * turn;
   const uint32_t top = (uint32_t)(frac >> 32) + (1u << 29);  // an eighth of a turn up: the quadrant is in the two top bits
   const float x = (float)((int)(top & 0x3FFFFFFFu) - (1 << 29)) * (1.0f / 2147483648.0f);  // in half turns, within +-1/4
   float s, c;
@@ -45,30 +50,44 @@ __device__ __forceinline__ float2 cos_sin_of(int pos, double f, float scale) {
   return make_float2(c * scale, s * scale);
 }
 
+// Division by a number that stays the same: n / d for n < 2^31 (d >= 1), by a multiplication with the rounded-up 2^(32 + s) / d.
+struct Div {
+  uint32_t d, mul, shift;
+};
+__host__ Div div_by(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return {d, d == 1 ? 0u : (uint32_t)(((1ull << (31 + s)) + d - 1) / d), s == 0 ? 0u : s - 1};
+}
+__device__ __forceinline__ uint32_t quotient(uint32_t n, Div v) { return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift; }
+
 // An item is two vectors of VEC elements of one head: the halves' parts of VEC pairs, or (interleaved, and dims that are
 // only copied) two neighbouring vectors.
 template <typename T, int VEC, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tok_per_cta, int splits, int rot_items,
-                                                        int head_items) {
-  extern __shared__ float2 table[];  // [token][rot / 2]
+                                                        Div head_items, Div token_items, Div pairs) {
+  extern __shared__ float2 table[];  // [token][rot / 2], and behind it the pairs' turns
   using P = Pack<T, VEC>;
   const int t0 = (int)(blockIdx.x / splits) * tok_per_cta, nt = min(tok_per_cta, a.n_tok - t0);
   const int split = (int)(blockIdx.x % splits);
   const int heads = a.hq + a.hk, half = a.rot >> 1;
   const int h0 = (int)((int64_t)heads * split / splits), nh = (int)((int64_t)heads * (split + 1) / splits) - h0;
-  const int per_tok = nh * head_items, total = nt * per_tok;
+  const int total = nt * nh * (int)head_items.d;
+  uint64_t* turns = reinterpret_cast<uint64_t*>(table + tok_per_cta * half);
   bool have_table = false;
 
   for (int base = 0; base < total; base += kThreads * kItems) {
     P u[kItems], v[kItems];
     T* out[kItems];
-    int d0[kItems], d1[kItems], tok[kItems];
+    int d0[kItems], d1[kItems], tok[kItems], pos[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int it = base + i * kThreads + (int)threadIdx.x;
       tok[i] = -1;
       if (it >= total) continue;
-      const int tl = it / per_tok, rest = it - tl * per_tok, hl = rest / head_items, j = rest - hl * head_items;
+      // without splits a token's items are token_items.d
+      const int tl = splits == 1 ? (int)quotient(it, token_items) : 0, rest = it - tl * (int)token_items.d;
+      const int hl = (int)quotient(rest, head_items), j = rest - hl * (int)head_items.d;
       const int t = t0 + tl, h = h0 + hl;
       const bool is_k = h >= a.hq;
       const int64_t in_off = is_k ? t * a.k_stride + (int64_t)(h - a.hq) * a.head_dim : t * a.q_stride + (int64_t)h * a.head_dim;
@@ -76,7 +95,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
       const int64_t out_off =
           is_k ? t * a.k_out_stride + (int64_t)(h - a.hq) * a.head_dim : t * a.q_out_stride + (int64_t)h * a.head_dim;
       out[i] = static_cast<T*>(is_k ? a.k_out : a.q_out) + out_off;
-      tok[i] = a.pos[t] < 0 ? -1 : tl;  // padding is read like the rest, but not written
+      tok[i] = tl;
+      pos[i] = a.pos[t];  // looked at below: padding is read like the rest, but not written
       if (INTER) {
         d0[i] = 2 * j * VEC;
         d1[i] = d0[i] + VEC;
@@ -91,16 +111,18 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
       if (d1[i] < a.head_dim) v[i] = *reinterpret_cast<const P*>(in + d1[i]);
     }
     if (!have_table) {
+      for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn_of(a.freqs[i]);
+      __syncthreads();
       for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int tl = i / half, p = a.pos[t0 + tl];
-        if (p >= 0) table[i] = cos_sin_of(p, a.freqs[i - tl * half], a.scale);
+        const int tl = (int)quotient(i, pairs);
+        table[i] = cos_sin_of(a.pos[t0 + tl], turns[i - tl * half], a.scale);  // of padding: not used
       }
       __syncthreads();
       have_table = true;
     }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      if (tok[i] < 0) continue;
+      if (tok[i] < 0 || pos[i] < 0) continue;
       const float2* cs = table + tok[i] * half;
       if (!INTER) {
         if (d0[i] < half) {
@@ -157,9 +179,10 @@ cudaError_t launch_t(const RopeArgs& a, cudaStream_t st) {
   tok_per_cta = std::min(tok_per_cta, std::max(1, 16384 / (a.rot * 4)));
   int splits = 1;
   if (a.n_tok < 304) splits = std::max(1, std::min({heads, 304 / a.n_tok, (per_tok + kThreads - 1) / kThreads}));
-  const size_t smem = (size_t)tok_per_cta * (a.rot / 2) * sizeof(float2);
+  const size_t smem = (size_t)(tok_per_cta + 1) * (a.rot / 2) * sizeof(float2);
   const int64_t grid = (int64_t)((a.n_tok + tok_per_cta - 1) / tok_per_cta) * splits;
-  rope_kernel<T, VEC, INTER><<<(unsigned)grid, kThreads, smem, st>>>(a, tok_per_cta, splits, rot_items, head_items);
+  rope_kernel<T, VEC, INTER><<<(unsigned)grid, kThreads, smem, st>>>(a, tok_per_cta, splits, rot_items, div_by(head_items), div_by(per_tok),
+                                                                            div_by(a.rot / 2));
   return cudaGetLastError();
 }
 
