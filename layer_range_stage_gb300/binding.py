@@ -717,72 +717,90 @@ def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_
 # include/stage_step.h.  8-bit rows are torch.float8_e4m3fn tensors (or uint8 codes); like the 4-bit cache's entry points
 # these check types, shapes and devices.
 
-def _f8(t, what: str):
-    """(pointer, rows, columns, row stride) of 8-bit rows, which may lie apart."""
-    if t.dtype is not _torch.float8_e4m3fn and t.dtype is not _torch.uint8:
+# They are called several times per block, so they read each property of a tensor once.
+
+def _launch_on(stream, dev: int) -> int:
+    """The stream to launch on, for tensors that are all on device `dev`: the current one, since a launch goes there."""
+    if dev < 0:
+        _invalid("device tensors are needed, all on one device")
+    current = _torch._C._cuda_getDevice()
+    if dev != current:
+        _invalid(f"tensors on device {dev}, but the current one is {current}")
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _f8(t, shape, dev: int, what: str):
+    """(pointer, row stride) of 8-bit rows, which may lie apart."""
+    dt = t.dtype
+    if dt is not _torch.float8_e4m3fn and dt is not _torch.uint8:
         _invalid(f"{what} must be float8_e4m3fn (or uint8 codes)")
-    if t.dim() != 2:
-        _invalid(f"{what} must be a matrix")
-    n, k = t.shape
+    if t.shape != shape or t.get_device() != dev:
+        _invalid(f"{what} must be {list(shape)}, on the device of the others")
     s0, s1 = t.stride()
-    if k > 1 and s1 != 1:
+    if s1 != 1 and shape[1] > 1:
         _invalid(f"the columns of {what} must lie side by side")
-    return t.data_ptr(), n, k, s0 if n > 1 else -(-k // 16) * 16
+    return t.data_ptr(), s0 if shape[0] > 1 else -(-shape[1] // 16) * 16
 
 
-def _matrix(t, n: int, k: int, what: str):
+def _matrix(t, shape, dev: int, what: str):
     """(pointer, dtype, row stride) of rows [n, k] of a float type, which may lie apart."""
     dt = _KV4_DTYPE.get(t.dtype)
     if dt is None:
         _invalid(f"{what} must be float32, float16 or bfloat16")
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != k:
-        _invalid(f"{what} must be [{n}, {k}]")
+    if t.shape != shape or t.get_device() != dev:
+        _invalid(f"{what} must be {list(shape)}, on the device of the others")
     s0, s1 = t.stride()
-    if k > 1 and s1 != 1:
+    if s1 != 1 and shape[1] > 1:
         _invalid(f"the columns of {what} must lie side by side")
-    return t.data_ptr(), dt, s0 if n > 1 else k
+    return t.data_ptr(), dt, s0 if shape[0] > 1 else shape[1]
 
 
-def _scales(t, blocks: int, n: int, what: str):
+def _scales(t, shape, dev: int, what: str):
     """(pointer, stride) of float32 scales [blocks, n]."""
-    if t.dtype is not _torch.float32 or t.dim() != 2 or t.shape[0] != blocks or t.shape[1] != n:
-        _invalid(f"{what} must be float32 [{blocks}, {n}]")
+    if t.dtype is not _torch.float32 or t.shape != shape or t.get_device() != dev:
+        _invalid(f"{what} must be float32 {list(shape)}, on the device of the others")
     s0, s1 = t.stride()
-    if n > 1 and s1 != 1:
+    if s1 != 1 and shape[1] > 1:
         _invalid(f"the columns of {what} must lie side by side")
-    return t.data_ptr(), s0 if blocks > 1 else n
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+
+
+def _array(t, dtype, n: int, dev: int, what: str) -> int:
+    """Pointer of n entries side by side."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        _invalid(f"{what} must be a contiguous {dtype} tensor of {n} entries, on the device of the others")
+    return t.data_ptr()
 
 
 def stage_op_norm_f8(x, q=None, scale=None, gamma=None, eps: float = 1e-5, resid=None, resid_out=None, y=None, stream=None) -> None:
     """Rows x [n_tok, n] plus resid (if given; the sum goes to resid_out, which may be resid), RMS norm with gamma (float32 [n]; None:
     no norm), as 8-bit rows q [n_tok, n] with scales [ceil(n / 128), n_tok] and/or as rows y of x's type."""
-    _torch or _load_torch()
-    if x.dim() != 2:
+    torch = _torch or _load_torch()
+    shape, dev = x.shape, x.get_device()
+    if len(shape) != 2:
         _invalid("x must be [n_tok, n]")
     if (resid is None) != (resid_out is None) or (q is None) != (scale is None):
         _invalid("resid and resid_out go together, and so do q and scale")
-    stream = _kv4_launch(stream, x, *[t for t in (q, scale, gamma, resid, resid_out, y) if t is not None])
-    n_tok, n = x.shape
-    xp, xt, xs = _matrix(x, n_tok, n, "x")
+    stream = _launch_on(stream, dev)
+    n_tok, n = shape
+    xp, xt, xs = _matrix(x, shape, dev, "x")
+    gp = None
     rp = rt = rs = op = os_ = qp = qs = sp = ss = yp = ys = 0
     if resid is not None:
-        rp, rt, rs = _matrix(resid, n_tok, n, "resid")
-        op, ot, os_ = _matrix(resid_out, n_tok, n, "resid_out")
+        rp, rt, rs = _matrix(resid, shape, dev, "resid")
+        op, ot, os_ = _matrix(resid_out, shape, dev, "resid_out")
         if ot != rt:
             _invalid("resid and resid_out must have one type")
-    if gamma is not None and (gamma.dtype is not _torch.float32 or gamma.numel() != n or not gamma.is_contiguous()):
-        _invalid(f"gamma must be a contiguous float32 tensor of {n} entries")
+    if gamma is not None:
+        gp = _array(gamma, torch.float32, n, dev, "gamma")
     if q is not None:
-        qp, qn, qk, qs = _f8(q, "q")
-        if qn != n_tok or qk != n:
-            _invalid(f"q must be [{n_tok}, {n}]")
-        sp, ss = _scales(scale, (n + 127) // 128, n_tok, "scale")
+        qp, qs = _f8(q, shape, dev, "q")
+        sp, ss = _scales(scale, ((n + 127) // 128, n_tok), dev, "scale")
     if y is not None:
-        yp, yt, ys = _matrix(y, n_tok, n, "y")
+        yp, yt, ys = _matrix(y, shape, dev, "y")
         if yt != xt:
             _invalid("y must have x's type")
-    rc = (_lib or lib()).stage_op_norm_f8(xp, xt, xs, rp, rt, rs, op, os_, None if gamma is None else gamma.data_ptr(), eps, n_tok, n,
-                                          qp, qs, sp, ss, yp, ys, stream)
+    rc = (_lib or lib()).stage_op_norm_f8(xp, xt, xs, rp, rt, rs, op, os_, gp, eps, n_tok, n, qp, qs, sp, ss, yp, ys, stream)
     if rc:
         _opcheck(rc)
 
@@ -792,18 +810,21 @@ def stage_op_f8_gemm(a, a_scale, w, w_scale, out, error=None, stream=None) -> No
     scales a_scale [ceil(K / 128), M] and w_scale [ceil(N / 128), ceil(K / 128)]; error: int32 [1], set to 1 once a call has
     given up waiting (what misses something is NaN)."""
     torch = _torch or _load_torch()
-    stream = _kv4_launch(stream, a, a_scale, w, w_scale, out) if error is None else _kv4_launch(stream, a, a_scale, w, w_scale, out, error)
-    ap, m, k, as_ = _f8(a, "a")
-    wp, n, wk, ws = _f8(w, "w")
-    if wk != k:
-        _invalid("a and w must have one number of columns")
+    sa, sw, dev = a.shape, w.shape, a.get_device()
+    if len(sa) != 2 or len(sw) != 2 or sa[1] != sw[1]:
+        _invalid("a must be [M, K] and w [N, K]")
+    stream = _launch_on(stream, dev)
+    m, k = sa
+    n = sw[0]
     kb = (k + 127) // 128
-    sp, ss = _scales(a_scale, kb, m, "a_scale")
-    if w_scale.dtype is not torch.float32 or w_scale.shape != ((n + 127) // 128, kb) or not w_scale.is_contiguous():
-        _invalid(f"w_scale must be contiguous float32 [{(n + 127) // 128}, {kb}]")
-    yp, yt, ys = _matrix(out, m, n, "out")
+    ap, as_ = _f8(a, sa, dev, "a")
+    wp, ws = _f8(w, sw, dev, "w")
+    sp, ss = _scales(a_scale, (kb, m), dev, "a_scale")
+    if w_scale.dtype is not torch.float32 or w_scale.shape != ((n + 127) // 128, kb) or not w_scale.is_contiguous() or w_scale.get_device() != dev:
+        _invalid(f"w_scale must be contiguous float32 [{(n + 127) // 128}, {kb}], on the device of the others")
+    yp, yt, ys = _matrix(out, (m, n), dev, "out")
     rc = (_lib or lib()).stage_op_f8_gemm(ap, as_, sp, ss, wp, ws, w_scale.data_ptr(), m, n, k, yp, yt, ys,
-                                          None if error is None else _i32dev(error, "error", 1), stream)
+                                          None if error is None else _array(error, torch.int32, 1, dev, "error"), stream)
     if rc:
         _opcheck(rc)
 
@@ -824,39 +845,46 @@ def stage_op_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = STA
     return f, scale.value
 
 
+def _heads(t, n_tok: int, d: int, dt: int, dev: int, what: str):
+    """(pointer, row stride, heads) of rows [n_tok, heads, d] whose heads lie side by side."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n_tok or shape[2] != d or _KV4_DTYPE.get(t.dtype) != dt or t.get_device() != dev:
+        _invalid(f"{what} must be [{n_tok}, heads, {d}], of q's type and on its device")
+    heads = shape[1]
+    s0, s1, s2 = t.stride()
+    if n_tok and (s2 != 1 or (s1 != d and heads > 1)):
+        _invalid(f"the heads of a row of {what} must lie side by side")
+    return t.data_ptr(), s0 if n_tok > 1 else heads * d, heads
+
+
 def stage_op_rope(q, k, pos, freqs, q_out=None, k_out=None, interleaved: bool = False, scale: float = 1.0, stream=None) -> None:
     """Rotary positions of the heads q [n_tok, n_q_heads, head_dim] and k [n_tok, n_k_heads, head_dim] (or None) at pos (int32 [n_tok];
     negative: padding, not written) with freqs (float64 [rot_dim / 2], radians per position), into q_out and k_out (default: in
     place).  Rows may lie apart; the heads of a row lie side by side."""
     torch = _torch or _load_torch()
-    if q_out is None:
-        q_out = q
-    if k_out is None:
-        k_out = k
-    if (k is None) != (k_out is None):
-        _invalid("k_out without k")
-    stream = _kv4_launch(stream, q, q_out, pos, freqs) if k is None else _kv4_launch(stream, q, q_out, pos, freqs, k, k_out)
-    if q.dim() != 3:
-        _invalid("q must be [n_tok, n_q_heads, head_dim]")
-    n_tok, hq, d = q.shape
-    qp, qt, qs = _rows(q, hq, d, "q")
-    qop, qot, qos = _rows(q_out, hq, d, "q_out")
+    shape, dt, dev = q.shape, _KV4_DTYPE.get(q.dtype), q.get_device()
+    if len(shape) != 3 or dt is None:
+        _invalid("q must be [n_tok, n_q_heads, head_dim], float32, float16 or bfloat16")
+    stream = _launch_on(stream, dev)
+    n_tok, _, d = shape
+    qp, qs, hq = qop, qos, _ = _heads(q, n_tok, d, dt, dev, "q")
     kp = ks = kop = kos = hk = 0
-    kt = kot = qt
+    if q_out is not None:
+        qop, qos, h = _heads(q_out, n_tok, d, dt, dev, "q_out")
+        if h != hq:
+            _invalid("q_out must have q's heads")
     if k is not None:
-        if k.dim() != 3:
-            _invalid("k must be [n_tok, n_k_heads, head_dim]")
-        hk = k.shape[1]
-        kp, kt, ks = _rows(k, hk, d, "k")
-        kop, kot, kos = _rows(k_out, hk, d, "k_out")
-        if k.shape[0] != n_tok or k_out.shape[0] != n_tok:
-            _invalid("q and k must have one number of tokens")
-    if q_out.shape[0] != n_tok or not qt == qot == kt == kot:
-        _invalid("q, k and their outputs must have one type and number of tokens")
-    if freqs.dtype is not torch.float64 or not freqs.is_contiguous():
-        _invalid("freqs must be a contiguous float64 tensor")
-    rc = (_lib or lib()).stage_op_rope(qp, qs, hq, kp, ks, hk, d, qt, _i32dev(pos, "pos", n_tok), n_tok, freqs.data_ptr(),
-                                       2 * freqs.numel(), int(bool(interleaved)), scale, qop, qos, kop, kos, stream)
+        kp, ks, hk = kop, kos, _ = _heads(k, n_tok, d, dt, dev, "k")
+        if k_out is not None:
+            kop, kos, h = _heads(k_out, n_tok, d, dt, dev, "k_out")
+            if h != hk:
+                _invalid("k_out must have k's heads")
+    elif k_out is not None:
+        _invalid("k_out without k")
+    half = freqs.numel()
+    rc = (_lib or lib()).stage_op_rope(qp, qs, hq, kp, ks, hk, d, dt, _array(pos, torch.int32, n_tok, dev, "pos"), n_tok,
+                                       _array(freqs, torch.float64, half, dev, "freqs"), 2 * half, 1 if interleaved else 0, scale, qop,
+                                       qos, kop, kos, stream)
     if rc:
         _opcheck(rc)
 
@@ -865,25 +893,33 @@ def stage_op_logprobs(logits, tokens=None, logprob=None, entropy=None, rank=None
     """From rows of logits [n, vocab] (which may lie apart): logprob (float32 [n]) and rank (int32 [n]) of tokens (int32 [n]), entropy
     (float32 [n]), and the k likeliest tokens top_ids (int32 [n, k]) with top_logprobs (float32 [n, k]); each may be None."""
     torch = _torch or _load_torch()
-    stream = _kv4_launch(stream, logits, *[t for t in (tokens, logprob, entropy, rank, top_ids, top_logprobs) if t is not None])
-    if logits.dim() != 2:
+    shape, dev = logits.shape, logits.get_device()
+    if len(shape) != 2:
         _invalid("logits must be [n, vocab]")
-    n, vocab = logits.shape
-    zp, zt, zs = _matrix(logits, n, vocab, "logits")
+    stream = _launch_on(stream, dev)
+    n, vocab = shape
+    zp, zt, zs = _matrix(logits, shape, dev, "logits")
     i32, f32 = torch.int32, torch.float32
-    for t, dt, what in ((tokens, i32, "tokens"), (logprob, f32, "logprob"), (entropy, f32, "entropy"), (rank, i32, "rank")):
-        if t is not None and (t.dtype is not dt or t.numel() != n or not t.is_contiguous()):
-            _invalid(f"{what} must be a contiguous {dt} tensor of {n} entries")
+    tp = lp = ep = rp = ip = bp = None
+    if tokens is not None:
+        tp = _array(tokens, i32, n, dev, "tokens")
+    if logprob is not None:
+        lp = _array(logprob, f32, n, dev, "logprob")
+    if entropy is not None:
+        ep = _array(entropy, f32, n, dev, "entropy")
+    if rank is not None:
+        rp = _array(rank, i32, n, dev, "rank")
     top = 0
-    for t, dt, what in ((top_ids, i32, "top_ids"), (top_logprobs, f32, "top_logprobs")):
-        if t is None:
-            continue
-        if t.dtype is not dt or t.dim() != 2 or t.shape[0] != n or not t.is_contiguous():
-            _invalid(f"{what} must be a contiguous {dt} tensor [{n}, k]")
-        if t is top_logprobs and top_ids is not None and t.shape[1] != top:
-            _invalid("top_ids and top_logprobs must have one shape")
-        top = t.shape[1]
-    p = [None if t is None else t.data_ptr() for t in (tokens, logprob, entropy, rank, top_ids, top_logprobs)]
-    rc = (_lib or lib()).stage_op_logprobs(zp, zt, zs, n, vocab, p[0], p[1], p[2], p[3], top, p[4], p[5], stream)
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != n:
+            _invalid(f"top_ids must be [{n}, k]")
+        top = top_ids.shape[1]
+        ip = _array(top_ids, i32, n * top, dev, "top_ids")
+    if top_logprobs is not None:
+        if top_logprobs.dim() != 2 or top_logprobs.shape[0] != n or (top_ids is not None and top_logprobs.shape[1] != top):
+            _invalid(f"top_logprobs must be [{n}, k], k that of top_ids")
+        top = top_logprobs.shape[1]
+        bp = _array(top_logprobs, f32, n * top, dev, "top_logprobs")
+    rc = (_lib or lib()).stage_op_logprobs(zp, zt, zs, n, vocab, tp, lp, ep, rp, top, ip, bp, stream)
     if rc:
         _opcheck(rc)

@@ -5,9 +5,9 @@
 //
 // The likeliest tokens: the row is cut into chunks of 32 bytes, a thread's load, and a chunk's largest logit (which the running
 // maximum needs anyway) is kept in shared memory.  The n_top first tokens lie in the n_top chunks that come first in the same order
-// by their largest logit, and those in the n_top threads that come first by theirs: a search over the bits of a threshold, a
-// barrier that counts per bit, finds a bound that few threads reach; their chunks above it are ranked by counting, and only
-// the n_top first are read again.
+// by their largest logit, and those in the n_top threads that come first by theirs.  The n_top-th of the largest of groups of eight
+// threads is a bound that few other threads reach (where more do, a search over its bits, a barrier that counts per bit, finds
+// one); their chunks above it are ranked by counting, and only the n_top first are read again.
 //
 // Few rows are split over a cluster's CTAs, whose parts meet in the first one's shared memory.
 #include <algorithm>
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kTop = 32, kMaxCluster = 8;
 constexpr int kMaxChunks = 16384;  // of a CTA: their maxima take 64 KB
-constexpr int kSlack = 8;          // threads above the bound beyond the n_top that are needed, at most
+constexpr int kSlack = 16;         // threads above the bound beyond the n_top that are needed, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // a NaN wins
@@ -50,17 +50,26 @@ __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(
 struct Sums {
   float ref, s, t;  // with d = (z - ref) log2 e: the sums of 2^d and of 2^d d; ref = -inf: nothing yet
 };
-__device__ __forceinline__ Sums merge(Sums a, Sums b) {
-  if (b.ref > a.ref) {
-    const Sums c = a;
-    a = b;
-    b = c;
+// The sums of 2 * FROM neighbouring lanes, in all of them: brought to the largest reference first, then added up.
+template <int FROM>
+__device__ __forceinline__ Sums merge_lanes(Sums m) {
+  float ref = m.ref;
+#pragma unroll
+  for (int o = FROM; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+  if (m.ref == -INFINITY) {
+    m.s = m.t = 0.f;  // nothing, or nothing but masked tokens
+  } else {
+    const float d = fmaxf((m.ref - ref) * kLog2e, -1000.f), f = ex2(d);
+    m.t = f * fmaf(d, m.s, m.t);
+    m.s *= f;  // a NaN stays in them
   }
-  if (b.ref == -INFINITY) return a;
-  const float d = (b.ref - a.ref) * kLog2e, f = ex2(d);  // a NaN in either's sums stays in them
-  a.s += f * b.s;
-  a.t += f > 0.f ? f * (b.t + d * b.s) : 0.f * b.s;
-  return a;
+  m.ref = ref;
+#pragma unroll
+  for (int o = FROM; o > 0; o >>= 1) {
+    m.s += __shfl_xor_sync(0xffffffffu, m.s, o);
+    m.t += __shfl_xor_sync(0xffffffffu, m.t, o);
+  }
+  return m;
 }
 
 template <typename T>
@@ -75,6 +84,7 @@ struct Shared {
   Sums all;
   int above_all;
   int n_chunks, n_cand;
+  uint64_t first_bound;    // 0: none
   uint32_t best_chunk[kTop];
   float bound;             // the last of these chunks' largest logit
   uint64_t list[kTop];     // this CTA's first tokens in order: (ordered logit, ~index)
@@ -88,10 +98,7 @@ __device__ __forceinline__ void load_chunk(const T* z, int off, int vocab, int c
   constexpr int E = 32 / sizeof(T);
   const int e0 = c * E - off;
   if (e0 >= 0 && e0 + E <= vocab) {
-    const uint4* src = reinterpret_cast<const uint4*>(z + e0);
-    uint4* dst = reinterpret_cast<uint4*>(&p);
-    dst[0] = ld_stream_u4(src);
-    dst[1] = ld_stream_u4(src + 1);
+    ld_stream_32(z + e0, reinterpret_cast<uint32_t(&)[8]>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i) p.v[i] = e0 + i >= 0 && e0 + i < vocab ? z[e0 + i] : from_f32<T>(-INFINITY);
@@ -144,6 +151,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
   const int t = a.tokens ? a.tokens[row] : -1;
   const bool given = t >= 0 && t < a.vocab;
   const float zt = given ? to_f32(z[t]) : INFINITY;
+  // the next float above zt (of -inf: the lowest number; of the two zeros: the smallest one)
+  const float above_zt = unordered(ordered(zt) + 1);
   Sums m{-INFINITY, 0.f, 0.f};
   int above = 0;
   uint64_t mine = 0;  // the thread's best chunk: (ordered maximum, ~chunk)
@@ -165,10 +174,16 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
       }
       if (top >= zt) {
         const int e0 = (c0 + c) * E - off;
+        if (e0 > t || (e0 >= 0 && e0 + E <= t)) {  // all of the chunk lies on one side of the token: >= before it, > behind
+          const float least = e0 > t ? above_zt : zt;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float f = to_f32(p[u].v[i]);
-          above += f > zt || (f == zt && e0 + i >= 0 && e0 + i < t) ? 1 : 0;
+          for (int i = 0; i < E; ++i) above += to_f32(p[u].v[i]) >= least;
+        } else {
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const float f = to_f32(p[u].v[i]);
+            above += f > zt || (f == zt && e0 + i >= 0 && e0 + i < t) ? 1 : 0;
+          }
         }
       }
       if (top == -INFINITY) continue;
@@ -194,15 +209,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
       m.t = td.x + td.y;
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.ref = __shfl_down_sync(0xffffffffu, m.ref, o);
-    b.s = __shfl_down_sync(0xffffffffu, m.s, o);
-    b.t = __shfl_down_sync(0xffffffffu, m.t, o);
-    m = merge(m, b);
-    above += __shfl_down_sync(0xffffffffu, above, o);
-  }
+  m = merge_lanes<16>(m);
+  above = __reduce_add_sync(0xffffffffu, above);
   if (lane == 0) {
     sh.sums[warp] = m;
     sh.above[warp] = above;
@@ -217,15 +225,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
       s = sh.sums[lane];
       n = sh.above[lane];
     }
-#pragma unroll
-    for (int o = NT / 64; o > 0; o >>= 1) {
-      Sums b;
-      b.ref = __shfl_down_sync(0xffffffffu, s.ref, o);
-      b.s = __shfl_down_sync(0xffffffffu, s.s, o);
-      b.t = __shfl_down_sync(0xffffffffu, s.t, o);
-      s = merge(s, b);
-      n += __shfl_down_sync(0xffffffffu, n, o);
-    }
+    s = merge_lanes<NT / 64>(s);
+    n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) {
       sh.all = s;
       sh.above_all = n;
@@ -233,15 +234,34 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
   }
   if (TOP && nc > 0) {
     uint64_t* chunk_list = reinterpret_cast<uint64_t*>(maxima + (chunks_per_cta + 1) / 2 * 2);
-    // a bound that at least min(n_top, threads with a chunk) threads' best chunks reach, and few more
+    // a bound that at least min(n_top, threads with a chunk) threads' best chunks reach, and few more: the n_top-th of the groups'
+    // of eight threads first ...
+    uint64_t group = mine;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) group = max(group, __shfl_xor_sync(0xffffffffu, group, o));
+    if ((tid & 7) == 0) sh.cand[tid >> 3] = group;
+    if (tid == 0) sh.first_bound = 0;
+    __syncthreads();
     const int want = min(a.top, min(nc, NT));
-    uint64_t bound = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t b = bound | 1ull << bit;
-      const int n = __syncthreads_count(mine >= b);
-      if (n >= want) {
-        bound = b;
-        if (n <= want + kSlack) break;
+    if (tid < NT / 8) {
+      const uint64_t key = sh.cand[tid];
+      int before = 0;
+#pragma unroll 8
+      for (int j = 0; j < NT / 8; ++j) before += sh.cand[j] > key;
+      if (key && before == want - 1) sh.first_bound = key;
+    }
+    __syncthreads();
+    uint64_t bound = sh.first_bound;
+    const int reach = __syncthreads_count(mine >= bound);
+    if (bound == 0 || reach > a.top + kSlack) {  // ... or bit by bit, where too many reach that, or there are fewer groups
+      bound = 0;
+      for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t b = bound | 1ull << bit;
+        const int n = __syncthreads_count(mine >= b);
+        if (n >= want) {
+          bound = b;
+          if (n <= want + kSlack) break;
+        }
       }
     }
     if (mine && mine >= bound) {
@@ -304,19 +324,11 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
           o = at->all;
           k = at->above_all;
         }
-#pragma unroll
-        for (int d = kMaxCluster / 2; d > 0; d >>= 1) {
-          Sums b;
-          b.ref = __shfl_down_sync(0xffffffffu, o.ref, d);
-          b.s = __shfl_down_sync(0xffffffffu, o.s, d);
-          b.t = __shfl_down_sync(0xffffffffu, o.t, d);
-          o = merge(o, b);
-          k += __shfl_down_sync(0xffffffffu, k, d);
-        }
-        s.ref = __shfl_sync(0xffffffffu, o.ref, 0);
-        s.s = __shfl_sync(0xffffffffu, o.s, 0);
-        s.t = __shfl_sync(0xffffffffu, o.t, 0);
-        n = __shfl_sync(0xffffffffu, k, 0);
+        s = merge_lanes<kMaxCluster / 2>(o);
+        s.ref = __shfl_sync(0xffffffffu, s.ref, 0);
+        s.s = __shfl_sync(0xffffffffu, s.s, 0);
+        s.t = __shfl_sync(0xffffffffu, s.t, 0);
+        n = __reduce_add_sync(0xffffffffu, k);
       }
       const float ls = log2f(s.s);
       const bool bad = !(s.s > 0.f) || !(s.ref < INFINITY);
@@ -370,7 +382,7 @@ cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t st) {
   constexpr int E = 32 / sizeof(T);
   const int chunks = (a.vocab + E - 1) / E + 1;  // a row that begins inside a chunk has one more
   int C = 1;
-  while (C < kMaxCluster && ((chunks + C - 1) / C > kMaxChunks || (a.rows * (int64_t)C < 304 && chunks / C >= 1024))) C *= 2;
+  while (C < kMaxCluster && ((chunks + C - 1) / C > kMaxChunks || (a.rows * (int64_t)C <= 152 && chunks / C >= 1024))) C *= 2;
   const int per = (chunks + C - 1) / C;
   // one row's latency counts where a cluster shares it: more threads, each with fewer loads after one another
   if (C > 1) return launch_k<T, TOP, 512, 4>(a, C, per, st);

@@ -8,6 +8,7 @@
 // A row is read and written once: the bytes bound it.  A CTA makes its tokens' table of cos and sin in
 // shared memory while its first loads are in flight, and every head of the token uses it.
 #include <algorithm>
+#include <cstring>
 
 #include "common.cuh"
 #include "step.cuh"
@@ -16,12 +17,33 @@ namespace lrs {
 
 namespace {
 
-constexpr int kThreads = 256, kItems = 4;  // items of a thread, all loaded before the table is waited for
+constexpr int kThreads = 256, kItems = 2;  // items of a thread, all loaded before the table is waited for
 
+// VEC elements as the words that they lie in: taken apart where they are loaded, a thread's loads would wait for one another.
 template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-  T v[VEC];
+struct Words {
+  uint4 q;
 };
+template <typename T>
+struct Words<T, 1> {
+  T q;
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void take_apart(const Words<T, VEC>& w, float (&f)[VEC]) {
+  T v[VEC];
+  memcpy(v, &w, sizeof(v));
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = to_f32(v[i]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Words<T, VEC> put_together(const float (&f)[VEC]) {
+  T v[VEC];
+  Words<T, VEC> w;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] = from_f32<T>(f[i]);
+  memcpy(&w, v, sizeof(v));
+  return w;
+}
 
 // f / 2 pi as a 64-bit fraction of a turn
 __device__ __forceinline__ uint64_t turn_of(double f) {
@@ -64,10 +86,10 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, Div v) { return v.d == 
 // An item is two vectors of VEC elements of one head: the halves' parts of VEC pairs, or (interleaved, and dims that are
 // only copied) two neighbouring vectors.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tok_per_cta, int splits, int rot_items,
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, int tok_per_cta, int splits, int rot_items,
                                                         Div head_items, Div token_items, Div pairs) {
   extern __shared__ float2 table[];  // [token][rot / 2], and behind it the pairs' turns
-  using P = Pack<T, VEC>;
+  using P = Words<T, VEC>;
   const int t0 = (int)(blockIdx.x / splits) * tok_per_cta, nt = min(tok_per_cta, a.n_tok - t0);
   const int split = (int)(blockIdx.x % splits);
   const int heads = a.hq + a.hk, half = a.rot >> 1;
@@ -124,39 +146,36 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
     for (int i = 0; i < kItems; ++i) {
       if (tok[i] < 0 || pos[i] < 0) continue;
       const float2* cs = table + tok[i] * half;
-      if (!INTER) {
-        if (d0[i] < half) {
+      float x[VEC], y[VEC];
+      if (!INTER || VEC == 1) {  // the pairs are across the two vectors
+        if (d0[i] < (INTER ? a.rot : half)) {
+          take_apart<T, VEC>(u[i], x);
+          take_apart<T, VEC>(v[i], y);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float2 w = cs[d0[i] + e];
-            const float x = to_f32(u[i].v[e]), y = to_f32(v[i].v[e]);
-            u[i].v[e] = from_f32<T>(x * w.x - y * w.y);
-            v[i].v[e] = from_f32<T>(y * w.x + x * w.y);
+            const float2 w = cs[INTER ? d0[i] >> 1 : d0[i] + e];
+            const float h = x[e];
+            x[e] = h * w.x - y[e] * w.y;
+            y[e] = y[e] * w.x + h * w.y;
           }
-        }
-      } else if (VEC == 1) {  // a pair is the two vectors
-        if (d0[i] < a.rot) {
-          const float2 w = cs[d0[i] >> 1];
-          const float x = to_f32(u[i].v[0]), y = to_f32(v[i].v[0]);
-          u[i].v[0] = from_f32<T>(x * w.x - y * w.y);
-          v[i].v[0] = from_f32<T>(y * w.x + x * w.y);
+          u[i] = put_together<T, VEC>(x);
+          v[i] = put_together<T, VEC>(y);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) {
-          constexpr int kHi = VEC > 1 ? 1 : 0;
-          if (d0[i] < a.rot) {
-            const float2 w = cs[(d0[i] + e) >> 1];
-            const float x = to_f32(u[i].v[e]), y = to_f32(u[i].v[e + kHi]);
-            u[i].v[e] = from_f32<T>(x * w.x - y * w.y);
-            u[i].v[e + kHi] = from_f32<T>(y * w.x + x * w.y);
+        for (int part = 0; part < 2; ++part) {
+          const int d = part ? d1[i] : d0[i];
+          if (d >= a.rot) continue;
+          take_apart<T, VEC>(part ? v[i] : u[i], x);
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) {
+            constexpr int kHi = VEC > 1 ? 1 : 0;
+            const float2 w = cs[(d + e) >> 1];
+            const float h = x[e];
+            x[e] = h * w.x - x[e + kHi] * w.y;
+            x[e + kHi] = x[e + kHi] * w.x + h * w.y;
           }
-          if (d1[i] < a.rot) {
-            const float2 w = cs[(d1[i] + e) >> 1];
-            const float x = to_f32(v[i].v[e]), y = to_f32(v[i].v[e + kHi]);
-            v[i].v[e] = from_f32<T>(x * w.x - y * w.y);
-            v[i].v[e + kHi] = from_f32<T>(y * w.x + x * w.y);
-          }
+          (part ? v[i] : u[i]) = put_together<T, VEC>(x);
         }
       }
       *reinterpret_cast<P*>(out[i] + d0[i]) = u[i];
