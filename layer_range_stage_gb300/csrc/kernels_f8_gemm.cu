@@ -147,7 +147,7 @@ __device__ __forceinline__ void store_rows(const float2 (&acc)[COLS / 2], unsign
 }
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     f8_gemm_kernel(const F8GemmArgs a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB) {
   using G = Big;
   constexpr int kHalf = kBN / 2;
@@ -158,9 +158,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   cg::cluster_group cluster = cg::this_cluster();
-  const uint32_t rank = cluster.block_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles_m = (a.M + kBM - 1) / kBM, tiles = tiles_m * ((a.N + kBN - 1) / kBN), nkb = a.nkb;
+  // S pairs of a cluster share a tile's K blocks; more than one only where a cluster has one tile
+  const uint32_t crank = cluster.block_rank(), rank = crank & 1, first = crank & ~1u;
+  const int S = (int)cluster.num_blocks() >> 1, share = (int)crank >> 1;
+  const int pair = (int)(blockIdx.x >> 1) / S, pairs = (int)(gridDim.x >> 1) / S;
+  const int tiles_m = (a.M + kBM - 1) / kBM, tiles = tiles_m * ((a.N + kBN - 1) / kBN);
+  const int kb0 = (int)((int64_t)a.nkb * share / S), nkb = (int)((int64_t)a.nkb * (share + 1) / S) - kb0;
 
   if (tid == 0) {
     for (int i = 0; i < G::kStages; ++i) {
@@ -195,10 +198,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % G::kStages;
           if (it >= G::kStages && !(ok = fwait(&B->empty[s], (uint32_t)(it / G::kStages + 1) & 1u, abort_flag, a.error))) break;
-          const uint32_t bar = at_rank(&B->full[s], 0);  // the first CTA's counts both CTAs' bytes
+          const uint32_t bar = at_rank(&B->full[s], first);  // the first CTA's counts both CTAs' bytes
           if (rank == 0) mbar_arrive_expect_tx(&B->full[s], 2 * G::kStage);
-          tma_load_2d_pair(sm + s * G::kStage, &tA, kb * kBK, m0, bar);
-          tma_load_2d_pair(sm + s * G::kStage + G::kTileA, &tB, kb * kBK, n0, bar);
+          tma_load_2d_pair(sm + s * G::kStage, &tA, (kb0 + kb) * kBK, m0, bar);
+          tma_load_2d_pair(sm + s * G::kStage + G::kTileA, &tB, (kb0 + kb) * kBK, n0, bar);
         }
       }
       if (*abort_flag) {  // nothing may still be landing in shared memory when the CTA leaves
@@ -224,11 +227,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk)
             umma_f8_pair(tmem + d * kBN, desc_sw128(pa + kk * 32), desc_sw128(pb + kk * 32), idesc, kk > 0);
-          umma_commit_pair(&B->empty[s]);
-          umma_commit_pair(&B->done[d]);
+          umma_commit_pair(&B->empty[s], first);
+          umma_commit_pair(&B->done[d], first);
         }
       if (!ok && it > 0) {  // given up: the products already issued finish before TMEM is released
-        umma_commit_pair(&B->drain);
+        umma_commit_pair(&B->drain, first);
         mbar_wait(&B->drain, 0u, kDrainNs);
       }
     }
@@ -237,14 +240,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp >> 2) - 1;
     const uint32_t lane_tmem = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(half * kHalf);
     unsigned char* stg = sm + G::kOffOut + (warp - 4) * 4096;
-    const uint32_t free0 = at_rank(&B->free_[0], 0), free1 = at_rank(&B->free_[1], 0);
+    const uint32_t free0 = at_rank(&B->free_[0], first), free1 = at_rank(&B->free_[1], first);
     int it = 0;
     bool ok = true;
     for (int tile = pair; tile < tiles; tile += pairs) {
       const int m0 = tile % tiles_m * kBM + 128 * rank, n0 = tile / tiles_m * kBN;
       const int row0 = m0 + 32 * quarter, col0 = n0 + half * kHalf;
-      const float* sa = a.sa + min(row0 + lane, a.M - 1);
-      const float* sw = a.sw + (int64_t)min(col0 >> 7, (a.N - 1) >> 7) * nkb;
+      const float* sa = a.sa + (int64_t)kb0 * a.sa_stride + min(row0 + lane, a.M - 1);
+      const float* sw = a.sw + (int64_t)min(col0 >> 7, (a.N - 1) >> 7) * a.nkb + kb0;
       float2 acc[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -284,7 +287,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 16 / 2; ++i) fma2(acc[c * (16 / 2) + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], f);
         }
       }
-      store_rows<kHalf, T>(acc, stg, a, row0, col0, ok);
+      if (S == 1) {
+        store_rows<kHalf, T>(acc, stg, a, row0, col0, ok);
+      } else {  // the stages' place is free: every copy and product of the tile is done
+        float4* row = reinterpret_cast<float4*>(sm) + (32 * quarter + lane) * (kBN / 4);
+#pragma unroll
+        for (int i = 0; i < kHalf / 4; ++i) {
+          const float2 p = unpack2(acc[2 * i]), q = unpack2(acc[2 * i + 1]);
+          row[(half * (kHalf / 4) + i) ^ lane] = make_float4(p.x, p.y, q.x, q.y);
+        }
+      }
+    }
+  }
+  if (S > 1) {  // each CTA adds up its share of its half's rows, the pairs' sums in their order
+    __syncthreads();
+    cluster.sync();
+    bool whole = true;
+    for (int j = 0; j < 2 * S; ++j) whole = whole && !*cluster.map_shared_rank(const_cast<int*>(abort_flag), j);
+    const int m0 = pair % tiles_m * kBM + 128 * rank, n0 = pair / tiles_m * kBN;
+    T* y = static_cast<T*>(a.y);
+    for (int e = tid; e < 128 / S * (kBN / 4); e += kThreads) {
+      const int r = 128 / S * share + e / (kBN / 4), u = e % (kBN / 4), gm = m0 + r, gn = n0 + 4 * u;
+      if (gm >= a.M || gn >= a.N) continue;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < S; ++j) {
+        const float4 p = cluster.map_shared_rank(reinterpret_cast<float4*>(sm), 2 * j + rank)[r * (kBN / 4) + (u ^ (r & 31))];
+        v[0] += p.x;
+        v[1] += p.y;
+        v[2] += p.z;
+        v[3] += p.w;
+      }
+      union {
+        T t[4];
+        uint2 h;
+        uint4 q;
+      } o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o.t[i] = from_f32<T>(whole ? v[i] : __int_as_float(0x7FC00000));
+      T* dst = y + (int64_t)gm * a.y_stride + gn;
+      if (a.vec && gn + 4 <= a.N) {
+        if (sizeof(T) == 4)
+          *reinterpret_cast<uint4*>(dst) = o.q;
+        else
+          *reinterpret_cast<uint2*>(dst) = o.h;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (gn + i < a.N) dst[i] = o.t[i];
+      }
     }
   }
   tc_fence_before();
@@ -602,10 +652,23 @@ cudaError_t launch_big(const F8GemmArgs& a, cudaStream_t st) {
       !encode_2d(&tB, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.w_stride, kBK, 128,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  static_assert(G::kStages * G::kStage >= 128 * kBN * 4, "the sums take the stages' place");
   const int64_t tiles = (int64_t)((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
-  const int grid = 2 * (int)std::min<int64_t>(tiles, std::max(1, sm_count() / 2));
-  f8_gemm_kernel<T><<<grid, kThreads, G::kSmem, st>>>(a, tA, tB);
-  return cudaGetLastError();
+  // few tiles: two pairs share one's K (256 x 4096 x 14336, 16 tiles: 38 us, 60 with one; with four pairs, whose clusters of eight SMs do
+  // not all find a place at once, 48)
+  const int S = 2 * tiles <= 64 && a.nkb >= 8 ? 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * S * (unsigned)std::min<int64_t>(tiles, std::max(1, sm_count() / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = G::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<T>, a, tA, tB);
 }
 
 template <int NT, typename T>
@@ -644,13 +707,16 @@ cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_t(const F8GemmArgs& a, cudaStream_t st) {
   if (!a.stall) {  // (the tests' stalled calls go where there is something to wait for)
+    // (8 rows, 57344 x 8192: 72 us, 89 by weight tiles; 16 rows: 92 and 89, but 9.5 and 13 with 6144 x 4096; 32 rows: 220 and 84)
     if (a.M <= 8) return launch_few<1, 2, T>(a, st);
     if (a.M <= 16) return launch_few<2, 2, T>(a, st);
   }
   if (a.M <= 16) return launch_small<16, T>(a, st);
   if (a.M <= 32) return launch_small<32, T>(a, st);
   if (a.M <= 64) return launch_small<64, T>(a, st);
-  if (a.M <= 128) return launch_small<128, T>(a, st);
+  // up to 128 rows by weight tiles only where few of them share K among eight CTAs (128 x 4096 x 14336: 27 us, 38 in pairs; 128 x 10240 x
+  // 8192: 54 and 37)
+  if (a.M <= 128 && (a.N + 127) / 128 * 8 <= 2 * sm_count()) return launch_small<128, T>(a, st);
   return launch_big<T>(a, st);
 }
 

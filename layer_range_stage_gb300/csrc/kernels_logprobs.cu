@@ -138,7 +138,7 @@ __device__ __forceinline__ float2 two_of(const Chunk<__nv_bfloat16>& p, int i) {
 template <typename T, bool TOP, int NT, int U>
 __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int chunks_per_cta) {
   constexpr int E = 32 / sizeof(T);
-  extern __shared__ uint32_t maxima[];  // [chunks_per_cta] ordered, then (8-byte aligned) the chunks above the bound
+  extern __shared__ float maxima[];  // [chunks_per_cta], then (8-byte aligned) the chunks above the bound
   __shared__ Shared<NT> sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
   const float zt = given ? to_f32(z[t]) : INFINITY;
   // the next float above zt (of -inf: the lowest number; of the two zeros: the smallest one)
   const float above_zt = unordered(ordered(zt) + 1);
-  Sums m{-INFINITY, 0.f, 0.f};
-  int above = 0;
-  uint64_t mine = 0;  // the thread's best chunk: (ordered maximum, ~chunk)
+  float ref = -INFINITY, best = -INFINITY;  // the largest logit, and the first chunk of the thread that has it
+  int best_at = tid, above = 0;
+  float2 s = make_float2(0.f, 0.f), td = s;
 
   for (int base = tid; base < nc; base += NT * U) {
     Chunk<T> p[U];
@@ -168,9 +168,11 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
       if (c >= nc) break;
       const float top = max_of(p[u]);
       if (TOP) {
-        const uint32_t k = ordered(top);
-        maxima[c] = k;
-        mine = max(mine, (uint64_t)k << 32 | (uint32_t)~c);
+        maxima[c] = top;
+        if (top > best) {
+          best = top;
+          best_at = c;
+        }
       }
       if (top >= zt) {
         const int e0 = (c0 + c) * E - off;
@@ -186,15 +188,18 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
           }
         }
       }
-      if (top == -INFINITY) continue;
-      if (!(top <= m.ref)) {  // above, or NaN (which then reaches the sums)
-        const float ref = top == top ? top : 0.f, d = (m.ref - ref) * kLog2e, g = ex2(d);
-        m.t = m.ref == -INFINITY ? 0.f : g * (m.t + fmaxf(d, -1000.f) * m.s);
-        m.s = m.ref == -INFINITY ? 0.f : g * m.s;
-        m.ref = ref;
+      if (!(top <= ref)) {  // above, or NaN (which then reaches the sums)
+        const float to = top == top ? top : 0.f, d = (ref - to) * kLog2e, g = ex2(d);
+        const bool any = ref != -INFINITY;
+        const float dd = fmaxf(d, -1000.f);
+        td.x = any ? g * fmaf(dd, s.x, td.x) : 0.f;
+        td.y = any ? g * fmaf(dd, s.y, td.y) : 0.f;
+        s.x = any ? g * s.x : 0.f;
+        s.y = any ? g * s.y : 0.f;
+        ref = to;
       }
-      const float2 down = make_float2(-m.ref, -m.ref), l2 = make_float2(kLog2e, kLog2e);
-      float2 s = make_float2(m.s, 0.f), td = make_float2(m.t, 0.f);
+      if (ref == -INFINITY) continue;  // nothing but masked tokens so far
+      const float2 down = make_float2(-ref, -ref), l2 = make_float2(kLog2e, kLog2e);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         float2 d = __fmul2_rn(__fadd2_rn(two_of(p[u], i), down), l2), e;
@@ -205,10 +210,10 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
         s = __fadd2_rn(s, e);
         td = __ffma2_rn(e, d, td);
       }
-      m.s = s.x + s.y;
-      m.t = td.x + td.y;
     }
   }
+  const uint64_t mine = tid < nc ? (uint64_t)ordered(best) << 32 | (uint32_t)~best_at : 0;
+  Sums m{ref, s.x + s.y, td.x + td.y};
   m = merge_lanes<16>(m);
   above = __reduce_add_sync(0xffffffffu, above);
   if (lane == 0) {
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a, int 
     }
     if (mine && mine >= bound) {
       for (int c = tid; c < nc; c += NT) {
-        const uint64_t k = (uint64_t)maxima[c] << 32 | (uint32_t)~c;
+        const uint64_t k = (uint64_t)ordered(maxima[c]) << 32 | (uint32_t)~c;
         if (k >= bound) chunk_list[atomicAdd(&sh.n_chunks, 1)] = k;
       }
     }

@@ -16,6 +16,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "kernels.cuh"
 #include "step.cuh"
 
 namespace lrs {
@@ -60,12 +61,12 @@ __device__ __forceinline__ float recip_root(Pair sum, float n, float eps) {
   return __fmaf_rn(__fmul_rn(0.5f, r), d, r);
 }
 
-// The same for two sums side by side.
-__device__ __forceinline__ float2 neg(float2 a) { return make_float2(-a.x, -a.y); }
+// The same for two sums side by side; a - b as a multiply-add, which is one packed instruction.
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
 __device__ __forceinline__ void two_sum2(float2 a, float2 b, float2& s, float2& e) {
   s = __fadd2_rn(a, b);
-  const float2 t = __fadd2_rn(s, neg(a));
-  e = __fadd2_rn(__fadd2_rn(a, neg(__fadd2_rn(s, neg(t)))), __fadd2_rn(b, neg(t)));
+  const float2 t = sub2(s, a);
+  e = __fadd2_rn(sub2(a, sub2(s, t)), sub2(b, t));
 }
 
 template <typename T>
@@ -82,22 +83,22 @@ template <typename T>
 struct Words {
   uint32_t w[sizeof(T)];
 };
+// The four columns from `at` on (VEC), or `at` + 32 i; those from n on are 0.
 template <bool VEC, typename T>
-__device__ __forceinline__ Words<T> load4(const T* row, int c0, int lane, int n) {
+__device__ __forceinline__ Words<T> load4(const T* row, int at, int n) {
   Words<T> p;
   if (VEC) {
-    const T* at = row + c0 + 4 * lane;
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T); ++i) p.w[i] = 0;
-    if (c0 + 4 * lane < n) {
+    if (at < n) {
       if (sizeof(T) == 4) {
-        const uint4 q = *reinterpret_cast<const uint4*>(at);
+        const uint4 q = *reinterpret_cast<const uint4*>(row + at);
         p.w[0] = q.x;
         p.w[1] = q.y;
         p.w[sizeof(T) - 2] = q.z;
         p.w[sizeof(T) - 1] = q.w;
       } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(at);
+        const uint2 q = *reinterpret_cast<const uint2*>(row + at);
         p.w[0] = q.x;
         p.w[1] = q.y;
       }
@@ -105,7 +106,7 @@ __device__ __forceinline__ Words<T> load4(const T* row, int c0, int lane, int n)
   } else {
     Four<T> v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v.v[i] = c0 + lane + 32 * i < n ? row[c0 + lane + 32 * i] : from_f32<T>(0.f);
+    for (int i = 0; i < 4; ++i) v.v[i] = at + 32 * i < n ? row[at + 32 * i] : from_f32<T>(0.f);
     memcpy(&p, &v, sizeof(p));
   }
   return p;
@@ -119,159 +120,148 @@ __device__ __forceinline__ float value_of(const Words<__half>& p, int i) {
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store4(T* row, int c0, int lane, int n, const Four<T>& p) {
+__device__ __forceinline__ void store4(T* row, int at, int n, const Four<T>& p) {
   if (VEC) {
-    if (c0 + 4 * lane < n) *reinterpret_cast<Four<T>*>(row + c0 + 4 * lane) = p;
+    if (at < n) *reinterpret_cast<Four<T>*>(row + at) = p;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (c0 + lane + 32 * i < n) row[c0 + lane + 32 * i] = p.v[i];
+      if (at + 32 * i < n) row[at + 32 * i] = p.v[i];
   }
 }
 
-// TR: the residual's type, or void.  W warps of a row (blockDim.x / 32), blockDim.y rows per CTA, CH blocks of 128 per warp.
+// TR: the residual's type, or void.  W warps of a row (blockDim.x / 32), blockDim.y rows per CTA, CH blocks of 128 per warp.  All of a
+// row is asked for before anything of it is used; the widest rows, whose values take the registers, four blocks at a time.
 template <typename TX, typename TR, int CH, bool VEC>
-__global__ void __launch_bounds__(512) norm_f8_kernel(const NormF8Args a) {
+__global__ void __launch_bounds__(512, CH <= 4 ? 2 : 1) norm_f8_kernel(const NormF8Args a) {
   __shared__ Pair part[16];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, W = blockDim.x >> 5;
-  const int row = blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row < a.n_tok;
-  const int nb = (a.n + 127) >> 7;
   constexpr bool kResid = !std::is_void<TR>::value;
   using TRv = typename std::conditional<kResid, TR, float>::type;
-
-  // all of the row is asked for before anything of it is used; the widest rows' residual (its registers) four blocks at a time
-  constexpr int kBatch = CH > 8 ? 4 : CH;
-  Words<TX> in[CH];
-  const TX* x = static_cast<const TX*>(a.x) + (int64_t)row * a.x_stride;
-  const TRv* res = static_cast<const TRv*>(a.resid) + (int64_t)row * a.resid_stride;
+  constexpr int kBatch = CH <= 8 ? CH : 4;
+  const int at0 = w * 128 + (VEC ? 4 * lane : lane), step = W * 128;  // of the warp's block c: at0 + c * step
+  const int n = a.n;
+  Words<TX> in[kBatch];
   Words<TRv> r0[kBatch];
+  auto fetch = [&](int row, int c0) {
+    const TX* x = static_cast<const TX*>(a.x) + (int64_t)row * a.x_stride;
+    const TRv* res = static_cast<const TRv*>(a.resid) + (int64_t)row * a.resid_stride;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int b = c * W + w;
-    if (live && b < nb) {
-      in[c] = load4<VEC>(x, b * 128, lane, a.n);
-      if (kResid && c < kBatch) r0[c] = load4<VEC>(res, b * 128, lane, a.n);
+    for (int j = 0; j < kBatch; ++j) {
+      in[j] = load4<VEC>(x, at0 + (c0 + j) * step, n);
+      if (kResid) r0[j] = load4<VEC>(res, at0 + (c0 + j) * step, n);
     }
-  }
-  float h[CH][4];
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[c][i] = live && c * W + w < nb ? value_of(in[c], i) : 0.f;
-  if (kResid) {
+  };
+  const int row = blockIdx.x * blockDim.y + threadIdx.y;
+  if (row < a.n_tok) {  // all warps of a CTA with more than one to a row
+    float2 h[CH][2];
     TRv* out = static_cast<TRv*>(a.resid_out) + (int64_t)row * a.resid_out_stride;
 #pragma unroll
     for (int c0 = 0; c0 < CH; c0 += kBatch) {
-      if (c0 > 0) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int b = (c0 + j) * W + w;
-          if (live && b < nb) r0[j] = load4<VEC>(res, b * 128, lane, a.n);
-        }
-      }
+      fetch(row, c0);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int b = (c0 + j) * W + w;
-        if (!live || b >= nb) continue;
-        Four<TRv> p;
+        float2(&v)[2] = h[c0 + j];
+        v[0] = make_float2(value_of(in[j], 0), value_of(in[j], 1));
+        v[1] = make_float2(value_of(in[j], 2), value_of(in[j], 3));
+        if constexpr (kResid) {
+          Four<TRv> p;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p.v[i] = from_f32<TRv>(__fadd_rn(h[c0 + j][i], value_of(r0[j], i)));
-          h[c0 + j][i] = to_f32(p.v[i]);  // the norm is of what the next block will read
+          for (int i = 0; i < 2; ++i) {
+            const float2 s = __fadd2_rn(v[i], make_float2(value_of(r0[j], 2 * i), value_of(r0[j], 2 * i + 1)));
+            p.v[2 * i] = from_f32<TRv>(s.x);
+            p.v[2 * i + 1] = from_f32<TRv>(s.y);
+          }
+          store4<VEC>(out, at0 + (c0 + j) * step, n, p);
+          Words<TRv> back;  // the norm is of what the next block will read
+          memcpy(&back, &p, sizeof(back));
+          v[0] = make_float2(value_of(back, 0), value_of(back, 1));
+          v[1] = make_float2(value_of(back, 2), value_of(back, 3));
         }
-        store4<VEC>(out, b * 128, lane, a.n, p);
       }
     }
-  }
-  if (a.gamma) {
-    float2 hi = make_float2(0.f, 0.f), lo = hi;
-    // a square of 12 bits or fewer is a float32
-    constexpr bool kExact = sizeof(TRv) == 2 || (!kResid && sizeof(TX) == 2);
+    if (a.gamma) {
+      float2 hi = make_float2(0.f, 0.f), lo = hi;
+      // a square of 12 bits or fewer is a float32
+      constexpr bool kExact = sizeof(TRv) == 2 || (!kResid && sizeof(TX) == 2);
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const float2 v = make_float2(h[c][i], h[c][i + 1]);
-        const float2 p = __fmul2_rn(v, v);
-        float2 e;
-        two_sum2(hi, p, hi, e);
-        if (!kExact) e = __fadd2_rn(e, __ffma2_rn(v, v, neg(p)));
-        lo = __fadd2_rn(lo, e);
-      }
-    Pair s = add(Pair{hi.x, lo.x}, Pair{hi.y, lo.y});
+        for (int i = 0; i < 2; ++i) {
+          const float2 v = h[c][i], p = __fmul2_rn(v, v);
+          float2 e;
+          two_sum2(hi, p, hi, e);
+          if (!kExact) e = __fadd2_rn(e, __ffma2_rn(v, v, make_float2(-p.x, -p.y)));
+          lo = __fadd2_rn(lo, e);
+        }
+      Pair s = add(Pair{hi.x, lo.x}, Pair{hi.y, lo.y});
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Pair t;
-      t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
-      t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-      s = add(s, t);
-    }
-    if (W > 1) {  // one row per CTA then
-      if (lane == 0) part[w] = s;
-      __syncthreads();
-      s = lane < W ? part[lane] : Pair{0.f, 0.f};
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
+      for (int o = 16; o > 0; o >>= 1) {
         Pair t;
         t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
         t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
         s = add(s, t);
       }
-      s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
-      s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
+      if (W > 1) {  // one row per CTA then
+        if (lane == 0) part[w] = s;
+        __syncthreads();
+        s = lane < W ? part[lane] : Pair{0.f, 0.f};
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+          Pair t;
+          t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+          t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+          s = add(s, t);
+        }
+        s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+        s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
+      }
+      const float r = recip_root(s, (float)a.n, a.eps);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const Words<float> g = load4<VEC>(a.gamma, at0 + c * step, a.n);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          h[c][i] = __fmul2_rn(__fmul2_rn(h[c][i], make_float2(r, r)), make_float2(value_of(g, 2 * i), value_of(g, 2 * i + 1)));
+      }
     }
-    const float r = recip_root(s, (float)a.n, a.eps);
+    if (a.y) {
+      TX* y = static_cast<TX*>(a.y) + (int64_t)row * a.y_stride;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int b = c * W + w;
-      if (b >= nb) continue;
-      const Words<float> g = load4<VEC>(a.gamma, b * 128, lane, a.n);
+      for (int c = 0; c < CH; ++c) {
+        Four<TX> p;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[c][i] = __fmul_rn(__fmul_rn(h[c][i], r), value_of(g, i));
+        for (int i = 0; i < 4; ++i) p.v[i] = from_f32<TX>(i & 1 ? h[c][i >> 1].y : h[c][i >> 1].x);
+        store4<VEC>(y, at0 + c * step, n, p);
+      }
     }
-  }
-  if (!live) return;
-  if (a.y) {
-    TX* y = static_cast<TX*>(a.y) + (int64_t)row * a.y_stride;
+    if (a.q) {
+      uint8_t* q = a.q + (int64_t)row * a.q_stride;
+      // lane c divides for the warp's block c
+      float top = 1.f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int b = c * W + w;
-      if (b >= nb) continue;
-      Four<TX> p;
+      for (int c = 0; c < CH; ++c) {
+        // magnitudes compare like their bits, and a NaN above all of them: it is not lost.  (A column from n on is 0, or 0 * r = NaN
+        // in a row that is NaN throughout.)
+        uint32_t m = 0x0D800000u;  // 2^-100
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p.v[i] = from_f32<TX>(h[c][i]);
-      store4<VEC>(y, b * 128, lane, a.n, p);
-    }
-  }
-  if (a.q) {
-    uint8_t* q = a.q + (int64_t)row * a.q_stride;
-    // lane c divides for the warp's block c
-    float top = 1.f;
+        for (int i = 0; i < 2; ++i)
+          m = max(m, max(__float_as_uint(h[c][i].x) & 0x7FFFFFFFu, __float_as_uint(h[c][i].y) & 0x7FFFFFFFu));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == c) top = __uint_as_float(m);
+      }
+      const float up = __fdiv_rn(448.f, top);
+      if (lane < CH && (lane * W + w) * 128 < n) a.scale[(int64_t)(lane * W + w) * a.scale_stride + row] = __fdiv_rn(top, 448.f);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      // magnitudes compare like their bits, and a NaN above all of them: it is not lost
-      uint32_t m = 0x0D800000u;  // 2^-100
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(h[c][i]) & 0x7FFFFFFFu);
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == c) top = __uint_as_float(m);
-    }
-    const float up = __fdiv_rn(448.f, top);
-    if (lane < CH && lane * W + w < nb) a.scale[(int64_t)(lane * W + w) * a.scale_stride + row] = __fdiv_rn(top, 448.f);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int b = c * W + w;
-      const float t = __shfl_sync(0xffffffffu, up, c);
-      if (b >= nb) continue;
-      const __nv_fp8x2_storage_t q0 = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[c][0], t), __fmul_rn(h[c][1], t)), __NV_SATFINITE, __NV_E4M3);
-      const __nv_fp8x2_storage_t q1 = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(h[c][2], t), __fmul_rn(h[c][3], t)), __NV_SATFINITE, __NV_E4M3);
-      Four<uint8_t> p;
-      p.v[0] = (uint8_t)q0;
-      p.v[1] = (uint8_t)(q0 >> 8);
-      p.v[2] = (uint8_t)q1;
-      p.v[3] = (uint8_t)(q1 >> 8);
-      store4<VEC>(q, b * 128, lane, a.n, p);
+      for (int c = 0; c < CH; ++c) {
+        const float t = __shfl_sync(0xffffffffu, up, c);
+        const float2 v0 = __fmul2_rn(h[c][0], make_float2(t, t)), v1 = __fmul2_rn(h[c][1], make_float2(t, t));
+        const uint32_t codes = (uint32_t)__nv_cvt_float2_to_fp8x2(v0, __NV_SATFINITE, __NV_E4M3) |
+                               (uint32_t)__nv_cvt_float2_to_fp8x2(v1, __NV_SATFINITE, __NV_E4M3) << 16;
+        Four<uint8_t> p;
+        memcpy(&p, &codes, sizeof(p));
+        store4<VEC>(q, at0 + c * step, n, p);
+      }
     }
   }
 }
@@ -289,9 +279,8 @@ cudaError_t launch_ch(const NormF8Args& a, int warps, int rows, cudaStream_t st)
 template <typename TX, typename TR>
 cudaError_t launch_t(const NormF8Args& a, cudaStream_t st) {
   const int nb = (a.n + 127) / 128;
-  // Blocks per warp: more loads of a row in flight per warp with eight (16411 x 8192: 210 us, 242 with four); a single short row is
-  // done sooner with more warps; 16 at the widest rows, whose 16 warps hold them
-  const int ch = nb > 128 ? 16 : nb > 32 ? 8 : 4;
+  // blocks per warp: few, so that a row is done soon, as long as 16 warps hold it
+  const int ch = nb > 128 ? 16 : nb > 64 ? 8 : 4;
   const int warps = (nb + ch - 1) / ch;
   const int rows = warps == 1 ? 4 : 1;
   if (ch == 16) return launch_ch<TX, TR, 16>(a, warps, rows, st);

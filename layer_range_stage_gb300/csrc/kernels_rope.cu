@@ -5,29 +5,44 @@
 // integer multiplication reduces the angle exactly, at any position.  The top two bits of the fraction (plus an eighth)
 // are the quadrant, the rest lies within an eighth of a turn of zero, where float32 holds it to 2^-28 of a turn.
 //
-// A row is read and written once: the bytes bound it.  A CTA makes its tokens' table of cos and sin in
-// shared memory while its first loads are in flight, and every head of the token uses it.
+// A row is read and written once: the bytes bound it.  A warp takes a token's heads (or, where tokens are few, a share of them), a
+// lane the same dims of every head it comes to, so that its cos and sin stay in registers; the warp makes the token's table while its
+// first heads are on their way.  (With CTAs that went by items of three tokens at a time, a third of the instructions found
+// the item's place, and a barrier stood between the loads and the table: 16384 tokens of 40 heads of 128: 82 us, now 65.)
 #include <algorithm>
 #include <cstring>
 
 #include "common.cuh"
+#include "kernels.cuh"
 #include "step.cuh"
 
 namespace lrs {
 
 namespace {
 
-constexpr int kThreads = 256, kItems = 2;  // items of a thread, all loaded before the table is waited for
+constexpr int kWarps = 8, kItems = 2;  // heads of a lane that are on their way together (four: 97 us below, for want of registers)
 
 // VEC elements as the words that they lie in: taken apart where they are loaded, a thread's loads would wait for one another.
-template <typename T, int VEC>
-struct Words {
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<2> {
+  uint16_t q;
+};
+template <>
+struct Raw<4> {
+  uint32_t q;
+};
+template <>
+struct Raw<8> {
+  uint2 q;
+};
+template <>
+struct Raw<16> {
   uint4 q;
 };
-template <typename T>
-struct Words<T, 1> {
-  T q;
-};
+template <typename T, int VEC>
+using Words = Raw<(int)sizeof(T) * VEC>;
 template <typename T, int VEC>
 __device__ __forceinline__ void take_apart(const Words<T, VEC>& w, float (&f)[VEC]) {
   T v[VEC];
@@ -72,114 +87,112 @@ __device__ __forceinline__ float2 cos_sin_of(int pos, uint64_t turn, float scale
   return make_float2(c * scale, s * scale);
 }
 
-// Division by a number that stays the same: n / d for n < 2^31 (d >= 1), by a multiplication with the rounded-up 2^(32 + s) / d.
-struct Div {
-  uint32_t d, mul, shift;
-};
-__host__ Div div_by(uint32_t d) {
-  uint32_t s = 0;
-  while ((1ull << s) < d) ++s;
-  return {d, d == 1 ? 0u : (uint32_t)(((1ull << (31 + s)) + d - 1) / d), s == 0 ? 0u : s - 1};
-}
-__device__ __forceinline__ uint32_t quotient(uint32_t n, Div v) { return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift; }
-
 // An item is two vectors of VEC elements of one head: the halves' parts of VEC pairs, or (interleaved, and dims that are
-// only copied) two neighbouring vectors.
+// only copied) two neighbouring vectors.  A token's heads are `chunks` shares of `share` heads.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeArgs a, int tok_per_cta, int splits, int rot_items,
-                                                        Div head_items, Div token_items, Div pairs) {
-  extern __shared__ float2 table[];  // [token][rot / 2], and behind it the pairs' turns
+__global__ void __launch_bounds__(32 * kWarps, 4) rope_kernel(const RopeArgs a, int chunks, int share, int rot_items, int head_items) {
+  extern __shared__ uint64_t turns[];  // [rot / 2], and behind it a table (cos, sin) [rot / 2] of each warp
   using P = Words<T, VEC>;
-  const int t0 = (int)(blockIdx.x / splits) * tok_per_cta, nt = min(tok_per_cta, a.n_tok - t0);
-  const int split = (int)(blockIdx.x % splits);
-  const int heads = a.hq + a.hk, half = a.rot >> 1;
-  const int h0 = (int)((int64_t)heads * split / splits), nh = (int)((int64_t)heads * (split + 1) / splits) - h0;
-  const int total = nt * nh * (int)head_items.d;
-  uint64_t* turns = reinterpret_cast<uint64_t*>(table + tok_per_cta * half);
-  bool have_table = false;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.rot >> 1, heads = a.hq + a.hk;
+  float2* table = reinterpret_cast<float2*>(turns + half) + warp * half;
+  for (int i = threadIdx.x; i < half; i += 32 * kWarps) turns[i] = turn_of(a.freqs[i]);
+  __syncthreads();
+  // lanes side by side in a head, and heads side by side in a pass
+  const bool narrow = head_items <= 32;
+  const int per_pass = narrow ? 32 / head_items : 1;
+  const int jl = narrow ? lane % head_items : lane, hl = narrow ? lane / head_items : 0;
+  const int64_t units = (int64_t)a.n_tok * chunks, stride = (int64_t)gridDim.x * kWarps;
 
-  for (int base = 0; base < total; base += kThreads * kItems) {
-    P u[kItems], v[kItems];
-    T* out[kItems];
-    int d0[kItems], d1[kItems], tok[kItems], pos[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int it = base + i * kThreads + (int)threadIdx.x;
-      tok[i] = -1;
-      if (it >= total) continue;
-      // without splits a token's items are token_items.d
-      const int tl = splits == 1 ? (int)quotient(it, token_items) : 0, rest = it - tl * (int)token_items.d;
-      const int hl = (int)quotient(rest, head_items), j = rest - hl * (int)head_items.d;
-      const int t = t0 + tl, h = h0 + hl;
-      const bool is_k = h >= a.hq;
-      const int64_t in_off = is_k ? t * a.k_stride + (int64_t)(h - a.hq) * a.head_dim : t * a.q_stride + (int64_t)h * a.head_dim;
-      const T* in = static_cast<const T*>(is_k ? a.k : a.q) + in_off;
-      const int64_t out_off =
-          is_k ? t * a.k_out_stride + (int64_t)(h - a.hq) * a.head_dim : t * a.q_out_stride + (int64_t)h * a.head_dim;
-      out[i] = static_cast<T*>(is_k ? a.k_out : a.q_out) + out_off;
-      tok[i] = tl;
-      pos[i] = a.pos[t];  // looked at below: padding is read like the rest, but not written
+  for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += stride) {
+    const int t = (int)(unit / chunks), h0 = (int)(unit - (int64_t)t * chunks) * share, h1 = min(heads, h0 + share);
+    const int pos = a.pos[t];
+    const T* q = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + t * a.k_stride;
+    T* q_out = static_cast<T*>(a.q_out) + t * a.q_out_stride;
+    T* k_out = static_cast<T*>(a.k_out) + t * a.k_out_stride;
+    bool have_table = false;
+    for (int jb = 0; jb < head_items; jb += 32) {
+      const int j = jb + jl;
+      const bool mine = hl < per_pass && j < head_items;
+      int d0, d1;
+      bool turn0, turn1;  // whether the vectors' dims turn (both or none but where pairs are neighbours)
       if (INTER) {
-        d0[i] = 2 * j * VEC;
-        d1[i] = d0[i] + VEC;
-      } else if (j < rot_items) {
-        d0[i] = j * VEC;
-        d1[i] = half + d0[i];
+        d0 = 2 * j * VEC;
+        d1 = d0 + VEC;
+        turn0 = d0 < a.rot;
+        turn1 = VEC == 1 ? turn0 : d1 < a.rot;
       } else {
-        d0[i] = a.rot + 2 * (j - rot_items) * VEC;
-        d1[i] = d0[i] + VEC;
+        turn0 = turn1 = j < rot_items;
+        d0 = turn0 ? j * VEC : a.rot + 2 * (j - rot_items) * VEC;
+        d1 = d0 + (turn0 ? half : VEC);
       }
-      u[i] = *reinterpret_cast<const P*>(in + d0[i]);
-      if (d1[i] < a.head_dim) v[i] = *reinterpret_cast<const P*>(in + d1[i]);
-    }
-    if (!have_table) {
-      for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn_of(a.freqs[i]);
-      __syncthreads();
-      for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int tl = (int)quotient(i, pairs);
-        table[i] = cos_sin_of(a.pos[t0 + tl], turns[i - tl * half], a.scale);  // of padding: not used
-      }
-      __syncthreads();
-      have_table = true;
-    }
+      const bool second = d1 < a.head_dim;
+      float2 cs[VEC];
+      bool have_cs = false;
+      for (int hb = h0; hb < h1; hb += per_pass * kItems) {
+        P u[kItems], v[kItems];
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      if (tok[i] < 0 || pos[i] < 0) continue;
-      const float2* cs = table + tok[i] * half;
-      float x[VEC], y[VEC];
-      if (!INTER || VEC == 1) {  // the pairs are across the two vectors
-        if (d0[i] < (INTER ? a.rot : half)) {
-          take_apart<T, VEC>(u[i], x);
-          take_apart<T, VEC>(v[i], y);
+        for (int i = 0; i < kItems; ++i) {
+          const int h = hb + i * per_pass + hl;
+          if (!mine || h >= h1) continue;
+          const T* in = h < a.hq ? q + h * a.head_dim : k + (h - a.hq) * a.head_dim;
+          u[i] = *reinterpret_cast<const P*>(in + d0);
+          if (second) v[i] = *reinterpret_cast<const P*>(in + d1);
+        }
+        if (!have_table) {
+          __syncwarp();  // the token before this one is done with it
+          if (pos >= 0)
+            for (int i = lane; i < half; i += 32) table[i] = cos_sin_of(pos, turns[i], a.scale);
+          __syncwarp();
+          have_table = true;
+        }
+        if (pos < 0) continue;  // padding was read like the rest, but is not written
+        if (!have_cs) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const float2 w = cs[INTER ? d0[i] >> 1 : d0[i] + e];
-            const float h = x[e];
-            x[e] = h * w.x - y[e] * w.y;
-            y[e] = y[e] * w.x + h * w.y;
+            const int at = !INTER ? d0 + e : VEC == 1 ? d0 >> 1 : ((e < VEC / 2 ? d0 : d1) >> 1) + e % ((VEC + 1) / 2);
+            cs[e] = mine && (e < (VEC + 1) / 2 || !INTER ? turn0 : turn1) ? table[at] : make_float2(1.f, 0.f);
           }
-          u[i] = put_together<T, VEC>(x);
-          v[i] = put_together<T, VEC>(y);
+          have_cs = true;
         }
-      } else {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const int d = part ? d1[i] : d0[i];
-          if (d >= a.rot) continue;
-          take_apart<T, VEC>(part ? v[i] : u[i], x);
+        for (int i = 0; i < kItems; ++i) {
+          const int h = hb + i * per_pass + hl;
+          if (!mine || h >= h1) continue;
+          T* out = h < a.hq ? q_out + h * a.head_dim : k_out + (h - a.hq) * a.head_dim;
+          float x[VEC], y[VEC];
+          if (!INTER || VEC == 1) {  // the pairs are across the two vectors
+            if (turn0) {
+              take_apart<T, VEC>(u[i], x);
+              take_apart<T, VEC>(v[i], y);
 #pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            constexpr int kHi = VEC > 1 ? 1 : 0;
-            const float2 w = cs[(d + e) >> 1];
-            const float h = x[e];
-            x[e] = h * w.x - x[e + kHi] * w.y;
-            x[e + kHi] = x[e + kHi] * w.x + h * w.y;
+              for (int e = 0; e < VEC; ++e) {
+                const float w = x[e];
+                x[e] = w * cs[e].x - y[e] * cs[e].y;
+                y[e] = y[e] * cs[e].x + w * cs[e].y;
+              }
+              u[i] = put_together<T, VEC>(x);
+              v[i] = put_together<T, VEC>(y);
+            }
+          } else {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (!(part ? turn1 : turn0)) continue;
+              take_apart<T, VEC>(part ? v[i] : u[i], x);
+#pragma unroll
+              for (int e = 0; e < VEC / 2; ++e) {
+                const float2 c = cs[part * (VEC / 2) + e];
+                const float w = x[2 * e];
+                x[2 * e] = w * c.x - x[2 * e + 1] * c.y;
+                x[2 * e + 1] = x[2 * e + 1] * c.x + w * c.y;
+              }
+              (part ? v[i] : u[i]) = put_together<T, VEC>(x);
+            }
           }
-          (part ? v[i] : u[i]) = put_together<T, VEC>(x);
+          *reinterpret_cast<P*>(out + d0) = u[i];
+          if (second) *reinterpret_cast<P*>(out + d1) = v[i];
         }
       }
-      *reinterpret_cast<P*>(out[i] + d0[i]) = u[i];
-      if (d1[i] < a.head_dim) *reinterpret_cast<P*>(out[i] + d1[i]) = v[i];
     }
   }
 }
@@ -190,26 +203,25 @@ cudaError_t launch_t(const RopeArgs& a, cudaStream_t st) {
   const int rot_items = INTER ? (a.rot + 2 * VEC - 1) / (2 * VEC) : a.rot / (2 * VEC);
   const int rest = a.copy ? a.head_dim - a.rot : 0;
   const int head_items = INTER ? ((a.copy ? a.head_dim : a.rot) + 2 * VEC - 1) / (2 * VEC) : rot_items + (rest + 2 * VEC - 1) / (2 * VEC);
-  const int heads = a.hq + a.hk, per_tok = heads * head_items;
-  // A CTA takes whole tokens, about a round of items, as long as there are some CTAs for each SM; else a token's heads are
-  // shared out (each share makes the table for itself).
-  const int round = kThreads * kItems;
-  int tok_per_cta = std::max(1, std::min(round / std::max(1, per_tok), a.n_tok / 608));
-  tok_per_cta = std::min(tok_per_cta, std::max(1, 16384 / (a.rot * 4)));
-  int splits = 1;
-  if (a.n_tok < 304) splits = std::max(1, std::min({heads, 304 / a.n_tok, (per_tok + kThreads - 1) / kThreads}));
-  const size_t smem = (size_t)(tok_per_cta + 1) * (a.rot / 2) * sizeof(float2);
-  const int64_t grid = (int64_t)((a.n_tok + tok_per_cta - 1) / tok_per_cta) * splits;
-  rope_kernel<T, VEC, INTER><<<(unsigned)grid, kThreads, smem, st>>>(a, tok_per_cta, splits, rot_items, div_by(head_items), div_by(per_tok),
-                                                                            div_by(a.rot / 2));
+  const int heads = a.hq + a.hk, per_pass = head_items <= 32 ? 32 / head_items : 1;
+  // shares of whole passes, as many as it takes for every SM to have its warps
+  const int sms = sm_count(), passes = (heads + per_pass - 1) / per_pass;
+  const int want = (int)std::min<int64_t>(passes, std::max<int64_t>(1, (int64_t)sms * 2 * kWarps / a.n_tok));
+  const int share = (passes + want - 1) / want * per_pass, chunks = (heads + share - 1) / share;
+  const size_t smem = (size_t)(kWarps + 1) * (a.rot / 2) * sizeof(float2);
+  const int64_t ctas = ((int64_t)a.n_tok * chunks + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, (int64_t)sms * 4);
+  rope_kernel<T, VEC, INTER><<<grid, 32 * kWarps, smem, st>>>(a, chunks, share, rot_items, head_items);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_d(const RopeArgs& a, cudaStream_t st) {
   constexpr int kVec = 16 / sizeof(T);
-  if (a.interleaved) return a.vec ? launch_t<T, kVec, true>(a, st) : launch_t<T, 1, true>(a, st);
-  return a.vec ? launch_t<T, kVec, false>(a, st) : launch_t<T, 1, false>(a, st);
+  // (8000 tokens of 36 heads of 80, 20 of them turned, bf16: 64 us by twos, 68 one by one)
+  if (a.interleaved)
+    return a.vec == 2 ? launch_t<T, kVec, true>(a, st) : a.vec == 1 ? launch_t<T, 2, true>(a, st) : launch_t<T, 1, true>(a, st);
+  return a.vec == 2 ? launch_t<T, kVec, false>(a, st) : a.vec == 1 ? launch_t<T, 2, false>(a, st) : launch_t<T, 1, false>(a, st);
 }
 
 }  // namespace

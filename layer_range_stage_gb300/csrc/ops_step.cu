@@ -211,18 +211,22 @@ int stage_op_rope(const void* q_dev, int64_t q_stride, int n_q_heads, const void
   if (int rc = check_rows(q_dev, q_stride, (int64_t)n_q_heads * head_dim, eb, "q")) return rc;
   if (int rc = check_rows(q_out_dev, q_out_stride, (int64_t)n_q_heads * head_dim, eb, "q_out")) return rc;
   if (q_dev == q_out_dev && q_stride != q_out_stride) return op_err(STAGE_E_INVALID, "q_out in q's place must have its stride");
-  bool vec = rows_at(q_dev, q_stride, eb, 16) && rows_at(q_out_dev, q_out_stride, eb, 16);
   bool copy = q_dev != q_out_dev;
   if (n_k_heads) {
     if (int rc = check_rows(k_dev, k_stride, (int64_t)n_k_heads * head_dim, eb, "k")) return rc;
     if (int rc = check_rows(k_out_dev, k_out_stride, (int64_t)n_k_heads * head_dim, eb, "k_out")) return rc;
     if (k_dev == k_out_dev && k_stride != k_out_stride) return op_err(STAGE_E_INVALID, "k_out in k's place must have its stride");
-    vec = vec && rows_at(k_dev, k_stride, eb, 16) && rows_at(k_out_dev, k_out_stride, eb, 16);
     copy = copy || k_dev != k_out_dev;
   }
   if (!pos_dev || !aligned(pos_dev, 4)) return op_err(STAGE_E_INVALID, "null or unaligned pos");
   if (!freqs_dev || !aligned(freqs_dev, 8)) return op_err(STAGE_E_INVALID, "null or unaligned freqs");
-  const int width = 16 / eb;
+  // whether everything allows accesses of `width` elements
+  auto by = [&](int width) {
+    const int unit = width * eb;
+    return rows_at(q_dev, q_stride, eb, unit) && rows_at(q_out_dev, q_out_stride, eb, unit) &&
+           (!n_k_heads || (rows_at(k_dev, k_stride, eb, unit) && rows_at(k_out_dev, k_out_stride, eb, unit))) && head_dim % width == 0 &&
+           rot_dim % (interleaved ? width : 2 * width) == 0;
+  };
   lrs::RopeArgs a;
   a.q = q_dev;
   a.k = k_dev;
@@ -241,7 +245,7 @@ int stage_op_rope(const void* q_dev, int64_t q_stride, int n_q_heads, const void
   a.n_tok = n_tok;
   a.interleaved = interleaved != 0;
   a.scale = scale;
-  a.vec = vec && head_dim % width == 0 && rot_dim % (interleaved ? width : 2 * width) == 0;
+  a.vec = by(16 / eb) ? 2 : by(2) ? 1 : 0;
   a.copy = copy && rot_dim < head_dim;
   const cudaError_t e = lrs::launch_rope(a, dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? STAGE_OK : op_cuda(e, "rope");

@@ -68,7 +68,7 @@ struct RopeArgs {
   int64_t q_stride = 0, k_stride = 0, q_out_stride = 0, k_out_stride = 0;
   int hq = 0, hk = 0, head_dim = 0, rot = 0, n_tok = 0, interleaved = 0;
   float scale = 1.f;
-  int vec = 0;   // bases, strides, heads and pairs allow accesses of 16 bytes
+  int vec = 0;   // bases, strides, heads and pairs allow accesses of 16 bytes (2), or of two elements (1)
   int copy = 0;  // dims from rot on are to be copied (some output is not in place)
 };
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t st);
