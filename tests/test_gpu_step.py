@@ -286,6 +286,29 @@ def test_product_is_repeatable_and_long(B, M):
     assert torch.equal(first, again)
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 1, 200), (17, 1, 50), (129, 100, 1100), (1, 5000, 16), (16, 17, 33), (256, 300, 2048), (512, 256, 1024)])
+def test_product_of_narrow_weights_and_shared_k(B, M, N, K):
+    rng = np.random.default_rng(M + N)
+    sa, sw = rng.uniform(0.1, 1, (-(-K // 128), M)).astype(np.float32), rng.uniform(0.1, 1, (-(-N // 128), -(-K // 128))).astype(np.float32)
+    for dtype, ygap in (("f32", 0), ("bf16", 3)):
+        check_gemm(B, random_f8(rng, M, K), sa, random_f8(rng, N, K), sw, dtype, ygap=ygap)
+
+
+def test_product_rows_do_not_depend_on_their_neighbours(B):
+    """The same row in calls of other rows: within a kernel's range of M the same bits, and beside NaN rows too."""
+    rng = np.random.default_rng(12)
+    K, N = 1536, 640
+    w, sw = put_f8(random_f8(rng, N, K)), dev(rng.uniform(0.1, 1, (5, 12)).astype(np.float32))
+    for M in (7, 15, 50, 100, 400):
+        a, sa = random_f8(rng, M, K), rng.uniform(0.1, 1, (12, M)).astype(np.float32)
+        y, z = torch.zeros(M, N, device="cuda"), torch.zeros(M, N, device="cuda")
+        B.stage_op_f8_gemm(put_f8(a), dev(sa), w, sw, y)
+        b = a.copy()
+        b[: M // 2] = 0x7F
+        B.stage_op_f8_gemm(put_f8(b), dev(sa), w, sw, z)
+        assert torch.isnan(z[: M // 2]).all() and torch.equal(y[M // 2:], z[M // 2:])
+
+
 def test_product_that_runs_out_of_time(B):
     rng = np.random.default_rng(8)
     for M in (5, 300):
@@ -452,6 +475,27 @@ def test_logprobs_rising_and_falling(B, dtype):
     check_logprobs(B, np.stack([up, up[::-1], up * 100 if dtype == "f32" else up]), [vocab - 1, 5, 17], 32, dtype)
 
 
+@pytest.mark.parametrize("rows,vocab,top", [(1, 5000, 32), (160, 20000, 20), (2, 100000, 32), (160, 100003, 5)])
+def test_logprobs_with_the_best_in_few_places(B, rows, vocab, top):
+    """The likeliest tokens all in one thread's chunks, all but one group's, or in one chunk: the first bound is too low, or its chunks many."""
+    rng = np.random.default_rng(vocab)
+    place = np.arange(vocab) // 8                    # 32 bytes of float32
+    z = rng.standard_normal((rows, vocab))
+    for i in range(rows):
+        kind, nt = i % 5, 256 if i % 2 else 512
+        if kind == 0:
+            z[i] += 30 * (place % nt == 3)
+        elif kind == 1:
+            z[i] -= 200 * (place % nt < 8)
+        elif kind == 2:
+            z[i] += 50 * (place == vocab // 16) + 40 * (place == vocab // 9)
+        elif kind == 3:
+            z[i] = np.where(place % nt == 7, 5.0, -5.0)
+        else:
+            z[i] += 30 * (place % nt < 2) + 0.01 * np.arange(vocab)
+    check_logprobs(B, z, rng.integers(0, vocab, rows), top)
+
+
 def test_logprobs_without_tokens_or_some_outputs(B):
     z = torch.randn(5, 3000, device="cuda")
     w = step.logprobs(z.cpu().numpy(), None, 3)
@@ -512,6 +556,62 @@ def test_other_streams_and_graphs(B):
             go(b, st)
     torch.cuda.synchronize()
     assert all(equal(want, b) for b in many)
+
+
+@pytest.mark.parametrize("M", [3, 12, 30, 200, 600])
+def test_products_of_every_kernel_captured_and_at_once(B, M):
+    rng = np.random.default_rng(M)
+    K, N = 2048, 768
+    w, sw = put_f8(random_f8(rng, N, K)), dev(rng.uniform(0.1, 1, (6, 16)).astype(np.float32))
+    inputs = [(put_f8(random_f8(rng, M, K)), dev(rng.uniform(0.1, 1, (16, M)).astype(np.float32))) for _ in range(3)]
+    want = [torch.zeros(M, N, dtype=torch.bfloat16, device="cuda") for _ in inputs]
+    for (a, s), y in zip(inputs, want):
+        B.stage_op_f8_gemm(a, s, w, sw, y)
+    a, s = inputs[0][0].clone(), inputs[0][1].clone()
+    y = torch.zeros_like(want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.stage_op_f8_gemm(a, s, w, sw, y)
+    for (b, r), expected in zip(inputs, want):
+        a.view(torch.uint8).copy_(b.view(torch.uint8))
+        s.copy_(r)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, expected)
+    streams, outs = [torch.cuda.Stream() for _ in inputs], [torch.zeros_like(y) for _ in inputs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for st, (b, r), o in zip(streams, inputs, outs):
+            B.stage_op_f8_gemm(b, r, w, sw, o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, e) for o, e in zip(outs, want))
+
+
+def test_refusals_of_the_binding_on_device_tensors(B):
+    c = dict(device="cuda")
+    x, q, s = torch.zeros(3, 256, **c), torch.zeros(3, 256, dtype=F8, **c), torch.zeros(2, 3, **c)
+    i, f = torch.zeros(3, dtype=torch.int32, **c), torch.zeros(32, dtype=torch.float64, **c)
+    h = x.view(3, 2, 128)
+    bad = [
+        lambda: B.stage_op_norm_f8(x, q, s.t()), lambda: B.stage_op_norm_f8(x, q, s[:1]), lambda: B.stage_op_norm_f8(x, q.float(), s), lambda: B.stage_op_norm_f8(x, q[:, :200], s),
+        lambda: B.stage_op_norm_f8(x, q, s, gamma=torch.zeros(255, **c)), lambda: B.stage_op_norm_f8(x, q, s, gamma=torch.zeros(256)), lambda: B.stage_op_norm_f8(x.t(), q, s),
+        lambda: B.stage_op_norm_f8(x, q, s, resid=x.half(), resid_out=x.half()), lambda: B.stage_op_norm_f8(x, q, s, y=x.half()), lambda: B.stage_op_norm_f8(x, q, s, eps=-1.0),
+        lambda: B.stage_op_norm_f8(x), lambda: B.stage_op_norm_f8(x.double(), q, s),
+        lambda: B.stage_op_f8_gemm(q, s, q[:, :250], torch.zeros(1, 2, **c), torch.zeros(3, 3, **c)), lambda: B.stage_op_f8_gemm(q, s, q, torch.zeros(1, 3, **c), torch.zeros(3, 3, **c)),
+        lambda: B.stage_op_f8_gemm(q, s, q, torch.zeros(1, 2, **c), torch.zeros(3, 4, **c)), lambda: B.stage_op_f8_gemm(q, s, q, torch.zeros(1, 2), torch.zeros(3, 3, **c)),
+        lambda: B.stage_op_f8_gemm(q[:, 1:], s, q[:, 1:], torch.zeros(1, 2, **c), torch.zeros(3, 3, **c)), lambda: B.stage_op_f8_gemm(x, s, q, torch.zeros(1, 2, **c), torch.zeros(3, 3, **c)),
+        lambda: B.stage_op_f8_gemm(q, s, q, torch.zeros(1, 2, **c), torch.zeros(3, 3, **c), torch.zeros(2, dtype=torch.int32, **c)),
+        lambda: B.stage_op_rope(h, None, i.long(), f), lambda: B.stage_op_rope(h, None, i, f.float()), lambda: B.stage_op_rope(h, None, i[:2], f), lambda: B.stage_op_rope(x, None, i, f),
+        lambda: B.stage_op_rope(h, h.half(), i, f), lambda: B.stage_op_rope(h, h[:, :, :64], i, f), lambda: B.stage_op_rope(h, None, i, f, k_out=h),
+        lambda: B.stage_op_rope(h, None, i, torch.zeros(65, dtype=torch.float64, **c)), lambda: B.stage_op_rope(h.transpose(1, 2), None, i, f), lambda: B.stage_op_rope(h, None, i, f, scale=float("nan")),
+        lambda: B.stage_op_logprobs(x, i.long(), torch.zeros(3, **c)), lambda: B.stage_op_logprobs(x, None, torch.zeros(3, **c)), lambda: B.stage_op_logprobs(x, i, torch.zeros(4, **c)),
+        lambda: B.stage_op_logprobs(x, i, top_ids=torch.zeros(3, 33, dtype=torch.int32, **c)), lambda: B.stage_op_logprobs(x, top_ids=i), lambda: B.stage_op_logprobs(x.t()[:, ::2], i),
+        lambda: B.stage_op_logprobs(x, top_ids=torch.zeros(3, 2, dtype=torch.int32, **c), top_logprobs=torch.zeros(3, 3, **c)), lambda: B.stage_op_logprobs(x, i.cpu(), torch.zeros(3, **c)),
+    ]
+    for n, call in enumerate(bad):
+        with pytest.raises(B.StageError) as e:
+            call()
+        assert e.value.code == B.STAGE_E_INVALID, n
 
 
 def test_a_decoding_step_of_single_ops(B):

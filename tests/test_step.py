@@ -152,3 +152,19 @@ def test_binding_refuses_host_tensors_shapes_and_types():
         L.stage_op_norm_f8(x, q)
     with pytest.raises(L.StageError, match="go together"):
         L.stage_op_norm_f8(x, q, s, resid=x)
+
+
+def test_the_product_has_the_registers_that_its_warpgroups_share_out(tmp_path):
+    """From a kernel with fewer, the warpgroup that asks for more would wait forever (the launch refuses it)."""
+    import os
+    import re
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = os.path.join(root, "layer_range_stage_gb300", "csrc", "kernels_f8_gemm.cu")
+    r = subprocess.run([lbuild.nvcc(), *lbuild.ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(root, "include"), "-Xptxas", "-v", "-c", src,
+                        "-o", str(tmp_path / "x.o")], capture_output=True, text=True, check=True)
+    text = open(src).read()
+    start, roles, sums = (int(re.search(rf"\b{n} = (\d+)", text).group(1)) for n in ("kRegsStart", "kRegsRoles", "kRegsSums"))
+    assert 128 * roles + 256 * sums <= 384 * start
+    found = {n: int(v) for n, v in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", r.stderr, re.S) if "14f8_gemm_kernel" in n}
+    assert len(found) == 3 and set(found.values()) == {start}, found
