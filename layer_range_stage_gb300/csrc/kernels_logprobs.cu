@@ -10,6 +10,10 @@
 // one); their chunks above it are ranked by counting, and only the n_top first are read again.
 //
 // Few rows are split over a cluster's CTAs, whose parts meet in the first one's shared memory.
+//
+// Many rows are bound by instructions (70 % of the issue slots): 4099 x 32000 in bfloat16 70 us, 3.7 TB/s; about 9 per logit in the loop
+// (the exponential unit's share alone would be 26 us), the rest per row.  128 threads a row take as long, 512 take 112 us.  64 x
+// 128256 in float32: 14 us; one row of 151936 with 20 alternatives 9.4 us, a chain of dependent steps.
 #include <algorithm>
 #include <atomic>
 
@@ -386,6 +390,7 @@ template <typename T, bool TOP>
 cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t st) {
   constexpr int E = 32 / sizeof(T);
   const int chunks = (a.vocab + E - 1) / E + 1;  // a row that begins inside a chunk has one more
+  // a cluster of as many CTAs as the SMs hold without a second wave, of 1024 chunks or more each (64 x 128256: 14 us with four, 22 with eight)
   int C = 1;
   while (C < kMaxCluster && ((chunks + C - 1) / C > kMaxChunks || (a.rows * (int64_t)C <= 152 && chunks / C >= 1024))) C *= 2;
   const int per = (chunks + C - 1) / C;

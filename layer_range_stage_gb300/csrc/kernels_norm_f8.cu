@@ -2,7 +2,10 @@
 //
 // One pass: a row's values stay in registers between the sum of squares and the codes.  A warp takes a
 // block of 128 columns at a time, four neighbouring columns a lane, so that a block's largest value is one warp
-// reduction and its codes are one store of 128 bytes.  The bytes in and out bound it.
+// reduction and its codes are one store of 128 bytes.  The bytes in and out are its floor; what bounds it is the chain from a row's
+// loads over its sum to its stores, with 32 warps on an SM: 2048 x 4096 (bfloat16 onto float32) 18 us, 5.1 TB/s; 16411 x 8192 in
+// bfloat16 212 us, 4.5 TB/s (its warps' sums and roots are a third of the instructions there; one warp that finishes for the row: 231,
+// for its second barrier); one row of 4096 2.7 us.
 //
 // The codes are defined by float32 roundings, so two machines agree if they agree on r = fl(1 / sqrt(mean + eps)).  A float32
 // sum would not do: its last bits depend on its order, and where r differs by one unit so does a code now and then.
@@ -279,7 +282,7 @@ cudaError_t launch_ch(const NormF8Args& a, int warps, int rows, cudaStream_t st)
 template <typename TX, typename TR>
 cudaError_t launch_t(const NormF8Args& a, cudaStream_t st) {
   const int nb = (a.n + 127) / 128;
-  // blocks per warp: few, so that a row is done soon, as long as 16 warps hold it
+  // blocks per warp: few, so that a row is done soon, as long as 16 warps hold it (16411 x 8192: 212 us with four, 222 with eight)
   const int ch = nb > 128 ? 16 : nb > 64 ? 8 : 4;
   const int warps = (nb + ch - 1) / ch;
   const int rows = warps == 1 ? 4 : 1;
