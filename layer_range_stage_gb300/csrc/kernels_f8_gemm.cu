@@ -355,13 +355,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Warps 0-3 hold the sums (a weight row per thread), warp 4 copies, warp 5 issues the products.
 constexpr int kSmallThreads = 192;
 
-template <int NT>
+template <int NT, int PER>
 struct Small {
-  static constexpr int kStages = NT >= 128 ? 3 : NT == 64 ? 4 : NT == 32 ? 5 : 6;  // two CTAs per SM
+  static constexpr int kStages = PER == 3 || NT >= 128 ? 3 : NT == 64 ? 4 : NT == 32 ? 5 : 6;  // PER CTAs per SM
   static constexpr uint32_t kTileW = 128 * kBK, kTileA = NT * kBK, kStage = kTileW + kTileA;
   static constexpr uint32_t kOffScale = kStages * kStage;             // 4 warps x 2 blocks x NT products of scales
   static constexpr uint32_t kOffBar = kOffScale + 4 * 2 * NT * 4;
-  static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
+  static constexpr uint32_t kSmem = kOffBar + 256;
   static constexpr uint32_t kCols = 2 * NT < 32 ? 32 : 2 * NT;
   static_assert(kStages * kStage >= 128 * NT * 4, "the sums take the stages' place");
   struct Bars {
@@ -369,12 +369,12 @@ struct Small {
   };
 };
 
-template <int NT, typename T>
-__global__ void __launch_bounds__(kSmallThreads)
+template <int NT, int PER, typename T>
+__global__ void __launch_bounds__(kSmallThreads, PER)
     f8_gemm_small_kernel(const F8GemmArgs a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tW) {
-  using G = Small<NT>;
-  extern __shared__ unsigned char raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  using G = Small<NT, PER>;
+  extern __shared__ __align__(1024) unsigned char aligned_raw[];  // (a swizzled tile begins at a multiple of 1024)
+  unsigned char* sm = aligned_raw;
   typename G::Bars* B = reinterpret_cast<typename G::Bars*>(sm + G::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + G::kOffBar + sizeof(typename G::Bars));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -677,13 +677,13 @@ cudaError_t launch_big(const F8GemmArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<T>, a, tA, tB);
 }
 
-template <int NT, typename T>
-cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
-  using G = Small<NT>;
+template <int NT, int PER, typename T>
+cudaError_t launch_small_per(const F8GemmArgs& a, cudaStream_t st) {
+  using G = Small<NT, PER>;
   static_assert(sizeof(typename G::Bars) + 8 <= 256, "barrier block");
-  static_assert(G::kSmem <= 227 * 1024, "shared memory");
+  static_assert(PER * (G::kSmem + 1024) <= 228 * 1024, "shared memory of PER CTAs");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = ready_once(f8_gemm_small_kernel<NT, T>, G::kSmem, 0, done);
+  cudaError_t e = ready_once(f8_gemm_small_kernel<NT, PER, T>, G::kSmem, 0, done);
   if (e != cudaSuccess) return e;
   CUtensorMap tA, tW;
   if (!encode_2d(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.a, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.a_stride, kBK, NT,
@@ -707,7 +707,15 @@ cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f8_gemm_small_kernel<NT, T>, a, tA, tW);
+  return cudaLaunchKernelEx(&cfg, f8_gemm_small_kernel<NT, PER, T>, a, tA, tW);
+}
+
+template <int NT, typename T>
+cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
+  // two CTAs per SM with more stages each, or three, where there are weight tiles for more than two (64 rows, 448 tiles of 64 blocks: 92 and
+  // 81 us; 250 tiles of 32 blocks: 27 and 34)
+  if (NT <= 64 && (a.N + 127) / 128 > 2 * sm_count()) return launch_small_per<NT, NT <= 64 ? 3 : 2, T>(a, st);
+  return launch_small_per<NT, 2, T>(a, st);
 }
 
 template <typename T>
