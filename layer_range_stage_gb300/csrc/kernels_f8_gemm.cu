@@ -721,9 +721,10 @@ cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_t(const F8GemmArgs& a, cudaStream_t st) {
   if (!a.stall) {  // (the tests' stalled calls go where there is something to wait for)
-    // (8 rows, 57344 x 8192: 72 us, 89 by weight tiles; 16 rows: 92 and 89, but 9.5 and 13 with 6144 x 4096; 32 rows: 220 and 84)
+    // (8 rows, 57344 x 8192: 72 us, as by weight tiles; one row, 6144 x 4096: 6.7 and 13.  16 rows, whose reads from L2 are as many as the
+    // weights': 6144 x 4096 9.6 us, 10.9 by weight tiles; 32000 x 4096 30 and 24.  32 rows: 220 and 80 for 57344 x 8192)
     if (a.M <= 8) return launch_few<1, 2, T>(a, st);
-    if (a.M <= 16) return launch_few<2, 2, T>(a, st);
+    if (a.M <= 16 && (a.N + 127) / 128 <= sm_count() / 2) return launch_few<2, 2, T>(a, st);
   }
   if (a.M <= 16) return launch_small<16, T>(a, st);
   if (a.M <= 32) return launch_small<32, T>(a, st);
