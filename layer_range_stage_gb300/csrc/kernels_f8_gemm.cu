@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < 2 * S; ++j) whole = whole && !*cluster.map_shared_rank(const_cast<int*>(abort_flag), j);
     const int m0 = pair % tiles_m * kBM + 128 * rank, n0 = pair / tiles_m * kBN;
     T* y = static_cast<T*>(a.y);
+#pragma unroll 2
     for (int e = tid; e < 128 / S * (kBN / 4); e += kThreads) {
       const int r = 128 / S * share + e / (kBN / 4), u = e % (kBN / 4), gm = m0 + r, gn = n0 + 4 * u;
       if (gm >= a.M || gn >= a.N) continue;
@@ -510,11 +511,19 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
     }
     cluster.sync();
     const int total = a.M * 128, e1 = (int)((int64_t)total * (rank + 1) / C);
-    for (int e = (int)((int64_t)total * rank / C) + tid; e < e1; e += kSmallThreads) {
-      float v = 0.f;
-      for (int r = 0; r < C; ++r) v += cluster.map_shared_rank(sums, r)[e];
-      const int n = n0 + (e & 127);
-      if (n < a.N) y[(int64_t)(e >> 7) * a.y_stride + n] = from_f32<T>(v);
+    constexpr int kAt = 4;  // values of a thread whose reads of the other CTAs are in flight together
+    for (int e = (int)((int64_t)total * rank / C) + tid; e < e1; e += kAt * kSmallThreads) {
+      float v[kAt] = {};
+      for (int r = 0; r < C; ++r) {
+        const float* from = cluster.map_shared_rank(sums, r);
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) v[i] += e + i * kSmallThreads < e1 ? from[e + i * kSmallThreads] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAt; ++i) {
+        const int at = e + i * kSmallThreads, n = n0 + (at & 127);
+        if (at < e1 && n < a.N) y[(int64_t)(at >> 7) * a.y_stride + n] = from_f32<T>(v[i]);
+      }
     }
     cluster.sync();  // the others read these sums until here
   }
@@ -661,8 +670,8 @@ cudaError_t launch_big(const F8GemmArgs& a, cudaStream_t st) {
   static_assert(G::kStages * G::kStage >= 128 * kBN * 4, "the sums take the stages' place");
   const int64_t tiles = (int64_t)((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
   // few tiles: two pairs share one's K (256 x 4096 x 14336, 16 tiles: 38 us, 60 with one; with four pairs, whose clusters of eight SMs do
-  // not all find a place at once, 48)
-  const int S = 2 * tiles <= 64 && a.nkb >= 8 ? 2 : 1;
+  // not all find a place at once, 48), unless K is short (256 x 4096 x 2048, 16 blocks: 13.9 us, 13.1 with one; 200 x 1001 x 4096, 32: 17 and 22)
+  const int S = 2 * tiles <= 64 && a.nkb >= 24 ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * S * (unsigned)std::min<int64_t>(tiles, std::max(1, sm_count() / 2)));
   cfg.blockDim = dim3(kThreads);
