@@ -587,6 +587,46 @@ def test_products_of_every_kernel_captured_and_at_once(B, M):
     assert all(torch.equal(o, e) for o, e in zip(outs, want))
 
 
+def test_first_calls_inside_a_capture(B):
+    """In a new process whose first calls are captured ones: nothing that a call does once may be what a capture forbids."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import layer_range_stage_gb300 as L
+c = dict(device="cuda")
+x = torch.randn(200, 1024, **c)
+w, sw = torch.randint(0, 120, (512, 1024), dtype=torch.uint8, **c), torch.rand(4, 8, **c)
+f = torch.rand(32, dtype=torch.float64, **c)
+sizes = (3, 12, 40, 100, 200)
+q = [torch.zeros(n, 1024, dtype=torch.uint8, **c) for n in sizes]
+s = [torch.zeros(8, n, **c) for n in sizes]
+def buffers():
+    return [torch.zeros(n, 512, **c) for n in sizes], [torch.zeros(n, 2, dtype=torch.int32, **c) for n in sizes]
+def go(y, ids):
+    for n, a, b, z, i in zip(sizes, q, s, y, ids):
+        L.stage_op_norm_f8(x[:n], a, b, gamma=x[0])
+        L.stage_op_f8_gemm(a, b, w, sw, z)
+        L.stage_op_rope(z.view(n, 8, 64), None, torch.arange(n, dtype=torch.int32, **c), f)
+        L.stage_op_logprobs(z, top_ids=i)
+got = buffers()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    go(*got)
+graph.replay()
+want = buffers()
+go(*want)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for u, v in zip(got, want) for a, b in zip(u, v))
+assert all(z.abs().max() > 0 for z in want[0])
+print("same")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=240)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_refusals_of_the_binding_on_device_tensors(B):
     c = dict(device="cuda")
     x, q, s = torch.zeros(3, 256, **c), torch.zeros(3, 256, dtype=F8, **c), torch.zeros(2, 3, **c)
