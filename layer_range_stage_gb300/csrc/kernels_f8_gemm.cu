@@ -210,14 +210,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(sm + s * G::kStage + G::kTileA, &tB, (kb0 + kb) * kBK, n0, bar);
         }
       }
-      if (*abort_flag) {  // nothing may still be landing in shared memory when the CTA leaves
-        if (rank == 0) {
-          for (int k = max(0, it - G::kStages); k < it; ++k)
-            mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
-        } else {  // only the first CTA can see these land: a time in which they have
-          const uint64_t t0 = global_ns();
-          while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
-        }
+      // Nothing may still be landing in shared memory when the CTAs leave, whoever has given up.  The first CTA sees both's copies land; the
+      // second one's leaves after it, and where it gave up itself, after a time in which they have.
+      if (rank == 0) {
+        for (int k = max(0, it - G::kStages); k < it; ++k)
+          mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
+      } else if (*abort_flag) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       constexpr uint32_t idesc = idesc_f8_f32(kBM, kBN);
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_pair(&B->empty[s], first);
           umma_commit_pair(&B->done[d], first);
         }
-      if (!ok && it > 0) {  // given up: the products already issued finish before TMEM is released
+      if (it > 0) {  // the products finish before TMEM is released, whoever has given up
         umma_commit_pair(&B->drain, first);
         mbar_wait(&B->drain, 0u, kDrainNs);
       }
@@ -421,9 +421,9 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
         tma_load_2d(sm + s * G::kStage, &tW, (k0 + it) * kBK, n0, &B->full[s]);
         tma_load_2d(sm + s * G::kStage + G::kTileW, &tA, (k0 + it) * kBK, 0, &B->full[s]);
       }
-      if (*abort_flag)  // nothing may still be landing in shared memory when the CTA leaves
-        for (int k = max(0, it - G::kStages); k < it; ++k)
-          mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
+      // nothing may still be landing in shared memory when the CTA leaves, whoever has given up
+      for (int k = max(0, it - G::kStages); k < it; ++k)
+        mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
     }
   } else if (warp == 5) {
     if (lane == 0) {
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
         umma_commit(&B->empty[s]);
         umma_commit(&B->done[d]);
       }
-      if (it < nk && it > 0) {  // given up: the products already issued finish before TMEM is released
+      if (it > 0) {  // the products finish before TMEM is released, whoever has given up
         umma_commit(&B->drain);
         mbar_wait(&B->drain, 0u, kDrainNs);
       }
