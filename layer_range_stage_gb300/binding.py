@@ -719,6 +719,9 @@ def stage_op_kv4_attention(cache, q, cu_q, seq_len, table, out, max_q: int, max_
 
 # They are called several times per block, so they read each property of a tensor once.
 
+_TOO_MANY = "a size beyond 31 bits"  # a C int would drop what lies above its bits
+
+
 def _launch_on(stream, dev: int) -> int:
     """The stream to launch on, for tensors that are all on device `dev`: the current one, since a launch goes there."""
     if dev < 0:
@@ -783,6 +786,8 @@ def stage_op_norm_f8(x, q=None, scale=None, gamma=None, eps: float = 1e-5, resid
         _invalid("resid and resid_out go together, and so do q and scale")
     stream = _launch_on(stream, dev)
     n_tok, n = shape
+    if (n_tok | n) >> 31:
+        _invalid(_TOO_MANY)
     xp, xt, xs = _matrix(x, shape, dev, "x")
     gp = None
     rp = rt = rs = op = os_ = qp = qs = sp = ss = yp = ys = 0
@@ -816,6 +821,8 @@ def stage_op_f8_gemm(a, a_scale, w, w_scale, out, error=None, stream=None) -> No
     stream = _launch_on(stream, dev)
     m, k = sa
     n = sw[0]
+    if (m | n | k) >> 31:
+        _invalid(_TOO_MANY)
     kb = (k + 127) // 128
     ap, as_ = _f8(a, sa, dev, "a")
     wp, ws = _f8(w, sw, dev, "w")
@@ -831,6 +838,8 @@ def stage_op_f8_gemm(a, a_scale, w, w_scale, out, error=None, stream=None) -> No
 
 def stage_op_f8_debug_stall(calls: int) -> None:
     """The next calls of stage_op_f8_gemm by this thread run out of time (tests of that path)."""
+    if _beyond_c_int(calls):
+        _invalid("calls outside [0, 16]")
     _opcheck(lib().stage_op_f8_debug_stall(calls))
 
 
@@ -882,6 +891,8 @@ def stage_op_rope(q, k, pos, freqs, q_out=None, k_out=None, interleaved: bool = 
     elif k_out is not None:
         _invalid("k_out without k")
     half = freqs.numel()
+    if (n_tok | hq | hk | d | half << 1) >> 31:
+        _invalid(_TOO_MANY)
     rc = (_lib or lib()).stage_op_rope(qp, qs, hq, kp, ks, hk, d, dt, _array(pos, torch.int32, n_tok, dev, "pos"), n_tok,
                                        _array(freqs, torch.float64, half, dev, "freqs"), 2 * half, 1 if interleaved else 0, scale, qop,
                                        qos, kop, kos, stream)
@@ -920,6 +931,8 @@ def stage_op_logprobs(logits, tokens=None, logprob=None, entropy=None, rank=None
             _invalid(f"top_logprobs must be [{n}, k], k that of top_ids")
         top = top_logprobs.shape[1]
         bp = _array(top_logprobs, f32, n * top, dev, "top_logprobs")
+    if (n | vocab | top) >> 31:
+        _invalid(_TOO_MANY)
     rc = (_lib or lib()).stage_op_logprobs(zp, zt, zs, n, vocab, tp, lp, ep, rp, top, ip, bp, stream)
     if rc:
         _opcheck(rc)

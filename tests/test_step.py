@@ -154,6 +154,64 @@ def test_binding_refuses_host_tensors_shapes_and_types():
         L.stage_op_norm_f8(x, q, s, resid=x)
 
 
+class Sized:
+    """What the binding asks of a device tensor, at sizes that no test allocates: rows side by side."""
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, shape
+
+    def get_device(self):
+        return 0
+
+    def stride(self):
+        return tuple(math.prod(self.shape[i + 1:]) for i in range(len(self.shape)))
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_binding_refuses_sizes_that_a_c_int_would_cut_off(monkeypatch):
+    """With 2^32 rows cut to none a call would return and do nothing."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(L.binding, "_launch_on", lambda stream, dev: 0)
+    f32, i32, f64, f8 = torch.float32, torch.int32, torch.float64, torch.float8_e4m3fn
+    for n in (1 << 32, (1 << 32) + (1 << 40), 1 << 31):
+        calls = [
+            lambda: L.stage_op_norm_f8(Sized(f32, n, 256), Sized(f8, n, 256), Sized(f32, 2, n)),
+            lambda: L.stage_op_norm_f8(Sized(f32, 0, n + 256), y=Sized(f32, 0, n + 256)),
+            lambda: L.stage_op_f8_gemm(Sized(f8, n, 256), Sized(f32, 2, n), Sized(f8, 128, 256), Sized(f32, 1, 2), Sized(f32, n, 128)),
+            lambda: L.stage_op_f8_gemm(Sized(f8, 0, 256), Sized(f32, 2, 0), Sized(f8, n + 128, 256), Sized(f32, n // 128 + 1, 2), Sized(f32, 0, n + 128)),
+            lambda: L.stage_op_f8_gemm(Sized(f8, 0, n + 256), Sized(f32, n // 128 + 2, 0), Sized(f8, 128, n + 256), Sized(f32, 1, n // 128 + 2), Sized(f32, 0, 128)),
+            lambda: L.stage_op_rope(Sized(f32, n, 2, 64), None, Sized(i32, n), Sized(f64, 32)),
+            lambda: L.stage_op_rope(Sized(f32, 0, n + 2, 64), None, Sized(i32, 0), Sized(f64, 32)),
+            lambda: L.stage_op_rope(Sized(f32, 0, 2, 64), Sized(f32, 0, n + 2, 64), Sized(i32, 0), Sized(f64, 32)),
+            lambda: L.stage_op_rope(Sized(f32, 0, 2, n + 64), None, Sized(i32, 0), Sized(f64, 32)),
+            lambda: L.stage_op_rope(Sized(f32, 0, 2, 64), None, Sized(i32, 0), Sized(f64, n + 32)),
+            lambda: L.stage_op_logprobs(Sized(f32, n, 50), entropy=Sized(f32, n)),
+            lambda: L.stage_op_logprobs(Sized(f32, 0, n + 50), entropy=Sized(f32, 0)),
+            lambda: L.stage_op_logprobs(Sized(f32, 0, 50), top_ids=Sized(i32, 0, n + 3)),
+            lambda: L.stage_op_f8_debug_stall(n if n > 1 << 31 else 1 << 33),
+        ]
+        for i, call in enumerate(calls):
+            with pytest.raises(L.StageError) as e:
+                call()
+            assert e.value.code == L.STAGE_E_INVALID, (n, i)
+    # the same calls of ordinary sizes reach the entry points, which do nothing for no rows
+    L.stage_op_norm_f8(Sized(f32, 0, 256), Sized(f8, 0, 256), Sized(f32, 2, 0))
+    L.stage_op_f8_gemm(Sized(f8, 0, 256), Sized(f32, 2, 0), Sized(f8, 128, 256), Sized(f32, 1, 2), Sized(f32, 0, 128))
+    L.stage_op_rope(Sized(f32, 0, 2, 64), Sized(f32, 0, 2, 64), Sized(i32, 0), Sized(f64, 32))
+    L.stage_op_logprobs(Sized(f32, 0, 50), top_ids=Sized(i32, 0, 3))
+
+
 def test_the_product_has_the_registers_that_its_warpgroups_share_out(tmp_path):
     """From a kernel with fewer, the warpgroup that asks for more would wait forever (the launch refuses it)."""
     import os
