@@ -32,7 +32,7 @@ extern "C" {
  *   per block of 128 columns:      a = max(largest |y|, 2^-100), scale = a / 448, code = e4m3(y * (448 / a))
  * with every quotient and product rounded to nearest in float32 and the code to nearest, ties to even: the same
  * codes on any machine.  (r is the float32 next to the exact one but for one row in about a million, where it
- * may be the neighbour, and where the mean is outside [2^-90, 2^90] it may be off by two units.)
+ * may be the neighbour.)
  *   x_dev: [n_tok] rows of x_dtype at x_stride elements; resid_dev, resid_out_dev: rows of resid_dtype, which is
  *     x_dtype or STAGE_F32; resid_out_dev may be resid_dev, with the same stride.
  *   gamma_dev: float32 [n]; eps >= 0.
@@ -40,8 +40,8 @@ extern "C" {
  *     elements (block after block, as stage_op_f8_gemm reads them).  Both may be NULL when y_dev is given.
  *   y_dev: y rounded once to x_dtype, rows at y_stride elements, or NULL.
  * Bytes between a row's n columns and the next row are left as they were.  A row whose sum of squares is no finite
- * float32 gives NaN throughout (with gamma); a block that holds an infinity or a NaN gets a scale that is not finite: all of it
- * reads as NaN.  Apart from resid_out = resid no output may overlap an input or another output.
+ * float32, or whose mean + eps is below 2^-256 (zeros with eps = 0), gives NaN throughout (with gamma); a
+ * block that holds an infinity or a NaN gets a scale that is not finite: all of it reads as NaN.  Apart from resid_out = resid no output may overlap an input or another output.
  * Rows need their elements' alignment only; with rows and bases at multiples of four elements they are read and written four
  * elements at a time.  Runs on `stream`.  n_tok = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned
  * pointers, types, n_tok outside [0, 2^24], n outside [1, 32768], strides below a row or above 2^32, eps negative

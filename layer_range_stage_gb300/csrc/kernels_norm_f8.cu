@@ -4,14 +4,15 @@
 // block of 128 columns at a time, four neighbouring columns a lane, so that a block's largest value is one warp
 // reduction and its codes are one store of 128 bytes.  The bytes in and out are its floor; what bounds it is the chain from a row's
 // loads over its sum to its stores, with 32 warps on an SM: 2048 x 4096 (bfloat16 onto float32) 18 us, 5.1 TB/s; 16411 x 8192 in
-// bfloat16 212 us, 4.5 TB/s (its warps' sums and roots are a third of the instructions there; one warp that finishes for the row: 231,
+// bfloat16 207 us, 4.6 TB/s (its warps' sums and roots are a third of the instructions there; one warp that finishes for the row: 231,
 // for its second barrier); one row of 4096 2.7 us.
 //
 // The codes are defined by float32 roundings, so two machines agree if they agree on r = fl(1 / sqrt(mean + eps)).  A float32
 // sum would not do: its last bits depend on its order, and where r differs by one unit so does a code now and then.
 // The sum is held as an unevaluated pair of float32 (every addition's error is caught exactly and added up: Knuth's
 // two-sum), about 2^-45 of it, and r comes from the reciprocal square root by one Newton step whose residual
-// 1 - m r^2 is formed in pairs as well, so that its only rounding that counts is the last.
+// 1 - m r^2 is formed in pairs as well, so that its only rounding that counts is the last.  Means beyond 2^+-90, whose squares or root
+// leave float32's range on the way, are scaled by a power of two first.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -44,8 +45,8 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   return r;
 }
 
-// fl(1 / sqrt(sum / n + eps))
-__device__ __forceinline__ float recip_root(Pair sum, float n, float eps) {
+// sum / n + eps
+__device__ __forceinline__ Pair mean_of(Pair sum, float n, float eps) {
   const float q = __fdiv_rn(sum.hi, n);
   const float rem = __fadd_rn(__fmaf_rn(-q, n, sum.hi), sum.lo);
   Pair m;
@@ -53,6 +54,12 @@ __device__ __forceinline__ float recip_root(Pair sum, float n, float eps) {
   two_sum(q, eps, m.hi, e);
   m.lo = __fadd_rn(__fdiv_rn(rem, n), e);
   two_sum(m.hi, m.lo, m.hi, m.lo);
+  return m;
+}
+// fl(1 / sqrt(m)) where it lies between these bounds: beyond them m's squares, r^2 or what r^2 leaves out are no float32, and what comes
+// out is beyond the bounds too, or NaN
+constexpr float kLeastRoot = 0x1p-45f, kMostRoot = 0x1p45f;
+__device__ __forceinline__ float recip_root(Pair m) {
   const float r = rsqrtf(m.hi);
   const float p = __fmul_rn(r, r), pe = __fmaf_rn(r, r, -p);
   const float t = __fmul_rn(m.hi, p), te = __fmaf_rn(m.hi, p, -t);
@@ -133,6 +140,61 @@ __device__ __forceinline__ void store4(T* row, int at, int n, const Four<T>& p) 
   }
 }
 
+// The sum of a row from its lanes' sums, for all of them.
+__device__ __forceinline__ Pair row_sum(float2 hi, float2 lo, Pair* part) {
+  const int lane = threadIdx.x & 31, W = blockDim.x >> 5;
+  Pair s = add(Pair{hi.x, lo.x}, Pair{hi.y, lo.y});
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Pair t;
+    t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+    t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+    s = add(s, t);
+  }
+  if (W > 1) {  // one row per CTA then
+    if (lane == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = lane < W ? part[lane] : Pair{0.f, 0.f};
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      Pair t;
+      t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
+      t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
+      s = add(s, t);
+    }
+    s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+    s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
+  }
+  return s;
+}
+
+// 1 / sqrt(mean + eps) where that is beyond kLeastRoot or kMostRoot, from the row itself: such rows are rare, and read again they cost the
+// others no registers.
+template <bool VEC, typename T>
+__device__ __noinline__ float far_root(const T* row, int at0, int step, int blocks, int n, float eps, Pair s, Pair* part) {
+  if (!(mean_of(s, (float)n, eps).hi < 1.f)) {  // (a sum that is no number stays one)
+    const Pair m = mean_of(Pair{__fmul_rn(s.hi, 0x1p-100f), __fmul_rn(s.lo, 0x1p-100f)}, (float)n, __fmul_rn(eps, 0x1p-100f));
+    return __fmul_rn(recip_root(m), 0x1p-50f);
+  }
+  // Squares have lost bits, or all of them: once more with the values (below 2^-37 then) times 2^80, of which the smallest number's
+  // square still has its 46 bits.
+  float2 hi = make_float2(0.f, 0.f), lo = hi;
+#pragma unroll 1
+  for (int c = 0; c < blocks; ++c) {
+    const Words<T> w = load4<VEC>(row, at0 + c * step, n);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 v = __fmul2_rn(make_float2(value_of(w, 2 * i), value_of(w, 2 * i + 1)), make_float2(0x1p80f, 0x1p80f)), p = __fmul2_rn(v, v);
+      float2 e;
+      two_sum2(hi, p, hi, e);
+      lo = __fadd2_rn(lo, __fadd2_rn(e, __ffma2_rn(v, v, make_float2(-p.x, -p.y))));
+    }
+  }
+  if (blockDim.x > 32) __syncthreads();  // the first sum's parts have been read
+  const Pair m = mean_of(row_sum(hi, lo, part), (float)n, __fmul_rn(__fmul_rn(eps, 0x1p80f), 0x1p80f));
+  return m.hi < 0x1p-96f ? __int_as_float(0x7FC00000) : __fmul_rn(recip_root(m), 0x1p80f);  // beyond float32 below 2^-256
+}
+
 // TR: the residual's type, or void.  W warps of a row (blockDim.x / 32), blockDim.y rows per CTA, CH blocks of 128 per warp.  All of a
 // row is asked for before anything of it is used; the widest rows, whose values take the registers, four blocks at a time.
 template <typename TX, typename TR, int CH, bool VEC>
@@ -197,29 +259,24 @@ __global__ void __launch_bounds__(512, CH <= 4 ? 2 : 1) norm_f8_kernel(const Nor
           if (!kExact) e = __fadd2_rn(e, __ffma2_rn(v, v, make_float2(-p.x, -p.y)));
           lo = __fadd2_rn(lo, e);
         }
-      Pair s = add(Pair{hi.x, lo.x}, Pair{hi.y, lo.y});
+      const Pair s = row_sum(hi, lo, part);
+      float r = recip_root(mean_of(s, (float)a.n, a.eps));
+      if (__builtin_expect(!(r >= kLeastRoot && r <= kMostRoot), 0)) {
+        using TH = typename std::conditional<kResid, TRv, TX>::type;
+        const TH* back;
+        if constexpr (kResid)
+          back = out;
+        else
+          back = static_cast<const TX*>(a.x) + (int64_t)row * a.x_stride;
+        r = far_root<VEC>(back, at0, step, CH, n, a.eps, s, part);
+        if constexpr (kBatch < CH)  // the widest rows have no registers to outlive the call (4096 x 28672 in bfloat16: 300 us, 336 if they do)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        Pair t;
-        t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
-        t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-        s = add(s, t);
+          for (int c = 0; c < CH; ++c) {
+            const Words<TH> v = load4<VEC>(back, at0 + c * step, n);
+            h[c][0] = make_float2(value_of(v, 0), value_of(v, 1));
+            h[c][1] = make_float2(value_of(v, 2), value_of(v, 3));
+          }
       }
-      if (W > 1) {  // one row per CTA then
-        if (lane == 0) part[w] = s;
-        __syncthreads();
-        s = lane < W ? part[lane] : Pair{0.f, 0.f};
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          Pair t;
-          t.hi = __shfl_xor_sync(0xffffffffu, s.hi, o);
-          t.lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-          s = add(s, t);
-        }
-        s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
-        s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
-      }
-      const float r = recip_root(s, (float)a.n, a.eps);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const Words<float> g = load4<VEC>(a.gamma, at0 + c * step, a.n);

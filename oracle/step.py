@@ -47,7 +47,7 @@ def norm_f8(x, resid=None, gamma=None, eps: float = 1e-5, store=lambda h: h):
         if gamma is not None:
             m = np.array([math.fsum(v) if np.isfinite(v).all() else np.nan for v in h.astype(np.float64) ** 2]) / n
             r = (1.0 / np.sqrt(m + np.float64(f32(eps)))).astype(f32)
-            r = np.where(m * n >= 2.0 ** 128, f32(np.nan), r)   # beyond float32's range
+            r = np.where((m * n >= 2.0 ** 128) | (m + np.float64(f32(eps)) < 2.0 ** -256), f32(np.nan), r)   # beyond float32's range
             y = (h * r[:, None]) * np.asarray(gamma, f32)
         nb = -(-n // 128)
         codes, scales = np.zeros((n_tok, n), np.uint8), np.zeros((nb, n_tok), f32)

@@ -163,6 +163,42 @@ def test_norm_of_zeros_tiny_huge_and_no_numbers(B):
     check_norm(B, x[7:], None, g)
 
 
+@pytest.mark.parametrize("xt,rt", [("f32", None), ("f32", "f32"), ("bf16", None), ("bf16", "f32")])
+@pytest.mark.parametrize("n", [100, 384, 4096, 8191, 8192, 14336, 28672])
+def test_norm_of_tiny_rows_and_huge_ones(B, xt, rt, n):
+    """Means whose squares, roots or squared roots leave float32's range: no eps, or one as small."""
+    rng = np.random.default_rng(n)
+    sizes = 10.0 ** np.array([-12.0, -13.5, -14, -18, -19, -19.5, -20, -22, -24, -30, -37, -38.5, -40, -43, 13, 14, 15, 16.5])
+    x = rng.standard_normal((len(sizes), n)) * sizes[:, None]
+    x[5, 1:] = 0                                  # one number among zeros
+    resid = None if rt is None else rng.standard_normal(x.shape) * sizes[:, None]
+    gamma = (1 + 0.3 * rng.standard_normal(n)).astype(np.float32)
+    for eps in (0.0, 1e-42, 3e-38, 1e-30, 2.0 ** -90, 1e-20):
+        with np.errstate(all="ignore"):
+            check_norm(B, x, resid, gamma, xt, rt or "f32", eps=eps)
+    zero = np.zeros((5, n))
+    with np.errstate(all="ignore"):
+        check_norm(B, zero, None, gamma, xt)
+        check_norm(B, zero, None, gamma, xt, eps=1e-42)
+        check_norm(B, zero, None, gamma, xt, eps=0.0)      # 0 / 0
+
+
+def test_norm_up_to_the_last_sum_of_squares(B):
+    """Sums of squares on both sides of 2^128, and an eps that takes their mean beyond it."""
+    n = 256
+    x = np.zeros((5, n), np.float32)
+    for i, at in enumerate((0.5, 0.999, 1.01, 0.97, 3.0)):
+        x[i] = np.sqrt(at * 2.0 ** 128 / n)
+        x[i, ::2] *= -1
+    sums = (x.astype(np.float64) ** 2).sum(1)
+    assert (sums[[0, 1, 3]] < 2.0 ** 128).all() and (sums[[2, 4]] > 2.0 ** 128).all()
+    for eps in (1e-5, 1e38, 3.4e38):
+        with np.errstate(all="ignore"):
+            check_norm(B, x, None, np.ones(n, np.float32), eps=eps)
+            y = run_norm(B, x, None, np.ones(n, np.float32), "f32", "f32", eps=eps)[3]
+        assert torch.isnan(y).all(1).tolist() == [False, False, True, False, True]
+
+
 def test_norm_ties_of_the_codes(B):
     """Every value halfway between two codes, at a scale of one."""
     v = step.e4m3_values()[:127]
