@@ -74,6 +74,12 @@ STAGE_API int stage_op_f8_gemm(const void* a_dev, int64_t a_stride, const float*
  * STAGE_E_INVALID (calls outside [0, 16]). */
 STAGE_API int stage_op_f8_debug_stall(int calls);
 
+/* For tests: in the next `calls` calls of stage_op_f8_gemm by this thread one product of each pair of SMs comes after the others have
+ * stopped waiting for it (M above 128 and more tiles of 256 x 256 than there are pairs; other calls are as ever).  What it
+ * misses is NaN, everything else right, and the error word is set.  calls = 0 takes it back.  Host only.  Errors: STAGE_E_INVALID
+ * (calls outside [0, 16]). */
+STAGE_API int stage_op_f8_debug_late(int calls);
+
 /* How the frequencies of rotary positions are scaled for contexts `factor` times as long as first_len. */
 enum {
   STAGE_ROPE_PLAIN = 0,  /* f_i = theta^(-2 i / rot_dim) */

@@ -138,6 +138,7 @@ _SIGS = {
     "stage_op_f8_gemm": (C.c_int, [C.c_void_p, C.c_int64] * 3 + [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int,
                                                                  C.c_int64, C.c_void_p, C.c_void_p]),
     "stage_op_f8_debug_stall": (C.c_int, [C.c_int]),
+    "stage_op_f8_debug_late": (C.c_int, [C.c_int]),
     "stage_op_rope_freqs": (C.c_int, [C.c_int, C.c_double, C.c_int] + [C.c_double] * 4 + [C.POINTER(C.c_double),
                                                                                         C.POINTER(C.c_float)]),
     "stage_op_rope": (C.c_int, [C.c_void_p, C.c_int64, C.c_int] * 2 + [C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
@@ -841,6 +842,13 @@ def stage_op_f8_debug_stall(calls: int) -> None:
     if _beyond_c_int(calls):
         _invalid("calls outside [0, 16]")
     _opcheck(lib().stage_op_f8_debug_stall(calls))
+
+
+def stage_op_f8_debug_late(calls: int) -> None:
+    """In the next calls of stage_op_f8_gemm by this thread a product of each pair of SMs comes too late (tests of that path)."""
+    if _beyond_c_int(calls):
+        _invalid("calls outside [0, 16]")
+    _opcheck(lib().stage_op_f8_debug_late(calls))
 
 
 def stage_op_rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: int = STAGE_ROPE_PLAIN, factor: float = 1.0,

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     regs_down<kRegsRoles>();
-    if (warp == 0 && lane == 0 && !a.stall) {
+    if (warp == 0 && lane == 0 && a.stall != kStallCopies) {
       int it = 0;
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
@@ -228,6 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = it % G::kStages, d = it & 1;
           if (!(ok = fwait(&B->full[s], (uint32_t)(it / G::kStages) & 1u, abort_flag, a.error))) break;
           if (it >= 2 && !(ok = fwait(&B->free_[d], (uint32_t)(it / 2 + 1) & 1u, abort_flag, a.error))) break;
+          if (a.stall == kStallLate && it == nkb) {  // (tests) the second tile's first product comes when the others have given it up
+            const uint64_t t0 = global_ns();
+            while (!*abort_flag && global_ns() - t0 < 2 * kWaitNs) __nanosleep(1000);
+          }
           tc_fence_after();
           const uint32_t pa = smem_u32(sm + s * G::kStage), pb = pa + G::kTileA;
 #pragma unroll
@@ -267,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const int d = it & 1;
-        ok = __all_sync(0xffffffffu, fwait(&B->done[d], (uint32_t)(it / 2) & 1u, abort_flag, a.error));
+        // a warp that has given up once is out of step for good: what is left of its tiles is NaN too
+        ok = ok && __all_sync(0xffffffffu, fwait(&B->done[d], (uint32_t)(it / 2) & 1u, abort_flag, a.error));
         if (!ok) break;
         tc_fence_after();
         const float f1 = fa[kb & 1] * fw[kb & 1];
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
   for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
   bool ok = true;
   if (warp == 4) {
-    if (lane == 0 && !a.stall) {
+    if (lane == 0 && a.stall != kStallCopies) {
       int it = 0;
       for (; it < nk; ++it) {
         const int s = it % G::kStages;
@@ -729,7 +734,7 @@ cudaError_t launch_small(const F8GemmArgs& a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t launch_t(const F8GemmArgs& a, cudaStream_t st) {
-  if (!a.stall) {  // (the tests' stalled calls go where there is something to wait for)
+  if (a.stall != kStallCopies) {  // (the tests' stalled calls go where there is something to wait for)
     // (8 rows, 57344 x 8192: 72 us, as by weight tiles; one row, 6144 x 4096: 6.7 and 13.  16 rows, whose reads from L2 are as many as the
     // weights': 6144 x 4096 9.6 us, 10.9 by weight tiles; 32000 x 4096 30 and 24.  32 rows: 220 and 80 for 57344 x 8192)
     if (a.M <= 8) return launch_few<1, 2, T>(a, st);

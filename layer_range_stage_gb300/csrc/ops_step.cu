@@ -21,7 +21,7 @@ bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0;
 bool known_dtype(int dtype) { return dtype == STAGE_F32 || dtype == STAGE_F16 || dtype == STAGE_BF16; }
 int elem_bytes(int dtype) { return dtype == STAGE_F32 ? 4 : 2; }
 constexpr int kMaxRows = 1 << 24;
-thread_local int g_stall = 0;  // calls of stage_op_f8_gemm that are to run out of time (tests)
+thread_local int g_stall = 0, g_late = 0;  // calls of stage_op_f8_gemm that are to run out of time (tests)
 
 // Rows of `width` elements at a stride; int64 products cannot overflow within these bounds.
 int check_rows(const void* p, int64_t stride, int64_t width, int bytes, const char* what) {
@@ -137,7 +137,10 @@ int stage_op_f8_gemm(const void* a_dev, int64_t a_stride, const float* a_scale_d
   g.vec = rows_at(y_dev, y_stride, yb, 16);
   if (g_stall > 0) {
     --g_stall;
-    g.stall = 1;
+    g.stall = lrs::kStallCopies;
+  } else if (g_late > 0) {
+    --g_late;
+    g.stall = lrs::kStallLate;
   }
   const cudaError_t e = lrs::launch_f8_gemm(g, y_dtype, (cudaStream_t)stream);
   return e == cudaSuccess ? STAGE_OK : op_cuda(e, "f8 gemm");
@@ -150,6 +153,16 @@ int stage_op_f8_gemm(const void* a_dev, int64_t a_stride, const float* a_scale_d
 int stage_op_f8_debug_stall(int calls) try {
   if (calls < 0 || calls > 16) return op_err(STAGE_E_INVALID, "calls outside [0, 16]");
   g_stall = calls;
+  return STAGE_OK;
+} catch (const std::exception& ex) {
+  return op_host_failure(ex.what());
+} catch (...) {
+  return op_host_failure("unknown exception");
+}
+
+int stage_op_f8_debug_late(int calls) try {
+  if (calls < 0 || calls > 16) return op_err(STAGE_E_INVALID, "calls outside [0, 16]");
+  g_late = calls;
   return STAGE_OK;
 } catch (const std::exception& ex) {
   return op_host_failure(ex.what());

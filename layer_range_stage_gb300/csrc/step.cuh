@@ -44,6 +44,8 @@ struct NormF8Args {
 };
 cudaError_t launch_norm_f8(const NormF8Args& a, int x_dtype, int resid_dtype, cudaStream_t st);
 
+// For tests: nothing is copied, so that the waits run out; one product of each pair of CTAs comes after its time.
+constexpr int kStallCopies = 1, kStallLate = 2;
 struct F8GemmArgs {
   const uint8_t* a = nullptr;
   const uint8_t* w = nullptr;
@@ -54,7 +56,7 @@ struct F8GemmArgs {
   int64_t a_stride = 0, w_stride = 0, sa_stride = 0, y_stride = 0;
   int M = 0, N = 0, K = 0, nkb = 0;
   int vec = 0;  // y's base and rows at multiples of 16 bytes
-  int stall = 0;  // tests: nothing is copied, so that the waits run out
+  int stall = 0;  // tests: kStallCopies or kStallLate
 };
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, int y_dtype, cudaStream_t st);
 

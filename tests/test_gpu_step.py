@@ -359,6 +359,49 @@ def test_product_that_runs_out_of_time(B):
         check_gemm(B, a, sa, w, sw)                # the next one is as ever
 
 
+@pytest.mark.parametrize("M,N,K", [(513, 12801, 300), (256, 512, 4096), (130, 300, 3200), (100, 700, 500), (40, 1300, 1500)])
+def test_product_that_runs_out_of_time_with_many_tiles_or_a_shared_k(B, M, N, K):
+    """(More tiles than pairs; K over two pairs, over a cluster's CTAs.)"""
+    rng = np.random.default_rng(M)
+    a, w = put_f8(random_f8(rng, M, K)), put_f8(random_f8(rng, N, K))
+    sa, sw = torch.ones(-(-K // 128), M, device="cuda"), torch.ones(-(-N // 128), -(-K // 128), device="cuda")
+    y, z = torch.zeros(M, N, device="cuda"), torch.zeros(M, N, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.stage_op_f8_debug_stall(1)
+    B.stage_op_f8_gemm(a, sa, w, sw, y, err)
+    torch.cuda.synchronize()
+    assert err.item() == 1 and torch.isnan(y).all()
+    err.zero_()
+    B.stage_op_f8_gemm(a, sa, w, sw, y, err)
+    B.stage_op_f8_gemm(a, sa, w, sw, z)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and torch.equal(y, z)
+
+
+@pytest.mark.parametrize("K", [200, 384])
+def test_product_that_comes_too_late(B, K):
+    """A product that completes after its readers have given up: it is not taken for the next tile's.  Three tiles or more for each pair."""
+    rng = np.random.default_rng(K)
+    M, N = 1000, 15360
+    kb = -(-K // 128)
+    ac, wc = random_f8(rng, M, K), random_f8(rng, N, K)
+    sa, sw = rng.uniform(0.5, 1, (kb, M)).astype(np.float32), rng.uniform(0.5, 1, (120, kb)).astype(np.float32)
+    a, w = put_f8(ac), put_f8(wc)
+    y = torch.zeros(M, N, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.stage_op_f8_debug_late(1)
+    B.stage_op_f8_gemm(a, dev(sa), w, dev(sw), y, err)
+    torch.cuda.synchronize()
+    assert err.item() == 1
+    got = y.double().cpu().numpy()
+    want, mag = step.f8_gemm(ac, sa, wc, sw)
+    some = ~np.isnan(got)
+    assert some.any() and not some.all()
+    err = np.abs(got - want)[some] / ((2.0 ** -16 + (kb + 3) * 2.0 ** -24) * mag)[some]
+    assert (err <= 1).all(), (err > 1).mean()
+    check_gemm(B, ac, sa, wc, sw)              # the next one is as ever
+
+
 # ------------------------------------------------------------------------------------------- rope
 
 def check_rope(B, q, k, pos, freqs, dtype="f32", interleaved=False, scale=1.0, gap=0, inplace=False):

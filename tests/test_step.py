@@ -154,6 +154,16 @@ def test_binding_refuses_host_tensors_shapes_and_types():
         L.stage_op_norm_f8(x, q, s, resid=x)
 
 
+def test_late_calls_are_counted_from_none_to_sixteen():
+    lib = L.lib()
+    for calls in (-1, 17, 1 << 20):
+        assert lib.stage_op_f8_debug_late(calls) == L.STAGE_E_INVALID and lib.stage_op_last_error().decode()
+    assert lib.stage_op_f8_debug_late(16) == L.STAGE_OK and lib.stage_op_f8_debug_late(0) == L.STAGE_OK
+    for calls in (17, 1 << 32, -(1 << 40)):
+        with pytest.raises(L.StageError):
+            L.stage_op_f8_debug_late(calls)
+
+
 class Sized:
     """What the binding asks of a device tensor, at sizes that no test allocates: rows side by side."""
 
