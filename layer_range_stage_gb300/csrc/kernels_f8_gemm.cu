@@ -674,17 +674,15 @@ cudaError_t launch_big(const F8GemmArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   static_assert(G::kStages * G::kStage >= 128 * kBN * 4, "the sums take the stages' place");
   const int64_t tiles = (int64_t)((a.M + kBM - 1) / kBM) * ((a.N + kBN - 1) / kBN);
-  // few tiles: two pairs share one's K (256 x 4096 x 14336, 16 tiles: 38 us, 60 with one; with four pairs, whose clusters of eight SMs do
-  // not all find a place at once, 48), unless K is short (256 x 4096 x 2048, 16 blocks: 13.9 us, 13.1 with one; 200 x 1001 x 4096, 32: 17 and 22)
-  const int S = 2 * tiles <= 64 && a.nkb >= 24 ? 2 : 1;
+  const BigSplit split = big_split(tiles, a.nkb, sm_count());
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * S * (unsigned)std::min<int64_t>(tiles, std::max(1, sm_count() / 2)));
+  cfg.gridDim = dim3(2 * split.S * split.clusters);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = G::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * S;
+  attr[0].val.clusterDim.x = 2 * split.S;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace lrs {
 
 // The types of stage_ops.h: STAGE_F32, STAGE_F16, STAGE_BF16 are 0, 1, 2.
@@ -58,6 +60,19 @@ struct F8GemmArgs {
   int vec = 0;  // y's base and rows at multiples of 16 bytes
   int stall = 0;  // tests: kStallCopies or kStallLate
 };
+// How the product of many rows shares `tiles` tiles of nkb blocks of K out on `sms` SMs: clusters of S pairs of CTAs, which share a tile's K.
+struct BigSplit {
+  int S;
+  unsigned clusters;
+};
+inline BigSplit big_split(int64_t tiles, int nkb, int sms) {
+  const int64_t most = std::max(1, sms / 2);
+  // Few tiles: two pairs share one's K (256 x 4096 x 14336, 16 tiles: 38 us, 60 with one; with four pairs, whose clusters of eight SMs do
+  // not all find a place at once, 48), unless K is short (256 x 4096 x 2048, 16 blocks: 13.9 us, 13.1 with one; 200 x 1001 x 4096, 32: 17 and
+  // 22).  Pairs that share a K have one tile each.
+  const int S = tiles <= std::min<int64_t>(32, most) && nkb >= 24 ? 2 : 1;
+  return {S, (unsigned)std::min(tiles, most)};
+}
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, int y_dtype, cudaStream_t st);
 
 struct RopeArgs {

@@ -154,6 +154,33 @@ def test_binding_refuses_host_tensors_shapes_and_types():
         L.stage_op_norm_f8(x, q, s, resid=x)
 
 
+def test_pairs_that_share_a_k_have_one_tile_each_however_many_sms(tmp_path):
+    """The kernel adds a cluster's sums up once: with more tiles than clusters those of all but the last would be lost."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "split.cu"
+    src.write_text("""
+#include <cstdio>
+#include "step.cuh"
+int main() {
+  int shared = 0;
+  for (int sms = 1; sms <= 200; ++sms)
+    for (long tiles = 1; tiles <= 300; ++tiles)
+      for (int nkb = 1; nkb <= 40; ++nkb) {
+        const lrs::BigSplit s = lrs::big_split(tiles, nkb, sms);
+        if (s.S < 1 || s.S > 2 || s.clusters < 1 || s.clusters > tiles || (s.S > 1 && s.clusters != tiles)) return printf("%d SMs, %ld tiles: %d, %u\\n", sms, tiles, s.S, s.clusters), 1;
+        shared += s.S == 2;
+      }
+  const lrs::BigSplit all = lrs::big_split(1 << 24, 112, 152);
+  return !(shared > 0 && all.S == 1 && all.clusters == 76);
+}
+""")
+    subprocess.run([lbuild.nvcc(), *lbuild.ARCH, "-std=c++17", "-I", os.path.join(root, "layer_range_stage_gb300", "csrc"), "-o", str(tmp_path / "split"), str(src)], check=True, capture_output=True)
+    r = subprocess.run([str(tmp_path / "split")], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
+
+
 def test_late_calls_are_counted_from_none_to_sixteen():
     lib = L.lib()
     for calls in (-1, 17, 1 << 20):
