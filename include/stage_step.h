@@ -74,10 +74,10 @@ STAGE_API int stage_op_f8_gemm(const void* a_dev, int64_t a_stride, const float*
  * STAGE_E_INVALID (calls outside [0, 16]). */
 STAGE_API int stage_op_f8_debug_stall(int calls);
 
-/* For tests: in the next `calls` calls of stage_op_f8_gemm by this thread one product of each pair of SMs comes after the others have
- * stopped waiting for it (M above 128 and more tiles of 256 x 256 than there are pairs; other calls are as ever).  What it
- * misses is NaN, everything else right, and the error word is set.  calls = 0 takes it back.  Host only.  Errors: STAGE_E_INVALID
- * (calls outside [0, 16]). */
+/* For tests: in the next `calls` calls of stage_op_f8_gemm by this thread one warp of each SM gives up on its second tile of 256 x 256,
+ * as if the product had come just too late (M above 128 and more such tiles than there are pairs of SMs; other calls are as ever).
+ * What it misses is NaN, everything else right, and the error word is set.  calls = 0 takes it back.  Host only.  Errors:
+ * STAGE_E_INVALID (calls outside [0, 16]). */
 STAGE_API int stage_op_f8_debug_late(int calls);
 
 /* How the frequencies of rotary positions are scaled for contexts `factor` times as long as first_len. */

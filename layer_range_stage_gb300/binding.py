@@ -845,7 +845,7 @@ def stage_op_f8_debug_stall(calls: int) -> None:
 
 
 def stage_op_f8_debug_late(calls: int) -> None:
-    """In the next calls of stage_op_f8_gemm by this thread a product of each pair of SMs comes too late (tests of that path)."""
+    """In the next calls of stage_op_f8_gemm by this thread a warp of each SM gives up just before its product comes (tests of that path)."""
     if _beyond_c_int(calls):
         _invalid("calls outside [0, 16]")
     _opcheck(lib().stage_op_f8_debug_late(calls))

@@ -228,10 +228,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = it % G::kStages, d = it & 1;
           if (!(ok = fwait(&B->full[s], (uint32_t)(it / G::kStages) & 1u, abort_flag, a.error))) break;
           if (it >= 2 && !(ok = fwait(&B->free_[d], (uint32_t)(it / 2 + 1) & 1u, abort_flag, a.error))) break;
-          if (a.stall == kStallLate && it == nkb) {  // (tests) the second tile's first product comes when the others have given it up
-            const uint64_t t0 = global_ns();
-            while (!*abort_flag && global_ns() - t0 < 2 * kWaitNs) __nanosleep(1000);
-          }
           tc_fence_after();
           const uint32_t pa = smem_u32(sm + s * G::kStage), pb = pa + G::kTileA;
 #pragma unroll
@@ -261,15 +257,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 acc[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      int blocks = nkb;
+      if (a.stall == kStallLate && warp == 4 && tile == pair + pairs) {  // (tests) as if this warp's wait had run out just before its product
+        blocks = 0;
+        ok = false;
+        *abort_flag = 1;
+        if (a.error && lane == 0) atomicExch(a.error, 1);
+      }
       // the factors of two blocks ahead, multiplied only when they are needed: nothing waits for a load that has just been made
       float fa[2], fw[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        fa[i] = i < nkb ? sa[(int64_t)i * a.sa_stride] : 0.f;
-        fw[i] = i < nkb ? sw[i] : 0.f;
+        fa[i] = i < blocks ? sa[(int64_t)i * a.sa_stride] : 0.f;
+        fw[i] = i < blocks ? sw[i] : 0.f;
       }
 #pragma unroll 2
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
+      for (int kb = 0; kb < blocks; ++kb, ++it) {
         const int d = it & 1;
         // a warp that has given up once is out of step for good: what is left of its tiles is NaN too
         ok = ok && __all_sync(0xffffffffu, fwait(&B->done[d], (uint32_t)(it / 2) & 1u, abort_flag, a.error));
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float f1 = fa[kb & 1] * fw[kb & 1];
         const float2 f = make_float2(f1, f1);
-        if (kb + 2 < nkb) {
+        if (kb + 2 < blocks) {
           fa[kb & 1] = sa[(int64_t)(kb + 2) * a.sa_stride];
           fw[kb & 1] = sw[kb + 2];
         }

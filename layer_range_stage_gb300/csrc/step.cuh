@@ -46,7 +46,7 @@ struct NormF8Args {
 };
 cudaError_t launch_norm_f8(const NormF8Args& a, int x_dtype, int resid_dtype, cudaStream_t st);
 
-// For tests: nothing is copied, so that the waits run out; one product of each pair of CTAs comes after its time.
+// For tests: nothing is copied, so that the waits run out; a warp of each CTA gives up on its second tile.
 constexpr int kStallCopies = 1, kStallLate = 2;
 struct F8GemmArgs {
   const uint8_t* a = nullptr;
