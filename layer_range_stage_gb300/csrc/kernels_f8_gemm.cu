@@ -55,6 +55,14 @@ __device__ __forceinline__ bool fwait(uint64_t* bar, uint32_t parity, volatile i
   return true;
 }
 
+// At a CTA's end: the same with a limit of its own, whoever has given up.
+__device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_ns();
+  while (!sleep_wait(bar, parity))
+    if (global_ns() - t0 > kDrainNs) return false;
+  return true;
+}
+
 // acc += s * d for two neighbouring columns.  (The same in inline PTX costs a move for each operand: 231 us for 2048 x 28672 x 4096 where
 // this takes 202, and single multiply-adds 233.)
 __device__ __forceinline__ void fma2(float2& acc, uint32_t d0, uint32_t d1, float2 s) {
@@ -210,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(sm + s * G::kStage + G::kTileA, &tB, (kb0 + kb) * kBK, n0, bar);
         }
       }
-      // Nothing may still be landing in shared memory when the CTAs leave, whoever has given up.  The first CTA sees both's copies land; the
-      // second one's leaves after it, and where it gave up itself, after a time in which they have.
+      // Nothing may still be on its way to shared memory when the CTAs leave, whoever has given up.  The first CTA sees both's copies land;
+      // the second one's leaves after it, and where it gave up itself, after a time in which they have.
       if (rank == 0) {
         for (int k = max(0, it - G::kStages); k < it; ++k)
           mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
@@ -219,6 +227,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < kDrainNs) __nanosleep(1000);
       }
+      // The products' last arrivals, which come to both CTAs and which no barrier between these waits for (none comes where somebody gave
+      // up; those on `done` are waited for by the warps of the sums).
+      for (int k = max(0, it - G::kStages); k < it && !*abort_flag; ++k)
+        if (!drain_wait(&B->empty[k % G::kStages], (uint32_t)(k / G::kStages) & 1u)) break;
     } else if (warp == 1 && lane == 0 && rank == 0) {
       constexpr uint32_t idesc = idesc_f8_f32(kBM, kBN);
       int it = 0;
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_pair(&B->done[d], first);
         }
       if (it > 0) {  // the products finish before TMEM is released, whoever has given up
-        umma_commit_pair(&B->drain, first);
+        umma_commit_pair(&B->drain, first, 1u);
         mbar_wait(&B->drain, 0u, kDrainNs);
       }
     }
@@ -429,9 +441,11 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
         tma_load_2d(sm + s * G::kStage, &tW, (k0 + it) * kBK, n0, &B->full[s]);
         tma_load_2d(sm + s * G::kStage + G::kTileW, &tA, (k0 + it) * kBK, 0, &B->full[s]);
       }
-      // nothing may still be landing in shared memory when the CTA leaves, whoever has given up
+      // nothing may still be on its way to shared memory when the CTA leaves, whoever has given up: neither copies nor the products' arrivals
       for (int k = max(0, it - G::kStages); k < it; ++k)
         mbar_wait(&B->full[k % G::kStages], (uint32_t)(k / G::kStages) & 1u, kDrainNs);
+      for (int k = max(0, it - G::kStages); k < it && !*abort_flag; ++k)
+        if (!drain_wait(&B->empty[k % G::kStages], (uint32_t)(k / G::kStages) & 1u)) break;
     }
   } else if (warp == 5) {
     if (lane == 0) {

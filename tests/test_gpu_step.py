@@ -666,6 +666,33 @@ def test_products_of_every_kernel_captured_and_at_once(B, M):
     assert all(torch.equal(o, e) for o, e in zip(outs, want))
 
 
+def test_products_right_behind_one_another(B):
+    """CTAs of one call on SMs that others have just left: what these had in flight is done (the arrivals of a pair come to both its CTAs)."""
+    rng = np.random.default_rng(3)
+    calls = []
+    for M, N, K in ((300, 700, 384), (40, 700, 384), (1024, 5120, 128), (256, 512, 3200), (100, 300, 640), (12, 9856, 256), (2, 600, 384), (129, 257, 64)):
+        sa, sw = dev(rng.uniform(0.5, 1, (-(-K // 128), M)).astype(np.float32)), dev(rng.uniform(0.5, 1, (-(-N // 128), -(-K // 128))).astype(np.float32))
+        calls.append((put_f8(random_f8(rng, M, K)), sa, put_f8(random_f8(rng, N, K)), sw, torch.zeros(M, N, device="cuda")))
+    want = []
+    for c in calls:
+        B.stage_op_f8_gemm(*c)
+        torch.cuda.synchronize()
+        want.append(c[-1].clone())
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in rng.integers(0, len(calls), 200):
+            B.stage_op_f8_gemm(*calls[i], err)
+        for c in calls:
+            B.stage_op_f8_gemm(*c, err)
+    for _ in range(5):
+        for c in calls:
+            c[-1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert err.item() == 0 and all(torch.equal(c[-1], w) for c, w in zip(calls, want))
+
+
 def test_first_calls_inside_a_capture(B):
     """In a new process whose first calls are captured ones: nothing that a call does once may be what a capture forbids."""
     import subprocess
