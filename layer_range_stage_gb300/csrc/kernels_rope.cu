@@ -60,12 +60,13 @@ __device__ __forceinline__ Words<T, VEC> put_together(const float (&f)[VEC]) {
   return w;
 }
 
-// f / 2 pi as a 64-bit fraction of a turn
+// f / 2 pi as a 64-bit fraction of a turn (a negative one's by its magnitude: a fraction taken up to its turn would lose f's last bits)
 __device__ __forceinline__ uint64_t turn_of(double f) {
   constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
-  double t = f * kTurn;
+  double t = fabs(f) * kTurn;
   t -= floor(t);
-  return __double2ull_rn(t * 18446744073709551616.0);
+  const uint64_t turn = __double2ull_rn(t * 18446744073709551616.0);
+  return f < 0.0 ? 0 - turn : turn;
 }
 
 __device__ __forceinline__ float2 cos_sin_of(int pos, uint64_t turn, float scale) {

@@ -467,6 +467,17 @@ def test_rope_positions_from_zero_to_the_last(B):
     check_rope(B, rng.standard_normal((100, 2, 16)), None, pos, -f, interleaved=True, scale=-0.5)
 
 
+def test_rope_of_negative_frequencies_at_the_last_positions(B):
+    """Turning backwards is as exact as turning forwards: small frequencies times positions next to 2^31."""
+    rng = np.random.default_rng(5)
+    f = -10.0 ** rng.uniform(-9, 0, 128)
+    pos = 2 ** 31 - 1 - rng.integers(0, 1000, 50)
+    q, k = rng.standard_normal((50, 4, 256)), rng.standard_normal((50, 2, 256))
+    check_rope(B, q, k, pos, f)
+    check_rope(B, q, k, pos, f, interleaved=True)
+    check_rope(B, q, k, pos, -f)
+
+
 def test_rope_of_no_numbers_and_padding_only(B):
     x = np.random.default_rng(1).standard_normal((3, 2, 64))
     x[1, 0, 3], x[2, 1, 40] = np.nan, np.inf
