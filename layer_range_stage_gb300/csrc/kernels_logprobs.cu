@@ -20,6 +20,7 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "kernels.cuh"
 #include "step.cuh"
 
 namespace cg = cooperative_groups;
@@ -28,8 +29,8 @@ namespace lrs {
 
 namespace {
 
-constexpr int kTop = 32, kMaxCluster = 8;
-constexpr int kMaxChunks = 16384;  // of a CTA: their maxima take 64 KB
+constexpr int kTop = 32, kMaxCluster = kLogprobsMaxCluster;
+constexpr int kMaxChunks = kLogprobsMaxChunks;  // of a CTA: their maxima take 64 KB
 constexpr int kSlack = 16;         // threads above the bound beyond the n_top that are needed, at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -390,9 +391,7 @@ template <typename T, bool TOP>
 cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t st) {
   constexpr int E = 32 / sizeof(T);
   const int chunks = (a.vocab + E - 1) / E + 1;  // a row that begins inside a chunk has one more
-  // a cluster of as many CTAs as the SMs hold without a second wave, of 1024 chunks or more each (64 x 128256: 14 us with four, 22 with eight)
-  int C = 1;
-  while (C < kMaxCluster && ((chunks + C - 1) / C > kMaxChunks || (a.rows * (int64_t)C <= 152 && chunks / C >= 1024))) C *= 2;
+  const int C = logprobs_cluster(chunks, a.rows, sm_count());
   const int per = (chunks + C - 1) / C;
   // one row's latency counts where a cluster shares it: more threads, each with fewer loads after one another
   if (C > 1) return launch_k<T, TOP, 512, 4>(a, C, per, st);

@@ -101,6 +101,14 @@ struct LogprobsArgs {
   int64_t stride = 0;
   int rows = 0, vocab = 0, top = 0;
 };
+constexpr int kLogprobsMaxCluster = 8, kLogprobsMaxChunks = 16384;  // chunks of 32 bytes of a CTA
+// CTAs of a row's cluster: as many as `sms` SMs hold without a second wave, of 1024 chunks or more each (64 x 128256: 14 us with four, 22 with
+// eight), and as many as a long row needs.
+inline int logprobs_cluster(int chunks, int rows, int sms) {
+  int C = 1;
+  while (C < kLogprobsMaxCluster && ((chunks + C - 1) / C > kLogprobsMaxChunks || (rows * (int64_t)C <= sms && chunks / C >= 1024))) C *= 2;
+  return C;
+}
 cudaError_t launch_logprobs(const LogprobsArgs& a, int dtype, cudaStream_t st);
 
 }  // namespace lrs

@@ -181,6 +181,32 @@ int main() {
     assert r.returncode == 0, r.stdout
 
 
+def test_a_rows_cluster_goes_by_the_sms_there_are(tmp_path):
+    """One wave of CTAs where rows are few, whatever the number of SMs, and never more of a row in a CTA than it has room for."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "cluster.cu"
+    src.write_text("""
+#include <cstdio>
+#include "step.cuh"
+int main() {
+  for (int sms = 1; sms <= 300; ++sms)
+    for (int rows = 1; rows <= 400; ++rows)
+      for (int chunks = 1; chunks <= (1 << 16) + 1; chunks = chunks < 3 ? chunks + 1 : chunks * 4 / 3 + 1) {
+        const int C = lrs::logprobs_cluster(chunks, rows, sms);
+        const bool room = (chunks + C - 1) / C <= lrs::kLogprobsMaxChunks;
+        const bool half = C > 1 && (chunks + C / 2 - 1) / (C / 2) <= lrs::kLogprobsMaxChunks;   // half of them would have the room
+        if (!room || C > lrs::kLogprobsMaxCluster || (half && (long)rows * (C / 2) > sms)) return printf("%d SMs, %d rows of %d chunks: %d\\n", sms, rows, chunks, C), 1;
+      }
+  return !(lrs::logprobs_cluster(18993, 1, 152) == 8 && lrs::logprobs_cluster(16033, 64, 152) == 4 && lrs::logprobs_cluster(2001, 4099, 152) == 1);
+}
+""")
+    subprocess.run([lbuild.nvcc(), *lbuild.ARCH, "-std=c++17", "-I", os.path.join(root, "layer_range_stage_gb300", "csrc"), "-o", str(tmp_path / "cluster"), str(src)], check=True, capture_output=True)
+    r = subprocess.run([str(tmp_path / "cluster")], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
+
+
 def test_late_calls_are_counted_from_none_to_sixteen():
     lib = L.lib()
     for calls in (-1, 17, 1 << 20):
