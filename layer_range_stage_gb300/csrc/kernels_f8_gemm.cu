@@ -68,7 +68,6 @@ __device__ __forceinline__ bool drain_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void fma2(float2& acc, uint32_t d0, uint32_t d1, float2 s) {
   acc = __ffma2_rn(make_float2(__uint_as_float(d0), __uint_as_float(d1)), s, acc);
 }
-__device__ __forceinline__ float2 unpack2(float2 v) { return v; }
 
 // ---- many rows: tiles of 256 rows x 256 columns, one persistent pair of CTAs per two SMs ----
 // A product of a pair reads from each SM's shared memory its 128 rows of a and half of the weights' 256, where two CTAs on their
@@ -79,15 +78,6 @@ __device__ __forceinline__ float2 unpack2(float2 v) { return v; }
 constexpr int kBM = 256, kBN = 256, kBK = 128, kThreads = 384;
 constexpr int kRegsStart = 168, kRegsRoles = 56, kRegsSums = 224;
 static_assert(128 * kRegsRoles + 256 * kRegsSums <= kThreads * kRegsStart, "the warpgroups share out what the block is launched with");
-
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 struct Big {
   static constexpr int kStages = 6;
@@ -119,7 +109,7 @@ __device__ __forceinline__ void store_rows(const float2 (&acc)[COLS / 2], unsign
       } o;
 #pragma unroll
       for (int i = 0; i < kUnit; i += 2) {
-        const float2 f = unpack2(acc[(p * kPiece + u * kUnit + i) / 2]);
+        const float2 f = acc[(p * kPiece + u * kUnit + i) / 2];
         o.v[i] = from_f32<T>(ok ? f.x : bad);
         o.v[i + 1] = from_f32<T>(ok ? f.y : bad);
       }
@@ -319,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4* row = reinterpret_cast<float4*>(sm) + (32 * quarter + lane) * (kBN / 4);
 #pragma unroll
         for (int i = 0; i < kHalf / 4; ++i) {
-          const float2 p = unpack2(acc[2 * i]), q = unpack2(acc[2 * i + 1]);
+          const float2 p = acc[2 * i], q = acc[2 * i + 1];
           row[(half * (kHalf / 4) + i) ^ lane] = make_float4(p.x, p.y, q.x, q.y);
         }
       }
@@ -517,7 +507,7 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
     if (warp < 4 && n0 + tid < a.N) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const float2 p = unpack2(acc[i / 2]);
+        const float2 p = acc[i / 2];
         if (i < a.M) y[(int64_t)i * a.y_stride + n0 + tid] = from_f32<T>(ok && whole ? (i & 1 ? p.y : p.x) : bad);
       }
     }
@@ -527,7 +517,7 @@ __global__ void __launch_bounds__(kSmallThreads, PER)
     if (warp < 4) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const float2 p = unpack2(acc[i / 2]);
+        const float2 p = acc[i / 2];
         if (i < a.M) sums[i * 128 + tid] = ok ? (i & 1 ? p.y : p.x) : bad;
       }
     }
