@@ -263,6 +263,37 @@ def test_product(B, dtype, M, N, K):
     check_gemm(B, random_f8(rng, M, K), sa, random_f8(rng, N, K), sw, dtype, gap=16 * (M % 3), ygap=M % 4)
 
 
+@pytest.mark.parametrize("M,N,K", [(513, 12801, 300), (1000, 10300, 512), (300, 30000, 100), (12, 9856, 700), (16, 9728, 300), (9, 9729, 300), (12, 39040, 300), (20, 39040, 140), (40, 39040, 300),
+                                   (64, 38912, 200), (33, 38913, 200)])
+def test_product_of_wide_weights(B, M, N, K):
+    """Several tiles of 256 x 256 for each pair of SMs, with an odd and an even number of blocks; few rows by more weight tiles than SMs, and than two
+    or three CTAs of each hold."""
+    rng = np.random.default_rng(M + N + K)
+    nb, kb = -(-N // 128), -(-K // 128)
+    sa, sw = rng.uniform(0.1, 1, (kb, M)).astype(np.float32), rng.uniform(0.1, 1, (nb, kb)).astype(np.float32)
+    a, w = random_f8(rng, M, K), random_f8(rng, N, K)
+    check_gemm(B, a, sa, w, sw, "f32", ygap=M % 2)
+    check_gemm(B, a, sa, w, sw, "bf16", gap=16)
+
+
+@pytest.mark.parametrize("M,N", [(1, 512), (8, 300), (12, 512), (12, 9856), (30, 512), (60, 400), (100, 512), (200, 600), (1024, 700)])
+def test_product_loses_no_bits_of_a_block(B, M, N):
+    """Whole numbers whose sums over a block stay below 2^24 (128 * 240^2 < 2^23): float32 holds each of them, in any order."""
+    t = step.e4m3_values()
+    whole = np.array([c for c in range(256) if t[c] == t[c] and t[c] == int(t[c]) and abs(t[c]) <= 240], np.uint8)
+    small = whole[np.abs(t[whole]) <= 3]
+    rng = np.random.default_rng(M)
+    for first in (False, True):
+        a, w = rng.choice(whole, (M, 128)), rng.choice(whole, (N, 128))
+        if first:                                    # one product of 240^2 beside small ones
+            a[:, 1:], a[:, 0], w[:, 0] = rng.choice(small, (M, 127)), 0x77, 0x77
+        y = torch.zeros(M, N, device="cuda")
+        B.stage_op_f8_gemm(put_f8(a), torch.ones(1, M, device="cuda"), put_f8(w), torch.ones(-(-N // 128), 1, device="cuda"), y)
+        want = t[a] @ t[w].T
+        assert (want % 2 != 0).any() and np.abs(want).max() > 2.0 ** 15
+        same(y.double().cpu().numpy(), want)
+
+
 def test_product_of_exact_numbers(B):
     """Small whole numbers with powers of two as scales: every sum is exact, whatever its order, so the result is too."""
     rng = np.random.default_rng(5)
@@ -465,6 +496,19 @@ def test_rope_positions_from_zero_to_the_last(B):
     pos = np.concatenate([np.arange(80), 2 ** 31 - 1 - np.arange(20)])
     check_rope(B, rng.standard_normal((100, 2, 16)), rng.standard_normal((100, 1, 16)), pos, f)
     check_rope(B, rng.standard_normal((100, 2, 16)), None, pos, -f, interleaved=True, scale=-0.5)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype,n,hq,hk,d,rot", [("f32", 6000, 2, 1, 64, 64), ("bf16", 6000, 2, 1, 64, 32), ("f16", 11003, 1, 0, 24, 8), ("f32", 5200, 1, 0, 1024, 1024), ("bf16", 5200, 1, 0, 1024, 512),
+                                                 ("f32", 5200, 1, 0, 301, 150), ("f32", 15000, 1, 1, 6, 4)])
+def test_rope_of_more_tokens_than_warps(B, dtype, interleaved, n, hq, hk, d, rot):
+    """A warp goes from token to token, padding among them: each token has its own cos and sin, in heads of more than 32 vectors too."""
+    rng = np.random.default_rng(n + d)
+    q, k = rng.standard_normal((n, hq, d)), rng.standard_normal((n, hk, d)) if hk else None
+    pos = rng.integers(0, 100000, n)
+    pos[rng.random(n) < 0.2] = -1
+    f, _ = step.rope_freqs(rot, 10000.0)
+    check_rope(B, q, k, pos, f, dtype, interleaved, 1.25, inplace=n % 1000 != 0)
 
 
 def test_rope_of_negative_frequencies_at_the_last_positions(B):
