@@ -62,7 +62,8 @@ STAGE_API int stage_op_norm_f8(const void* x_dev, int x_dtype, int64_t x_stride,
  * a_dev, w_dev and both row strides must be multiples of 16 bytes (what lies between a row's K codes and the next row does not
  * matter); y needs its elements' alignment, and is written 16 bytes at a time where base and rows are multiples of that.
  * Sums of a block are the tensor cores' float32, sums over blocks float32 in a fixed order: the same inputs give the same
- * bits for the same M.  Runs on `stream`.  M = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned pointers, type, M outside
+ * bits for the same M.  The two scales are multiplied first, in float32: where their product is below 2^-126 it loses bits, and where it
+ * is infinite so is what it scales, or NaN.  Runs on `stream`.  M = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned pointers, type, M outside
  * [0, 2^24], N outside [1, 2^24], K outside [1, 2^20], strides below a row, not a multiple of 16 bytes (a, w) or above
  * 2^32), STAGE_E_CUDA (tensor maps or the launch). */
 STAGE_API int stage_op_f8_gemm(const void* a_dev, int64_t a_stride, const float* a_scale_dev, int64_t a_scale_stride,

@@ -320,6 +320,24 @@ def test_product_every_tile_edge(B):
         same(y.double().cpu().numpy(), step.e4m3_values()[w][:, pick].T)
 
 
+@pytest.mark.parametrize("M,N", [(5, 300), (12, 9856), (40, 300), (100, 300), (300, 700)])
+def test_product_of_scales_at_the_ends_of_float32(B, M, N):
+    """The scales' product is one float32: 2^-140 is held, 2^130 is not."""
+    rng = np.random.default_rng(M)
+    a, w = (step.e4m3_codes(rng.integers(-8, 9, (n, 128))) for n in (M, N))
+    sa, sw = np.full((1, M), 2.0 ** -100, np.float32), np.full((-(-N // 128), 1), 2.0 ** -40, np.float32)
+    sa[0, 1], sa[0, 2] = 2.0 ** 100, 2.0 ** -20           # 2^60, and 2^-60
+    sw[1] = 2.0 ** 30                                     # 2^-70; 2^130 in the first of these rows
+    y = torch.zeros(M, N, device="cuda")
+    B.stage_op_f8_gemm(put_f8(a), dev(sa), put_f8(w), dev(sw), y)
+    got = y.double().cpu().numpy()
+    with np.errstate(over="ignore", invalid="ignore"):
+        factor = (sa.T * np.repeat(sw[:, 0], 128)[:N][None]).astype(np.float32).astype(np.float64)
+        want = step.f8_gemm(a, np.ones_like(sa), w, np.ones_like(sw))[0] * factor
+    assert np.isinf(factor[1, 128]) and 0 < factor[0, 0] < 2.0 ** -139
+    same(got, want)
+
+
 def test_product_keeps_rows_apart(B):
     """NaN in one row or weight row, infinite or zero scales: nothing else changes."""
     rng = np.random.default_rng(7)
