@@ -87,7 +87,7 @@ struct Big {
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
   static constexpr uint32_t kCols = 2 * kBN;
   struct Bars {
-    uint64_t full[kStages], empty[kStages], done[2], free_[2], drain;
+    uint64_t full[kStages], empty[kStages], done[2], free_[2];
   };
 };
 
@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B->done[i], 1);
       mbar_init(&B->free_[i], 16);
     }
-    mbar_init(&B->drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -238,10 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_pair(&B->empty[s], first);
           umma_commit_pair(&B->done[d], first);
         }
-      if (it > 0) {  // the products finish before TMEM is released, whoever has given up
-        umma_commit_pair(&B->drain, first, 1u);
-        mbar_wait(&B->drain, 0u, kDrainNs);
-      }
+      // the products finish before TMEM is released, whoever has given up
+      if (it > 0) drain_wait(&B->done[(it - 1) & 1], (uint32_t)((it - 1) / 2) & 1u);
     }
   } else {
     regs_up<kRegsSums>();

@@ -124,12 +124,12 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// arrive on the mbarrier at this place in both CTAs (the first one's rank in the cluster: `first`; ctas = 1: in that one alone) once every
-// MMA issued so far by this thread has completed
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t first, uint32_t ctas = 3u) {
+// arrive on the mbarrier at this place in both CTAs (the first one's rank in the cluster: `first`) once every MMA issued so far by this
+// thread has completed
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t first) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)(ctas << first))
+      "h"((uint16_t)(3u << first))
       : "memory");
 }
 // The address, in the cluster's window, of this CTA's shared-memory place in CTA `rank`.
