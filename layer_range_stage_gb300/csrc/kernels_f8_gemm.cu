@@ -5,11 +5,12 @@
 // registers.  A row of the output lies in one TMEM lane and 128 columns share a weight scale, so a thread's factor is one number
 // per block.  Two TMEM buffers: the products of the next block run while this one's are read.
 //
-// 2048 x 28672 x 4096: 204 us, 2.36 PFLOP/s.  The copies and products alone take 141 us (half the bytes: 121), with the
+// 2048 x 28672 x 4096: 208 us, 2.31 PFLOP/s.  The copies and products alone take 141 us (half the bytes: 121), with the
 // buffers handed over 159, read back 174, added up 204: reading and adding is what bounds it, though no unit of it is busy for half
 // the time.  Tried on it: columns in two halves with four buffers (292: a product of 128 columns takes as long as one of 256), 16
 // warps of sums with 64 columns each (220), 32 TMEM columns at a time (221..231: registers), the factors by asynchronous copies
-// (209..216), one commit per block (the same), a lane that waits for its warp (240), waits that ask all the time (266).
+// (209..216), one commit per block (the same), a lane that waits for its warp (240), waits that ask all the
+// time (266); one comparison more in the loop that issues the products takes 237.
 #include <algorithm>
 #include <atomic>
 

@@ -5,7 +5,8 @@
 // reduction and its codes are one store of 128 bytes.  The bytes in and out are its floor; what bounds it is the chain from a row's
 // loads over its sum to its stores, with 32 warps on an SM: 2048 x 4096 (bfloat16 onto float32) 18 us, 5.1 TB/s; 16411 x 8192 in
 // bfloat16 207 us, 4.6 TB/s (its warps' sums and roots are a third of the instructions there; one warp that finishes for the row: 231,
-// for its second barrier); one row of 4096 2.7 us.
+// for its second barrier); float32 255 us, 6.9 TB/s; one row of 4096 2.7 us.  Rows of more than 16384 columns do not fit their registers:
+// 4096 x 28672 in bfloat16 99 us without gamma, 3.6 TB/s.
 //
 // The codes are defined by float32 roundings, so two machines agree if they agree on r = fl(1 / sqrt(mean + eps)).  A float32
 // sum would not do: its last bits depend on its order, and where r differs by one unit so does a code now and then.
@@ -339,7 +340,8 @@ cudaError_t launch_ch(const NormF8Args& a, int warps, int rows, cudaStream_t st)
 template <typename TX, typename TR>
 cudaError_t launch_t(const NormF8Args& a, cudaStream_t st) {
   const int nb = (a.n + 127) / 128;
-  // blocks per warp: few, so that a row is done soon, as long as 16 warps hold it (16411 x 8192: 212 us with four, 222 with eight)
+  // blocks per warp: few, so that a row is done soon, as long as 16 warps hold it (16411 x 8192: bfloat16 207 us with four, 230 with eight;
+  // float32 255 and 263)
   const int ch = nb > 128 ? 16 : nb > 64 ? 8 : 4;
   const int warps = (nb + ch - 1) / ch;
   const int rows = warps == 1 ? 4 : 1;
