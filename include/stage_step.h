@@ -40,8 +40,9 @@ extern "C" {
  *     elements (block after block, as stage_op_f8_gemm reads them).  Both may be NULL when y_dev is given.
  *   y_dev: y rounded once to x_dtype, rows at y_stride elements, or NULL.
  * Bytes between a row's n columns and the next row are left as they were.  A row whose sum of squares is no finite
- * float32, or whose mean + eps is below 2^-256 (zeros with eps = 0), gives NaN throughout (with gamma); a
- * block that holds an infinity or a NaN gets a scale that is not finite: all of it reads as NaN.  Apart from resid_out = resid no output may overlap an input or another output.
+ * float32, or whose mean + eps is below 2^-256 (zeros with eps = 0), gives NaN throughout (with gamma); a block that holds an
+ * infinity or a NaN gets a scale that is not finite: all of it reads as NaN.  Apart from resid_out = resid no output may overlap
+ * an input or another output.
  * Rows need their elements' alignment only; with rows and bases at multiples of four elements they are read and written four
  * elements at a time.  Runs on `stream`.  n_tok = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned
  * pointers, types, n_tok outside [0, 2^24], n outside [1, 32768], strides below a row or above 2^32, eps negative
@@ -62,9 +63,10 @@ STAGE_API int stage_op_norm_f8(const void* x_dev, int x_dtype, int64_t x_stride,
  * a_dev, w_dev and both row strides must be multiples of 16 bytes (what lies between a row's K codes and the next row does not
  * matter); y needs its elements' alignment, and is written 16 bytes at a time where base and rows are multiples of that.
  * Sums of a block are the tensor cores' float32, sums over blocks float32 in a fixed order: the same inputs give the same
- * bits for the same M.  The two scales are multiplied first, in float32: where their product is below 2^-126 it loses bits, and where it
- * is infinite so is what it scales, or NaN.  Runs on `stream`.  M = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned pointers, type, M outside
- * [0, 2^24], N outside [1, 2^24], K outside [1, 2^20], strides below a row, not a multiple of 16 bytes (a, w) or above
+ * bits for the same M.  The two scales are multiplied first, in float32: where their product is below 2^-126 it loses bits, and
+ * where it is infinite so is what it scales, or NaN.
+ * Runs on `stream`.  M = 0 does nothing.  Errors: STAGE_E_INVALID (null or unaligned pointers, type, M outside
+ * [0, 2^24], N outside [1, 2^24], M * N above 2^40, K outside [1, 2^20], strides below a row, not a multiple of 16 bytes (a, w) or above
  * 2^32), STAGE_E_CUDA (tensor maps or the launch). */
 STAGE_API int stage_op_f8_gemm(const void* a_dev, int64_t a_stride, const float* a_scale_dev, int64_t a_scale_stride,
                                const void* w_dev, int64_t w_stride, const float* w_scale_dev, int M, int N, int K,
